@@ -77,6 +77,7 @@ def draw(rng):
                     pad=rng.choice([0, 0, k // 7]), type=rng.choice(["bf16", "fp16"]))
     if op == "heads":
         dim, block, kv = rng.choice([64, 128]), rng.choice([1, 1, 2, 4, 8, 16]), rng.randint(1, 8)
+        block = min(block, 1024 // dim)                            # a row holds at most 4096 bytes
         kv = max(1, min(kv, (4096 - 80) // (2 * dim * block)))
         k = max(1, _log(rng, 1, 2048) // block)
         return dict(op=op, requests=_log(rng, 1, 64), k=k, heads=kv * _log(rng, 1, 16), kv_heads=kv, head_dim=dim,
