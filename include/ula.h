@@ -240,6 +240,36 @@ int ula_append(ula_ctx* ctx, int32_t group, int32_t n, const int32_t* la_host,
  * changes on error. */
 int ula_release(ula_ctx* ctx, int32_t group, int32_t n, const int32_t* la_host, uint64_t stream);
 
+/* Copy the n entries at addresses src .. src + n - 1 of group g to the new
+ * addresses dst .. dst + n - 1 (a request that forks, in a beam or for several
+ * samples: sections 1 and 2, one shared pool, placement is the library's):
+ * exactly ula_append of the destination addresses, in ascending order, with the
+ * sources' rows, whichever pool holds them; the rows never pass through the host
+ * program. Sources stay as they are (under ULA_PLACE_RING an append may move one
+ * to the host pool, as any entry). The new entries belong to no step yet: select
+ * them in the next one, or gather them before it through the mapping table
+ * (ULA_ENOTRESIDENT if they were placed in the host pool). Enqueued on `stream`,
+ * ordered after the group's earlier calls like ula_append; not in a graph
+ * capture (ULA_EINVAL).
+ * Validated on the host first: ULA_EINVAL (bad g or n < 0), ULA_ERANGE (an address
+ * outside [0, N), or a source not appended), ULA_EDUP (a destination already
+ * appended, so also ranges that overlap), ULA_EHOSTFULL (not enough free slots in
+ * total), ULA_ESTATE; nothing changes on error. */
+int ula_fork(ula_ctx* ctx, int32_t group, int32_t src, int32_t dst, int32_t n, uint64_t stream);
+
+/* Give the n entries at addresses src .. src + n - 1 of group g the addresses dst
+ * .. dst + n - 1 (section 2: the table maps addresses to places; here only the
+ * table and the owner words change, no row moves): compaction of the address
+ * space after releases. The ranges may overlap, as in memmove; a destination
+ * must be absent or one of the sources. Slots, buckets, timestamps, the
+ * completion counter and the statistics do not change. Gathers of the last step's
+ * selection afterwards resolve through the mapping table (an old address is then
+ * ULA_ERANGE or another entry). Enqueued and ordered like ula_fork.
+ * Validated on the host first: ULA_EINVAL, ULA_ERANGE (an address outside [0, N),
+ * or a source not appended), ULA_EDUP (a destination taken by another entry),
+ * ULA_ESTATE; nothing changes on error. */
+int ula_rename(ula_ctx* ctx, int32_t group, int32_t src, int32_t dst, int32_t n, uint64_t stream);
+
 /* One decode step (one scheduling round) of group g over n_sets x k selected
  * addresses (device memory, row-major, -1 = padding), section 3: de-duplicate
  * (first occurrence in row-major order) and look up once for the group; advance
@@ -316,6 +346,146 @@ int ula_gather(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32
  * layers_per_group. */
 int ula_gather_layers(ula_ctx* ctx, int32_t group, int32_t layer0, int32_t n_layers, int32_t n_sets,
                       int32_t k, const int32_t* sel_dev, void* out_dev, uint64_t stream);
+
+/* ---- Operators on the rows' contents ------------------------------------
+ * The calls above move rows as opaque bytes. The ones below read or write what
+ * is in them, in one of two formats with values in e4m3 (OCP 8-bit floating
+ * point, 4 exponent and 3 fraction bits, no infinities) and fp32 scales
+ * (section 4: the KV cache is held in FP8). Integers and floats are stored
+ * little-endian, in this order and without gaps:
+ *
+ *  ULA_ROWS_LATENT, 656 bytes: 512 latent channels e4m3 | 64 rotary channels
+ *    bf16 | 4 scales fp32, one per 128 latent channels. One token per entry; one
+ *    representation serves every query head (section 1).
+ *      key   = [latent channel x its scale (512), rotary channels (64)]
+ *      value = [latent channel x its scale (512)]
+ *  ULA_ROWS_HEADS: keys e4m3 [kv_heads][block_tokens][head_dim] | values e4m3,
+ *    the same shape | key scales fp32 [kv_heads] | value scales fp32 [kv_heads]
+ *    | int32 tokens of the block in use, 0..block_tokens (outside that range it
+ *    counts as the nearest end) | zeros up to a multiple of 16 bytes. An entry
+ *    is a block of block_tokens tokens with one scale per head for its keys and
+ *    one for its values; tokens behind the count are never used. Query heads
+ *    are shared evenly: head h reads KV head h / (heads / kv_heads). */
+enum { ULA_BF16 = 0, ULA_FP16 = 1, ULA_FP32 = 2 };
+enum { ULA_ROWS_LATENT = 0, ULA_ROWS_HEADS = 1 };
+
+typedef struct {
+  int32_t kind;              /* ULA_ROWS_LATENT or ULA_ROWS_HEADS */
+  int32_t kv_heads;          /* heads rows: >= 1 (latent rows: this and the next two are not read) */
+  int32_t head_dim;          /* heads rows: 64 or 128 */
+  int32_t block_tokens;      /* heads rows: 1, 2, 4, 8 or 16 */
+} ula_row_format;
+
+/* Bytes of one row (one layer of one entry) of a format, a multiple of 16; 0 for
+ * an invalid one or one that is longer than 4096 bytes, the most a row can be. */
+size_t ula_row_format_bytes(const ula_row_format* rows);
+
+/* Rotary positions. Of R rotated channels, pair i (0 <= i < R / 2) turns by the
+ * angle pos[axis(i)] * theta^(-2i / R): (x0, x1) becomes (x0 cos - x1 sin,
+ * x0 sin + x1 cos). Pair i is channels (i, i + R / 2), or (2i, 2i + 1) if
+ * interleaved. The first sections[0] pairs go by the first axis, the next
+ * sections[1] by the second, the rest by the third (for text one axis; for images
+ * and video two or three, such as time, height, width). Positions are int32,
+ * negative ones too; angles are computed in 64 bits. */
+typedef struct {
+  int32_t axes;              /* 1, 2 or 3 */
+  int32_t sections[3];       /* pairs of each axis, >= 0; those of the axes in use sum to R / 2 */
+  int32_t interleaved;       /* 0 or 1 */
+  double theta;              /* base, finite and > 0 */
+} ula_rotary;
+
+typedef struct {
+  ula_row_format rows;
+  int32_t type;              /* of the inputs: ULA_BF16, ULA_FP16 or ULA_FP32 */
+  int32_t n;                 /* entries */
+  int32_t layers;            /* rows per entry */
+  const void* a;             /* latent rows: latent channels [n][layers][512]
+                                heads rows: keys [n][layers][block_tokens][kv_heads][head_dim] */
+  const void* b;             /* latent rows: rotary channels [n][layers][64]
+                                heads rows: values, shaped as the keys */
+  int64_t a_stride[4];       /* strides in elements: entry, layer, then (heads rows) token, head; */
+  int64_t b_stride[4];       /*   the last dimension is contiguous */
+  const int32_t* positions;  /* nullable (nothing turns): [n][axes], heads rows [n][block_tokens][axes], packed */
+  const int32_t* count;      /* heads rows, nullable (all in use): tokens in use of each entry, [n] */
+  ula_rotary rotary;         /* read if positions is given; turns the rotary channels, or whole keys */
+} ula_pack_args;
+
+/* Write n x layers rows in the given format to rows_dev (device memory, packed,
+ * 16-byte aligned: what ula_append takes as device rows). scale = max(amax / 448,
+ * 2^-126) over each scale's values (heads rows: over the tokens in use; the
+ * others' codes are 0), code = value / scale rounded to nearest even. An infinity
+ * takes the largest code and a NaN the NaN code; neither enters amax. Rotary
+ * channels are turned in 32 bits and rounded to bf16 once. A pure function of its
+ * device inputs: nothing of an engine is involved, and it may be captured into a
+ * graph. Errors: ULA_EINVAL (null pointer, n or layers < 0, unknown type, invalid
+ * format or rotary, misaligned pointers), ULA_EHIP. */
+int ula_pack_rows(const ula_pack_args* args, void* rows_dev, uint64_t stream);
+
+typedef struct {
+  int32_t type;              /* of x and out: ULA_BF16, ULA_FP16 or ULA_FP32 */
+  int32_t n, heads, dim;     /* tokens, heads, channels of a head: even, 2..256, all turned */
+  int32_t inverse;           /* 1: turn back, which is also the gradient of the turn */
+  const void* x;             /* [n][heads][dim], last dimension contiguous */
+  void* out;                 /* the same shape; x itself with the same strides, or no overlap */
+  int64_t x_stride[2];       /* strides in elements: token, head */
+  int64_t out_stride[2];
+  const int32_t* positions;  /* [n][axes] packed */
+  ula_rotary rotary;
+} ula_rotate_args;
+
+/* Turn the heads of n tokens (the rotary part of queries, or its way back) by
+ * their positions; each result is rounded to its type once. A pure function of
+ * its device inputs; it may be captured into a graph. Errors: ULA_EINVAL, ULA_EHIP. */
+int ula_rotate(const ula_rotate_args* args, uint64_t stream);
+
+typedef struct {
+  ula_row_format rows;       /* the group's rows; its bytes must equal the configuration's row_bytes */
+  int32_t type;              /* of q and out: ULA_BF16 or ULA_FP16 */
+  int32_t heads;             /* query heads, >= 1; heads rows: a multiple of kv_heads */
+  float scale;               /* factor of the logits, finite */
+  const void* q;             /* [n_sets][heads][576 (latent) or head_dim], last dimension contiguous */
+  int64_t q_set_stride;      /* strides in elements */
+  int64_t q_head_stride;
+  void* out;                 /* [n_sets][heads][512 (latent) or head_dim], last dimension contiguous */
+  int64_t out_set_stride;
+  int64_t out_head_stride;
+  float* lse;                /* nullable, [n_sets][heads] packed: ln of the sum of exp(logits) */
+  void* workspace;           /* device memory of ula_attend_bytes bytes, 16-byte aligned; may be NULL for 0 */
+  size_t workspace_bytes;
+} ula_attend_args;
+
+/* Bytes of workspace that ula_attend needs for these sizes (0: none, or an
+ * invalid argument, which ula_attend reports). A pure host function. */
+size_t ula_attend_bytes(const ula_row_format* rows, int32_t n_sets, int32_t k, int32_t heads);
+
+/* Attention of every selection set's queries over its selected entries of layer
+ * `layer` of group g, read from the GPU pool where they lie (introduction:
+ * attention reads only the selected KV rows; section 3: after the completion
+ * signal):
+ *   logit_j = scale * q . key_j,  out = sum_j softmax(logit)_j value_j
+ * over the entries j of the set (every token in use of each entry for heads
+ * rows). -1 entries contribute nothing; a set with nothing else gives out = 0
+ * and lse = -inf. An address listed more than once counts as often. Sums, the
+ * softmax and the products' accumulators are in 32 bits; keys enter exactly,
+ * softmax weights times value scales are rounded to bf16 before the second
+ * product, results once to the type of out. A NaN or an infinite logit makes that
+ * head's outputs NaN; no unselected row is ever read. The order of the sums
+ * depends on the sizes alone, so the same call gives the same bits.
+ * Results split over several workgroups are joined through the workspace, which
+ * belongs to the call until the stream has run it: calls that may run at the
+ * same time need workspaces of their own. q, out, lse and the workspace must not
+ * overlap. 16-byte aligned q rows and 8-byte aligned out rows (pointer and
+ * strides) are read and written in vectors, others element by element.
+ * Which entries, streams and errors: as for ula_gather (the selection is looked
+ * up through the group's last step where it is that step's, else through the
+ * mapping table; on another stream the call must be ordered after the step; the
+ * library orders the group's later row moves after it). It may not be captured
+ * into a graph, since the step it belongs to is fixed at the call: ULA_EINVAL.
+ * Host errors: ULA_EINVAL, ULA_ESTATE, ULA_ENOTRESIDENT (no step yet), ULA_EHIP.
+ * Device errors (reported by ula_sync): ULA_ENOTRESIDENT, ULA_ERANGE; an entry
+ * with such an error counts as padding. */
+int ula_attend(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32_t k,
+               const int32_t* sel_dev, const ula_attend_args* args, uint64_t stream);
 
 /* Wait for `stream`, then report the first latched device error of any group
  * (poisoning the context) or ULA_OK (section 3: a host waiter for the steps'

@@ -1,8 +1,7 @@
 """Build libula.so (the HIP engine) for gfx950 with hipcc, in-tree.
 
 Each translation unit compiles in parallel into _build/, then one hipcc link
-produces serving_pb_lru_amd/libula.so. Packed FP32 instructions are turned off
-(no float math lives here, the flag only keeps the compiler from emitting them).
+produces serving_pb_lru_amd/libula.so. Packed FP32 instructions are turned off.
 """
 
 from __future__ import annotations
@@ -18,6 +17,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libula.so")
 SOURCES = ["k_init.hip", "k_lookup.hip", "k_select.hip", "k_lru.hip", "k_move.hip", "k_gather.hip",
+           "k_attend.hip", "k_attend_heads.hip", "k_rows.hip", "k_entries.hip",
            "runtime.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")

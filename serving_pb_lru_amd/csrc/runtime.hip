@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -11,7 +12,7 @@
 #include <string>
 #include <vector>
 
-#include "ula_internal.h"
+#include "row_format.h"
 
 using namespace ula;
 
@@ -348,6 +349,44 @@ static int wait_gathers(GroupHost& gh, hipStream_t s) {
     p.live = false;
   }
   return ULA_OK;
+}
+
+// Whether stream s is being captured into a graph (the engine's calls keep host
+// state that a replay would not see).
+static int refuse_capture(hipStream_t s) {
+  hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+  HIP_TRY(hipStreamIsCapturing(s, &st));
+  return st == hipStreamCaptureStatusNone ? ULA_OK : ULA_EINVAL;
+}
+
+// The host mirror over a range of addresses: whether any (all) are appended, and
+// marking them, whole words at a time.
+template <typename F>
+static bool for_words(int32_t first, int32_t n, F f) {
+  for (int64_t la = first, end = (int64_t)first + n; la < end;) {
+    const int64_t stop = std::min<int64_t>(end, (la | 63) + 1);
+    const int width = (int)(stop - la);
+    const uint64_t mask = (width == 64 ? ~0ull : (1ull << width) - 1) << (la & 63);
+    if (!f((size_t)(la >> 6), mask)) return false;
+    la = stop;
+  }
+  return true;
+}
+
+static bool none_appended(const GroupHost& gh, int32_t first, int32_t n) {
+  return for_words(first, n, [&](size_t w, uint64_t m) { return (gh.appended[w] & m) == 0; });
+}
+
+static bool all_appended(const GroupHost& gh, int32_t first, int32_t n) {
+  return for_words(first, n, [&](size_t w, uint64_t m) { return (gh.appended[w] & m) == m; });
+}
+
+static void mark_range(GroupHost& gh, int32_t first, int32_t n, bool on) {
+  for_words(first, n, [&](size_t w, uint64_t m) {
+    if (on) gh.appended[w] |= m;
+    else gh.appended[w] &= ~m;
+    return true;
+  });
 }
 
 extern "C" {
@@ -751,6 +790,95 @@ int ula_release(ula_ctx* ctx, int32_t group, int32_t n, const int32_t* la_host, 
   return ULA_OK;
 }
 
+// Checks that fork and rename share.
+static int validate_ranges(const ula_ctx* ctx, int32_t group, int32_t src, int32_t dst, int32_t n) {
+  if (!ctx) return ULA_EINVAL;
+  if (ctx->poisoned) return ULA_ESTATE;
+  if (group < 0 || group >= ctx->cfg.num_groups || n < 0) return ULA_EINVAL;
+  if (n == 0) return ULA_OK;
+  if (src < 0 || dst < 0 || n > ctx->dims.N || src > ctx->dims.N - n || dst > ctx->dims.N - n) return ULA_ERANGE;
+  if (!all_appended(ctx->groups[group], src, n)) return ULA_ERANGE;
+  return ULA_OK;
+}
+
+int ula_fork(ula_ctx* ctx, int32_t group, int32_t src, int32_t dst, int32_t n, uint64_t stream) {
+  {
+    const int rc = validate_ranges(ctx, group, src, dst, n);
+    if (rc || n == 0) return rc;
+  }
+  GroupHost& gh = ctx->groups[group];
+  const Dims& d = ctx->dims;
+  if (!none_appended(gh, dst, n)) return ULA_EDUP;
+  if (gh.n_appended + n > d.P + d.H) return ULA_EHOSTFULL;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  {
+    const int rc = refuse_capture(s);
+    if (rc) return rc;
+  }
+  const GroupDev& g = gh.d;
+  const bool ring = d.placement == ULA_PLACE_RING;
+  if (ring) {   // it evicts GPU entries: pending gathers first
+    const int rc = wait_gathers(gh, s);
+    if (rc) return rc;
+  }
+  for (int64_t done = 0; done < n; done += d.maxApp) {
+    const int32_t off = (int32_t)done;
+    const int32_t cnt = (int32_t)std::min<int64_t>(n - done, d.maxApp);
+    if (ring) {
+      HIP_TRY(launch_fork_collect(g, src + off, dst + off, cnt, s));
+      const PlanArgs a = ring_append_plan(cnt, (int32_t)(gh.steps % d.B), (int32_t)d.B);
+      HIP_TRY(launch_plan(g, a, s));
+      HIP_TRY(launch_extract(g, kPlanAppendRing, a.dest, 2 * cnt, s));
+      HIP_TRY(launch_place_ring(g, cnt, g.app_rows, s));
+    } else {
+      PlanArgs a{};
+      a.mode = kPlanAppend;
+      a.n = cnt;
+      a.norder = 2;
+      a.dest = kCold;
+      a.order[0] = kFree;
+      a.order[1] = kHostFreeId;
+      HIP_TRY(launch_plan(g, a, s));
+      HIP_TRY(launch_extract(g, kPlanAppend, kCold, cnt, s));
+      HIP_TRY(launch_fork_place(g, src + off, dst + off, cnt, s));
+    }
+    mark_range(gh, dst + off, cnt, true);
+    gh.n_appended += cnt;
+  }
+  return ULA_OK;
+}
+
+int ula_rename(ula_ctx* ctx, int32_t group, int32_t src, int32_t dst, int32_t n, uint64_t stream) {
+  {
+    const int rc = validate_ranges(ctx, group, src, dst, n);
+    if (rc || n == 0) return rc;
+  }
+  if (src == dst) return ULA_OK;
+  GroupHost& gh = ctx->groups[group];
+  // the destinations that are not sources: all of them, or the part that sticks out
+  const int64_t apart = std::llabs((int64_t)src - dst);
+  const int32_t out = (int32_t)std::min<int64_t>(n, apart);
+  const int32_t out0 = dst < src ? dst : dst + n - out;
+  if (!none_appended(gh, out0, out)) return ULA_EDUP;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  {
+    const int rc = refuse_capture(s);
+    if (rc) return rc;
+  }
+  // chunks in memmove's order: a chunk's destinations are never sources of a later one
+  const int32_t most = (int32_t)std::min<int64_t>(ctx->dims.maxApp, n);
+  const int32_t chunks = (n + most - 1) / most;
+  for (int32_t c = 0; c < chunks; ++c) {
+    const int32_t at = (dst < src ? c : chunks - 1 - c) * most;
+    const int32_t cnt = std::min(most, n - at);
+    HIP_TRY(launch_rename(gh.d, src + at, dst + at, cnt, s));
+  }
+  mark_range(gh, src, n, false);
+  mark_range(gh, dst, n, true);
+  gh.last_n = 0;   // the last step's resolved selection names the old addresses
+  return ULA_OK;
+}
+
 // The evicted rows a step stages reach the host in the group's next step (the
 // write-back workgroups of its mark launch). Before the host reads rows, a
 // stand-alone write-back puts the staged rows there too (those of the last
@@ -927,6 +1055,214 @@ int ula_gather(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32
 int ula_gather_layers(ula_ctx* ctx, int32_t group, int32_t layer0, int32_t n_layers, int32_t n_sets,
                       int32_t k, const int32_t* sel_dev, void* out_dev, uint64_t stream) {
   return gather_impl(ctx, group, layer0, n_layers, n_sets, k, sel_dev, out_dev, stream);
+}
+
+// ---- operators on the rows' contents --------------------------------------
+
+size_t ula_row_format_bytes(const ula_row_format* f) {
+  if (!f) return 0;
+  if (f->kind == ULA_ROWS_LATENT) return kLatentRow;
+  if (f->kind != ULA_ROWS_HEADS) return 0;
+  if (f->kv_heads < 1 || f->kv_heads > 4096) return 0;
+  if (f->head_dim != 64 && f->head_dim != 128) return 0;
+  const int t = f->block_tokens;
+  if (t != 1 && t != 2 && t != 4 && t != 8 && t != 16) return 0;
+  const size_t bytes = ((size_t)f->kv_heads * (2 * t * f->head_dim + 8) + 4 + 15) / 16 * 16;
+  return bytes <= 4096 ? bytes : 0;
+}
+
+// Device form of rotary positions over `pairs` pairs; false for invalid ones.
+static bool rotary_dev(const ula_rotary& r, int pairs, RotaryDev* d) {
+  if (r.axes < 1 || r.axes > 3 || pairs < 1 || pairs > kMostPairs) return false;
+  if (r.interleaved != 0 && r.interleaved != 1) return false;
+  if (!std::isfinite(r.theta) || !(r.theta > 0)) return false;
+  int64_t sum = 0;
+  for (int i = 0; i < r.axes; ++i) {
+    if (r.sections[i] < 0) return false;
+    sum += r.sections[i];
+  }
+  if (sum != pairs) return false;
+  d->axes = r.axes;
+  d->end0 = r.sections[0];
+  d->end1 = r.sections[0] + (r.axes > 1 ? r.sections[1] : 0);
+  d->interleaved = r.interleaved;
+  for (int i = 0; i < pairs; ++i) {
+    d->turns[i] = std::pow(r.theta, -(double)i / pairs) / 6.283185307179586476925;
+    if (!std::isfinite(d->turns[i])) return false;
+  }
+  return true;
+}
+
+static bool element_size(int type, int* size) {
+  if (type == ULA_BF16 || type == ULA_FP16) *size = 2;
+  else if (type == ULA_FP32) *size = 4;
+  else return false;
+  return true;
+}
+
+int ula_pack_rows(const ula_pack_args* args, void* rows_dev, uint64_t stream) {
+  if (!args) return ULA_EINVAL;
+  const ula_pack_args& u = *args;
+  const size_t row_bytes = ula_row_format_bytes(&u.rows);
+  int size;
+  if (!row_bytes || !element_size(u.type, &size) || u.n < 0 || u.layers < 0) return ULA_EINVAL;
+  const bool latent = u.rows.kind == ULA_ROWS_LATENT;
+  if (latent && u.count) return ULA_EINVAL;
+  const int64_t rows = (int64_t)u.n * u.layers;
+  // one workgroup per row and KV head, twice; 2^31 - 1 workgroups are the most
+  if (rows * (latent ? 1 : 2 * u.rows.kv_heads) >= (1ll << 31)) return ULA_EINVAL;
+  RotaryDev rot{};
+  if (u.positions && !rotary_dev(u.rotary, latent ? kRope / 2 : u.rows.head_dim / 2, &rot)) return ULA_EINVAL;
+  if (rows == 0) return ULA_OK;
+  if (!u.a || !u.b || !rows_dev || (uintptr_t)rows_dev % 16) return ULA_EINVAL;
+  if (((uintptr_t)u.a | (uintptr_t)u.b) % size || ((uintptr_t)u.positions | (uintptr_t)u.count) % 4) return ULA_EINVAL;
+  PackDev a{};
+  a.a = u.a;
+  a.b = u.b;
+  a.positions = u.positions;
+  a.count = u.count;
+  a.rows = static_cast<uint8_t*>(rows_dev);
+  for (int i = 0; i < 4; ++i) {
+    a.a_stride[i] = u.a_stride[i];
+    a.b_stride[i] = u.b_stride[i];
+  }
+  a.n = u.n;
+  a.layers = u.layers;
+  a.latent = latent;
+  a.aligned = (uintptr_t)u.a % 16 == 0 && u.a_stride[0] * size % 16 == 0 && u.a_stride[1] * size % 16 == 0;
+  a.kv_heads = u.rows.kv_heads;
+  a.head_dim = u.rows.head_dim;
+  a.block_tokens = u.rows.block_tokens;
+  a.row_bytes = (int32_t)row_bytes;
+  HIP_TRY(launch_pack(a, rot, u.type, reinterpret_cast<hipStream_t>(stream)));
+  return ULA_OK;
+}
+
+int ula_rotate(const ula_rotate_args* args, uint64_t stream) {
+  if (!args) return ULA_EINVAL;
+  const ula_rotate_args& u = *args;
+  int size;
+  if (!element_size(u.type, &size) || u.n < 0 || u.heads < 0) return ULA_EINVAL;
+  if (u.dim < 2 || u.dim % 2 || u.dim > 2 * kMostPairs || (u.inverse != 0 && u.inverse != 1)) return ULA_EINVAL;
+  if ((int64_t)u.n * u.heads >= (1ll << 31)) return ULA_EINVAL;
+  RotaryDev rot{};
+  if (!rotary_dev(u.rotary, u.dim / 2, &rot)) return ULA_EINVAL;
+  if (u.n == 0 || u.heads == 0) return ULA_OK;
+  if (!u.x || !u.out || !u.positions) return ULA_EINVAL;
+  if (((uintptr_t)u.x | (uintptr_t)u.out) % size || (uintptr_t)u.positions % 4) return ULA_EINVAL;
+  RotateDev a{};
+  a.x = u.x;
+  a.out = u.out;
+  a.positions = u.positions;
+  // vectors of four pairs: 8 interleaved elements, or 4 from each half
+  const int vec = (u.rotary.interleaved ? 8 : 4) * size;
+  a.aligned = u.dim % 8 == 0 && ((uintptr_t)u.x | (uintptr_t)u.out) % vec == 0;
+  for (int i = 0; i < 2; ++i) {
+    a.x_stride[i] = u.x_stride[i];
+    a.out_stride[i] = u.out_stride[i];
+    if (u.x_stride[i] * size % vec || u.out_stride[i] * size % vec) a.aligned = 0;
+  }
+  a.n = u.n;
+  a.heads = u.heads;
+  a.dim = u.dim;
+  a.inverse = u.inverse;
+  HIP_TRY(launch_rotate(a, rot, u.type, reinterpret_cast<hipStream_t>(stream)));
+  return ULA_OK;
+}
+
+// The sizes of an attention call as a plan; false for invalid ones.
+static bool plan_attend(const ula_row_format* f, int32_t n_sets, int32_t k, int32_t heads, AttendPlan* plan,
+                        int* width) {
+  if (ula_row_format_bytes(f) == 0 || n_sets < 0 || k < 0 || heads < 1 || heads > (1 << 16)) return false;
+  if ((int64_t)n_sets * k >= (1ll << 30) || (int64_t)n_sets * heads >= (1ll << 30)) return false;
+  if (f->kind == ULA_ROWS_LATENT) {
+    *plan = plan_attend_latent(n_sets, k, heads);
+    *width = kLatent;
+  } else {
+    if (heads % f->kv_heads) return false;
+    if ((int64_t)k * f->block_tokens >= (1ll << 30)) return false;
+    *plan = plan_attend_heads(n_sets, k * f->block_tokens, heads, f->kv_heads);
+    *width = f->head_dim;
+  }
+  return (int64_t)n_sets * plan->head_blocks * plan->splits < (1ll << 31);
+}
+
+static size_t attend_bytes(const AttendPlan& p, int32_t n_sets, int32_t heads, int width) {
+  if (p.splits <= 1) return 0;
+  return align_up((size_t)n_sets * heads * p.splits * width * sizeof(float)) +
+         align_up((size_t)n_sets * heads * p.splits * sizeof(float));
+}
+
+size_t ula_attend_bytes(const ula_row_format* rows, int32_t n_sets, int32_t k, int32_t heads) {
+  AttendPlan plan;
+  int width;
+  if (!plan_attend(rows, n_sets, k, heads, &plan, &width)) return 0;
+  return attend_bytes(plan, n_sets, heads, width);
+}
+
+int ula_attend(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32_t k, const int32_t* sel_dev,
+               const ula_attend_args* args, uint64_t stream) {
+  if (!ctx || !args) return ULA_EINVAL;
+  if (ctx->poisoned) return ULA_ESTATE;
+  if (group < 0 || group >= ctx->cfg.num_groups) return ULA_EINVAL;
+  if (layer < 0 || layer >= ctx->cfg.layers_per_group) return ULA_EINVAL;
+  if (n_sets < 0 || k < 0 || n_sets > ctx->cfg.max_sets || k > ctx->cfg.max_k) return ULA_EINVAL;
+  const ula_attend_args& u = *args;
+  AttendPlan plan;
+  int width;
+  if (!plan_attend(&u.rows, n_sets, k, u.heads, &plan, &width)) return ULA_EINVAL;
+  if (ula_row_format_bytes(&u.rows) != (size_t)ctx->dims.row_bytes) return ULA_EINVAL;
+  if (u.type != ULA_BF16 && u.type != ULA_FP16) return ULA_EINVAL;
+  if (!std::isfinite(u.scale)) return ULA_EINVAL;
+  const size_t need = attend_bytes(plan, n_sets, u.heads, width);
+  if (n_sets > 0) {
+    if ((k > 0 && !sel_dev) || !u.q || !u.out) return ULA_EINVAL;
+    if (((uintptr_t)u.q | (uintptr_t)u.out) % 2 || (uintptr_t)u.lse % 4 || (uintptr_t)sel_dev % 4) return ULA_EINVAL;
+    if (need && (!u.workspace || u.workspace_bytes < need || (uintptr_t)u.workspace % 16)) return ULA_EINVAL;
+  }
+  GroupHost& gh = ctx->groups[group];
+  if (gh.steps == 0) return ULA_ENOTRESIDENT;
+  if (n_sets == 0) return ULA_OK;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  {
+    const int rc = refuse_capture(s);
+    if (rc) return rc;
+  }
+  AttendDev a{};
+  a.sel = sel_dev;
+  a.q = u.q;
+  a.out = u.out;
+  a.lse = u.lse;
+  a.part_o = static_cast<float*>(u.workspace);
+  if (need)
+    a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(u.workspace) +
+                                          align_up((size_t)n_sets * u.heads * plan.splits * width * sizeof(float)));
+  a.q_set_stride = u.q_set_stride;
+  a.q_head_stride = u.q_head_stride;
+  a.out_set_stride = u.out_set_stride;
+  a.out_head_stride = u.out_head_stride;
+  a.want_flag = (long long)gh.steps;
+  a.scale_log2 = (float)(u.scale * 1.4426950408889634);
+  a.k = k;
+  a.heads = u.heads;
+  a.layer = layer;
+  a.n_res = gh.last_n;
+  a.splits = plan.splits;
+  a.split_keys = plan.split_keys;
+  a.head_blocks = plan.head_blocks;
+  a.q_aligned = ((uintptr_t)u.q % 16 == 0 && u.q_set_stride % 8 == 0 && u.q_head_stride % 8 == 0) ? 1 : 0;
+  a.out_aligned = ((uintptr_t)u.out % 8 == 0 && u.out_set_stride % 4 == 0 && u.out_head_stride % 4 == 0) ? 1 : 0;
+  GroupDev g = gh.d;
+  g.res = res_for(ctx, gh, gh.steps);
+  if (u.rows.kind == ULA_ROWS_LATENT) {
+    HIP_TRY(launch_attend_latent(g, a, u.type, n_sets, s));
+  } else {
+    a.kv_heads = u.rows.kv_heads;
+    while ((1 << a.block_shift) < u.rows.block_tokens) ++a.block_shift;
+    HIP_TRY(launch_attend_heads(g, a, u.type, n_sets, u.rows.head_dim, s));
+  }
+  if (plan.splits > 1) HIP_TRY(launch_attend_join(g, a, u.type, n_sets, width, s));
+  return note_gather(gh, s);
 }
 
 static int read_counters(ula_ctx* ctx, std::vector<Counters>& out) {

@@ -245,6 +245,11 @@ hipError_t launch_tag_append(const GroupDev& g, const SmallAppend& a, const uint
 hipError_t launch_place(const GroupDev& g, int32_t n, const uint8_t* rows, hipStream_t s);
 hipError_t launch_place_ring(const GroupDev& g, int32_t n, const uint8_t* rows, hipStream_t s);
 hipError_t launch_release(const GroupDev& g, int32_t n, hipStream_t s);
+// copies of entries src0 .. under addresses dst0 .. into the places of app_dst, or
+// into the append's staging buffers; new addresses for entries (k_entries.hip)
+hipError_t launch_fork_place(const GroupDev& g, int32_t src0, int32_t dst0, int32_t n, hipStream_t s);
+hipError_t launch_fork_collect(const GroupDev& g, int32_t src0, int32_t dst0, int32_t n, hipStream_t s);
+hipError_t launch_rename(const GroupDev& g, int32_t src0, int32_t dst0, int32_t n, hipStream_t s);
 hipError_t launch_swap_commit(const GroupDev& g, uint32_t t, int32_t max_pairs, hipStream_t s);
 hipError_t launch_writeback(const GroupDev& g, int32_t max_pairs, hipStream_t s);
 // exact-LRU victim selection (k_lru.hip)

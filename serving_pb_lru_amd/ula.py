@@ -50,6 +50,47 @@ class UlaStateHost(ctypes.Structure):
                 ("last", UlaStepStats), ("stamps", ctypes.c_void_p)]
 
 
+BF16, FP16, FP32 = 0, 1, 2
+ROWS_LATENT, ROWS_HEADS = 0, 1
+LATENT_CHANNELS, ROPE_CHANNELS = 512, 64
+
+
+class RowFormat(ctypes.Structure):
+    """What a row's bytes hold (ula_row_format); see latent_rows and head_rows."""
+    _fields_ = [("kind", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("block_tokens", ctypes.c_int32)]
+
+    @property
+    def row_bytes(self) -> int:
+        return lib().ula_row_format_bytes(ctypes.byref(self))
+
+
+class UlaAttendArgs(ctypes.Structure):
+    _fields_ = [("rows", RowFormat), ("type", ctypes.c_int32), ("heads", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q", ctypes.c_void_p), ("q_set_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("out_set_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("lse", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class UlaRotary(ctypes.Structure):
+    _fields_ = [("axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 3), ("interleaved", ctypes.c_int32),
+                ("theta", ctypes.c_double)]
+
+
+class UlaPackArgs(ctypes.Structure):
+    _fields_ = [("rows", RowFormat), ("type", ctypes.c_int32), ("n", ctypes.c_int32), ("layers", ctypes.c_int32),
+                ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("a_stride", ctypes.c_int64 * 4),
+                ("b_stride", ctypes.c_int64 * 4), ("positions", ctypes.c_void_p), ("count", ctypes.c_void_p),
+                ("rotary", UlaRotary)]
+
+
+class UlaRotateArgs(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("n", ctypes.c_int32), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("x", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("x_stride", ctypes.c_int64 * 2), ("out_stride", ctypes.c_int64 * 2), ("positions", ctypes.c_void_p),
+                ("rotary", UlaRotary)]
+
+
 class UlaError(RuntimeError):
     def __init__(self, code: int, where: str, text: str):
         self.code = code
@@ -67,6 +108,16 @@ SIGNATURES = [
                                 ctypes.c_uint64, ctypes.POINTER(ctypes.c_void_p)]),
     ("ula_init_static", ctypes.c_int, [ctypes.POINTER(UlaConfig), ctypes.c_void_p, ctypes.c_uint64,
                                        ctypes.POINTER(ctypes.c_void_p)]),
+    ("ula_row_format_bytes", ctypes.c_size_t, [ctypes.POINTER(RowFormat)]),
+    ("ula_pack_rows", ctypes.c_int, [ctypes.POINTER(UlaPackArgs), ctypes.c_void_p, ctypes.c_uint64]),
+    ("ula_rotate", ctypes.c_int, [ctypes.POINTER(UlaRotateArgs), ctypes.c_uint64]),
+    ("ula_attend_bytes", ctypes.c_size_t, [ctypes.POINTER(RowFormat), ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
+    ("ula_attend", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                  ctypes.c_void_p, ctypes.POINTER(UlaAttendArgs), ctypes.c_uint64]),
+    ("ula_fork", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                ctypes.c_uint64]),
+    ("ula_rename", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                  ctypes.c_uint64]),
     ("ula_append", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
                                   ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint64]),
     ("ula_release", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
@@ -152,6 +203,168 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def latent_rows() -> RowFormat:
+    """656-byte rows of one shared representation: 512 e4m3 channels, 64 bf16 rotary channels,
+    one fp32 scale per 128 channels."""
+    return RowFormat(ROWS_LATENT, 0, 0, 0)
+
+
+def head_rows(kv_heads: int, head_dim: int, block_tokens: int = 1) -> RowFormat:
+    """Rows of block_tokens tokens' e4m3 keys and values of every KV head, with an fp32 scale
+    for each block and head."""
+    fmt = RowFormat(ROWS_HEADS, kv_heads, head_dim, block_tokens)
+    if not fmt.row_bytes:
+        raise UlaError(-1, "head_rows", "kv_heads >= 1, head_dim 64 or 128, block_tokens 1, 2, 4, 8 or 16, "
+                                        "and at most 4096 bytes a row")
+    return fmt
+
+
+_TYPES = {"torch.bfloat16": BF16, "torch.float16": FP16, "torch.float32": FP32}
+
+
+def _tensor(t, shape, what: str, types=(BF16, FP16, FP32)):
+    """(pointer, type code, strides) of a CUDA tensor of the given shape (None: any size)
+    whose last dimension is contiguous."""
+    if not (hasattr(t, "is_cuda") and t.is_cuda):
+        raise ValueError(f"{what}: a CUDA tensor is required")
+    code = _TYPES.get(str(t.dtype))
+    if code not in types:
+        raise ValueError(f"{what}: dtype {t.dtype} is not supported")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)} (None: any)")
+    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    return t.data_ptr(), code, t.stride()
+
+
+def _same_device(first, *others) -> None:
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+
+
+class _On:
+    """Makes a tensor's device current and `stream` (None: that device's current stream) the
+    stream that what is allocated inside belongs to; as a context it gives the stream's handle."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.device = device
+        if stream is None:
+            self.stream = torch.cuda.current_stream(device)
+        elif hasattr(stream, "cuda_stream"):
+            self.stream = stream
+        else:
+            self.stream = torch.cuda.ExternalStream(int(stream), device=device)
+        cur = torch.cuda.current_stream()
+        self.ctx = None if cur == self.stream else torch.cuda.stream(self.stream)
+
+    def __enter__(self) -> int:
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _rotary(positions, sections, theta, interleaved, pairs: int, lead, what: str):
+    """(tensor to keep, pointer, UlaRotary) of int32 positions [*lead][axes] (or [*lead] for one
+    axis); (None, None, zeros) without positions."""
+    r = UlaRotary()
+    if positions is None:
+        return None, None, r
+    if positions.dim() == len(lead):
+        positions = positions.unsqueeze(-1)
+    axes = positions.shape[-1]
+    if tuple(positions.shape) != (*lead, axes) or not 1 <= axes <= 3:
+        raise ValueError(f"{what} positions: shape {tuple(positions.shape)}, expected {tuple(lead)} and 1 to 3 axes")
+    sections = (pairs,) if sections is None and axes == 1 else sections
+    if sections is None or len(sections) != axes:
+        raise ValueError(f"{what}: one section for each of the {axes} axes is required")
+    n = 1
+    for x in positions.shape:
+        n *= x
+    ptr = _dev(positions, "int32", n, f"{what} positions")
+    r.axes, r.interleaved, r.theta = axes, int(bool(interleaved)), float(theta)
+    for i, s in enumerate(sections):
+        r.sections[i] = int(s)
+    return positions, ptr, r
+
+
+def pack_rows(fmt: RowFormat, a, b, positions=None, sections=None, theta: float = 10000.0, interleaved: bool = False,
+              counts=None, out=None, stream=None):
+    """Rows [n][layers][fmt.row_bytes] (uint8) from bf16, fp16 or fp32 tensors: latent channels
+    [n][layers][512] and rotary channels [n][layers][64], or for heads rows keys and values
+    [n][layers][block_tokens][kv_heads][head_dim] with `counts` (int32 [n], tokens in use).
+    With int32 positions ([n][axes], heads rows [n][block_tokens][axes]) the rotary channels, or
+    the whole keys, are turned first; sections: pairs of each axis."""
+    import torch
+    args = UlaPackArgs()
+    args.rows = fmt
+    row_bytes = fmt.row_bytes
+    if not row_bytes:
+        raise UlaError(-1, "pack_rows", "invalid row format")
+    latent = fmt.kind == ROWS_LATENT
+    if latent:
+        if a.dim() != 3:
+            raise ValueError(f"pack_rows latent: shape {tuple(a.shape)}, expected (None, None, {LATENT_CHANNELS})")
+        n, layers = a.shape[:2]
+        args.a, args.type, st_a = _tensor(a, (None, None, LATENT_CHANNELS), "pack_rows latent")
+        args.b, type_b, st_b = _tensor(b, (n, layers, ROPE_CHANNELS), "pack_rows rotary channels")
+        pairs, lead = ROPE_CHANNELS // 2, (n,)
+        if counts is not None:
+            raise ValueError("pack_rows counts: heads rows only")
+    else:
+        shape = (None, None, fmt.block_tokens, fmt.kv_heads, fmt.head_dim)
+        args.a, args.type, st_a = _tensor(a, shape, "pack_rows keys")
+        n, layers = a.shape[:2]
+        args.b, type_b, st_b = _tensor(b, (n, layers, *shape[2:]), "pack_rows values")
+        pairs, lead = fmt.head_dim // 2, (n, fmt.block_tokens)
+        if counts is not None:
+            args.count = _dev(counts, "int32", n, "pack_rows counts")
+    if type_b != args.type:
+        raise ValueError(f"pack_rows: dtypes {a.dtype} and {b.dtype}")
+    for i, (x, y) in enumerate(zip(st_a[:-1], st_b[:-1])):
+        args.a_stride[i], args.b_stride[i] = x, y
+    args.n, args.layers = n, layers
+    _keep, args.positions, args.rotary = _rotary(positions, sections, theta, interleaved, pairs, lead, "pack_rows")
+    _same_device(a, b, positions, counts, out)
+    with _On(a.device, stream) as s:
+        if out is None:
+            out = torch.empty((n, layers, row_bytes), dtype=torch.uint8, device=a.device)
+        ptr = _dev(out, "uint8", n * layers * row_bytes, "pack_rows out")
+        _check(lib().ula_pack_rows(ctypes.byref(args), ptr, s), "ula_pack_rows")
+    return out
+
+
+def rotate(x, positions, sections=None, theta: float = 10000.0, interleaved: bool = False, inverse: bool = False,
+           out=None, stream=None):
+    """x [n][heads][dim] turned by int32 positions [n][axes] (or [n]); inverse turns back. out:
+    a tensor of x's shape and dtype, x itself for in place."""
+    import torch
+    args = UlaRotateArgs()
+    args.x, args.type, st = _tensor(x, (None, None, None), "rotate x")
+    args.n, args.heads, args.dim = x.shape
+    _keep, args.positions, args.rotary = _rotary(positions, sections, theta, interleaved, x.shape[2] // 2,
+                                                 (x.shape[0],), "rotate")
+    if args.positions is None and x.shape[0]:
+        raise ValueError("rotate positions: required")
+    args.inverse = int(bool(inverse))
+    _same_device(x, positions, out)
+    with _On(x.device, stream) as s:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        args.out, code, st_out = _tensor(out, x.shape, "rotate out")
+        if code != args.type:
+            raise ValueError(f"rotate out: dtype {out.dtype}, expected {x.dtype}")
+        for i in range(2):
+            args.x_stride[i], args.out_stride[i] = st[i], st_out[i]
+        _check(lib().ula_rotate(ctypes.byref(args), s), "ula_rotate")
+    return out
+
+
 class Engine:
     """One engine context: per group a GPU pool, a pinned host pool and PB-LRU state."""
 
@@ -216,6 +429,14 @@ class Engine:
         _check(lib().ula_release(self.ctx, group, las.size, las.ctypes.data, _stream(stream)),
                "ula_release")
 
+    def fork(self, group: int, src: int, dst: int, n: int, stream=None) -> None:
+        """Copy entries src .. src + n - 1 to the new addresses dst .. dst + n - 1."""
+        _check(lib().ula_fork(self.ctx, group, src, dst, n, _stream(stream)), "ula_fork")
+
+    def rename(self, group: int, src: int, dst: int, n: int, stream=None) -> None:
+        """Give entries src .. src + n - 1 the addresses dst .. dst + n - 1; no row moves."""
+        _check(lib().ula_rename(self.ctx, group, src, dst, n, _stream(stream)), "ula_rename")
+
     def step(self, group: int, sel, stream=None) -> None:
         """sel: torch CUDA int32 tensor [n_sets][k] (or [k] for one set)."""
         n_sets, k = _sets(sel)
@@ -256,6 +477,45 @@ class Engine:
             _dev(out, "uint8", max(n_layers, 0) * n_sets * k * self.row_bytes, "ula_gather_layers out"),
             _stream(stream)), "ula_gather_layers")
         return out
+
+    def attend(self, group: int, layer: int, sel, q, fmt: RowFormat, scale: Optional[float] = None, out=None,
+               lse=None, stream=None):
+        """(out, lse): attention of q [n_sets][heads][576 or head_dim] (bf16 or fp16) over the selected
+        entries' rows of one layer, which are in format `fmt`. out [n_sets][heads][512 or head_dim] in
+        q's dtype, lse fp32 [n_sets][heads]. scale: factor of the logits, default 1 / sqrt(q's width).
+        The workspace of a split call is allocated here, on the call's stream."""
+        import torch
+        n_sets, k = _sets(sel)
+        args = UlaAttendArgs()
+        args.rows = fmt
+        latent = fmt.kind == ROWS_LATENT
+        width = LATENT_CHANNELS + ROPE_CHANNELS if latent else fmt.head_dim
+        back = LATENT_CHANNELS if latent else fmt.head_dim
+        if q.dim() != 3:
+            raise ValueError(f"ula_attend q: shape {tuple(q.shape)}, expected ({n_sets}, None, {width})")
+        heads = q.shape[1]
+        args.q, args.type, st = _tensor(q, (n_sets, None, width), "ula_attend q", (BF16, FP16))
+        args.q_set_stride, args.q_head_stride, args.heads = st[0], st[1], heads
+        args.scale = 1.0 / width ** 0.5 if scale is None else scale
+        _same_device(q, sel, out, lse)
+        with _On(q.device, stream) as s:
+            if out is None:
+                out = torch.empty((n_sets, heads, back), dtype=q.dtype, device=q.device)
+            args.out, code, st = _tensor(out, (n_sets, heads, back), "ula_attend out")
+            if code != args.type:
+                raise ValueError(f"ula_attend out: dtype {out.dtype}, expected {q.dtype}")
+            args.out_set_stride, args.out_head_stride = st[0], st[1]
+            if lse is None:
+                lse = torch.empty((n_sets, heads), dtype=torch.float32, device=q.device)
+            args.lse = _dev(lse, "float32", n_sets * heads, "ula_attend lse")
+            args.workspace_bytes = lib().ula_attend_bytes(ctypes.byref(fmt), n_sets, k, heads)
+            if args.workspace_bytes:
+                work = torch.empty(args.workspace_bytes, dtype=torch.uint8, device=q.device)
+                args.workspace = work.data_ptr()
+            _check(lib().ula_attend(self.ctx, group, layer, n_sets, k,
+                                    _dev(sel, "int32", n_sets * k, "ula_attend sel"), ctypes.byref(args), s),
+                   "ula_attend")
+        return out, lse
 
     def sync(self, stream=None) -> List[tuple]:
         st = (UlaStepStats * self.num_groups)()
