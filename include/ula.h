@@ -474,8 +474,8 @@ size_t ula_attend_bytes(const ula_row_format* rows, int32_t n_sets, int32_t k, i
  * Results split over several workgroups are joined through the workspace, which
  * belongs to the call until the stream has run it: calls that may run at the
  * same time need workspaces of their own. q, out, lse and the workspace must not
- * overlap. 16-byte aligned q rows and 8-byte aligned out rows (pointer and
- * strides) are read and written in vectors, others element by element.
+ * overlap. q and out rows whose pointer and strides keep them 16-byte aligned are
+ * read and written in vectors, others element by element.
  * Which entries, streams and errors: as for ula_gather (the selection is looked
  * up through the group's last step where it is that step's, else through the
  * mapping table; on another stream the call must be ordered after the step; the

@@ -20,6 +20,13 @@ SOURCES = ["k_init.hip", "k_lookup.hip", "k_select.hip", "k_lru.hip", "k_move.hi
            "k_attend.hip", "k_attend_heads.hip", "k_rows.hip", "k_entries.hip",
            "runtime.hip"]
 
+# The attention kernels hold their accumulators in vector registers (vector
+# instructions rescale and read them) and what only feeds matrix instructions in
+# the accumulation registers; the compiler's default puts them the other way round
+# and spills.
+EXTRA = {"k_attend.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+         "k_attend_heads.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -41,7 +48,7 @@ def build(out: str = OUT, jobs: int = 8) -> str:
     for src in SOURCES:
         obj = os.path.join(bdir, src.replace(".hip", ".o"))
         objs.append(obj)
-        cmds.append([HIPCC, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj])
+        cmds.append([HIPCC, *FLAGS, *EXTRA.get(src, []), "-c", os.path.join(CSRC, src), "-o", obj])
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
         list(ex.map(_run, cmds))
     tmp = out + ".tmp"

@@ -9,25 +9,40 @@
 // With k8 a row's e4m3 channels, s_b the scale of channel block b (128
 // channels), r its rotary channels and c = scale log2(e), for head h:
 //   S_j  = c (sum_b s_bj (q_b . k8_bj) + q_r . r_j)
-//   p_j  = 2^(S_j - m)          m the running maximum, l = sum_j p_j
+//   p_j  = 2^(S_j - m)          m a running reference, l = sum_j p_j
 //   o_d  = sum_j p_j s_b(d)j k8_dj / l,   lse = (m + log2 l) ln 2
-// e4m3 values are exact in bf16 and fp16, so both products run on 16-bit matrix
-// instructions with the block scales applied in 32 bits: to the four partial
-// products of S, and to p (rounded to bf16 once per block, at most 2^-8 of its value)
-// before the second product.
+// The block scales are applied in 32 bits, to the four partial products of S and
+// to p, so e4m3 codes enter the matrix instructions as they are:
+//   - first product, bf16 q: the 8-bit matrix instruction, with q as the sum of
+//     two e4m3 values (4 + 4 bits hold its 8; per head a power of two brings its
+//     largest value to 128..256, so what is lost is below 2^-17 of that). As many
+//     cycles as one 16-bit product, and no key is widened.
+//   - first product, fp16 q: the codes widened to fp16, which holds them exactly.
+//   - second product: codes widened to fp16, and p s_b rounded to fp16. m follows
+//     the largest p_j max_b s_bj, which stays within 2^7..2^15, so the rounding is
+//     at most 2^-11 of the value, or 2^-25 (2^-32 of the largest) for small ones.
+// Both products have 32-bit accumulators.
 //
 // Layout. Both products are taken transposed: S^T = K Q^T puts heads in the
-// lanes' columns and keys in registers, which is the operand layout that
-// O^T = V^T P^T wants once V's keys are named in the same order, so p never
-// crosses lanes. A wave holds 32 heads: Q in 144 registers, O (512 channels) in
-// 256 accumulators, one wave per SIMD; with 16 heads per wave and two waves per
-// SIMD every key would be read from LDS and widened twice as often. Of a
-// workgroup's 4 waves, NHG take different heads, NKG different keys, and NCG
-// different channels of O.
-// Keys come in tiles of 32 rows: the first 640 bytes of each row as 16-byte
-// pieces straight into LDS (no registers), the scales transposed to [block][key].
-// Piece c of key j lies at c ^ ((j >> 1) & 7): without that the 640-byte row
-// stride maps every other key to the same banks.
+// lanes' columns and keys in registers, O^T = V^T P^T the same way. The eight
+// waves of a workgroup split the first product by heads, 16 each (and, with at
+// most 64 heads, by the halves of a tile's 32 keys), and the second by channels of
+// O, 64 each with all heads: so no wave holds another's Q, every key is read from
+// LDS by the waves of different heads and every value once in all. In between p
+// goes through LDS, scaled for each block and in the operand order of the second
+// product.
+// One barrier per tile. Between two of them a wave computes S of one tile, p of
+// the tile before (once both halves' largest logits are known) and the second
+// product of the one before that: three independent streams of matrix, vector
+// and LDS work, in two waves per SIMD. With more than 64 heads a wave has all of
+// a tile's keys and p follows S at once.
+// (256 sets of 2048 keys and 64 heads: 206 us with a wave that kept 32 heads to
+// itself for both products, reading and widening every key and value four times;
+// 160 us in this form with one wave per SIMD and two streams.)
+// Tiles: the first 640 bytes of each row as 16-byte pieces straight into LDS (no
+// registers), the scales transposed to [block][key]. Piece c of key j lies at
+// c ^ ((j >> 1) & 7): without that the 640-byte row stride maps every other key
+// to the same banks.
 #include <algorithm>
 #include <type_traits>
 
@@ -38,13 +53,9 @@ namespace ula {
 constexpr int kTileKeys = 32;
 constexpr int kTilePieces = kLatentScaleAt / 16;                 // 40 pieces of a row go to LDS
 constexpr int kTileBytes = kTileKeys * kLatentScaleAt;           // 20 KB
-constexpr int kTiles = 6;                                        // ring of tiles
 constexpr int kComputeUnits = 256;
 constexpr double kStartTiles = 6, kJoinTiles = 8, kJoinTilesPerRow = 2.0e-4;   // see plan_attend_latent
-constexpr int kWaves = 4;
 constexpr int kTileLoads = kTileBytes / 1024;                    // wave-wide 16-byte loads of a tile: 20
-constexpr int kLoadsPerWave = 6;                                 // vector loads each wave issues per tile
-static_assert(kTileLoads + kLatentGroups == kWaves * kLoadsPerWave, "pieces and scales fill the waves' loads");
 
 // rows that stand in for padding: zeros, so that a masked key adds 0 x 0
 __device__ __align__(16) uint8_t g_zero_row[kLatentRow];
@@ -73,35 +84,208 @@ __device__ __forceinline__ void barrier_keep_loads() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// The value again, as one the compiler cannot trace back: what is computed from
-// it inside a loop is not kept in registers across the loop.
+// The value again, as one the compiler cannot trace back: sums of it and a
+// constant become instruction offsets, where it would otherwise keep the sums of
+// its parts and each constant in registers across the loop.
 __device__ __forceinline__ int opaque(int x) {
   asm volatile("" : "+v"(x));
   return x;
 }
 
+// x *= f element by element in x's own registers. Without the empty assembly the
+// compiler gathers the products into new registers, and a branch around them
+// then costs a copy of the accumulators where it is not taken.
+__device__ __forceinline__ void scale_in_place(f32x16& x, float f) {
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    x[r] *= f;
+    asm volatile("" : "+v"(x));
+  }
+}
+
+constexpr int kWaves = 8;
+constexpr int kLoadsPerWave = (kTileLoads + kLatentGroups) / kWaves;   // vector loads a wave issues per tile
+static_assert(kLoadsPerWave == 3 && kTileLoads % kWaves == kLatentGroups, "see issue()");
+
+template <int HEADS, int KU, int TILES, int KEYS>
 struct LatentLds {
-  alignas(1024) uint8_t ring[kTiles][kTileBytes];
-  alignas(16) float scale[kTiles][kLatentGroups][kTileKeys];
-  uint32_t slot[kAttendKeys];
-  uint32_t live[kAttendKeys / kTileKeys];   // bit per key: not padding
+  alignas(1024) uint8_t ring[TILES][kTileBytes];
+  // p x scale of two tiles: [block][head][key], key chunk c (8 keys) of head h at c ^ ((h >> 2) & 3)
+  alignas(1024) _Float16 p[2][kLatentGroups][HEADS][kTileKeys];
+  alignas(16) float scale[TILES][kLatentGroups][kTileKeys];
+  float top[2][2 / KU][HEADS];              // largest logit (with its scale's exponent) of a tile's part
+  float alpha[2][HEADS];                    // factor of O before the tile's second product
+  uint32_t moved[2][HEADS / 16];            // whether any of 16 heads has a factor other than 1
+  const uint8_t* row[KEYS];                 // each key's row in this layer; zeros for padding
+  uint32_t live[KEYS / kTileKeys];          // bit per key: not padding
   int ok;
 };
-static_assert(sizeof(LatentLds) <= 160 * 1024, "LDS of a compute unit");
 
-template <typename Q8, int NHG, int NKG>
-__global__ __launch_bounds__(kWaves * kWave, 1) void k_attend_latent(GroupDev g, AttendDev a) {
-  constexpr int NCG = kWaves / (NHG * NKG);  // waves that share heads and keys, each with its channels of O
-  constexpr int kRounds = kTiles / NKG;      // rounds of NKG tiles the ring holds
-  constexpr int kOut = kLatent / 32 / NCG;   // 32-channel tiles of O per wave
-  constexpr int kOutBlocks = kLatentGroups / NCG;   // scale blocks of those channels
-  static_assert(kLatentGroups % NCG == 0, "a wave's channels are whole scale blocks");
-  __shared__ LatentLds s;
+// One wave's 16 heads of q as they are in memory. Lane quad x holds channels 64 t
+// + 16 x + (0..15) of each 64-channel piece t, as the 16-byte key reads do.
+template <typename Q8>
+struct QueryRaw {
+  Q8 x[kLatent / 32];
+  Q8 rope[kRope / 32];
+  template <bool ALIGNED>
+  __device__ __forceinline__ void load(const uint16_t* q, bool any, int quad) {
+#pragma unroll
+    for (int t = 0; t < kLatent / 32; ++t)
+      x[t] = any ? load8<Q8, ALIGNED>(q + 64 * (t / 2) + 16 * quad + 8 * (t % 2)) : Q8{};
+#pragma unroll
+    for (int j = 0; j < kRope / 32; ++j)
+      rope[j] = any ? load8<Q8, ALIGNED>(q + kLatent + 32 * j + 8 * quad) : Q8{};
+  }
+  // all values present before any asynchronous load is issued: the compiler's
+  // wait for them would wait for those too
+  __device__ __forceinline__ void settle() {
+#pragma unroll
+    for (int t = 0; t < kLatent / 32; ++t) asm volatile("" : "+v"(x[t]));
+#pragma unroll
+    for (int j = 0; j < kRope / 32; ++j) asm volatile("" : "+v"(rope[j]));
+  }
+};
+
+// The same as the operands of the first product.
+template <typename Q8>
+struct QueryOperand;
+
+template <>
+struct QueryOperand<bf16x8> {
+  i32x8 hi[kLatentGroups], lo[kLatentGroups];   // e4m3 x 32: pieces 2 b and 2 b + 1
+  bf16x8 rope[kRope / 32];
+  float up;                                     // the power of two in hi and lo
+  __device__ __forceinline__ void take(const QueryRaw<bf16x8>& raw) {
+    const bf16x8* x = raw.x;
+    float top = 0.0f;
+#pragma unroll
+    for (int t = 0; t < kLatent / 32; ++t)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, finite_abs((float)x[t][e]));
+#pragma unroll
+    for (int j = 0; j < kRope / 32; ++j) rope[j] = raw.rope[j];
+    top = max_quads(top);
+    // 2^s with top x 2^s in [128, 256); s within +-60, far beyond which q has no effect or overflows
+    const int s = top > 0.0f ? min(max(8 - __builtin_amdgcn_frexp_expf(top), -60), 60) : 0;
+    up = ldexpf(1.0f, s);
+#pragma unroll
+    for (int b = 0; b < kLatentGroups; ++b)
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {               // four values a word
+        float v[4], r[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float y = (float)x[4 * b + w / 2][4 * (w % 2) + e];
+          v[e] = fabsf(y) < __builtin_inff() ? y * up : __builtin_nanf("");   // an infinity is not an e4m3 value
+        }
+        const uint32_t h = e4m3x4(v[0], v[1], v[2], v[3]);
+        const auto h0 = __builtin_amdgcn_cvt_pk_f32_fp8(h, false), h1 = __builtin_amdgcn_cvt_pk_f32_fp8(h, true);
+        r[0] = v[0] - h0[0];
+        r[1] = v[1] - h0[1];
+        r[2] = v[2] - h1[0];
+        r[3] = v[3] - h1[1];
+        hi[b][w] = (int)h;
+        lo[b][w] = (int)e4m3x4(r[0], r[1], r[2], r[3]);
+      }
+  }
+  __device__ __forceinline__ f32x4 rope_product(const bf16x8* kr) const {
+    f32x4 s{};
+#pragma unroll
+    for (int j = 0; j < kRope / 32; ++j) s = mfma16(kr[j], rope[j], s);
+    return s * up;
+  }
+  __device__ __forceinline__ f32x4 block_product(int b, vec4u k0, vec4u k1) const {
+    const i32x8 k = {(int)k0.x, (int)k0.y, (int)k0.z, (int)k0.w, (int)k1.x, (int)k1.y, (int)k1.z, (int)k1.w};
+    const f32x4 s = mfma16_e4m3(k, hi[b], f32x4{});
+    return mfma16_e4m3(k, lo[b], s);
+  }
+};
+
+template <>
+struct QueryOperand<f16x8> {
+  f16x8 x[kLatent / 32];
+  bf16x8 rope_hi[kRope / 32], rope_lo[kRope / 32];   // fp16 as the sum of two bf16 values (8 + 8 bits hold its 11)
+  static constexpr float up = 1.0f;
+  __device__ __forceinline__ void take(const QueryRaw<f16x8>& raw) {
+#pragma unroll
+    for (int t = 0; t < kLatent / 32; ++t) x[t] = raw.x[t];
+#pragma unroll
+    for (int j = 0; j < kRope / 32; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        rope_hi[j][e] = (__bf16)(float)raw.rope[j][e];
+        rope_lo[j][e] = (__bf16)((float)raw.rope[j][e] - (float)rope_hi[j][e]);
+      }
+  }
+  __device__ __forceinline__ f32x4 rope_product(const bf16x8* kr) const {
+    f32x4 s{};
+#pragma unroll
+    for (int j = 0; j < kRope / 32; ++j) s = mfma16(kr[j], rope_lo[j], mfma16(kr[j], rope_hi[j], s));
+    return s;
+  }
+  __device__ __forceinline__ f32x4 block_product(int b, vec4u k0, vec4u k1) const {
+    f32x4 s{};
+    s = mfma16(widen8<f16x8>(k0.x, k0.y), x[4 * b], s);
+    s = mfma16(widen8<f16x8>(k0.z, k0.w), x[4 * b + 1], s);
+    s = mfma16(widen8<f16x8>(k1.x, k1.y), x[4 * b + 2], s);
+    return mfma16(widen8<f16x8>(k1.z, k1.w), x[4 * b + 3], s);
+  }
+};
+
+// The workgroup's O (o[t][h] of wave w: channels 64 w + 32 t .., heads 32 h ..) as
+// type T, times inv, through the LDS at `box`; put(head, channel, 16 bytes) for
+// heads first + 0.. below `heads`.
+template <typename T, int CT, int HT, typename F>
+__device__ __forceinline__ void store_heads(uint8_t* box, const f32x16 (&o)[CT][HT], const float (&inv)[HT], int first,
+                                            int heads, F put) {
+  constexpr int kSpan = 32 * kWaves;              // channels at a time
+  constexpr int kRow = kSpan * sizeof(T) + 16;
+  constexpr int kPer = 16 / sizeof(T);            // channels per 16 bytes
+  constexpr int kLanes = kSpan / kPer;            // lanes per head
+  const int lane = lane_id(), wave = threadIdx.x / kWave, half = lane / 32, col32 = lane % 32;
+#pragma unroll
+  for (int t = 0; t < CT; ++t) {
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < HT; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        typedef T vec __attribute__((ext_vector_type(4)));
+        vec v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = (T)(o[t][h][4 * i + e] * inv[h]);
+        *reinterpret_cast<vec*>(box + (32 * h + col32) * kRow + (32 * wave + 8 * i + 4 * half) * sizeof(T)) = v;
+      }
+    __syncthreads();
+    for (int e = threadIdx.x; e < 32 * HT * kLanes; e += kWaves * kWave) {
+      const int h = e / kLanes, c = e % kLanes * kPer;
+      if (first + h < heads)
+        put(first + h, c / 32 * (kLatent / kWaves) + 32 * t + c % 32,
+            *reinterpret_cast<const vec4u*>(box + h * kRow + c * sizeof(T)));
+    }
+  }
+}
+
+// HT tiles of 32 heads; KU 16-key parts of a tile per wave of the first product;
+// TILES tiles in the ring; at most KEYS keys.
+template <typename Q8, int HT, int KU, int TILES, int KEYS>
+__global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g, AttendDev a) {
+  constexpr int kHeads = 32 * HT;                 // heads of a workgroup
+  constexpr int kGroups = kHeads / 16;            // of 16
+  constexpr int kCh = kLatent / kWaves;           // channels of O per wave
+  constexpr int CT = kCh / 32;                    // in tiles of 32
+  constexpr int kAhead = KU == 2 ? 1 : 2;         // tiles that the first product runs ahead of the second
+  static_assert(kGroups * (2 / KU) <= kWaves, "every head and part has a wave in the first product");
+  static_assert(TILES >= kAhead + 2, "a tile on its way beside those in use");
+  __shared__ LatentLds<kHeads, KU, TILES, KEYS> s;
+  static_assert(sizeof(s) <= 160 * 1024, "LDS of a compute unit");
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);   // uniform: its branches are scalar
-  const int hg = wave % NHG, cg = (wave / NHG) % NCG, kg = wave / (NHG * NCG);
-  const int half = lane / 32;                // which 8 of an operand's 16 k
-  const int col = lane % 32;
+  const int quad = lane / 16, col = lane % 16;    // first product: 16 heads, quads of keys
+  const int half = lane / 32, col32 = lane % 32;  // second product: 32 heads
+  const int hg = wave % kGroups;                  // this wave's heads in the first product
+  const int part0 = KU == 2 ? 0 : wave / kGroups; // and its part of a tile's keys
+  const bool works = wave < kGroups * (2 / KU);   // whether it has any
 
   // work item: consecutive sets (which share rows under speculative selection)
   // run on one XCD at about the same time
@@ -111,272 +295,352 @@ __global__ __launch_bounds__(kWaves * kWave, 1) void k_attend_latent(GroupDev g,
     const int x = item % 8;
     item = x * per + min(x, rest) + item / 8;
   }
-  const int split = item % a.splits;
-  const int hb = (item / a.splits) % a.head_blocks;
+  const int hb = item % a.head_blocks;
+  const int split = item / a.head_blocks % a.splits;
   const int set = item / (a.splits * a.head_blocks);
   const int key0 = split * a.split_keys;
   const int nkeys = max(0, min(a.split_keys, a.k - key0));
-  const int ntiles = (nkeys + kTileKeys - 1) / kTileKeys;
-  const int rounds = (ntiles + NKG - 1) / NKG;
-  const int total = rounds * NKG;
+  const int tiles = (nkeys + kTileKeys - 1) / kTileKeys;
 
-  // resolve the keys' slots once (whole waves take part: the ballot below)
+  // q on its way while the keys' rows are looked up
+  QueryRaw<Q8> raw;
+  {
+    const int head = hb * kHeads + hg * 16 + col;
+    const bool any = works && head < a.heads;
+    const uint16_t* p = static_cast<const uint16_t*>(a.q) + set * a.q_set_stride + head * a.q_head_stride;
+    if (a.q_aligned) raw.template load<true>(p, any, quad);
+    else raw.template load<false>(p, any, quad);
+  }
   int err = 0;
   if (threadIdx.x == 0) s.ok = reader_ready(g, a.want_flag);
-  for (int i0 = wave * kWave; i0 < total * kTileKeys; i0 += kWaves * kWave) {
-    const int i = i0 + lane;
-    const uint32_t slot = i < nkeys ? resolve_slot(g, a.sel, set * a.k + key0 + i, a.n_res, err) : kAbsent;
-    s.slot[i] = slot;
-    const unsigned long long live = __ballot(slot != kAbsent);
-    if (lane < 2) s.live[i0 / 32 + lane] = (uint32_t)(live >> (32 * lane));
+  {
+    const uint8_t* pool = g.pool + (size_t)a.layer * g.row_bytes;
+    constexpr int kAtOnce = 4;                    // lookups in flight per lane
+    const int n = tiles * kTileKeys;
+    for (int i0 = wave * kWave; i0 < n; i0 += kAtOnce * kWaves * kWave) {
+      uint32_t slot[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int i = i0 + j * kWaves * kWave + lane;
+        slot[j] = i < nkeys ? resolve_slot(g, a.sel, set * a.k + key0 + i, a.n_res, err) : kAbsent;
+      }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int first = i0 + j * kWaves * kWave;   // uniform: whole waves take part in the ballot
+        if (first >= n) break;
+        s.row[first + lane] = slot[j] != kAbsent ? pool + (size_t)slot[j] * g.slot_bytes : g_zero_row;
+        const unsigned long long live = __ballot(slot[j] != kAbsent);
+        if (lane < 2) s.live[first / 32 + lane] = (uint32_t)(live >> (32 * lane));
+      }
+    }
   }
   if (err) latch_gather(g.ctr, err);
-
-  // this wave's 32 heads of q. A 32-channel piece t gives two operands: lane half
-  // x holds channels 32 t + 16 x + 8 j + i, as the 16-byte key reads do.
-  const int head = (hb * NHG + hg) * 32 + col;
-  Q8 ql[kLatent / 16];
-  Q8 qr[kRope / 16];
-  if (head < a.heads) {
-    const uint16_t* q = static_cast<const uint16_t*>(a.q) + set * a.q_set_stride + head * a.q_head_stride;
-    auto load_q = [&](auto aligned) {
-#pragma unroll
-      for (int t = 0; t < kLatent / 32; ++t)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) ql[2 * t + j] = load8<Q8, aligned>(q + 32 * t + 16 * half + 8 * j);
-#pragma unroll
-      for (int j = 0; j < kRope / 16; ++j) qr[j] = load8<Q8, aligned>(q + kLatent + 16 * j + 8 * half);
-    };
-    if (a.q_aligned) load_q(std::true_type{});
-    else load_q(std::false_type{});
-  } else {
-#pragma unroll
-    for (int t = 0; t < kLatent / 16; ++t) ql[t] = Q8{};
-#pragma unroll
-    for (int j = 0; j < kRope / 16; ++j) qr[j] = Q8{};
-  }
-  // q has arrived before any asynchronous load is issued: a wait for it inside the
-  // main loop would wait for those too
-#pragma unroll
-  for (int t = 0; t < kLatent / 16; ++t) asm volatile("" : "+v"(ql[t]));
-#pragma unroll
-  for (int j = 0; j < kRope / 16; ++j) asm volatile("" : "+v"(qr[j]));
+  raw.settle();
   __syncthreads();
   if (!s.ok) return;
 
-  const uint8_t* pool = g.pool + (size_t)a.layer * g.row_bytes;
-  auto row_of = [&](uint32_t slot) -> const uint8_t* {
-    return slot == kAbsent ? g_zero_row : pool + (size_t)slot * g.slot_bytes;
-  };
-  // a tile's loads: 5 wave-wide ones for pieces and one for a scale block, per wave
+  // This wave's three loads of a tile's 20 wave-wide ones of pieces and 4 of
+  // scales: two of pieces, and one more or a scale block's.
   auto issue = [&](int tile) {
-    const int at = tile % kTiles;
-    const uint32_t slots = lds_address(s.slot) + tile * kTileKeys * 4;
-    const int lane = opaque(lane_id());   // registers are scarce in the main loop
-#pragma unroll
-    for (int i = 0; i < kTileLoads / kWaves; ++i) {
-      const int n = i * kWaves + wave;
-      const int p = n * kWave + lane;
-      const int key = p / kTilePieces, c = p % kTilePieces;
-      lds_load16(row_of(lds_get<uint32_t>(slots + key * 4)) + (c ^ ((key >> 1) & 7)) * 16,
-                 lds_address(s.ring) + at * kTileBytes + n * kWave * 16);
+    const int at = tile % TILES;
+    const uint32_t rows = lds_address(s.row) + tile * kTileKeys * 8;
+    const uint32_t ring = lds_address(s.ring) + at * kTileBytes;
+    const int lane = HT > 1 ? opaque(lane_id()) : lane_id();   // registers are scarce with more heads
+    auto piece = [&](int n) { return n * kWave + lane; };
+    auto row_of = [&](int key) { return lds_get<const uint8_t*>(rows + key * 8); };
+    auto source = [&](int p) { return (p % kTilePieces ^ (p / kTilePieces >> 1 & 7)) * 16; };
+    const bool scales = wave >= kWaves - kLatentGroups;
+    const int p0 = piece(wave), p1 = piece(kWaves + wave), p2 = piece(2 * kWaves + wave);
+    const uint8_t* r0 = row_of(p0 / kTilePieces);
+    const uint8_t* r1 = row_of(p1 / kTilePieces);
+    const uint8_t* r2 = row_of(scales ? lane % kTileKeys : p2 / kTilePieces);
+    lds_load16(r0 + source(p0), ring + wave * kWave * 16);
+    lds_load16(r1 + source(p1), ring + (kWaves + wave) * kWave * 16);
+    if (scales) {
+      const int b = wave - (kWaves - kLatentGroups);
+      if (lane < kTileKeys)
+        lds_load4(r2 + kLatentScaleAt + 4 * b, lds_address(s.scale) + (at * kLatentGroups + b) * kTileKeys * 4);
+    } else {
+      lds_load16(r2 + source(p2), ring + (2 * kWaves + wave) * kWave * 16);
     }
-    if (lane < kTileKeys)
-      lds_load4(row_of(lds_get<uint32_t>(slots + lane * 4)) + kLatentScaleAt + 4 * wave,
-                lds_address(s.scale) + (at * kLatentGroups + wave) * kTileKeys * 4);
   };
 
-  // Keys of a tile: register r in lane half x is key 8 (r / 4) + 4 x + r % 4.
-  // koff: this lane's key (col), piece `half` of a scale block; piece 2 t + half is
-  // ^ (t << 5). voff: the row this lane names in a transposed read of keys 0..15
-  // and the channels of its 16 lanes; 32-channel tile t is ^ (t << 5).
+  // First product: register r of part u (0, 1) in quad x is key 8 x + 4 u + r.
+  // koff: this lane's key of the wave's first part, piece quad of a scale block.
+  // Piece 4 + quad is ^ 64; part 1's key, four rows on, is ^ 32 (its swizzle) and +
+  // 4 rows. Second product: voff is the row (key) this lane names in a transposed
+  // read of keys 0..15, and the channels of its 16 lanes; 32-channel tile t is ^ (t << 5).
   int koff, voff;
   {
-    koff = col * kLatentScaleAt + ((half ^ ((col >> 1) & 7)) << 4);
-    const int r = lane % 16 / 2;
-    const int key = 8 * (r / 4) + 4 * half + r % 4;
-    voff = key * kLatentScaleAt + (((lane / 16 % 2) ^ ((key >> 1) & 7)) << 4) + (lane & 1) * 8;
+    const int key = 8 * (col / 4) + 4 * part0 + col % 4;
+    koff = key * kLatentScaleAt + ((quad ^ ((key >> 1) & 7)) << 4);
+    const int vkey = 8 * half + col / 2;
+    voff = (vkey * kLatentScaleAt + (((quad % 2) ^ ((vkey >> 1) & 7)) << 4) + (col & 1) * 8 +
+            wave * kCh / kScaleGroup * kScaleGroup) ^ (wave * kCh % kScaleGroup);
   }
   static_assert(kLatentScaleAt % 128 == 0 && kTileBytes % 128 == 0, "the swizzle's bits are free in every row address");
+  const int block = wave * kCh / kScaleGroup;     // the scale block of this wave's channels
+  const int phead = hg * 16 + col;
+  const uint32_t pwrite = lds_address(s.p) + phead * kTileKeys * 2 + ((quad ^ ((phead >> 2) & 3)) << 4) + part0 * 8;
+  const uint32_t pread = lds_address(s.p) + (block * kHeads + col32) * kTileKeys * 2 + ((half ^ ((col32 >> 2) & 3)) << 4);
 
-  f32x16 o[kOut];
+  f32x16 o[CT][HT];
 #pragma unroll
-  for (int t = 0; t < kOut; ++t) o[t] = f32x16{};
-  float m = -__builtin_inff(), l = 0.0f;
+  for (int t = 0; t < CT; ++t)
+#pragma unroll
+    for (int h = 0; h < HT; ++h) o[t][h] = f32x16{};
+  float m = -__builtin_inff(), l = 0.0f;          // of this wave's 16 heads; l of this lane's keys alone
 
 #pragma unroll 1
-  for (int t = 0; t < kRounds * NKG && t < total; ++t) issue(t);
-#pragma unroll 1
-  for (int round = 0; round < rounds; ++round) {
-    // this round's tiles are in LDS once every wave's loads for them are
-    if (round + kRounds <= rounds) wait_loads<(kRounds - 1) * NKG * kLoadsPerWave>();
+  for (int t = 0; t < TILES - 1 && t < tiles; ++t) issue(t);
+  QueryOperand<Q8> q;
+  q.take(raw);
+  const float c_log2 = a.scale_log2 / q.up;
+  f32x4 S[KU], Sn[KU];                            // logits (base 2) of the tile at hand, and of the next one
+
+  // Sn of a tile in LDS, and its largest values to s.top. LDS reads run one block
+  // ahead of the products; the scheduling barriers keep the compiler from moving
+  // them back to their uses.
+  auto first_product = [&](int tile) {
+    const int at = tile % TILES;
+    const uint32_t krow = opaque(lds_address(s.ring) + at * kTileBytes + koff);
+    const uint32_t krow64 = opaque(krow ^ 64);
+    const uint32_t scale = opaque(lds_address(s.scale) + (at * kLatentGroups * kTileKeys + 8 * quad + 4 * part0) * 4);
+    auto kpiece = [&](int u, int t) { return ((t ? krow64 : krow) ^ (32 * u)) + u * 4 * kLatentScaleAt; };
+    bf16x8 kr[KU][2];
+    vec4u kb[2][KU][2];
+    f32x4 sc[2][KU], part[KU];
+    float big = 0x1p-60f;                         // largest scale of the lane's keys
+    auto read_block = [&](int b) {
+#pragma unroll
+      for (int u = 0; u < KU; ++u) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) kb[b & 1][u][t] = lds_get<vec4u>(kpiece(u, t) + b * kScaleGroup);
+        sc[b & 1][u] = lds_get<f32x4>(scale + (kTileKeys * b + 4 * u) * 4);
+      }
+    };
+    auto add_block = [&](int b) {
+#pragma unroll
+      for (int u = 0; u < KU; ++u) {
+        Sn[u] += sc[b & 1][u] * part[u];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) big = fmaxf(big, sc[b & 1][u][r]);
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < KU; ++u)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) kr[u][j] = lds_get<bf16x8>(kpiece(u, j) + kRopeAt);
+    read_block(0);
+    const uint32_t live = __builtin_amdgcn_readfirstlane(s.live[tile]) >> (8 * quad + 4 * part0);
+#pragma unroll
+    for (int b = 0; b < kLatentGroups; ++b) {
+      if (b > 0) add_block(b - 1);
+      if (b + 1 < kLatentGroups) read_block(b + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int u = 0; u < KU; ++u) {
+        if (b == 0) Sn[u] = q.rope_product(kr[u]);
+        part[u] = q.block_product(b, kb[b & 1][u][0], kb[b & 1][u][1]);
+      }
+    }
+    add_block(kLatentGroups - 1);
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int u = 0; u < KU; ++u)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        Sn[u][r] = live & (1u << (4 * u + r)) ? Sn[u][r] * c_log2 : -__builtin_inff();
+        top = fmaxf(top, Sn[u][r]);
+      }
+    top = max_quads(top + (float)__builtin_amdgcn_frexp_expf(big));
+    if (quad == 0) s.top[tile & 1][part0][phead] = top;
+  };
+  // p of the tile whose S is at hand and whose s.top every part has written,
+  // scaled, to LDS for the second product
+  auto softmax = [&](int tile) {
+    const int at = tile % TILES, buf = tile & 1;
+    const uint32_t scale = opaque(lds_address(s.scale) + (at * kLatentGroups * kTileKeys + 8 * quad + 4 * part0) * 4);
+    const uint32_t tops = opaque(lds_address(s.top) + (buf * (2 / KU) * kHeads + phead) * 4);
+    const uint32_t pw = opaque(pwrite + buf * kLatentGroups * kHeads * kTileKeys * 2);
+    float top = lds_get<float>(tops);
+    if constexpr (KU == 1) top = fmaxf(top, lds_get<float>(tops + kHeads * 4));
+    f32x4 sc[kLatentGroups][KU];
+#pragma unroll
+    for (int b = 0; b < kLatentGroups; ++b)
+#pragma unroll
+      for (int u = 0; u < KU; ++u) sc[b][u] = lds_get<f32x4>(scale + (kTileKeys * b + 4 * u) * 4);
+    const bool move = top > m + 15.0f;
+    const float nm = move ? top - 8.0f : m;
+    const float al = move ? __builtin_amdgcn_exp2f(m - nm) : 1.0f;
+    m = nm;
+    l *= al;
+    const float base = nm == -__builtin_inff() ? 0.0f : nm;
+    f32x4 e[KU];
+#pragma unroll
+    for (int u = 0; u < KU; ++u)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        e[u][r] = __builtin_amdgcn_exp2f(S[u][r] - base);
+        l += e[u][r];
+      }
+#pragma unroll
+    for (int b = 0; b < kLatentGroups; ++b)
+#pragma unroll
+      for (int u = 0; u < KU; ++u) {
+        f16x4 w;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) w[r] = (_Float16)(e[u][r] * sc[b][u][r]);
+        lds_put(pw + b * kHeads * kTileKeys * 2 + u * 8, w);
+      }
+    const bool moved = __any(move);
+    if (part0 == 0) {
+      if (quad == 0) s.alpha[buf][phead] = al;
+      if (lane == 0) s.moved[buf][hg] = moved;
+    }
+  };
+
+  // O of a tile whose p is in LDS
+  auto second_product = [&](int tile) {
+    const int buf = tile & 1;
+    const uint32_t vrow = opaque(lds_address(s.ring) + (tile % TILES) * kTileBytes + voff);
+    // chunk 2 x + half of this lane's head: ^ 32 for x
+    const uint32_t prow = opaque(pread + buf * kLatentGroups * kHeads * kTileKeys * 2);
+    i32x2 v8[CT][2];
+    f16x8 p[HT][2];
+#pragma unroll
+    for (int t = 0; t < CT; ++t)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) v8[t][x] = lds_read_transposed((vrow ^ (t << 5)) + x * 16 * kLatentScaleAt);
+#pragma unroll
+    for (int h = 0; h < HT; ++h)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        p[h][x] = lds_get<f16x8>((prow ^ (32 * x)) + 32 * h * kTileKeys * 2);
+    uint32_t moved = 0;                           // a reference moved: O's factors
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) moved |= s.moved[buf][i];
+    if (__builtin_amdgcn_readfirstlane(moved)) {
+#pragma unroll
+      for (int h = 0; h < HT; ++h) {
+        const float al = lds_get<float>(lds_address(s.alpha) + (buf * kHeads + 32 * h + opaque(col32)) * 4);
+#pragma unroll
+        for (int t = 0; t < CT; ++t) scale_in_place(o[t][h], al);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < CT; ++t)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const f16x8 v = widen8<f16x8>((uint32_t)v8[t][x].x, (uint32_t)v8[t][x].y);
+#pragma unroll
+        for (int h = 0; h < HT; ++h) o[t][h] = mfma32(v, p[h][x], o[t][h]);
+      }
+  };
+  auto take_next = [&] {
+#pragma unroll
+    for (int u = 0; u < KU; ++u) S[u] = Sn[u];
+  };
+
+  if (tiles > 0) {
+    if (tiles >= TILES - 1) wait_loads<(TILES - 1 - kAhead) * kLoadsPerWave>();
     else wait_loads<0>();
     barrier_keep_loads();
-    const int tile = round * NKG + kg;
-    const int at = tile % kTiles;
-    // LDS addresses: everything below is one of these plus a constant
-    const uint32_t ring = lds_address(s.ring) + at * kTileBytes;
-    const uint32_t krow = ring + koff, vrow = ring + voff;
-    const uint32_t scale = lds_address(s.scale) + (at * kLatentGroups * kTileKeys + 4 * half) * 4;
-    const uint32_t live = __builtin_amdgcn_readfirstlane(s.live[tile]);
-    if (live) {
-      f32x16 S{};
-#pragma unroll
-      for (int j = 0; j < kRope / 16; ++j) {   // rotary part: bf16 in the row
-        const bf16x8 kr = lds_get<bf16x8>((krow ^ (j << 5)) + kRopeAt);
-        if constexpr (__is_same(Q8, bf16x8)) {
-          S = mfma32(kr, qr[j], S);
-        } else {
-          // an fp16 q as the sum of two bf16 values (8 + 8 bits hold its 11)
-          bf16x8 hi, lo;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            hi[e] = (__bf16)(float)qr[j][e];
-            lo[e] = (__bf16)((float)qr[j][e] - (float)hi[e]);
-          }
-          S = mfma32(kr, hi, S);
-          S = mfma32(kr, lo, S);
-        }
+    if (works) first_product(0);
+    take_next();
+    if constexpr (KU == 1) {
+      barrier_keep_loads();
+      if (works) {
+        softmax(0);
+        if (tiles > 1) first_product(1);
+        take_next();
       }
-#pragma unroll
-      for (int b = 0; b < kLatentGroups; ++b) {
-        f32x16 part{};
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const vec4u k8 = lds_get<vec4u>((krow ^ (t << 5)) + b * kScaleGroup);
-          part = mfma32(widen8<Q8>(k8.x, k8.y), ql[8 * b + 2 * t], part);
-          part = mfma32(widen8<Q8>(k8.z, k8.w), ql[8 * b + 2 * t + 1], part);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const f32x4 sc = lds_get<f32x4>(scale + (kTileKeys * b + 8 * i) * 4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) S[4 * i + e] += sc[e] * part[4 * i + e];
-        }
-      }
-      float top = -__builtin_inff();
-      const uint32_t mine = live >> (4 * half);
-#pragma unroll
-      for (int r = 0; r < 16; ++r) S[r] *= a.scale_log2;
-      if (live != 0xFFFFFFFFu) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (!(mine & (1u << (8 * (r / 4) + r % 4)))) S[r] = -__builtin_inff();
-      }
-#pragma unroll
-      for (int r = 0; r < 16; ++r) top = fmaxf(top, S[r]);
-      top = max_halves(top);
-      // The maximum moves only when it rises by more than 2^8: p then stays below
-      // 2^8, exact in its exponent, and most tiles leave O as it is.
-      if (__any(top > m + 8.0f)) {
-        const float nm = fmaxf(m, top);
-        const float al = nm == -__builtin_inff() ? 1.0f : exp2f(m - nm);
-        m = nm;
-        l *= al;
-#pragma unroll
-        for (int t = 0; t < kOut; ++t) o[t] *= al;
-      }
-      const float base = m == -__builtin_inff() ? 0.0f : m;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        S[r] = __builtin_amdgcn_exp2f(S[r] - base);
-        l += S[r];
-      }
-#pragma unroll
-      for (int bi = 0; bi < kOutBlocks; ++bi) {
-        const int b = cg * kOutBlocks + bi;
-        bf16x8 p[2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const f32x4 sc = lds_get<f32x4>(scale + (kTileKeys * b + 8 * i) * 4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) p[i / 2][4 * (i % 2) + e] = (__bf16)(S[4 * i + e] * sc[e]);
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const i32x2 v8 = lds_read_transposed((vrow ^ (t << 5)) + b * kScaleGroup + x * 16 * kLatentScaleAt);
-            o[4 * bi + t] = mfma32(widen8<bf16x8>((uint32_t)v8.x, (uint32_t)v8.y), p[x], o[4 * bi + t]);
-          }
-      }
-    }
-    barrier_keep_loads();   // every wave is done with this round's tiles
-#pragma unroll
-    for (int x = 0; x < NKG; ++x) {
-      const int next = (round + kRounds) * NKG + x;
-      if (next < total) issue(next);
+    } else {
+      if (works) softmax(0);
     }
   }
-  l = sum_halves(l);
+  // The two waves of a SIMD (w and w + 4) go through a tile's work in opposite
+  // orders, so that one's matrix instructions meet the other's vector work.
+  const bool products_first = wave >= kWaves / 2;
+#pragma unroll 1
+  for (int tile = 0; tile < tiles; ++tile) {
+    // Tile i + kAhead is in LDS once every wave's loads for it are; the barrier also
+    // makes p of tile i (and s.top of tile i + 1) visible and ends the reads of tile
+    // i - 1, whose place the next loads take.
+    if (tile + TILES - 1 <= tiles) wait_loads<(TILES - 2 - kAhead) * kLoadsPerWave>();
+    else wait_loads<0>();
+    barrier_keep_loads();
+    if (tile + TILES - 1 < tiles) issue(tile + TILES - 1);
+    const bool soft = works && tile + 1 < tiles, first = works && tile + kAhead < tiles;
+    if (!products_first) {
+      if constexpr (KU == 1) {
+        if (soft) softmax(tile + 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (first) first_product(tile + kAhead);
+      take_next();
+      if constexpr (KU == 2) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (soft) softmax(tile + 1);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    second_product(tile);
+    __builtin_amdgcn_sched_barrier(0);
+    if (products_first) {
+      if (first) first_product(tile + kAhead);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (KU == 2) take_next();
+      if (soft) softmax(tile + 1);
+      if constexpr (KU == 1) take_next();
+    }
+  }
+  l = sum_quads(l);
 
-  // join the two key groups: the second hands (m, l, O) over in quarters of O
-  if constexpr (NKG == 2) {
-    constexpr int kPart = kOut / 4;
-    float* box = reinterpret_cast<float*>(s.ring) + (wave % (NHG * NCG)) * (kPart * 16 + 2) * kWave + lane;
-    static_assert((kWaves / 2) * (kPart * 16 + 2) * kWave * 4 <= kTiles * kTileBytes, "the ring holds a quarter of O");
-    float w1 = 1.0f, w2 = 0.0f;
-#pragma unroll
-    for (int part = 0; part < 4; ++part) {
-      if (kg == 1) {
-#pragma unroll
-        for (int t = 0; t < kPart; ++t)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) box[(16 * t + r) * kWave] = o[part * kPart + t][r];
-        box[kPart * 16 * kWave] = m;
-        box[(kPart * 16 + 1) * kWave] = l;
-      }
-      __syncthreads();
-      if (kg == 0) {
-        if (part == 0) {
-          const float m2 = box[kPart * 16 * kWave], l2 = box[(kPart * 16 + 1) * kWave];
-          const float nm = fmaxf(m, m2);
-          w1 = nm == -__builtin_inff() ? 0.0f : exp2f(m - nm);
-          w2 = nm == -__builtin_inff() ? 0.0f : exp2f(m2 - nm);
-          m = nm;
-          l = l * w1 + l2 * w2;
-        }
-#pragma unroll
-        for (int t = 0; t < kPart; ++t)
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            o[part * kPart + t][r] = o[part * kPart + t][r] * w1 + box[(16 * t + r) * kWave] * w2;
-      }
-      __syncthreads();
-    }
-    if (kg) return;
+  // every wave needs every head's l and m
+  float* ml = reinterpret_cast<float*>(s.p);      // m, then l of each part
+  __syncthreads();
+  if (quad == 0 && works) {
+    if (part0 == 0) ml[phead] = m;
+    ml[(1 + part0) * kHeads + phead] = l;
   }
-
-  if (head >= a.heads) return;
-  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-  const float lse2 = l != 0.0f ? m + log2f(l) : -__builtin_inff();
-  const int c0 = cg * (kLatent / NCG) + 4 * half;
-  if (a.splits > 1) {   // this split's own result, joined by k_attend_join
-    const size_t row = ((size_t)set * a.heads + head) * a.splits + split;
-    float* po = a.part_o + row * kLatent + c0;
+  __syncthreads();
+  float inv[HT];
 #pragma unroll
-    for (int t = 0; t < kOut; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f32x4 v;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = o[t][4 * i + e] * inv;
-        *reinterpret_cast<f32x4*>(po + 32 * t + 8 * i) = v;
-      }
-    if (half == 0 && cg == 0) a.part_lse[row] = lse2;
-    return;
-  }
-  uint16_t* out = static_cast<uint16_t*>(a.out) + set * a.out_set_stride + head * a.out_head_stride + c0;
-#pragma unroll
-  for (int t = 0; t < kOut; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float v[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = o[t][4 * i + e] * inv;
-      store4<Q8>(out + 32 * t + 8 * i, v, a.out_aligned);
+  for (int h = 0; h < HT; ++h) {
+    float lh = ml[kHeads + 32 * h + col32];
+    if constexpr (KU == 1) lh += ml[2 * kHeads + 32 * h + col32];
+    inv[h] = lh != 0.0f ? 1.0f / lh : 0.0f;
+    const int head = hb * kHeads + 32 * h + col32;
+    if (wave == 0 && half == 0 && head < a.heads) {
+      const float lse2 = lh != 0.0f ? ml[32 * h + col32] + log2f(lh) : -__builtin_inff();
+      if (a.splits > 1) a.part_lse[((size_t)set * a.heads + head) * a.splits + split] = lse2;
+      else if (a.lse) a.lse[(size_t)set * a.heads + head] = lse2 * kLn2;
     }
-  if (half == 0 && cg == 0 && a.lse) a.lse[(size_t)set * a.heads + head] = lse2 * kLn2;
+  }
+  // O through LDS, 32 channels of every wave at a time, so that memory is written
+  // in whole segments (8 bytes per lane from the registers' order took 18 us of a
+  // 256-set call). Rows are padded by 16 bytes for the banks.
+  if (a.splits > 1) {   // this split's own result in 32 bits, joined by k_attend_join
+    float* po = a.part_o + ((size_t)set * a.heads * a.splits + split) * kLatent;
+    store_heads<float>(s.ring[0], o, inv, hb * kHeads, a.heads, [&](int head, int ch, const vec4u v) {
+      *reinterpret_cast<vec4u*>(po + (size_t)head * a.splits * kLatent + ch) = v;
+    });
+  } else {
+    uint16_t* out = static_cast<uint16_t*>(a.out) + set * a.out_set_stride;
+    const bool aligned = a.out_aligned;
+    using Out = std::conditional_t<std::is_same_v<Q8, bf16x8>, __bf16, _Float16>;
+    store_heads<Out>(s.ring[0], o, inv, hb * kHeads, a.heads, [&](int head, int ch, const vec4u v) {
+      uint16_t* p = out + head * a.out_head_stride + ch;
+      if (aligned) {
+        *reinterpret_cast<vec4u*>(p) = v;
+      } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
+      }
+    });
+  }
 }
 
 // Joins the splits of one (set, head): o = sum_s w_s o_s / sum_s w_s with
@@ -446,15 +710,16 @@ AttendPlan plan_attend_latent(int n_sets, int k, int heads) {
   return best;
 }
 
-template <typename Q8, int NHG, int NKG>
+template <typename Q8, int HT, int KU, int TILES, int KEYS>
 static void launch_latent(const GroupDev& g, const AttendDev& a, int n_sets, hipStream_t s) {
-  k_attend_latent<Q8, NHG, NKG><<<n_sets * a.head_blocks * a.splits, kWaves * kWave, 0, s>>>(g, a);
+  k_attend_latent<Q8, HT, KU, TILES, KEYS><<<n_sets * a.head_blocks * a.splits, kWaves * kWave, 0, s>>>(g, a);
 }
 
 template <typename Q8>
 static hipError_t launch_latent_of(const GroupDev& g, const AttendDev& a, int n_sets, hipStream_t s) {
-  if (a.heads <= 32) launch_latent<Q8, 1, 2>(g, a, n_sets, s);
-  else launch_latent<Q8, 2, 1>(g, a, n_sets, s);
+  if (a.heads <= 32) launch_latent<Q8, 1, 1, 5, kAttendKeys>(g, a, n_sets, s);
+  else if (latent_wg_heads(a.heads) == 64) launch_latent<Q8, 2, 1, 5, kAttendKeys>(g, a, n_sets, s);
+  else launch_latent<Q8, 4, 2, 4, kAttendKeys / 2>(g, a, n_sets, s);
   return hipGetLastError();
 }
 

@@ -40,24 +40,12 @@ __device__ __forceinline__ void load_f32(const T* p, float* x) {
   }
 }
 
-__device__ __forceinline__ float finite_abs(float x) {
-  const float a = fabsf(x);
-  return a < __builtin_inff() ? a : 0.0f;   // false for NaN too
-}
-
 __device__ __forceinline__ float scale_of(float amax) { return fmaxf(amax / kE4m3Max, 0x1p-126f); }
 
 // x / scale clamped to e4m3's range; a NaN stays one.
 __device__ __forceinline__ float to_e4m3_range(float x, float scale) {
   const float y = x / scale;
   return y != y ? y : fminf(fmaxf(y, -kE4m3Max), kE4m3Max);
-}
-
-// Four values as e4m3 codes, the first in the lowest byte.
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-  w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
-  return (uint32_t)w;
 }
 
 // cos and sin of 2 pi x turns.

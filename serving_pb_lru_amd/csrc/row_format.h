@@ -42,7 +42,7 @@ struct AttendDev {
   float scale_log2;        // scale x log2(e)
   int32_t k, heads, layer, n_res;
   int32_t splits, split_keys, head_blocks;
-  int32_t q_aligned, out_aligned;   // 16-byte (8-byte) vector accesses are possible
+  int32_t q_aligned, out_aligned;   // 16-byte vector accesses are possible
   int32_t kv_heads, block_shift;    // heads rows
 };
 
@@ -100,6 +100,7 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // Eight e4m3 codes (low byte first) as bf16 or fp16: exact, both hold every e4m3
 // value, so the scales can wait until the products are in 32 bits.
@@ -140,6 +141,12 @@ __device__ __forceinline__ f32x4 mfma16(f16x8 a, f16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
+// 16 x 128 and 128 x 16 in e4m3: lane l holds 32 of the 128 k, the same ones in
+// both operands; D as above.
+__device__ __forceinline__ f32x4 mfma16_e4m3(i32x8 a, i32x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+
 // LDS addresses as 32-bit numbers: the compiler folds a constant added to one
 // into the instruction's offset.
 template <typename T>
@@ -149,6 +156,23 @@ __device__ __forceinline__ uint32_t lds_address(const T& x) {
 template <typename T>
 __device__ __forceinline__ T lds_get(uint32_t addr) {
   return *(const __attribute__((address_space(3))) T*)(uintptr_t)addr;
+}
+
+template <typename T>
+__device__ __forceinline__ void lds_put(uint32_t addr, T v) {
+  *(__attribute__((address_space(3))) T*)(uintptr_t)addr = v;
+}
+
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = fabsf(x);
+  return a < __builtin_inff() ? a : 0.0f;   // false for NaN too
+}
+
+// Four values as e4m3 codes, the first in the lowest byte.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+  return (uint32_t)w;
 }
 
 // A lane's value and that of the lane 32 away (16 away), in either order.

@@ -1251,7 +1251,7 @@ int ula_attend(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32
   a.split_keys = plan.split_keys;
   a.head_blocks = plan.head_blocks;
   a.q_aligned = ((uintptr_t)u.q % 16 == 0 && u.q_set_stride % 8 == 0 && u.q_head_stride % 8 == 0) ? 1 : 0;
-  a.out_aligned = ((uintptr_t)u.out % 8 == 0 && u.out_set_stride % 4 == 0 && u.out_head_stride % 4 == 0) ? 1 : 0;
+  a.out_aligned = ((uintptr_t)u.out % 16 == 0 && u.out_set_stride % 8 == 0 && u.out_head_stride % 8 == 0) ? 1 : 0;
   GroupDev g = gh.d;
   g.res = res_for(ctx, gh, gh.steps);
   if (u.rows.kind == ULA_ROWS_LATENT) {
