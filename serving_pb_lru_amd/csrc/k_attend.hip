@@ -41,8 +41,9 @@
 // 160 us in this form with one wave per SIMD and two streams.)
 // Tiles: the first 640 bytes of each row as 16-byte pieces straight into LDS (no
 // registers), the scales transposed to [block][key]. Piece c of key j lies at
-// c ^ ((j >> 1) & 7): without that the 640-byte row stride maps every other key
-// to the same banks.
+// c ^ swizzle(j), which keeps the 16 lanes that a 16-byte read serves at once
+// (0-3, 12-15, 20-27 and the other such sets) and the 32 of a transposed read on
+// different banks; (j >> 1) & 7 in its place took 8.3 cycles per read, this 4.6.
 #include <algorithm>
 #include <type_traits>
 
@@ -66,16 +67,22 @@ __device__ __align__(16) uint8_t g_zero_row[kLatentRow];
 // knows of before every transposed LDS read. (m0 is never allocated; the kernel
 // has nothing else that uses it.)
 __device__ __forceinline__ void lds_load16(const uint8_t* src, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(dst), "v"(src) : "memory");
+  const uint32_t at = __builtin_amdgcn_readfirstlane(dst);   // a scalar register, whatever the compiler knows
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory");
 }
 __device__ __forceinline__ void lds_load4(const uint8_t* src, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(dst), "v"(src) : "memory");
+  const uint32_t at = __builtin_amdgcn_readfirstlane(dst);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(at), "v"(src) : "memory");
 }
 
 template <int N>
 __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
+
+// The piece bits of key j in a tile that are exchanged (see above): bit 1 from the
+// key's bit 1, bit 2 from bits 2 and 3.
+__device__ __forceinline__ int swizzle(int key) { return (key & 2) | ((key >> 2 ^ key >> 3) & 1) << 2; }
 
 // A workgroup barrier that leaves vector loads in flight (__syncthreads waits
 // for them): this wave's LDS accesses are done, loads into LDS are waited for by
@@ -117,7 +124,7 @@ struct LatentLds {
   float alpha[2][HEADS];                    // factor of O before the tile's second product
   uint32_t moved[2][HEADS / 16];            // whether any of 16 heads has a factor other than 1
   const uint8_t* row[KEYS];                 // each key's row in this layer; zeros for padding
-  uint32_t live[KEYS / kTileKeys];          // bit per key: not padding
+  uint32_t live[KEYS / kTileKeys + 2];      // bit per key: not padding; none behind the last tile
   int ok;
 };
 
@@ -338,6 +345,9 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
   raw.settle();
   __syncthreads();
   if (!s.ok) return;
+  // Tiles behind the last one are computed on whatever lies in their place and
+  // masked, so that the main loop has no branches.
+  if (threadIdx.x < kAhead) s.live[tiles + threadIdx.x] = 0;
 
   // This wave's three loads of a tile's 20 wave-wide ones of pieces and 4 of
   // scales: two of pieces, and one more or a scale block's.
@@ -348,7 +358,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
     const int lane = HT > 1 ? opaque(lane_id()) : lane_id();   // registers are scarce with more heads
     auto piece = [&](int n) { return n * kWave + lane; };
     auto row_of = [&](int key) { return lds_get<const uint8_t*>(rows + key * 8); };
-    auto source = [&](int p) { return (p % kTilePieces ^ (p / kTilePieces >> 1 & 7)) * 16; };
+    auto source = [&](int p) { return (p % kTilePieces ^ swizzle(p / kTilePieces)) * 16; };
     const bool scales = wave >= kWaves - kLatentGroups;
     const int p0 = piece(wave), p1 = piece(kWaves + wave), p2 = piece(2 * kWaves + wave);
     const uint8_t* r0 = row_of(p0 / kTilePieces);
@@ -367,15 +377,15 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
 
   // First product: register r of part u (0, 1) in quad x is key 8 x + 4 u + r.
   // koff: this lane's key of the wave's first part, piece quad of a scale block.
-  // Piece 4 + quad is ^ 64; part 1's key, four rows on, is ^ 32 (its swizzle) and +
+  // Piece 4 + quad is ^ 64; part 1's key, four rows on, is ^ 64 (its swizzle) and +
   // 4 rows. Second product: voff is the row (key) this lane names in a transposed
   // read of keys 0..15, and the channels of its 16 lanes; 32-channel tile t is ^ (t << 5).
   int koff, voff;
   {
     const int key = 8 * (col / 4) + 4 * part0 + col % 4;
-    koff = key * kLatentScaleAt + ((quad ^ ((key >> 1) & 7)) << 4);
+    koff = key * kLatentScaleAt + ((quad ^ swizzle(key)) << 4);
     const int vkey = 8 * half + col / 2;
-    voff = (vkey * kLatentScaleAt + (((quad % 2) ^ ((vkey >> 1) & 7)) << 4) + (col & 1) * 8 +
+    voff = (vkey * kLatentScaleAt + (((quad % 2) ^ swizzle(vkey)) << 4) + (col & 1) * 8 +
             wave * kCh / kScaleGroup * kScaleGroup) ^ (wave * kCh % kScaleGroup);
   }
   static_assert(kLatentScaleAt % 128 == 0 && kTileBytes % 128 == 0, "the swizzle's bits are free in every row address");
@@ -406,7 +416,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
     const uint32_t krow = opaque(lds_address(s.ring) + at * kTileBytes + koff);
     const uint32_t krow64 = opaque(krow ^ 64);
     const uint32_t scale = opaque(lds_address(s.scale) + (at * kLatentGroups * kTileKeys + 8 * quad + 4 * part0) * 4);
-    auto kpiece = [&](int u, int t) { return ((t ? krow64 : krow) ^ (32 * u)) + u * 4 * kLatentScaleAt; };
+    auto kpiece = [&](int u, int t) { return (t != u ? krow64 : krow) + u * 4 * kLatentScaleAt; };
     bf16x8 kr[KU][2];
     vec4u kb[2][KU][2];
     f32x4 sc[2][KU], part[KU];
@@ -500,26 +510,70 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
     }
   };
 
-  // O of a tile whose p is in LDS
-  auto second_product = [&](int tile) {
+  auto take_next = [&] {
+#pragma unroll
+    for (int u = 0; u < KU; ++u) S[u] = Sn[u];
+  };
+
+  if (tiles > 0) {
+    if (tiles >= TILES - 1) wait_loads<(TILES - 1 - kAhead) * kLoadsPerWave>();
+    else wait_loads<0>();
+    barrier_keep_loads();
+    if (works) first_product(0);
+    take_next();
+    if constexpr (KU == 1) {
+      barrier_keep_loads();
+      if (works) {
+        softmax(0);
+        first_product(1);
+      }
+      take_next();
+    } else {
+      if (works) softmax(0);
+    }
+  }
+  // The two waves of a SIMD (w and w + 4) go through a tile's work in opposite
+  // orders, so that one's matrix instructions meet the other's vector work.
+  const bool products_first = wave >= kWaves / 2;
+#pragma unroll 1
+  for (int tile = 0; tile < tiles; ++tile) {
+    // Tile i + kAhead is in LDS once every wave's loads for it are; the barrier also
+    // makes p of tile i (and s.top of tile i + 1) visible and ends the reads of tile
+    // i - 1, whose place the next loads take.
+    if (tile + TILES - 1 <= tiles) wait_loads<(TILES - 2 - kAhead) * kLoadsPerWave>();
+    else wait_loads<0>();
+    barrier_keep_loads();
+    // operands of this tile's second product, read ahead of the work in between
     const int buf = tile & 1;
     const uint32_t vrow = opaque(lds_address(s.ring) + (tile % TILES) * kTileBytes + voff);
     // chunk 2 x + half of this lane's head: ^ 32 for x
     const uint32_t prow = opaque(pread + buf * kLatentGroups * kHeads * kTileKeys * 2);
     i32x2 v8[CT][2];
     f16x8 p[HT][2];
-#pragma unroll
-    for (int t = 0; t < CT; ++t)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) v8[t][x] = lds_read_transposed((vrow ^ (t << 5)) + x * 16 * kLatentScaleAt);
-#pragma unroll
-    for (int h = 0; h < HT; ++h)
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        p[h][x] = lds_get<f16x8>((prow ^ (32 * x)) + 32 * h * kTileKeys * 2);
     uint32_t moved = 0;                           // a reference moved: O's factors
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) moved |= s.moved[buf][i];
+    for (int i = 0; i < kGroups; ++i) moved |= lds_get<uint32_t>(lds_address(s.moved) + (buf * kGroups + i) * 4);
+    auto read_second = [&] {
+#pragma unroll
+      for (int t = 0; t < CT; ++t)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) v8[t][x] = lds_read_transposed((vrow ^ (t << 5)) + x * 16 * kLatentScaleAt);
+#pragma unroll
+      for (int h = 0; h < HT; ++h)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) p[h][x] = lds_get<f16x8>((prow ^ (32 * x)) + 32 * h * kTileKeys * 2);
+    };
+    if (tile + TILES - 1 < tiles) issue(tile + TILES - 1);
+    if (works && !products_first) {
+      if constexpr (KU == 1) softmax(tile + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      first_product(tile + kAhead);
+      take_next();
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (KU == 2) softmax(tile + 1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    read_second();
     if (__builtin_amdgcn_readfirstlane(moved)) {
 #pragma unroll
       for (int h = 0; h < HT; ++h) {
@@ -536,62 +590,12 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
 #pragma unroll
         for (int h = 0; h < HT; ++h) o[t][h] = mfma32(v, p[h][x], o[t][h]);
       }
-  };
-  auto take_next = [&] {
-#pragma unroll
-    for (int u = 0; u < KU; ++u) S[u] = Sn[u];
-  };
-
-  if (tiles > 0) {
-    if (tiles >= TILES - 1) wait_loads<(TILES - 1 - kAhead) * kLoadsPerWave>();
-    else wait_loads<0>();
-    barrier_keep_loads();
-    if (works) first_product(0);
-    take_next();
-    if constexpr (KU == 1) {
-      barrier_keep_loads();
-      if (works) {
-        softmax(0);
-        if (tiles > 1) first_product(1);
-        take_next();
-      }
-    } else {
-      if (works) softmax(0);
-    }
-  }
-  // The two waves of a SIMD (w and w + 4) go through a tile's work in opposite
-  // orders, so that one's matrix instructions meet the other's vector work.
-  const bool products_first = wave >= kWaves / 2;
-#pragma unroll 1
-  for (int tile = 0; tile < tiles; ++tile) {
-    // Tile i + kAhead is in LDS once every wave's loads for it are; the barrier also
-    // makes p of tile i (and s.top of tile i + 1) visible and ends the reads of tile
-    // i - 1, whose place the next loads take.
-    if (tile + TILES - 1 <= tiles) wait_loads<(TILES - 2 - kAhead) * kLoadsPerWave>();
-    else wait_loads<0>();
-    barrier_keep_loads();
-    if (tile + TILES - 1 < tiles) issue(tile + TILES - 1);
-    const bool soft = works && tile + 1 < tiles, first = works && tile + kAhead < tiles;
-    if (!products_first) {
-      if constexpr (KU == 1) {
-        if (soft) softmax(tile + 1);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if (first) first_product(tile + kAhead);
-      take_next();
-      if constexpr (KU == 2) {
-        __builtin_amdgcn_sched_barrier(0);
-        if (soft) softmax(tile + 1);
-      }
-    }
     __builtin_amdgcn_sched_barrier(0);
-    second_product(tile);
-    __builtin_amdgcn_sched_barrier(0);
-    if (products_first) {
-      if (first) first_product(tile + kAhead);
+    if (works && products_first) {
+      first_product(tile + kAhead);
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (KU == 2) take_next();
-      if (soft) softmax(tile + 1);
+      softmax(tile + 1);
       if constexpr (KU == 1) take_next();
     }
   }
