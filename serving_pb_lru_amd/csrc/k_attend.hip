@@ -25,17 +25,17 @@
 //
 // Layout. Both products are taken transposed: S^T = K Q^T puts heads in the
 // lanes' columns and keys in registers, O^T = V^T P^T the same way. The eight
-// waves of a workgroup split the first product by heads, 16 each (and, with at
-// most 64 heads, by the halves of a tile's 32 keys), and the second by channels of
-// O, 64 each with all heads: so no wave holds another's Q, every key is read from
-// LDS by the waves of different heads and every value once in all. In between p
-// goes through LDS, scaled for each block and in the operand order of the second
-// product.
-// One barrier per tile. Between two of them a wave computes S of one tile, p of
-// the tile before (once both halves' largest logits are known) and the second
-// product of the one before that: three independent streams of matrix, vector
-// and LDS work, in two waves per SIMD. With more than 64 heads a wave has all of
-// a tile's keys and p follows S at once.
+// waves of a workgroup split the first product by 16 heads and half of a tile's 32
+// keys, and the second by 64 channels of O with all heads: so no wave holds
+// another's Q, every key is read from LDS by the waves of different heads and
+// every value once in all. In between p goes through LDS, scaled for each block
+// and in the operand order of the second product.
+// One barrier per tile. Between two of them a wave computes the second product of
+// one tile, p of the next (once both halves' largest logits are known) and S of
+// the one after that: three streams that do not depend on each other, so the
+// softmax's vector work runs under the second product's matrix instructions and
+// the LDS reads of each run ahead. A wave's way through them is bound by latency,
+// which is why the reads are grouped as they are.
 // (256 sets of 2048 keys and 64 heads: 206 us with a wave that kept 32 heads to
 // itself for both products, reading and widening every key and value four times;
 // 160 us in this form with one wave per SIMD and two streams.)
@@ -114,13 +114,13 @@ constexpr int kWaves = 8;
 constexpr int kLoadsPerWave = (kTileLoads + kLatentGroups) / kWaves;   // vector loads a wave issues per tile
 static_assert(kLoadsPerWave == 3 && kTileLoads % kWaves == kLatentGroups, "see issue()");
 
-template <int HEADS, int KU, int TILES, int KEYS>
+template <int HEADS, int TILES, int KEYS>
 struct LatentLds {
   alignas(1024) uint8_t ring[TILES][kTileBytes];
   // p x scale of two tiles: [block][head][key], key chunk c (8 keys) of head h at c ^ ((h >> 2) & 3)
   alignas(1024) _Float16 p[2][kLatentGroups][HEADS][kTileKeys];
   alignas(16) float scale[TILES][kLatentGroups][kTileKeys];
-  float top[2][2 / KU][HEADS];              // largest logit (with its scale's exponent) of a tile's part
+  float top[2][2][HEADS];                   // largest logit (with its scale's exponent) of a tile's halves
   float alpha[2][HEADS];                    // factor of O before the tile's second product
   uint32_t moved[2][HEADS / 16];            // whether any of 16 heads has a factor other than 1
   const uint8_t* row[KEYS];                 // each key's row in this layer; zeros for padding
@@ -201,10 +201,16 @@ struct QueryOperand<bf16x8> {
     for (int j = 0; j < kRope / 32; ++j) s = mfma16(kr[j], rope[j], s);
     return s * up;
   }
-  __device__ __forceinline__ f32x4 block_product(int b, vec4u k0, vec4u k1) const {
-    const i32x8 k = {(int)k0.x, (int)k0.y, (int)k0.z, (int)k0.w, (int)k1.x, (int)k1.y, (int)k1.z, (int)k1.w};
-    const f32x4 s = mfma16_e4m3(k, hi[b], f32x4{});
-    return mfma16_e4m3(k, lo[b], s);
+  static __device__ __forceinline__ i32x8 join(const vec4u* k) {
+    return i32x8{(int)k[0].x, (int)k[0].y, (int)k[0].z, (int)k[0].w, (int)k[1].x, (int)k[1].y, (int)k[1].z, (int)k[1].w};
+  }
+  // products of blocks b and b + 1, interleaved so that none waits for the one before it
+  __device__ __forceinline__ void block_products(int b, const vec4u* k0, const vec4u* k1, f32x4& s0, f32x4& s1) const {
+    const i32x8 x = join(k0), y = join(k1);
+    s0 = mfma16_e4m3(x, hi[b], f32x4{});
+    s1 = mfma16_e4m3(y, hi[b + 1], f32x4{});
+    s0 = mfma16_e4m3(x, lo[b], s0);
+    s1 = mfma16_e4m3(y, lo[b + 1], s1);
   }
 };
 
@@ -230,12 +236,15 @@ struct QueryOperand<f16x8> {
     for (int j = 0; j < kRope / 32; ++j) s = mfma16(kr[j], rope_lo[j], mfma16(kr[j], rope_hi[j], s));
     return s;
   }
-  __device__ __forceinline__ f32x4 block_product(int b, vec4u k0, vec4u k1) const {
-    f32x4 s{};
-    s = mfma16(widen8<f16x8>(k0.x, k0.y), x[4 * b], s);
-    s = mfma16(widen8<f16x8>(k0.z, k0.w), x[4 * b + 1], s);
-    s = mfma16(widen8<f16x8>(k1.x, k1.y), x[4 * b + 2], s);
-    return mfma16(widen8<f16x8>(k1.z, k1.w), x[4 * b + 3], s);
+  __device__ __forceinline__ void block_products(int b, const vec4u* k0, const vec4u* k1, f32x4& s0, f32x4& s1) const {
+    s0 = s1 = f32x4{};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      s0 = mfma16(widen8<f16x8>(k0[j].x, k0[j].y), x[4 * b + 2 * j], s0);
+      s1 = mfma16(widen8<f16x8>(k1[j].x, k1[j].y), x[4 * b + 4 + 2 * j], s1);
+      s0 = mfma16(widen8<f16x8>(k0[j].z, k0[j].w), x[4 * b + 2 * j + 1], s0);
+      s1 = mfma16(widen8<f16x8>(k1[j].z, k1[j].w), x[4 * b + 4 + 2 * j + 1], s1);
+    }
   }
 };
 
@@ -273,26 +282,26 @@ __device__ __forceinline__ void store_heads(uint8_t* box, const f32x16 (&o)[CT][
   }
 }
 
-// HT tiles of 32 heads; KU 16-key parts of a tile per wave of the first product;
+// HT tiles of 32 heads;
 // TILES tiles in the ring; at most KEYS keys.
-template <typename Q8, int HT, int KU, int TILES, int KEYS>
+template <typename Q8, int HT, int TILES, int KEYS>
 __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g, AttendDev a) {
   constexpr int kHeads = 32 * HT;                 // heads of a workgroup
   constexpr int kGroups = kHeads / 16;            // of 16
   constexpr int kCh = kLatent / kWaves;           // channels of O per wave
   constexpr int CT = kCh / 32;                    // in tiles of 32
-  constexpr int kAhead = KU == 2 ? 1 : 2;         // tiles that the first product runs ahead of the second
-  static_assert(kGroups * (2 / KU) <= kWaves, "every head and part has a wave in the first product");
+  constexpr int kAhead = 2;                       // tiles that the first product runs ahead of the second
+  static_assert(kGroups * 2 <= kWaves, "every head and half has a wave in the first product");
   static_assert(TILES >= kAhead + 2, "a tile on its way beside those in use");
-  __shared__ LatentLds<kHeads, KU, TILES, KEYS> s;
+  __shared__ LatentLds<kHeads, TILES, KEYS> s;
   static_assert(sizeof(s) <= 160 * 1024, "LDS of a compute unit");
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);   // uniform: its branches are scalar
   const int quad = lane / 16, col = lane % 16;    // first product: 16 heads, quads of keys
   const int half = lane / 32, col32 = lane % 32;  // second product: 32 heads
   const int hg = wave % kGroups;                  // this wave's heads in the first product
-  const int part0 = KU == 2 ? 0 : wave / kGroups; // and its part of a tile's keys
-  const bool works = wave < kGroups * (2 / KU);   // whether it has any
+  const int part0 = wave / kGroups;               // and its half of a tile's keys
+  const bool works = kGroups * 2 == kWaves || wave < kGroups * 2;   // whether it has any
 
   // work item: consecutive sets (which share rows under speculative selection)
   // run on one XCD at about the same time
@@ -350,35 +359,40 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
   if (threadIdx.x < kAhead) s.live[tiles + threadIdx.x] = 0;
 
   // This wave's three loads of a tile's 20 wave-wide ones of pieces and 4 of
-  // scales: two of pieces, and one more or a scale block's.
+  // scales: two of pieces, and one more or a scale block's. The rows' addresses are
+  // read from LDS one tile earlier.
+  const bool scales = wave >= kWaves - kLatentGroups;
+  int row_at[kLoadsPerWave], source[kLoadsPerWave];   // LDS offset of the row's address, offset in the row
+#pragma unroll
+  for (int i = 0; i < kLoadsPerWave; ++i) {
+    const int p = (i * kWaves + wave) * kWave + lane, key = p / kTilePieces;
+    row_at[i] = 8 * key;
+    source[i] = (p % kTilePieces ^ swizzle(key)) * 16;
+  }
+  const int scale_block = wave - (kWaves - kLatentGroups);
+  if (scales) {
+    row_at[2] = 8 * (lane % kTileKeys);
+    source[2] = kLatentScaleAt + 4 * scale_block;
+  }
+  const uint8_t* row[kLoadsPerWave];
+  auto read_rows = [&](int tile) {
+    const uint32_t rows = lds_address(s.row) + min(tile, max(tiles - 1, 0)) * kTileKeys * 8;
+#pragma unroll
+    for (int i = 0; i < kLoadsPerWave; ++i) row[i] = lds_get<const uint8_t*>(rows + row_at[i]);
+  };
   auto issue = [&](int tile) {
     const int at = tile % TILES;
-    const uint32_t rows = lds_address(s.row) + tile * kTileKeys * 8;
     const uint32_t ring = lds_address(s.ring) + at * kTileBytes;
-    const int lane = HT > 1 ? opaque(lane_id()) : lane_id();   // registers are scarce with more heads
-    auto piece = [&](int n) { return n * kWave + lane; };
-    auto row_of = [&](int key) { return lds_get<const uint8_t*>(rows + key * 8); };
-    auto source = [&](int p) { return (p % kTilePieces ^ swizzle(p / kTilePieces)) * 16; };
-    const bool scales = wave >= kWaves - kLatentGroups;
-    const int p0 = piece(wave), p1 = piece(kWaves + wave), p2 = piece(2 * kWaves + wave);
-    const uint8_t* r0 = row_of(p0 / kTilePieces);
-    const uint8_t* r1 = row_of(p1 / kTilePieces);
-    const uint8_t* r2 = row_of(scales ? lane % kTileKeys : p2 / kTilePieces);
-    lds_load16(r0 + source(p0), ring + wave * kWave * 16);
-    lds_load16(r1 + source(p1), ring + (kWaves + wave) * kWave * 16);
-    if (scales) {
-      const int b = wave - (kWaves - kLatentGroups);
-      if (lane < kTileKeys)
-        lds_load4(r2 + kLatentScaleAt + 4 * b, lds_address(s.scale) + (at * kLatentGroups + b) * kTileKeys * 4);
-    } else {
-      lds_load16(r2 + source(p2), ring + (2 * kWaves + wave) * kWave * 16);
-    }
+    lds_load16(row[0] + source[0], ring + wave * kWave * 16);
+    lds_load16(row[1] + source[1], ring + (kWaves + wave) * kWave * 16);
+    if (!scales) lds_load16(row[2] + source[2], ring + (2 * kWaves + wave) * kWave * 16);
+    else if (lane < kTileKeys)
+      lds_load4(row[2] + source[2], lds_address(s.scale) + (at * kLatentGroups + scale_block) * kTileKeys * 4);
   };
 
   // First product: register r of part u (0, 1) in quad x is key 8 x + 4 u + r.
-  // koff: this lane's key of the wave's first part, piece quad of a scale block.
-  // Piece 4 + quad is ^ 64; part 1's key, four rows on, is ^ 64 (its swizzle) and +
-  // 4 rows. Second product: voff is the row (key) this lane names in a transposed
+  // koff: this lane's key of the wave's part, piece quad of a scale block; piece
+  // 4 + quad is ^ 64. Second product: voff is the row (key) this lane names in a transposed
   // read of keys 0..15, and the channels of its 16 lanes; 32-channel tile t is ^ (t << 5).
   int koff, voff;
   {
@@ -402,107 +416,100 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
   float m = -__builtin_inff(), l = 0.0f;          // of this wave's 16 heads; l of this lane's keys alone
 
 #pragma unroll 1
-  for (int t = 0; t < TILES - 1 && t < tiles; ++t) issue(t);
+  for (int t = 0; t < TILES - 1 && t < tiles; ++t) {
+    read_rows(t);
+    issue(t);
+  }
   QueryOperand<Q8> q;
   q.take(raw);
   const float c_log2 = a.scale_log2 / q.up;
-  f32x4 S[KU], Sn[KU];                            // logits (base 2) of the tile at hand, and of the next one
+  f32x4 S{};                                      // logits (base 2) of the tile at hand
 
-  // Sn of a tile in LDS, and its largest values to s.top. LDS reads run one block
-  // ahead of the products; the scheduling barriers keep the compiler from moving
-  // them back to their uses.
+  // S of a tile in LDS, and its largest value to s.top, in three steps: reads of
+  // the first two blocks' keys, the products, and the sums.
+  bf16x8 kr[2];
+  vec4u kb[kLatentGroups][2];
+  auto key_address = [&](int tile) { return opaque(lds_address(s.ring) + tile % TILES * kTileBytes + koff); };
+  auto read_block = [&](uint32_t krow, int b) {
+    kb[b][0] = lds_get<vec4u>(krow + b * kScaleGroup);
+    kb[b][1] = lds_get<vec4u>((krow ^ 64) + b * kScaleGroup);
+  };
+  auto read_keys = [&](int tile) {
+    const uint32_t krow = key_address(tile);
+    kr[0] = lds_get<bf16x8>(krow + kRopeAt);
+    kr[1] = lds_get<bf16x8>((krow ^ 64) + kRopeAt);
+    read_block(krow, 0);
+    read_block(krow, 1);
+  };
+  auto scale_address = [&](int tile) {
+    return opaque(lds_address(s.scale) + (tile % TILES * kLatentGroups * kTileKeys + 8 * quad + 4 * part0) * 4);
+  };
+  f32x4 part[kLatentGroups], next{};
   auto first_product = [&](int tile) {
-    const int at = tile % TILES;
-    const uint32_t krow = opaque(lds_address(s.ring) + at * kTileBytes + koff);
-    const uint32_t krow64 = opaque(krow ^ 64);
-    const uint32_t scale = opaque(lds_address(s.scale) + (at * kLatentGroups * kTileKeys + 8 * quad + 4 * part0) * 4);
-    auto kpiece = [&](int u, int t) { return (t != u ? krow64 : krow) + u * 4 * kLatentScaleAt; };
-    bf16x8 kr[KU][2];
-    vec4u kb[2][KU][2];
-    f32x4 sc[2][KU], part[KU];
-    float big = 0x1p-60f;                         // largest scale of the lane's keys
-    auto read_block = [&](int b) {
+    const uint32_t krow = key_address(tile);
+    read_block(krow, 2);
+    read_block(krow, 3);
+    __builtin_amdgcn_sched_barrier(0);
+    next = q.rope_product(kr);
+    q.block_products(0, kb[0], kb[1], part[0], part[1]);
+    q.block_products(2, kb[2], kb[3], part[2], part[3]);
+  };
+  auto finish_logits = [&](int tile) {
+    const uint32_t scale = scale_address(tile);
+    f32x4 sc[kLatentGroups];
 #pragma unroll
-      for (int u = 0; u < KU; ++u) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) kb[b & 1][u][t] = lds_get<vec4u>(kpiece(u, t) + b * kScaleGroup);
-        sc[b & 1][u] = lds_get<f32x4>(scale + (kTileKeys * b + 4 * u) * 4);
-      }
-    };
-    auto add_block = [&](int b) {
-#pragma unroll
-      for (int u = 0; u < KU; ++u) {
-        Sn[u] += sc[b & 1][u] * part[u];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) big = fmaxf(big, sc[b & 1][u][r]);
-      }
-    };
-#pragma unroll
-    for (int u = 0; u < KU; ++u)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) kr[u][j] = lds_get<bf16x8>(kpiece(u, j) + kRopeAt);
-    read_block(0);
+    for (int b = 0; b < kLatentGroups; ++b) sc[b] = lds_get<f32x4>(scale + kTileKeys * b * 4);
     const uint32_t live = __builtin_amdgcn_readfirstlane(s.live[tile]) >> (8 * quad + 4 * part0);
+    float big = 0x1p-60f;                         // largest scale of the lane's keys
 #pragma unroll
     for (int b = 0; b < kLatentGroups; ++b) {
-      if (b > 0) add_block(b - 1);
-      if (b + 1 < kLatentGroups) read_block(b + 1);
-      __builtin_amdgcn_sched_barrier(0);
+      next += sc[b] * part[b];
 #pragma unroll
-      for (int u = 0; u < KU; ++u) {
-        if (b == 0) Sn[u] = q.rope_product(kr[u]);
-        part[u] = q.block_product(b, kb[b & 1][u][0], kb[b & 1][u][1]);
-      }
+      for (int r = 0; r < 4; ++r) big = fmaxf(big, sc[b][r]);
     }
-    add_block(kLatentGroups - 1);
     float top = -__builtin_inff();
 #pragma unroll
-    for (int u = 0; u < KU; ++u)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        Sn[u][r] = live & (1u << (4 * u + r)) ? Sn[u][r] * c_log2 : -__builtin_inff();
-        top = fmaxf(top, Sn[u][r]);
-      }
+    for (int r = 0; r < 4; ++r) {
+      next[r] = live & (1u << r) ? next[r] * c_log2 : -__builtin_inff();
+      top = fmaxf(top, next[r]);
+    }
     top = max_quads(top + (float)__builtin_amdgcn_frexp_expf(big));
     if (quad == 0) s.top[tile & 1][part0][phead] = top;
   };
-  // p of the tile whose S is at hand and whose s.top every part has written,
+  // p of the tile whose S is at hand and whose s.top both halves have written,
   // scaled, to LDS for the second product
+  f32x4 soft_scale[kLatentGroups];
+  float soft_top = 0.0f, soft_top1 = 0.0f;
+  auto read_softmax = [&](int tile) {
+    const uint32_t scale = scale_address(tile);
+    const uint32_t tops = opaque(lds_address(s.top) + ((tile & 1) * 2 * kHeads + phead) * 4);
+    soft_top = lds_get<float>(tops);
+    soft_top1 = lds_get<float>(tops + kHeads * 4);
+#pragma unroll
+    for (int b = 0; b < kLatentGroups; ++b) soft_scale[b] = lds_get<f32x4>(scale + kTileKeys * b * 4);
+  };
   auto softmax = [&](int tile) {
-    const int at = tile % TILES, buf = tile & 1;
-    const uint32_t scale = opaque(lds_address(s.scale) + (at * kLatentGroups * kTileKeys + 8 * quad + 4 * part0) * 4);
-    const uint32_t tops = opaque(lds_address(s.top) + (buf * (2 / KU) * kHeads + phead) * 4);
+    const int buf = tile & 1;
     const uint32_t pw = opaque(pwrite + buf * kLatentGroups * kHeads * kTileKeys * 2);
-    float top = lds_get<float>(tops);
-    if constexpr (KU == 1) top = fmaxf(top, lds_get<float>(tops + kHeads * 4));
-    f32x4 sc[kLatentGroups][KU];
-#pragma unroll
-    for (int b = 0; b < kLatentGroups; ++b)
-#pragma unroll
-      for (int u = 0; u < KU; ++u) sc[b][u] = lds_get<f32x4>(scale + (kTileKeys * b + 4 * u) * 4);
+    const float top = fmaxf(soft_top, soft_top1);
     const bool move = top > m + 15.0f;
     const float nm = move ? top - 8.0f : m;
     const float al = move ? __builtin_amdgcn_exp2f(m - nm) : 1.0f;
     m = nm;
     l *= al;
     const float base = nm == -__builtin_inff() ? 0.0f : nm;
-    f32x4 e[KU];
 #pragma unroll
-    for (int u = 0; u < KU; ++u)
+    for (int r = 0; r < 4; ++r) {
+      S[r] = __builtin_amdgcn_exp2f(S[r] - base);
+      l += S[r];
+    }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        e[u][r] = __builtin_amdgcn_exp2f(S[u][r] - base);
-        l += e[u][r];
-      }
+    for (int b = 0; b < kLatentGroups; ++b) {
+      f16x4 w;
 #pragma unroll
-    for (int b = 0; b < kLatentGroups; ++b)
-#pragma unroll
-      for (int u = 0; u < KU; ++u) {
-        f16x4 w;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) w[r] = (_Float16)(e[u][r] * sc[b][u][r]);
-        lds_put(pw + b * kHeads * kTileKeys * 2 + u * 8, w);
-      }
+      for (int r = 0; r < 4; ++r) w[r] = (_Float16)(S[r] * soft_scale[b][r]);
+      lds_put(pw + b * kHeads * kTileKeys * 2, w);
+    }
     const bool moved = __any(move);
     if (part0 == 0) {
       if (quad == 0) s.alpha[buf][phead] = al;
@@ -510,70 +517,54 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
     }
   };
 
-  auto take_next = [&] {
-#pragma unroll
-    for (int u = 0; u < KU; ++u) S[u] = Sn[u];
-  };
-
   if (tiles > 0) {
     if (tiles >= TILES - 1) wait_loads<(TILES - 1 - kAhead) * kLoadsPerWave>();
     else wait_loads<0>();
     barrier_keep_loads();
-    if (works) first_product(0);
-    take_next();
-    if constexpr (KU == 1) {
-      barrier_keep_loads();
-      if (works) {
-        softmax(0);
-        first_product(1);
-      }
-      take_next();
-    } else {
-      if (works) softmax(0);
+    if (works) {
+      read_keys(0);
+      first_product(0);
+      finish_logits(0);
+      S = next;
     }
+    barrier_keep_loads();
+    if (works) {
+      read_softmax(0);
+      softmax(0);
+      read_keys(1);
+      first_product(1);
+      finish_logits(1);
+      S = next;
+    }
+    read_rows(TILES - 1);
   }
-  // The two waves of a SIMD (w and w + 4) go through a tile's work in opposite
-  // orders, so that one's matrix instructions meet the other's vector work.
-  const bool products_first = wave >= kWaves / 2;
 #pragma unroll 1
   for (int tile = 0; tile < tiles; ++tile) {
     // Tile i + kAhead is in LDS once every wave's loads for it are; the barrier also
-    // makes p of tile i (and s.top of tile i + 1) visible and ends the reads of tile
+    // makes p of tile i and s.top of tile i + 1 visible and ends the reads of tile
     // i - 1, whose place the next loads take.
     if (tile + TILES - 1 <= tiles) wait_loads<(TILES - 2 - kAhead) * kLoadsPerWave>();
     else wait_loads<0>();
     barrier_keep_loads();
-    // operands of this tile's second product, read ahead of the work in between
     const int buf = tile & 1;
-    const uint32_t vrow = opaque(lds_address(s.ring) + (tile % TILES) * kTileBytes + voff);
+    const uint32_t vrow = opaque(lds_address(s.ring) + tile % TILES * kTileBytes + voff);
     // chunk 2 x + half of this lane's head: ^ 32 for x
     const uint32_t prow = opaque(pread + buf * kLatentGroups * kHeads * kTileKeys * 2);
-    i32x2 v8[CT][2];
-    f16x8 p[HT][2];
     uint32_t moved = 0;                           // a reference moved: O's factors
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) moved |= lds_get<uint32_t>(lds_address(s.moved) + (buf * kGroups + i) * 4);
-    auto read_second = [&] {
+    i32x2 v8[CT][2];
+    f16x8 p[HT][2];
 #pragma unroll
-      for (int t = 0; t < CT; ++t)
+    for (int t = 0; t < CT; ++t)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) v8[t][x] = lds_read_transposed((vrow ^ (t << 5)) + x * 16 * kLatentScaleAt);
+      for (int x = 0; x < 2; ++x) v8[t][x] = lds_read_transposed((vrow ^ (t << 5)) + x * 16 * kLatentScaleAt);
 #pragma unroll
-      for (int h = 0; h < HT; ++h)
+    for (int h = 0; h < HT; ++h)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) p[h][x] = lds_get<f16x8>((prow ^ (32 * x)) + 32 * h * kTileKeys * 2);
-    };
+      for (int x = 0; x < 2; ++x) p[h][x] = lds_get<f16x8>((prow ^ (32 * x)) + 32 * h * kTileKeys * 2);
+    if (works) read_softmax(tile + 1);
     if (tile + TILES - 1 < tiles) issue(tile + TILES - 1);
-    if (works && !products_first) {
-      if constexpr (KU == 1) softmax(tile + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      first_product(tile + kAhead);
-      take_next();
-      __builtin_amdgcn_sched_barrier(0);
-      if constexpr (KU == 2) softmax(tile + 1);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    read_second();
     if (__builtin_amdgcn_readfirstlane(moved)) {
 #pragma unroll
       for (int h = 0; h < HT; ++h) {
@@ -582,21 +573,29 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
         for (int t = 0; t < CT; ++t) scale_in_place(o[t][h], al);
       }
     }
+    auto second_product = [&] {
 #pragma unroll
-    for (int t = 0; t < CT; ++t)
+      for (int t = 0; t < CT; ++t)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const f16x8 v = widen8<f16x8>((uint32_t)v8[t][x].x, (uint32_t)v8[t][x].y);
+        for (int x = 0; x < 2; ++x) {
+          const f16x8 v = widen8<f16x8>((uint32_t)v8[t][x].x, (uint32_t)v8[t][x].y);
 #pragma unroll
-        for (int h = 0; h < HT; ++h) o[t][h] = mfma32(v, p[h][x], o[t][h]);
-      }
+          for (int h = 0; h < HT; ++h) o[t][h] = mfma32(v, p[h][x], o[t][h]);
+        }
+    };
     __builtin_amdgcn_sched_barrier(0);
-    if (works && products_first) {
-      first_product(tile + kAhead);
-      __builtin_amdgcn_sched_barrier(0);
-      if constexpr (KU == 2) take_next();
+    if (works) read_keys(tile + kAhead);
+    second_product();
+    if (works) {
       softmax(tile + 1);
-      if constexpr (KU == 1) take_next();
+      __builtin_amdgcn_sched_barrier(0);
+      first_product(tile + kAhead);
+    }
+    read_rows(tile + TILES);
+    if (works) {
+      __builtin_amdgcn_sched_barrier(0);
+      finish_logits(tile + kAhead);
+      S = next;
     }
   }
   l = sum_quads(l);
@@ -613,7 +612,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
 #pragma unroll
   for (int h = 0; h < HT; ++h) {
     float lh = ml[kHeads + 32 * h + col32];
-    if constexpr (KU == 1) lh += ml[2 * kHeads + 32 * h + col32];
+    lh += ml[2 * kHeads + 32 * h + col32];
     inv[h] = lh != 0.0f ? 1.0f / lh : 0.0f;
     const int head = hb * kHeads + 32 * h + col32;
     if (wave == 0 && half == 0 && head < a.heads) {
@@ -714,16 +713,15 @@ AttendPlan plan_attend_latent(int n_sets, int k, int heads) {
   return best;
 }
 
-template <typename Q8, int HT, int KU, int TILES, int KEYS>
+template <typename Q8, int HT, int TILES, int KEYS>
 static void launch_latent(const GroupDev& g, const AttendDev& a, int n_sets, hipStream_t s) {
-  k_attend_latent<Q8, HT, KU, TILES, KEYS><<<n_sets * a.head_blocks * a.splits, kWaves * kWave, 0, s>>>(g, a);
+  k_attend_latent<Q8, HT, TILES, KEYS><<<n_sets * a.head_blocks * a.splits, kWaves * kWave, 0, s>>>(g, a);
 }
 
 template <typename Q8>
 static hipError_t launch_latent_of(const GroupDev& g, const AttendDev& a, int n_sets, hipStream_t s) {
-  if (a.heads <= 32) launch_latent<Q8, 1, 1, 5, kAttendKeys>(g, a, n_sets, s);
-  else if (latent_wg_heads(a.heads) == 64) launch_latent<Q8, 2, 1, 5, kAttendKeys>(g, a, n_sets, s);
-  else launch_latent<Q8, 4, 2, 4, kAttendKeys / 2>(g, a, n_sets, s);
+  if (a.heads <= 32) launch_latent<Q8, 1, 5, kAttendKeys>(g, a, n_sets, s);
+  else launch_latent<Q8, 2, 5, kAttendKeys>(g, a, n_sets, s);
   return hipGetLastError();
 }
 
