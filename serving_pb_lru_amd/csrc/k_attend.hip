@@ -24,21 +24,19 @@
 // Both products have 32-bit accumulators.
 //
 // Layout. Both products are taken transposed: S^T = K Q^T puts heads in the
-// lanes' columns and keys in registers, O^T = V^T P^T the same way. The eight
-// waves of a workgroup split the first product by 16 heads and half of a tile's 32
-// keys, and the second by 64 channels of O with all heads: so no wave holds
-// another's Q, every key is read from LDS by the waves of different heads and
-// every value once in all. In between p goes through LDS, scaled for each block
-// and in the operand order of the second product.
-// One barrier per tile. Between two of them a wave computes the second product of
-// one tile, p of the next (once both halves' largest logits are known) and S of
-// the one after that: three streams that do not depend on each other, so the
-// softmax's vector work runs under the second product's matrix instructions and
-// the LDS reads of each run ahead. A wave's way through them is bound by latency,
-// which is why the reads are grouped as they are.
+// lanes' columns and keys in registers, O^T = V^T P^T the same way. A workgroup
+// has four waves for the first product and the softmax, 16 heads each, and four
+// for the second product, 128 channels of O (one scale block) with all heads
+// each: so no wave holds another's Q, every key is read from LDS by the waves of
+// different heads and every value once. In between p goes through LDS, scaled for
+// each block and in the operand order of the second product. Each SIMD has a wave
+// of either kind, whose matrix and vector work overlap; a wave of the first kind
+// issues the products of one tile under the softmax of the tile before.
+// One barrier per tile of 32 keys.
 // (256 sets of 2048 keys and 64 heads: 206 us with a wave that kept 32 heads to
 // itself for both products, reading and widening every key and value four times;
-// 160 us in this form with one wave per SIMD and two streams.)
+// 128 us with eight equal waves that went through first product, softmax and
+// second product in turn, which left the younger wave of a SIMD waiting.)
 // Tiles: the first 640 bytes of each row as 16-byte pieces straight into LDS (no
 // registers), the scales transposed to [block][key]. Piece c of key j lies at
 // c ^ swizzle(j), which keeps the 16 lanes that a 16-byte read serves at once
@@ -111,20 +109,21 @@ __device__ __forceinline__ void scale_in_place(f32x16& x, float f) {
 }
 
 constexpr int kWaves = 8;
-constexpr int kLoadsPerWave = (kTileLoads + kLatentGroups) / kWaves;   // vector loads a wave issues per tile
-static_assert(kLoadsPerWave == 3 && kTileLoads % kWaves == kLatentGroups, "see issue()");
+constexpr int kFirstWaves = 4;                    // waves 0..3: first product and softmax
+constexpr int kSecondWaves = kWaves - kFirstWaves;
+constexpr int kLoadsPerWave = (kTileLoads + kLatentGroups) / kSecondWaves;   // a second wave's vector loads per tile
+static_assert(kSecondWaves == kLatentGroups, "one scale block per second wave");
 
-template <int HEADS, int TILES, int KEYS>
+template <int HEADS, int TILES>
 struct LatentLds {
   alignas(1024) uint8_t ring[TILES][kTileBytes];
   // p x scale of two tiles: [block][head][key], key chunk c (8 keys) of head h at c ^ ((h >> 2) & 3)
   alignas(1024) _Float16 p[2][kLatentGroups][HEADS][kTileKeys];
   alignas(16) float scale[TILES][kLatentGroups][kTileKeys];
-  float top[2][2][HEADS];                   // largest logit (with its scale's exponent) of a tile's halves
   float alpha[2][HEADS];                    // factor of O before the tile's second product
-  uint32_t moved[2][HEADS / 16];            // whether any of 16 heads has a factor other than 1
-  const uint8_t* row[KEYS];                 // each key's row in this layer; zeros for padding
-  uint32_t live[KEYS / kTileKeys + 2];      // bit per key: not padding; none behind the last tile
+  alignas(16) uint32_t moved[2][4];         // whether any of 16 heads has a factor other than 1
+  const uint8_t* row[kAttendKeys];          // each key's row in this layer; zeros for padding
+  uint32_t live[kAttendKeys / kTileKeys + 2];   // bit per key: not padding; none behind the last tile
   int ok;
 };
 
@@ -142,14 +141,6 @@ struct QueryRaw {
 #pragma unroll
     for (int j = 0; j < kRope / 32; ++j)
       rope[j] = any ? load8<Q8, ALIGNED>(q + kLatent + 32 * j + 8 * quad) : Q8{};
-  }
-  // all values present before any asynchronous load is issued: the compiler's
-  // wait for them would wait for those too
-  __device__ __forceinline__ void settle() {
-#pragma unroll
-    for (int t = 0; t < kLatent / 32; ++t) asm volatile("" : "+v"(x[t]));
-#pragma unroll
-    for (int j = 0; j < kRope / 32; ++j) asm volatile("" : "+v"(rope[j]));
   }
 };
 
@@ -248,60 +239,59 @@ struct QueryOperand<f16x8> {
   }
 };
 
-// The workgroup's O (o[t][h] of wave w: channels 64 w + 32 t .., heads 32 h ..) as
-// type T, times inv, through the LDS at `box`; put(head, channel, 16 bytes) for
-// heads first + 0.. below `heads`.
+// The second waves' O (o[t][h] of wave w: channels 128 w + 32 t .., heads 32 h ..)
+// as type T, times inv, through the LDS at `box`; put(head, channel, 16 bytes) for
+// heads first + 0.. below `heads`. 32 channels of every wave at a time, so that
+// memory is written in whole segments (8 bytes per lane from the registers' order
+// took 18 us of a 256-set call). Rows are padded by 16 bytes for the banks.
 template <typename T, int CT, int HT, typename F>
 __device__ __forceinline__ void store_heads(uint8_t* box, const f32x16 (&o)[CT][HT], const float (&inv)[HT], int first,
                                             int heads, F put) {
-  constexpr int kSpan = 32 * kWaves;              // channels at a time
+  constexpr int kSpan = 32 * kSecondWaves;        // channels at a time
   constexpr int kRow = kSpan * sizeof(T) + 16;
   constexpr int kPer = 16 / sizeof(T);            // channels per 16 bytes
   constexpr int kLanes = kSpan / kPer;            // lanes per head
-  const int lane = lane_id(), wave = threadIdx.x / kWave, half = lane / 32, col32 = lane % 32;
+  const int lane = lane_id(), half = lane / 32, col32 = lane % 32;
+  const int wave = (int)(threadIdx.x / kWave) - kFirstWaves;
 #pragma unroll
   for (int t = 0; t < CT; ++t) {
     __syncthreads();
+    if (wave >= 0) {
 #pragma unroll
-    for (int h = 0; h < HT; ++h)
+      for (int h = 0; h < HT; ++h)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        typedef T vec __attribute__((ext_vector_type(4)));
-        vec v;
+        for (int i = 0; i < 4; ++i) {
+          typedef T vec __attribute__((ext_vector_type(4)));
+          vec v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = (T)(o[t][h][4 * i + e] * inv[h]);
-        *reinterpret_cast<vec*>(box + (32 * h + col32) * kRow + (32 * wave + 8 * i + 4 * half) * sizeof(T)) = v;
-      }
+          for (int e = 0; e < 4; ++e) v[e] = (T)(o[t][h][4 * i + e] * inv[h]);
+          *reinterpret_cast<vec*>(box + (32 * h + col32) * kRow + (32 * wave + 8 * i + 4 * half) * sizeof(T)) = v;
+        }
+    }
     __syncthreads();
     for (int e = threadIdx.x; e < 32 * HT * kLanes; e += kWaves * kWave) {
       const int h = e / kLanes, c = e % kLanes * kPer;
       if (first + h < heads)
-        put(first + h, c / 32 * (kLatent / kWaves) + 32 * t + c % 32,
+        put(first + h, c / 32 * (kLatent / kSecondWaves) + 32 * t + c % 32,
             *reinterpret_cast<const vec4u*>(box + h * kRow + c * sizeof(T)));
     }
   }
 }
 
-// HT tiles of 32 heads;
-// TILES tiles in the ring; at most KEYS keys.
-template <typename Q8, int HT, int TILES, int KEYS>
+// HT tiles of 32 heads; TILES tiles in the ring.
+template <typename Q8, int HT, int TILES>
 __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g, AttendDev a) {
   constexpr int kHeads = 32 * HT;                 // heads of a workgroup
-  constexpr int kGroups = kHeads / 16;            // of 16
-  constexpr int kCh = kLatent / kWaves;           // channels of O per wave
-  constexpr int CT = kCh / 32;                    // in tiles of 32
-  constexpr int kAhead = 2;                       // tiles that the first product runs ahead of the second
-  static_assert(kGroups * 2 <= kWaves, "every head and half has a wave in the first product");
-  static_assert(TILES >= kAhead + 2, "a tile on its way beside those in use");
-  __shared__ LatentLds<kHeads, TILES, KEYS> s;
+  constexpr int CT = kScaleGroup / 32;            // 32-channel tiles of a second wave's O
+  static_assert(kHeads <= 16 * kFirstWaves, "every head has a wave in the first product");
+  static_assert(TILES >= 4, "a tile on its way beside the three in use");
+  __shared__ LatentLds<kHeads, TILES> s;
   static_assert(sizeof(s) <= 160 * 1024, "LDS of a compute unit");
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);   // uniform: its branches are scalar
+  const bool second = wave >= kFirstWaves;
   const int quad = lane / 16, col = lane % 16;    // first product: 16 heads, quads of keys
   const int half = lane / 32, col32 = lane % 32;  // second product: 32 heads
-  const int hg = wave % kGroups;                  // this wave's heads in the first product
-  const int part0 = wave / kGroups;               // and its half of a tile's keys
-  const bool works = kGroups * 2 == kWaves || wave < kGroups * 2;   // whether it has any
 
   // work item: consecutive sets (which share rows under speculative selection)
   // run on one XCD at about the same time
@@ -321,8 +311,8 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
   // q on its way while the keys' rows are looked up
   QueryRaw<Q8> raw;
   {
-    const int head = hb * kHeads + hg * 16 + col;
-    const bool any = works && head < a.heads;
+    const int head = hb * kHeads + wave * 16 + col;
+    const bool any = wave * 16 < kHeads && head < a.heads;
     const uint16_t* p = static_cast<const uint16_t*>(a.q) + set * a.q_set_stride + head * a.q_head_stride;
     if (a.q_aligned) raw.template load<true>(p, any, quad);
     else raw.template load<false>(p, any, quad);
@@ -351,229 +341,99 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
     }
   }
   if (err) latch_gather(g.ctr, err);
-  raw.settle();
   __syncthreads();
   if (!s.ok) return;
   // Tiles behind the last one are computed on whatever lies in their place and
-  // masked, so that the main loop has no branches.
-  if (threadIdx.x < kAhead) s.live[tiles + threadIdx.x] = 0;
+  // masked, so that the main loop has no branches. (Read two barriers later.)
+  if (threadIdx.x < 2) s.live[tiles + threadIdx.x] = 0;
+  if (threadIdx.x < 8) s.moved[threadIdx.x / 4][threadIdx.x % 4] = 0;   // groups without a first wave never move
 
-  // This wave's three loads of a tile's 20 wave-wide ones of pieces and 4 of
-  // scales: two of pieces, and one more or a scale block's. The rows' addresses are
-  // read from LDS one tile earlier.
-  const bool scales = wave >= kWaves - kLatentGroups;
-  int row_at[kLoadsPerWave], source[kLoadsPerWave];   // LDS offset of the row's address, offset in the row
-#pragma unroll
-  for (int i = 0; i < kLoadsPerWave; ++i) {
-    const int p = (i * kWaves + wave) * kWave + lane, key = p / kTilePieces;
-    row_at[i] = 8 * key;
-    source[i] = (p % kTilePieces ^ swizzle(key)) * 16;
-  }
-  const int scale_block = wave - (kWaves - kLatentGroups);
-  if (scales) {
-    row_at[2] = 8 * (lane % kTileKeys);
-    source[2] = kLatentScaleAt + 4 * scale_block;
-  }
-  const uint8_t* row[kLoadsPerWave];
-  auto read_rows = [&](int tile) {
-    const uint32_t rows = lds_address(s.row) + min(tile, max(tiles - 1, 0)) * kTileKeys * 8;
-#pragma unroll
-    for (int i = 0; i < kLoadsPerWave; ++i) row[i] = lds_get<const uint8_t*>(rows + row_at[i]);
-  };
-  auto issue = [&](int tile) {
-    const int at = tile % TILES;
-    const uint32_t ring = lds_address(s.ring) + at * kTileBytes;
-    lds_load16(row[0] + source[0], ring + wave * kWave * 16);
-    lds_load16(row[1] + source[1], ring + (kWaves + wave) * kWave * 16);
-    if (!scales) lds_load16(row[2] + source[2], ring + (2 * kWaves + wave) * kWave * 16);
-    else if (lane < kTileKeys)
-      lds_load4(row[2] + source[2], lds_address(s.scale) + (at * kLatentGroups + scale_block) * kTileKeys * 4);
-  };
+  f32x16 o[CT][HT];                               // a second wave's alone: unset in the others, whose registers it would fill
+  float m = -__builtin_inff(), l = 0.0f;          // of a first wave's 16 heads; l of the lane's keys alone
 
-  // First product: register r of part u (0, 1) in quad x is key 8 x + 4 u + r.
-  // koff: this lane's key of the wave's part, piece quad of a scale block; piece
-  // 4 + quad is ^ 64. Second product: voff is the row (key) this lane names in a transposed
-  // read of keys 0..15, and the channels of its 16 lanes; 32-channel tile t is ^ (t << 5).
-  int koff, voff;
-  {
-    const int key = 8 * (col / 4) + 4 * part0 + col % 4;
-    koff = key * kLatentScaleAt + ((quad ^ swizzle(key)) << 4);
-    const int vkey = 8 * half + col / 2;
-    voff = (vkey * kLatentScaleAt + (((quad % 2) ^ swizzle(vkey)) << 4) + (col & 1) * 8 +
-            wave * kCh / kScaleGroup * kScaleGroup) ^ (wave * kCh % kScaleGroup);
-  }
-  static_assert(kLatentScaleAt % 128 == 0 && kTileBytes % 128 == 0, "the swizzle's bits are free in every row address");
-  const int block = wave * kCh / kScaleGroup;     // the scale block of this wave's channels
-  const int phead = hg * 16 + col;
-  const uint32_t pwrite = lds_address(s.p) + phead * kTileKeys * 2 + ((quad ^ ((phead >> 2) & 3)) << 4) + part0 * 8;
-  const uint32_t pread = lds_address(s.p) + (block * kHeads + col32) * kTileKeys * 2 + ((half ^ ((col32 >> 2) & 3)) << 4);
-
-  f32x16 o[CT][HT];
-#pragma unroll
-  for (int t = 0; t < CT; ++t)
-#pragma unroll
-    for (int h = 0; h < HT; ++h) o[t][h] = f32x16{};
-  float m = -__builtin_inff(), l = 0.0f;          // of this wave's 16 heads; l of this lane's keys alone
-
-#pragma unroll 1
-  for (int t = 0; t < TILES - 1 && t < tiles; ++t) {
-    read_rows(t);
-    issue(t);
-  }
-  QueryOperand<Q8> q;
-  q.take(raw);
-  const float c_log2 = a.scale_log2 / q.up;
-  f32x4 S{};                                      // logits (base 2) of the tile at hand
-
-  // S of a tile in LDS, and its largest value to s.top, in three steps: reads of
-  // the first two blocks' keys, the products, and the sums.
-  bf16x8 kr[2];
-  vec4u kb[kLatentGroups][2];
-  auto key_address = [&](int tile) { return opaque(lds_address(s.ring) + tile % TILES * kTileBytes + koff); };
-  auto read_block = [&](uint32_t krow, int b) {
-    kb[b][0] = lds_get<vec4u>(krow + b * kScaleGroup);
-    kb[b][1] = lds_get<vec4u>((krow ^ 64) + b * kScaleGroup);
-  };
-  auto read_keys = [&](int tile) {
-    const uint32_t krow = key_address(tile);
-    kr[0] = lds_get<bf16x8>(krow + kRopeAt);
-    kr[1] = lds_get<bf16x8>((krow ^ 64) + kRopeAt);
-    read_block(krow, 0);
-    read_block(krow, 1);
-  };
-  auto scale_address = [&](int tile) {
-    return opaque(lds_address(s.scale) + (tile % TILES * kLatentGroups * kTileKeys + 8 * quad + 4 * part0) * 4);
-  };
-  f32x4 part[kLatentGroups], next{};
-  auto first_product = [&](int tile) {
-    const uint32_t krow = key_address(tile);
-    read_block(krow, 2);
-    read_block(krow, 3);
-    __builtin_amdgcn_sched_barrier(0);
-    next = q.rope_product(kr);
-    q.block_products(0, kb[0], kb[1], part[0], part[1]);
-    q.block_products(2, kb[2], kb[3], part[2], part[3]);
-  };
-  auto finish_logits = [&](int tile) {
-    const uint32_t scale = scale_address(tile);
-    f32x4 sc[kLatentGroups];
-#pragma unroll
-    for (int b = 0; b < kLatentGroups; ++b) sc[b] = lds_get<f32x4>(scale + kTileKeys * b * 4);
-    const uint32_t live = __builtin_amdgcn_readfirstlane(s.live[tile]) >> (8 * quad + 4 * part0);
-    float big = 0x1p-60f;                         // largest scale of the lane's keys
-#pragma unroll
-    for (int b = 0; b < kLatentGroups; ++b) {
-      next += sc[b] * part[b];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) big = fmaxf(big, sc[b][r]);
-    }
-    float top = -__builtin_inff();
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      next[r] = live & (1u << r) ? next[r] * c_log2 : -__builtin_inff();
-      top = fmaxf(top, next[r]);
-    }
-    top = max_quads(top + (float)__builtin_amdgcn_frexp_expf(big));
-    if (quad == 0) s.top[tile & 1][part0][phead] = top;
-  };
-  // p of the tile whose S is at hand and whose s.top both halves have written,
-  // scaled, to LDS for the second product
-  f32x4 soft_scale[kLatentGroups];
-  float soft_top = 0.0f, soft_top1 = 0.0f;
-  auto read_softmax = [&](int tile) {
-    const uint32_t scale = scale_address(tile);
-    const uint32_t tops = opaque(lds_address(s.top) + ((tile & 1) * 2 * kHeads + phead) * 4);
-    soft_top = lds_get<float>(tops);
-    soft_top1 = lds_get<float>(tops + kHeads * 4);
-#pragma unroll
-    for (int b = 0; b < kLatentGroups; ++b) soft_scale[b] = lds_get<f32x4>(scale + kTileKeys * b * 4);
-  };
-  auto softmax = [&](int tile) {
-    const int buf = tile & 1;
-    const uint32_t pw = opaque(pwrite + buf * kLatentGroups * kHeads * kTileKeys * 2);
-    const float top = fmaxf(soft_top, soft_top1);
-    const bool move = top > m + 15.0f;
-    const float nm = move ? top - 8.0f : m;
-    const float al = move ? __builtin_amdgcn_exp2f(m - nm) : 1.0f;
-    m = nm;
-    l *= al;
-    const float base = nm == -__builtin_inff() ? 0.0f : nm;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      S[r] = __builtin_amdgcn_exp2f(S[r] - base);
-      l += S[r];
-    }
-#pragma unroll
-    for (int b = 0; b < kLatentGroups; ++b) {
-      f16x4 w;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) w[r] = (_Float16)(S[r] * soft_scale[b][r]);
-      lds_put(pw + b * kHeads * kTileKeys * 2, w);
-    }
-    const bool moved = __any(move);
-    if (part0 == 0) {
-      if (quad == 0) s.alpha[buf][phead] = al;
-      if (lane == 0) s.moved[buf][hg] = moved;
-    }
-  };
-
-  if (tiles > 0) {
-    if (tiles >= TILES - 1) wait_loads<(TILES - 1 - kAhead) * kLoadsPerWave>();
-    else wait_loads<0>();
-    barrier_keep_loads();
-    if (works) {
-      read_keys(0);
-      first_product(0);
-      finish_logits(0);
-      S = next;
-    }
-    barrier_keep_loads();
-    if (works) {
-      read_softmax(0);
-      softmax(0);
-      read_keys(1);
-      first_product(1);
-      finish_logits(1);
-      S = next;
-    }
-    read_rows(TILES - 1);
-  }
-#pragma unroll 1
-  for (int tile = 0; tile < tiles; ++tile) {
-    // Tile i + kAhead is in LDS once every wave's loads for it are; the barrier also
-    // makes p of tile i and s.top of tile i + 1 visible and ends the reads of tile
-    // i - 1, whose place the next loads take.
-    if (tile + TILES - 1 <= tiles) wait_loads<(TILES - 2 - kAhead) * kLoadsPerWave>();
-    else wait_loads<0>();
-    barrier_keep_loads();
-    const int buf = tile & 1;
-    const uint32_t vrow = opaque(lds_address(s.ring) + tile % TILES * kTileBytes + voff);
-    // chunk 2 x + half of this lane's head: ^ 32 for x
-    const uint32_t prow = opaque(pread + buf * kLatentGroups * kHeads * kTileKeys * 2);
-    uint32_t moved = 0;                           // a reference moved: O's factors
-#pragma unroll
-    for (int i = 0; i < kGroups; ++i) moved |= lds_get<uint32_t>(lds_address(s.moved) + (buf * kGroups + i) * 4);
-    i32x2 v8[CT][2];
-    f16x8 p[HT][2];
+  // Barriers: one when tile 0 is in LDS, then one per tile i = -1, 0, ..: tile
+  // i + 2 is in LDS, p of tile i is there, and nobody reads tile i - 1 any more.
+  if (second) {
+    // This wave's six loads of a tile: five of pieces, one of a scale block. The
+    // rows' addresses are read from LDS one tile earlier.
+    const int sw = wave - kFirstWaves;
 #pragma unroll
     for (int t = 0; t < CT; ++t)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) v8[t][x] = lds_read_transposed((vrow ^ (t << 5)) + x * 16 * kLatentScaleAt);
+      for (int h = 0; h < HT; ++h) o[t][h] = f32x16{};
+    constexpr int kPieceLoads = kLoadsPerWave - 1;
+    static_assert(kPieceLoads * kSecondWaves == kTileLoads, "pieces fill the waves' loads");
+    int row_at[kLoadsPerWave], source[kLoadsPerWave];   // LDS offset of the row's address, offset in the row
 #pragma unroll
-    for (int h = 0; h < HT; ++h)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) p[h][x] = lds_get<f16x8>((prow ^ (32 * x)) + 32 * h * kTileKeys * 2);
-    if (works) read_softmax(tile + 1);
-    if (tile + TILES - 1 < tiles) issue(tile + TILES - 1);
-    if (__builtin_amdgcn_readfirstlane(moved)) {
-#pragma unroll
-      for (int h = 0; h < HT; ++h) {
-        const float al = lds_get<float>(lds_address(s.alpha) + (buf * kHeads + 32 * h + opaque(col32)) * 4);
-#pragma unroll
-        for (int t = 0; t < CT; ++t) scale_in_place(o[t][h], al);
-      }
+    for (int i = 0; i < kPieceLoads; ++i) {
+      const int p = (i * kSecondWaves + sw) * kWave + lane, key = p / kTilePieces;
+      row_at[i] = 8 * key;
+      source[i] = (p % kTilePieces ^ swizzle(key)) * 16;
     }
-    auto second_product = [&] {
+    row_at[kPieceLoads] = 8 * (lane % kTileKeys);
+    source[kPieceLoads] = kLatentScaleAt + 4 * sw;
+    const uint8_t* row[kLoadsPerWave];
+    auto read_rows = [&](int tile) {
+      const uint32_t rows = lds_address(s.row) + min(tile, max(tiles - 1, 0)) * kTileKeys * 8;
+#pragma unroll
+      for (int i = 0; i < kLoadsPerWave; ++i) row[i] = lds_get<const uint8_t*>(rows + row_at[i]);
+    };
+    auto issue = [&](int tile) {
+      const int at = tile % TILES;
+      const uint32_t ring = lds_address(s.ring) + at * kTileBytes;
+#pragma unroll
+      for (int i = 0; i < kPieceLoads; ++i) lds_load16(row[i] + source[i], ring + (i * kSecondWaves + sw) * kWave * 16);
+      if (lane < kTileKeys)
+        lds_load4(row[kPieceLoads] + source[kPieceLoads], lds_address(s.scale) + (at * kLatentGroups + sw) * kTileKeys * 4);
+    };
+#pragma unroll 1
+    for (int t = 0; t < TILES - 1 && t < tiles; ++t) {
+      read_rows(t);
+      issue(t);
+    }
+    // voff: the row (key) this lane names in a transposed read of keys 0..15, and the
+    // channels of its 16 lanes; 32-channel tile t is ^ (t << 5).
+    const int vkey = 8 * half + col / 2;
+    const int voff = vkey * kLatentScaleAt + (((quad % 2) ^ swizzle(vkey)) << 4) + (col & 1) * 8 + sw * kScaleGroup;
+    static_assert(kLatentScaleAt % 128 == 0 && kTileBytes % 128 == 0, "the swizzle's bits are free in every row address");
+    const uint32_t pread = lds_address(s.p) + (sw * kHeads + col32) * kTileKeys * 2 + ((half ^ ((col32 >> 2) & 3)) << 4);
+    if (tiles >= TILES - 1) wait_loads<(TILES - 2) * kLoadsPerWave>();
+    else wait_loads<0>();
+    barrier_keep_loads();
+    read_rows(TILES - 1);
+#pragma unroll 1
+    for (int tile = -1; tile < tiles; ++tile) {
+      // tiles up to tile + TILES - 2 (at least TILES - 2) were issued; tile + 2 must have arrived
+      if (tile < 0 ? tiles >= TILES - 1 : tile + TILES - 1 <= tiles)
+        wait_loads<(TILES - 4) * kLoadsPerWave>();
+      else
+        wait_loads<0>();
+      barrier_keep_loads();
+      if (tile < 0) continue;
+      const int buf = tile & 1;
+      const uint32_t vrow = opaque(lds_address(s.ring) + tile % TILES * kTileBytes + voff);
+      // chunk 2 x + half of this lane's head: ^ 32 for x
+      const uint32_t prow = opaque(pread + buf * kLatentGroups * kHeads * kTileKeys * 2);
+      const vec4u mv = lds_get<vec4u>(lds_address(s.moved) + buf * 16);
+      i32x2 v8[CT][2];
+      f16x8 p[HT][2];
+#pragma unroll
+      for (int t = 0; t < CT; ++t)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) v8[t][x] = lds_read_transposed((vrow ^ (t << 5)) + x * 16 * kLatentScaleAt);
+#pragma unroll
+      for (int h = 0; h < HT; ++h)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) p[h][x] = lds_get<f16x8>((prow ^ (32 * x)) + 32 * h * kTileKeys * 2);
+      if (tile + TILES - 1 < tiles) issue(tile + TILES - 1);
+      if (__builtin_amdgcn_readfirstlane(mv.x | mv.y | mv.z | mv.w)) {   // a reference moved: O's factors
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+          const float al = lds_get<float>(lds_address(s.alpha) + (buf * kHeads + 32 * h + col32) * 4);
+#pragma unroll
+          for (int t = 0; t < CT; ++t) scale_in_place(o[t][h], al);
+        }
+      }
 #pragma unroll
       for (int t = 0; t < CT; ++t)
 #pragma unroll
@@ -582,37 +442,124 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
 #pragma unroll
           for (int h = 0; h < HT; ++h) o[t][h] = mfma32(v, p[h][x], o[t][h]);
         }
+      read_rows(tile + TILES);
+    }
+  } else if (wave * 16 < kHeads) {
+    QueryOperand<Q8> q;
+    q.take(raw);
+    const float c_log2 = a.scale_log2 / q.up;
+    // Register r of part u (0, 1) in quad x is key 8 x + 4 u + r. koff: this lane's
+    // key of part 0, piece quad of a scale block. Piece 4 + quad is ^ 64; part 1's
+    // key, four rows on, is ^ 64 (its swizzle) and + 4 rows.
+    const int key = 8 * (col / 4) + col % 4;
+    const int koff = key * kLatentScaleAt + ((quad ^ swizzle(key)) << 4);
+    const int head = wave * 16 + col;
+    const uint32_t pwrite = lds_address(s.p) + head * kTileKeys * 2 + ((quad ^ ((head >> 2) & 3)) << 4);
+    f32x4 part[2][kLatentGroups], rope[2];        // of the tile after the one in the softmax
+    // first product of a tile in LDS, two blocks' keys at a time
+    auto products = [&](int tile) {
+      const uint32_t krow = opaque(lds_address(s.ring) + tile % TILES * kTileBytes + koff);
+      const uint32_t krow64 = opaque(krow ^ 64);
+      auto kpiece = [&](int u, int t) { return (t != u ? krow64 : krow) + u * 4 * kLatentScaleAt; };
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        bf16x8 kr[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) kr[j] = lds_get<bf16x8>(kpiece(u, j) + kRopeAt);
+        rope[u] = q.rope_product(kr);
+      }
+#pragma unroll
+      for (int b = 0; b < kLatentGroups; b += 2)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          vec4u k[2][2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) k[i][t] = lds_get<vec4u>(kpiece(u, t) + (b + i) * kScaleGroup);
+          q.block_products(b, k[0], k[1], part[u][b], part[u][b + 1]);
+        }
     };
-    __builtin_amdgcn_sched_barrier(0);
-    if (works) read_keys(tile + kAhead);
-    second_product();
-    if (works) {
-      softmax(tile + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      first_product(tile + kAhead);
+    barrier_keep_loads();
+    products(0);
+#pragma unroll 1
+    for (int tile = 0; tile <= tiles; ++tile) {   // softmax of `tile`, products of the next one
+      barrier_keep_loads();
+      const int buf = tile & 1;
+      const uint32_t scale = opaque(lds_address(s.scale) + (tile % TILES * kLatentGroups * kTileKeys + 8 * quad) * 4);
+      f32x4 sc[2][kLatentGroups], S[2];
+#pragma unroll
+      for (int b = 0; b < kLatentGroups; ++b)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) sc[u][b] = lds_get<f32x4>(scale + (kTileKeys * b + 4 * u) * 4);
+      const uint32_t live = __builtin_amdgcn_readfirstlane(s.live[tile]) >> (8 * quad);
+      float big = 0x1p-60f;                       // largest scale of the lane's keys
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        S[u] = rope[u];
+#pragma unroll
+        for (int b = 0; b < kLatentGroups; ++b) {
+          S[u] += sc[u][b] * part[u][b];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) big = fmaxf(big, sc[u][b][r]);
+        }
+      }
+      products(tile + 1);
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          S[u][r] = live & (1u << (4 * u + r)) ? S[u][r] * c_log2 : -__builtin_inff();
+          top = fmaxf(top, S[u][r]);
+        }
+      top = max_quads(top + (float)__builtin_amdgcn_frexp_expf(big));
+      const bool move = top > m + 15.0f;
+      const float nm = move ? top - 8.0f : m;
+      const float al = move ? __builtin_amdgcn_exp2f(m - nm) : 1.0f;
+      m = nm;
+      l *= al;
+      const float base = nm == -__builtin_inff() ? 0.0f : nm;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          S[u][r] = __builtin_amdgcn_exp2f(S[u][r] - base);
+          l += S[u][r];
+        }
+      const uint32_t pw = opaque(pwrite + buf * kLatentGroups * kHeads * kTileKeys * 2);
+#pragma unroll
+      for (int b = 0; b < kLatentGroups; ++b) {
+        f16x8 w;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) w[4 * u + r] = (_Float16)(S[u][r] * sc[u][b][r]);
+        lds_put(pw + b * kHeads * kTileKeys * 2, w);
+      }
+      const bool moved = __any(move);
+      if (quad == 0) s.alpha[buf][head] = al;
+      if (lane == 0) s.moved[buf][wave] = moved;
     }
-    read_rows(tile + TILES);
-    if (works) {
-      __builtin_amdgcn_sched_barrier(0);
-      finish_logits(tile + kAhead);
-      S = next;
-    }
+    l = sum_quads(l);
+  } else {
+    barrier_keep_loads();
+#pragma unroll 1
+    for (int tile = 0; tile <= tiles; ++tile) barrier_keep_loads();
   }
-  l = sum_quads(l);
 
-  // every wave needs every head's l and m
-  float* ml = reinterpret_cast<float*>(s.p);      // m, then l of each part
+  // every second wave needs every head's l and m
+  float* ml = reinterpret_cast<float*>(s.p);
   __syncthreads();
-  if (quad == 0 && works) {
-    if (part0 == 0) ml[phead] = m;
-    ml[(1 + part0) * kHeads + phead] = l;
+  if (!second && wave * 16 < kHeads && quad == 0) {
+    ml[wave * 16 + col] = m;
+    ml[kHeads + wave * 16 + col] = l;
   }
   __syncthreads();
   float inv[HT];
 #pragma unroll
   for (int h = 0; h < HT; ++h) {
-    float lh = ml[kHeads + 32 * h + col32];
-    lh += ml[2 * kHeads + 32 * h + col32];
+    const float lh = ml[kHeads + 32 * h + col32];
     inv[h] = lh != 0.0f ? 1.0f / lh : 0.0f;
     const int head = hb * kHeads + 32 * h + col32;
     if (wave == 0 && half == 0 && head < a.heads) {
@@ -621,9 +568,6 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
       else if (a.lse) a.lse[(size_t)set * a.heads + head] = lse2 * kLn2;
     }
   }
-  // O through LDS, 32 channels of every wave at a time, so that memory is written
-  // in whole segments (8 bytes per lane from the registers' order took 18 us of a
-  // 256-set call). Rows are padded by 16 bytes for the banks.
   if (a.splits > 1) {   // this split's own result in 32 bits, joined by k_attend_join
     float* po = a.part_o + ((size_t)set * a.heads * a.splits + split) * kLatent;
     store_heads<float>(s.ring[0], o, inv, hb * kHeads, a.heads, [&](int head, int ch, const vec4u v) {
@@ -713,15 +657,15 @@ AttendPlan plan_attend_latent(int n_sets, int k, int heads) {
   return best;
 }
 
-template <typename Q8, int HT, int TILES, int KEYS>
+template <typename Q8, int HT, int TILES>
 static void launch_latent(const GroupDev& g, const AttendDev& a, int n_sets, hipStream_t s) {
-  k_attend_latent<Q8, HT, TILES, KEYS><<<n_sets * a.head_blocks * a.splits, kWaves * kWave, 0, s>>>(g, a);
+  k_attend_latent<Q8, HT, TILES><<<n_sets * a.head_blocks * a.splits, kWaves * kWave, 0, s>>>(g, a);
 }
 
 template <typename Q8>
 static hipError_t launch_latent_of(const GroupDev& g, const AttendDev& a, int n_sets, hipStream_t s) {
-  if (a.heads <= 32) launch_latent<Q8, 1, 5, kAttendKeys>(g, a, n_sets, s);
-  else launch_latent<Q8, 2, 5, kAttendKeys>(g, a, n_sets, s);
+  if (a.heads <= 32) launch_latent<Q8, 1, 5>(g, a, n_sets, s);
+  else launch_latent<Q8, 2, 5>(g, a, n_sets, s);
   return hipGetLastError();
 }
 
