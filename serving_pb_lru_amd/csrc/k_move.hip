@@ -203,49 +203,118 @@ __global__ __launch_bounds__(256) void k_writeback(GroupDev g, FastDiv per_slot)
   if (t != 0) writeback_rows(g, t, n, t, per_slot, blockIdx.x, gridDim.x);
 }
 
+// Calls f(bits, lanes) once for each distinct key among the wavefront's lanes with
+// `on` set, in the first of them: how many lanes have the key and (with BITS)
+// their bits together. The first kLeaders keys are found one after another; a lane whose key is
+// not among them calls for itself, which bounds the work of a wavefront of
+// scattered entries. Every lane of the wavefront must call it.
+template <bool BITS, typename F>
+__device__ __forceinline__ void each_key(bool on, uint32_t key, uint32_t bits, F&& f) {
+  constexpr int kLeaders = 4;
+  unsigned long long left = __ballot(on);
+#pragma unroll 1
+  for (int i = 0; i < kLeaders && left; ++i) {
+    const int lead = __builtin_ctzll(left);
+    const uint32_t k = (uint32_t)__builtin_amdgcn_readlane((int)key, lead);
+    const bool mine = on && key == k;
+    uint32_t all = mine ? bits : 0u;
+    if constexpr (BITS) {
+#pragma unroll
+      for (int d = kWave / 2; d >= 1; d >>= 1) all |= (uint32_t)__shfl_xor((int)all, d, kWave);
+    }
+    const unsigned long long same = __ballot(mine);
+    if (lane_id() == lead) f(all, __popcll(same));
+    left &= ~same;
+  }
+  if (left >> lane_id() & 1ull) f(bits, 1);
+}
+
 // Release of finished entries (app_la[0..n), validated on the host): a GPU slot
 // leaves whichever bucket holds it and joins the free set, a host slot joins the
 // free host set (its staging record cleared, so no later miss reads a staged
 // copy of the released row); the address becomes absent. Bucket words and span
 // counts are shared between threads, hence atomics. Any staged write-back has
 // been written out before this kernel runs.
+//
+// A request's entries mostly lie in neighbouring slots, so its lanes meet in the
+// same words and span counts, and atomics on one address run one after another:
+// a wavefront adds its lanes' shares up first, and a workgroup the totals.
+// (65536 entries released in order: 882 us with an atomic for each entry and
+// count, 10 us so.)
 __global__ __launch_bounds__(256) void k_release(GroupDev g, int32_t n) {
-  if (status_of(g.ctr)) return;
-  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) {
-    const int32_t la = g.app_la[i];
-    const uint32_t loc = g.map[la];
-    if (loc == kAbsent) {          // the host checked this: an inconsistent state
-      latch(g.ctr, ULA_ESTATE);
-      continue;
+  __shared__ int s_bucket[kMaxBuckets];
+  __shared__ int s_free, s_host, s_free_lo, s_host_lo;
+  for (int i = threadIdx.x; i < g.NB; i += blockDim.x) s_bucket[i] = 0;
+  if (threadIdx.x == 0) {
+    s_free = s_host = 0;
+    s_free_lo = s_host_lo = 0x7FFFFFFF;
+  }
+  if (block_failed(g.ctr)) return;
+  __syncthreads();
+  for (int base = blockIdx.x * blockDim.x; base < n; base += gridDim.x * blockDim.x) {
+    const int i = base + (int)threadIdx.x;
+    uint32_t loc = kAbsent;
+    if (i < n) {
+      const int32_t la = g.app_la[i];
+      loc = g.map[la];
+      if (loc == kAbsent) latch(g.ctr, ULA_ESTATE);   // the host checked this: an inconsistent state
+      else g.map[la] = kAbsent;
     }
-    g.map[la] = kAbsent;
-    if (loc & kHostBit) {
-      const uint32_t h = loc & ~kHostBit;
-      g.hown[h] = -1;
-      g.hs_stage[h] = ~0ull;
-      atomicOr(&g.hbm[h >> 5], 1u << (h & 31));
-      atomicAdd(&g.htcnt[h >> kTileShift], 1u);
-      atomicAdd(&g.ctr->hfree, 1);
-      atomicMin(&g.ctr->hfree_lo, (int32_t)(h >> kTileShift));
-      continue;
+    const bool there = loc != kAbsent;
+    const bool host = there && (loc & kHostBit), gpu = there && !host;
+    const uint32_t s = loc & ~kHostBit;
+    const uint32_t w = s >> 5, bit = 1u << (s & 31), tile = s >> kTileShift;
+    if (host) {
+      g.hown[s] = -1;
+      g.hs_stage[s] = ~0ull;
     }
-    const uint32_t s = loc;
-    const uint32_t bit = 1u << (s & 31);
-    const int w = (int)(s >> 5), tile = (int)(s >> kTileShift);
-    for (int id = kCold; id < g.NB; ++id) {     // the bucket holding the slot, if any
-      if (g.bm[(size_t)id * g.W + w] & bit) {
-        atomicAnd(&g.bm[(size_t)id * g.W + w], ~bit);
-        atomicSub(&g.tcnt[(size_t)id * g.T + tile], 1u);
-        atomicSub(&g.ctr->bcnt[id], 1);
-        break;
+    if (__any(host)) {
+      each_key<true>(host, w, bit, [&](uint32_t bits, int) { atomicOr(&g.hbm[w], bits); });
+      each_key<false>(host, tile, 0u, [&](uint32_t, int c) {
+        atomicAdd(&g.htcnt[tile], (uint32_t)c);
+        atomicAdd(&s_host, c);
+        atomicMin(&s_host_lo, (int)tile);
+      });
+    }
+    if (!__any(gpu)) continue;
+    int id = g.NB;                              // the bucket holding the slot, if any
+    if (gpu) {
+      constexpr int kAtOnce = 4;                // loads in flight: a bucket's word does not depend on another's
+      for (int id0 = kCold; id0 < g.NB && id == g.NB; id0 += kAtOnce) {
+        uint32_t word[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) word[j] = g.bm[(size_t)min(id0 + j, g.NB - 1) * g.W + w];
+#pragma unroll
+        for (int j = kAtOnce - 1; j >= 0; --j)
+          if (id0 + j < g.NB && (word[j] & bit)) id = id0 + j;
       }
+      g.gown[s] = -1;
+      if (g.lru_ts) g.lru_ts[s] = 0;   // exact LRU: a slot appended later counts as never stamped
     }
-    atomicOr(&g.bm[(size_t)kFree * g.W + w], bit);
-    atomicAdd(&g.tcnt[(size_t)kFree * g.T + tile], 1u);
-    atomicAdd(&g.ctr->bcnt[kFree], 1);
-    atomicMin(&g.ctr->free_lo, tile);
-    g.gown[s] = -1;
-    if (g.lru_ts) g.lru_ts[s] = 0;   // exact LRU: a slot appended later counts as never stamped
+    const bool held = gpu && id < g.NB;
+    each_key<true>(held, (uint32_t)id * (uint32_t)g.W + w, bit,
+             [&](uint32_t bits, int) { atomicAnd(&g.bm[(size_t)id * g.W + w], ~bits); });
+    each_key<false>(held, (uint32_t)id * (uint32_t)g.T + tile, 0u, [&](uint32_t, int c) {
+      atomicSub(&g.tcnt[(size_t)id * g.T + tile], (uint32_t)c);
+      atomicAdd(&s_bucket[id], c);
+    });
+    each_key<true>(gpu, w, bit, [&](uint32_t bits, int) { atomicOr(&g.bm[(size_t)kFree * g.W + w], bits); });
+    each_key<false>(gpu, tile, 0u, [&](uint32_t, int c) {
+      atomicAdd(&g.tcnt[(size_t)kFree * g.T + tile], (uint32_t)c);
+      atomicAdd(&s_free, c);
+      atomicMin(&s_free_lo, (int)tile);
+    });
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < g.NB; i += blockDim.x)
+    if (s_bucket[i]) atomicSub(&g.ctr->bcnt[i], s_bucket[i]);
+  if (threadIdx.x == 0 && s_free) {
+    atomicAdd(&g.ctr->bcnt[kFree], s_free);
+    atomicMin(&g.ctr->free_lo, s_free_lo);
+  }
+  if (threadIdx.x == 0 && s_host) {
+    atomicAdd(&g.ctr->hfree, s_host);
+    atomicMin(&g.ctr->hfree_lo, s_host_lo);
   }
 }
 

@@ -389,6 +389,38 @@ static void mark_range(GroupHost& gh, int32_t first, int32_t n, bool on) {
   });
 }
 
+// A batch of addresses as runs of consecutive ones, in the batch's order: requests
+// own ranges, so the host's work for a batch is mostly that of a few runs.
+struct Run {
+  int32_t first, n;
+};
+static std::vector<Run> runs_of(const int32_t* la, int32_t n) {
+  std::vector<Run> r;
+  for (int32_t i = 0; i < n;) {
+    int32_t e = i + 1;
+    while (e < n && la[e] == (int64_t)la[e - 1] + 1) ++e;
+    r.push_back({la[i], e - i});
+    i = e;
+  }
+  return r;
+}
+
+// Whether two of the runs overlap: an address is in the batch twice.
+static bool overlapping(std::vector<Run> r) {
+  auto before = [](const Run& a, const Run& b) { return a.first < b.first; };
+  if (!std::is_sorted(r.begin(), r.end(), before)) std::sort(r.begin(), r.end(), before);
+  for (size_t i = 1; i < r.size(); ++i)
+    if (r[i].first < r[i - 1].first + r[i - 1].n) return true;
+  return false;
+}
+
+// The checks that appends and releases share: every address in range, none twice.
+static int validate_batch(const std::vector<Run>& runs, int64_t N) {
+  for (const Run& r : runs)
+    if (r.first < 0 || (int64_t)r.first + r.n > N) return ULA_ERANGE;
+  return overlapping(runs) ? ULA_EDUP : ULA_OK;
+}
+
 extern "C" {
 
 size_t ula_device_bytes(const ula_config* cfg) {
@@ -613,26 +645,16 @@ int ula_destroy(ula_ctx* ctx) {
 // Host validation of an append batch (nothing changes on error).
 static int validate_append(const ula_ctx* ctx, const GroupHost& gh, int32_t n, const int32_t* la_host) {
   const Dims& d = ctx->dims;
-  for (int32_t i = 0; i < n; ++i)
-    if (la_host[i] < 0 || la_host[i] >= d.N) return ULA_ERANGE;
-  {
-    std::vector<int32_t> sorted(la_host, la_host + n);
-    std::sort(sorted.begin(), sorted.end());
-    if (std::adjacent_find(sorted.begin(), sorted.end()) != sorted.end()) return ULA_EDUP;
-  }
-  for (int32_t i = 0; i < n; ++i) {
-    const uint32_t la = (uint32_t)la_host[i];
-    if (gh.appended[la >> 6] >> (la & 63) & 1ull) return ULA_EDUP;
-  }
+  const std::vector<Run> runs = runs_of(la_host, n);
+  if (const int rc = validate_batch(runs, d.N)) return rc;
+  for (const Run& r : runs)
+    if (!none_appended(gh, r.first, r.n)) return ULA_EDUP;
   if (gh.n_appended + n > d.P + d.H) return ULA_EHOSTFULL;
   return ULA_OK;
 }
 
 static void note_appended(GroupHost& gh, int32_t n, const int32_t* la_host) {
-  for (int32_t i = 0; i < n; ++i) {
-    const uint32_t la = (uint32_t)la_host[i];
-    gh.appended[la >> 6] |= 1ull << (la & 63);
-  }
+  for (const Run& r : runs_of(la_host, n)) mark_range(gh, r.first, r.n, true);
   gh.n_appended += n;
 }
 
@@ -741,17 +763,10 @@ int ula_release(ula_ctx* ctx, int32_t group, int32_t n, const int32_t* la_host, 
   GroupHost& gh = ctx->groups[group];
   const Dims& d = ctx->dims;
   // validate the whole batch first; nothing changes on error
-  for (int32_t i = 0; i < n; ++i)
-    if (la_host[i] < 0 || la_host[i] >= d.N) return ULA_ERANGE;
-  {
-    std::vector<int32_t> sorted(la_host, la_host + n);
-    std::sort(sorted.begin(), sorted.end());
-    if (std::adjacent_find(sorted.begin(), sorted.end()) != sorted.end()) return ULA_EDUP;
-  }
-  for (int32_t i = 0; i < n; ++i) {
-    const uint32_t la = (uint32_t)la_host[i];
-    if (!(gh.appended[la >> 6] >> (la & 63) & 1ull)) return ULA_ERANGE;
-  }
+  const std::vector<Run> runs = runs_of(la_host, n);
+  if (const int rc = validate_batch(runs, d.N)) return rc;
+  for (const Run& r : runs)
+    if (!all_appended(gh, r.first, r.n)) return ULA_ERANGE;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const GroupDev& g = gh.d;
   {   // a released GPU slot may be taken by the next append: pending gathers first
@@ -781,10 +796,7 @@ int ula_release(ula_ctx* ctx, int32_t group, int32_t n, const int32_t* la_host, 
     }
     HIP_TRY(launch_release(g, cnt, s));
   }
-  for (int32_t i = 0; i < n; ++i) {
-    const uint32_t la = (uint32_t)la_host[i];
-    gh.appended[la >> 6] &= ~(1ull << (la & 63));
-  }
+  for (const Run& r : runs) mark_range(gh, r.first, r.n, false);
   gh.n_appended -= n;
   gh.last_n = 0;   // the last step's resolved selection may name released entries
   return ULA_OK;
