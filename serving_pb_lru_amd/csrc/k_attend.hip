@@ -501,7 +501,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
         for (int b = 0; b < kLatentGroups; ++b) {
           S[u] += sc[u][b] * part[u][b];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) big = fmaxf(big, sc[u][b][r]);
+          for (int r = 0; r < 4; ++r) big = fmaxf(big, fabsf(sc[u][b][r]));
         }
       }
       products(tile + 1);

@@ -6,8 +6,11 @@
 // head, c = scale log2(e):
 //   S_j = c ks_j (q . k8_j),  p_j = 2^(S_j - m),  o = sum_j p_j vs_j v8_j / l
 // e4m3 values are exact in bf16 and fp16, so both products run on 16-bit matrix
-// instructions and the scales are applied in 32 bits, to S and to p (then
-// rounded to bf16, at most 2^-8 of its value).
+// instructions and the scales are applied in 32 bits, to S and to p. p vs is then
+// rounded to fp16 (at most 2^-11 of its value). m follows the largest p vs, not
+// the largest p, so that fp16's range serves whatever the scales are: the
+// largest p vs lies between 2^7 and 2^15, and one below fp16's least value (its
+// rounding: 2^-25) is off by less than 2^-32 of it.
 //
 // Bound by HBM: 2 x heads / kv_heads operations per byte. So a wave works by
 // itself, on one KV head's up to 16 query heads and one range of tokens, with
@@ -161,8 +164,8 @@ __global__ __launch_bounds__(kHeadWaves * kWave) void k_attend_heads(GroupDev g,
       load(tile + 1, cur);
     }
     if (now == 0) continue;
-    f32x4 S[2] = {};
-    float top = -__builtin_inff();
+    f32x4 S[2] = {}, sv[2];
+    float top = -__builtin_inff();               // of log2(p vs), to 1 upwards; vs below 2^-60 counts as that
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
@@ -171,39 +174,40 @@ __global__ __launch_bounds__(kHeadWaves * kWave) void k_attend_heads(GroupDev g,
         S[u] = mfma16(widen8<Q8>(k8[u][j].z, k8[u][j].w), q[2 * j + 1], S[u]);
       }
       const f32x4 sc = lds_get<f32x4>(lds_address(s.ks) + (8 * quad + 4 * u) * 4);
+      sv[u] = lds_get<f32x4>(lds_address(s.vs) + (8 * quad + 4 * u) * 4);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         S[u][r] *= sc[r] * a.scale_log2;
         if (!(now >> (8 * quad + 4 * u + r) & 1u)) S[u][r] = -__builtin_inff();
-        top = fmaxf(top, S[u][r]);
+        top = fmaxf(top, S[u][r] + (float)__builtin_amdgcn_frexp_expf(fmaxf(fabsf(sv[u][r]), 0x1p-60f)));
       }
     }
+    // p vs in fp16: the reference m moves when p vs could pass 2^15, and then so that
+    // the largest is between 2^7 and 2^8
     top = max_quads(top);
-    // the maximum moves only when it rises by more than 2^8 (p stays below that)
-    if (__any(top > m + 8.0f)) {
-      const float nm = fmaxf(m, top);
-      const float al = nm == -__builtin_inff() ? 1.0f : exp2f(m - nm);
+    if (__any(top > m + 15.0f)) {
+      const bool move = top > m + 15.0f;
+      const float nm = move ? top - 8.0f : m;
+      const float al = move ? __builtin_amdgcn_exp2f(m - nm) : 1.0f;
       m = nm;
       l *= al;
 #pragma unroll
       for (int t = 0; t < D / 16; ++t) o[t] *= al;
     }
     const float base = m == -__builtin_inff() ? 0.0f : m;
-    bf16x8 p;
+    f16x8 p;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const f32x4 sc = lds_get<f32x4>(lds_address(s.vs) + (8 * quad + 4 * u) * 4);
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float w = __builtin_amdgcn_exp2f(S[u][r] - base);
         l += w;
-        p[4 * u + r] = (__bf16)(w * sc[r]);
+        p[4 * u + r] = (_Float16)(w * sv[u][r]);
       }
-    }
 #pragma unroll
     for (int t = 0; t < D / 16; ++t) {
       const i32x2 v8 = lds_read_transposed(vrow ^ (t << 4));
-      o[t] = mfma16(widen8<bf16x8>((uint32_t)v8.x, (uint32_t)v8.y), p, o[t]);
+      o[t] = mfma16(widen8<f16x8>((uint32_t)v8.x, (uint32_t)v8.y), p, o[t]);
     }
   }
   if (err) latch_gather(g.ctr, err);
