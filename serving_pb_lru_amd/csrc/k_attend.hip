@@ -154,15 +154,38 @@ struct QueryOperand<bf16x8> {
   bf16x8 rope[kRope / 32];
   float up;                                     // the power of two in hi and lo
   __device__ __forceinline__ void take(const QueryRaw<bf16x8>& raw) {
-    const bf16x8* x = raw.x;
-    float top = 0.0f;
+    vec4u x[kLatent / 32];
+#pragma unroll
+    for (int t = 0; t < kLatent / 32; ++t) x[t] = __builtin_bit_cast(vec4u, raw.x[t]);
+    // The largest |q|, two values at a time: bf16 magnitudes are in the order of their bits.
+    u16x2 top2{};
 #pragma unroll
     for (int t = 0; t < kLatent / 32; ++t)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, finite_abs((float)x[t][e]));
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t mag = x[t][w] & 0x7FFF7FFFu;
+        top2 = __builtin_elementwise_max(top2, __builtin_bit_cast(u16x2, mag));
+      }
+    uint32_t most = max((uint32_t)top2.x, (uint32_t)top2.y);
+    constexpr uint32_t kInf = 0x7F80u;
+    if (__any(most >= kInf)) {   // infinities, which are not e4m3 values, become NaN; the finite values set the scale
+      most = 0u;
+#pragma unroll
+      for (int t = 0; t < kLatent / 32; ++t)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t v = x[t][w];
+          const uint32_t first = v & 0x7FFFu, second = v >> 16 & 0x7FFFu;
+          if (first >= kInf) v |= 0x7FFFu;
+          else most = max(most, first);
+          if (second >= kInf) v |= 0x7FFF0000u;
+          else most = max(most, second);
+          x[t][w] = v;
+        }
+    }
 #pragma unroll
     for (int j = 0; j < kRope / 32; ++j) rope[j] = raw.rope[j];
-    top = max_quads(top);
+    const float top = max_quads(__uint_as_float(most << 16));
     // 2^s with top x 2^s in [128, 256); s within +-60, far beyond which q has no effect or overflows
     const int s = top > 0.0f ? min(max(8 - __builtin_amdgcn_frexp_expf(top), -60), 60) : 0;
     up = ldexpf(1.0f, s);
@@ -172,9 +195,10 @@ struct QueryOperand<bf16x8> {
       for (int w = 0; w < 8; ++w) {               // four values a word
         float v[4], r[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float y = (float)x[4 * b + w / 2][4 * (w % 2) + e];
-          v[e] = fabsf(y) < __builtin_inff() ? y * up : __builtin_nanf("");   // an infinity is not an e4m3 value
+        for (int e = 0; e < 4; e += 2) {
+          const uint32_t y = x[4 * b + w / 2][2 * (w % 2) + e / 2];
+          v[e] = __uint_as_float(y << 16) * up;
+          v[e + 1] = __uint_as_float(y & 0xFFFF0000u) * up;
         }
         const uint32_t h = e4m3x4(v[0], v[1], v[2], v[3]);
         const auto h0 = __builtin_amdgcn_cvt_pk_f32_fp8(h, false), h1 = __builtin_amdgcn_cvt_pk_f32_fp8(h, true);
@@ -243,7 +267,8 @@ struct QueryOperand<f16x8> {
 // as type T, times inv, through the LDS at `box`; put(head, channel, 16 bytes) for
 // heads first + 0.. below `heads`. 32 channels of every wave at a time, so that
 // memory is written in whole segments (8 bytes per lane from the registers' order
-// took 18 us of a 256-set call). Rows are padded by 16 bytes for the banks.
+// took 18 us of a 256-set call), and the stores of one step are on their way
+// during the next. Rows are padded by 16 bytes for the banks.
 template <typename T, int CT, int HT, typename F>
 __device__ __forceinline__ void store_heads(uint8_t* box, const f32x16 (&o)[CT][HT], const float (&inv)[HT], int first,
                                             int heads, F put) {
@@ -255,7 +280,7 @@ __device__ __forceinline__ void store_heads(uint8_t* box, const f32x16 (&o)[CT][
   const int wave = (int)(threadIdx.x / kWave) - kFirstWaves;
 #pragma unroll
   for (int t = 0; t < CT; ++t) {
-    __syncthreads();
+    barrier_keep_loads();
     if (wave >= 0) {
 #pragma unroll
       for (int h = 0; h < HT; ++h)
@@ -268,7 +293,7 @@ __device__ __forceinline__ void store_heads(uint8_t* box, const f32x16 (&o)[CT][
           *reinterpret_cast<vec*>(box + (32 * h + col32) * kRow + (32 * wave + 8 * i + 4 * half) * sizeof(T)) = v;
         }
     }
-    __syncthreads();
+    barrier_keep_loads();
     for (int e = threadIdx.x; e < 32 * HT * kLanes; e += kWaves * kWave) {
       const int h = e / kLanes, c = e % kLanes * kPer;
       if (first + h < heads)
@@ -308,40 +333,43 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
   const int nkeys = max(0, min(a.split_keys, a.k - key0));
   const int tiles = (nkeys + kTileKeys - 1) / kTileKeys;
 
-  // q on its way while the keys' rows are looked up
+  // The second waves look the keys' rows up and start their loads; the first waves'
+  // q, which takes longer to arrive and to convert, is on its way meanwhile.
   QueryRaw<Q8> raw;
-  {
+  if (!second) {
+    const ReaderState state = reader_state(g);
     const int head = hb * kHeads + wave * 16 + col;
     const bool any = wave * 16 < kHeads && head < a.heads;
     const uint16_t* p = static_cast<const uint16_t*>(a.q) + set * a.q_set_stride + head * a.q_head_stride;
     if (a.q_aligned) raw.template load<true>(p, any, quad);
     else raw.template load<false>(p, any, quad);
-  }
-  int err = 0;
-  if (threadIdx.x == 0) s.ok = reader_ready(g, a.want_flag);
-  {
+    if (threadIdx.x == 0) s.ok = reader_ready(g, state, a.want_flag);
+  } else {
+    int err = 0;
     const uint8_t* pool = g.pool + (size_t)a.layer * g.row_bytes;
     constexpr int kAtOnce = 4;                    // lookups in flight per lane
     const int n = tiles * kTileKeys;
-    for (int i0 = wave * kWave; i0 < n; i0 += kAtOnce * kWaves * kWave) {
-      uint32_t slot[kAtOnce];
+    for (int i0 = (wave - kFirstWaves) * kWave; i0 < n; i0 += kAtOnce * kSecondWaves * kWave) {
+      Lookup at[kAtOnce];
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) {
-        const int i = i0 + j * kWaves * kWave + lane;
-        slot[j] = i < nkeys ? resolve_slot(g, a.sel, set * a.k + key0 + i, a.n_res, err) : kAbsent;
+        const int i = i0 + j * kSecondWaves * kWave + lane;
+        at[j].la = -1;
+        if (i < nkeys) at[j] = look_up(g, a.sel, set * a.k + key0 + i, a.n_res);
       }
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) {
-        const int first = i0 + j * kWaves * kWave;   // uniform: whole waves take part in the ballot
+        const int first = i0 + j * kSecondWaves * kWave;   // uniform: whole waves take part in the ballot
         if (first >= n) break;
-        s.row[first + lane] = slot[j] != kAbsent ? pool + (size_t)slot[j] * g.slot_bytes : g_zero_row;
-        const unsigned long long live = __ballot(slot[j] != kAbsent);
+        const uint32_t slot = slot_of(g, at[j], a.n_res, err);
+        s.row[first + lane] = slot != kAbsent ? pool + (size_t)slot * g.slot_bytes : g_zero_row;
+        const unsigned long long live = __ballot(slot != kAbsent);
         if (lane < 2) s.live[first / 32 + lane] = (uint32_t)(live >> (32 * lane));
       }
     }
+    if (err) latch_gather(g.ctr, err);
   }
-  if (err) latch_gather(g.ctr, err);
-  __syncthreads();
+  barrier_keep_loads();
   if (!s.ok) return;
   // Tiles behind the last one are computed on whatever lies in their place and
   // masked, so that the main loop has no branches. (Read two barriers later.)
@@ -550,12 +578,12 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
 
   // every second wave needs every head's l and m
   float* ml = reinterpret_cast<float*>(s.p);
-  __syncthreads();
+  barrier_keep_loads();
   if (!second && wave * 16 < kHeads && quad == 0) {
     ml[wave * 16 + col] = m;
     ml[kHeads + wave * 16 + col] = l;
   }
-  __syncthreads();
+  barrier_keep_loads();
   float inv[HT];
 #pragma unroll
   for (int h = 0; h < HT; ++h) {
@@ -591,38 +619,71 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
 }
 
 // Joins the splits of one (set, head): o = sum_s w_s o_s / sum_s w_s with
-// w_s = 2^(lse_s - max lse). One wave per `kWave * 4` channels or fewer.
+// w_s = 2^(lse_s - max lse). Bound by the latency of its reads, not their bytes:
+// a workgroup reads as many splits at a time as its threads cover, whose sums
+// meet in LDS, and the first of them while it finds the largest lse (16 sets, 32
+// heads, 16 splits of 128 channels: 10.2 us with 32 threads that read one split
+// after another, 4.2 us so).
 template <typename Q8>
-__global__ __launch_bounds__(128) void k_attend_join(GroupDev g, AttendDev a, int width) {
+__global__ __launch_bounds__(kJoinThreads) void k_attend_join(GroupDev g, AttendDev a, int width) {
+  constexpr int kJoinWaves = kJoinThreads / kWave;
   __shared__ int ok;
-  if (threadIdx.x == 0) ok = reader_ready(g, a.want_flag);
-  __syncthreads();
-  if (!ok) return;
+  __shared__ float s_w[kAttendMaxSplits];
+  __shared__ float s_red[kJoinWaves];
+  __shared__ f32x4 s_acc[kJoinThreads];
+  const ReaderState state = reader_state(g);
   const size_t row = blockIdx.x;
+  // `per` threads read a split's row; thread group `at` takes splits at, at + groups, ..
+  const int per = width / 4, groups = kJoinThreads / per;
+  const int at = threadIdx.x / per, c = 4 * (threadIdx.x % per);
+  const float* po = a.part_o + row * a.splits * width + c;
+  constexpr int kAhead = 4;                       // on their way while the weights are computed
+  f32x4 first[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (at + u * groups < a.splits) first[u] = *reinterpret_cast<const f32x4*>(po + (size_t)(at + u * groups) * width);
+  if (threadIdx.x == 0) ok = reader_ready(g, state, a.want_flag);
   const float* lse = a.part_lse + row * a.splits;
   float top = -__builtin_inff();
-  for (int i = 0; i < a.splits; ++i) top = fmaxf(top, lse[i]);
-  const float base = top == -__builtin_inff() ? 0.0f : top;
-  const int c = 4 * threadIdx.x;
-  f32x4 acc{};
-  float sum = 0.0f;
-  for (int i = 0; i < a.splits; ++i) {
-    const float w = exp2f(lse[i] - base);
-    sum += w;
-    if (c < width) {
-      const f32x4 v = *reinterpret_cast<const f32x4*>(a.part_o + (row * a.splits + i) * width + c);
+  for (int i = threadIdx.x; i < a.splits; i += kJoinThreads) top = fmaxf(top, s_w[i] = lse[i]);
+  for (int d = kWave / 2; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
+  if (lane_id() == 0) s_red[threadIdx.x / kWave] = top;
+  barrier_keep_loads();
+  if (!ok) return;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] += w * v[e];
-    }
+  for (int w = 0; w < kJoinWaves; ++w) top = fmaxf(top, s_red[w]);
+  const float base = top == -__builtin_inff() ? 0.0f : top;
+  f32x4 acc{};
+  float sum = 0.0f;                               // of the group's splits
+  auto add = [&](int i, const f32x4& v) {
+    const float w = exp2f(s_w[i] - base);
+    sum += w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] += w * v[e];
+  };
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (at + u * groups < a.splits) add(at + u * groups, first[u]);
+#pragma unroll 4
+  for (int i = at + kAhead * groups; i < a.splits; i += groups)
+    add(i, *reinterpret_cast<const f32x4*>(po + (size_t)i * width));
+  s_acc[threadIdx.x] = acc;
+  __syncthreads();                                // every weight was read: s_w holds the groups' sums from here
+  if (c == 0) s_w[at] = sum;
+  __syncthreads();
+  if (at != 0) return;
+  for (int j = 1; j < groups; ++j) {
+    const f32x4 v = s_acc[threadIdx.x + j * per];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] += v[e];
+    sum += s_w[j];
   }
   const int set = (int)(row / a.heads), head = (int)(row % a.heads);
   const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-  if (c < width) {
-    float v[4];
+  float v[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = acc[e] * inv;
-    store4<Q8>(static_cast<uint16_t*>(a.out) + set * a.out_set_stride + head * a.out_head_stride + c, v, a.out_aligned);
-  }
+  for (int e = 0; e < 4; ++e) v[e] = acc[e] * inv;
+  store4<Q8>(static_cast<uint16_t*>(a.out) + set * a.out_set_stride + head * a.out_head_stride + c, v, a.out_aligned);
   if (threadIdx.x == 0 && a.lse) a.lse[row] = sum != 0.0f ? (top + log2f(sum)) * kLn2 : -__builtin_inff();
 }
 
@@ -641,7 +702,7 @@ AttendPlan plan_attend_latent(int n_sets, int k, int heads) {
   const int tiles = (k + kTileKeys - 1) / kTileKeys;
   double best_cost = 0;
   const int least = std::max(1, (k + kAttendKeys - 1) / kAttendKeys);
-  for (int want = least; want <= std::max(least, std::min(tiles, 256)); ++want) {
+  for (int want = least; want <= std::max(least, std::min(tiles, kComputeUnits)); ++want) {
     const int per = (tiles + want - 1) / want;            // tiles per split
     const int splits = std::max(1, (tiles + per - 1) / per);
     if (splits != want && want != least) continue;        // the same split as a smaller one
@@ -675,8 +736,8 @@ hipError_t launch_attend_latent(const GroupDev& g, const AttendDev& a, int type,
 
 hipError_t launch_attend_join(const GroupDev& g, const AttendDev& a, int type, int n_sets, int width, hipStream_t s) {
   const int blocks = n_sets * a.heads;
-  if (type == ULA_BF16) k_attend_join<bf16x8><<<blocks, 128, 0, s>>>(g, a, width);
-  else k_attend_join<f16x8><<<blocks, 128, 0, s>>>(g, a, width);
+  if (type == ULA_BF16) k_attend_join<bf16x8><<<blocks, kJoinThreads, 0, s>>>(g, a, width);
+  else k_attend_join<f16x8><<<blocks, kJoinThreads, 0, s>>>(g, a, width);
   return hipGetLastError();
 }
 

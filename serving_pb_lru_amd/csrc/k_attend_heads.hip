@@ -46,9 +46,7 @@ __global__ __launch_bounds__(kHeadWaves * kWave) void k_attend_heads(GroupDev g,
   const int quad = lane / 16, col = lane % 16;
   const int item = blockIdx.x * kHeadWaves + wave;
   if (item >= n_items) return;                 // waves are independent: no barrier below
-  int ok = 0;
-  if (lane == 0) ok = reader_ready(g, a.want_flag);
-  if (!__builtin_amdgcn_readfirstlane(ok)) return;
+  const ReaderState state = reader_state(g);
   WaveLds& s = s_all[wave];
 
   const int unit = item % a.head_blocks;
@@ -81,11 +79,11 @@ __global__ __launch_bounds__(kHeadWaves * kWave) void k_attend_heads(GroupDev g,
   const int scale_at = 2 * val_at + 4 * kvh;
   int err = 0;
 
-  // slot of this lane's token (lane % 32) of a tile
-  auto resolve = [&](int tile) -> uint32_t {
+  // the selection entry of this lane's token (lane % 32) of a tile
+  auto look = [&](int tile) -> Lookup {
     const int t = tile * kTok + lane % kTok;
-    if (t >= ntok) return kAbsent;
-    return resolve_slot(g, a.sel, set * a.k + ((tok0 + t) >> a.block_shift), a.n_res, err);
+    if (t >= ntok) return {make_uint2(kAbsent, kAbsent), -1};
+    return look_up(g, a.sel, set * a.k + ((tok0 + t) >> a.block_shift), a.n_res);
   };
   vec4u kreg[2][kKeyLoads], vreg[kValLoads];
   float ks = 0.0f, vs = 0.0f;
@@ -131,12 +129,12 @@ __global__ __launch_bounds__(kHeadWaves * kWave) void k_attend_heads(GroupDev g,
   auto swizzle = [](int tok) { return D == 128 ? (tok >> 1) & 7 : (tok >> 2) & 1; };
   const uint32_t vrow = lds_address(s.v) + vtok * D + (swizzle(vtok) << 4) + (col & 1) * 8;
 
-  uint32_t next = kAbsent;
-  if (tiles > 0) {
-    const uint32_t first = resolve(0);
-    next = tiles > 1 ? resolve(1) : kAbsent;
-    load(0, first);
-  }
+  const Lookup first = look(0);
+  Lookup next = look(1);
+  int ok = 0;
+  if (lane == 0) ok = reader_ready(g, state, a.want_flag);
+  if (!__builtin_amdgcn_readfirstlane(ok)) return;
+  if (tiles > 0) load(0, slot_of(g, first, a.n_res, err));
 #pragma unroll 1
   for (int tile = 0; tile < tiles; ++tile) {
     // this tile out of the staging registers
@@ -159,8 +157,8 @@ __global__ __launch_bounds__(kHeadWaves * kWave) void k_attend_heads(GroupDev g,
     }
     // the next tile's loads, and the slots of the one after it
     if (tile + 1 < tiles) {
-      const uint32_t cur = next;
-      next = tile + 2 < tiles ? resolve(tile + 2) : kAbsent;
+      const uint32_t cur = slot_of(g, next, a.n_res, err);
+      next = look(tile + 2);
       load(tile + 1, cur);
     }
     if (now == 0) continue;
@@ -240,7 +238,7 @@ AttendPlan plan_attend_heads(int n_sets, int tokens, int heads, int kv_heads) {
   p.head_blocks = kv_heads * ((shared + kHeadsPerWave - 1) / kHeadsPerWave);
   const long long base = std::max<long long>(1, (long long)n_sets * p.head_blocks);
   const int tiles = std::max(1, (tokens + kTok - 1) / kTok);
-  const int want = (int)std::min<long long>((kWaveTarget + base - 1) / base, std::max(1, tiles / kLeastTiles));
+  const int want = (int)std::min<long long>(std::min<long long>((kWaveTarget + base - 1) / base, kAttendMaxSplits), std::max(1, tiles / kLeastTiles));
   const int per = (tiles + want - 1) / want;
   p.splits = (tiles + per - 1) / per;
   p.split_keys = per * kTok;

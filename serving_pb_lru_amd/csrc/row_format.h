@@ -28,6 +28,8 @@ static_assert(kLatentRow == 656, "latent row bytes");
 constexpr float kE4m3Max = 448.0f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kAttendKeys = 2048;                      // most keys one latent work item takes
+constexpr int kAttendMaxSplits = 1024;             // parts of a row that the join takes
+constexpr int kJoinThreads = 256;
 
 // Device arguments of an attention call.
 struct AttendDev {
@@ -95,6 +97,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
@@ -242,17 +245,25 @@ __device__ __forceinline__ void store4(uint16_t* p, const float* v, bool aligned
   }
 }
 
-// The GPU slot of entry r of a selection: from the step's resolved selection
-// where that names the same address, else through the mapping table. kAbsent
-// for padding and for an address that is not on the GPU (err says why).
-__device__ __forceinline__ uint32_t resolve_slot(const GroupDev& g, const int32_t* __restrict__ sel, int r,
-                                                 int n_res, int& err) {
-  const uint2 rs = r < n_res ? g.res[r] : make_uint2(kAbsent, kAbsent);
-  const int32_t la = sel[r];
+// Entry r of a selection and of the step's resolved selection, as loaded: apart
+// from their use, so that several lookups' loads are in flight at once.
+struct Lookup {
+  uint2 res;
+  int32_t la;
+};
+__device__ __forceinline__ Lookup look_up(const GroupDev& g, const int32_t* __restrict__ sel, int r, int n_res) {
+  return {r < n_res ? g.res[r] : make_uint2(kAbsent, kAbsent), sel[r]};
+}
+
+// Its GPU slot: from the resolved selection where that names the same address,
+// else through the mapping table. kAbsent for padding and for an address that is
+// not on the GPU (err says why).
+__device__ __forceinline__ uint32_t slot_of(const GroupDev& g, const Lookup& at, int n_res, int& err) {
+  const int32_t la = at.la;
   if (la == -1) return kAbsent;
   uint32_t slot = kAbsent;
-  if (r < n_res && rs.x == (uint32_t)la) {
-    slot = rs.y;
+  if (at.res.x == (uint32_t)la) {
+    slot = at.res.y;
     if ((slot & kHostBit) && slot != kAbsent && (int32_t)(slot & ~kHostBit) < n_res) {
       const uint2 first = g.res[slot & ~kHostBit];   // a repeated miss
       slot = first.x == (uint32_t)la ? first.y : kAbsent;
@@ -272,12 +283,19 @@ __device__ __forceinline__ uint32_t resolve_slot(const GroupDev& g, const int32_
   return slot;
 }
 
-// Whether a reader of step want_flag's rows may go on (one thread's answer):
-// the group has no latched error and its completion counter is at that step.
-__device__ __forceinline__ bool reader_ready(const GroupDev& g, long long want_flag) {
-  if (status_of(g.ctr)) return false;
-  const long long f = __hip_atomic_load(&g.ctr->flag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  if (f == want_flag) return true;
+// Whether a reader of step want_flag's rows may go on (one thread's answer): the
+// group has no latched error and its completion counter is at that step. The two
+// loads are apart from the answer, as a lookup's are.
+struct ReaderState {
+  int status;
+  long long flag;
+};
+__device__ __forceinline__ ReaderState reader_state(const GroupDev& g) {
+  return {status_of(g.ctr), __hip_atomic_load(&g.ctr->flag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)};
+}
+__device__ __forceinline__ bool reader_ready(const GroupDev& g, const ReaderState& at, long long want_flag) {
+  if (at.status) return false;
+  if (at.flag == want_flag) return true;
   latch_gather(g.ctr, ULA_ENOTRESIDENT);
   return false;
 }

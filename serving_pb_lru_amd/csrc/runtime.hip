@@ -1186,8 +1186,10 @@ int ula_rotate(const ula_rotate_args* args, uint64_t stream) {
 static bool plan_attend(const ula_row_format* f, int32_t n_sets, int32_t k, int32_t heads, AttendPlan* plan,
                         int* width) {
   if (ula_row_format_bytes(f) == 0 || n_sets < 0 || k < 0 || heads < 1 || heads > (1 << 16)) return false;
-  if ((int64_t)n_sets * k >= (1ll << 30) || (int64_t)n_sets * heads >= (1ll << 30)) return false;
+  // a launch has fewer than 2^32 threads: kJoinThreads for each (set, head) here
+  if ((int64_t)n_sets * k >= (1ll << 30) || (int64_t)n_sets * heads >= (1ll << 24)) return false;
   if (f->kind == ULA_ROWS_LATENT) {
+    if (k > kAttendKeys * kAttendMaxSplits) return false;
     *plan = plan_attend_latent(n_sets, k, heads);
     *width = kLatent;
   } else {
@@ -1196,7 +1198,7 @@ static bool plan_attend(const ula_row_format* f, int32_t n_sets, int32_t k, int3
     *plan = plan_attend_heads(n_sets, k * f->block_tokens, heads, f->kv_heads);
     *width = f->head_dim;
   }
-  return (int64_t)n_sets * plan->head_blocks * plan->splits < (1ll << 31);
+  return (int64_t)n_sets * plan->head_blocks * plan->splits < (1ll << 23);   // at most 512 threads each
 }
 
 static size_t attend_bytes(const AttendPlan& p, int32_t n_sets, int32_t heads, int width) {
