@@ -53,7 +53,6 @@ constexpr int kTileKeys = 32;
 constexpr int kTilePieces = kLatentScaleAt / 16;                 // 40 pieces of a row go to LDS
 constexpr int kTileBytes = kTileKeys * kLatentScaleAt;           // 20 KB
 constexpr int kComputeUnits = 256;
-constexpr double kStartTiles = 6, kJoinTiles = 8, kJoinTilesPerRow = 2.0e-4;   // see plan_attend_latent
 constexpr int kTileLoads = kTileBytes / 1024;                    // wave-wide 16-byte loads of a tile: 20
 
 // rows that stand in for padding: zeros, so that a masked key adds 0 x 0
@@ -691,9 +690,18 @@ constexpr int latent_wg_heads(int heads) { return heads <= 32 ? 32 : 64; }
 
 // How a call's keys are split over workgroups (one per compute unit at a time):
 // the number of splits with the least estimated time, in units of one tile's
-// time on one compute unit. A workgroup costs its tiles plus a fixed start
-// (resolving slots, loading q); with more than one split each also writes, and
-// the join reads, its 32-bit results.
+// time on one compute unit (1.1 us with 64 heads, 0.8 us with 32). A workgroup
+// costs its tiles plus its start and end (lookups, q, results: 18 us with 64
+// heads, 9 us with 32). With more than one split the join costs a launch, on the
+// host too (7 tiles; 4 on the device), a part for each row and one for each split
+// of a row. Measured, kernel and join, us:
+//   sets x heads, keys    splits
+//   1 x 16, 2048          1: 61    8: 19    16: 16   32: 15   64: 16
+//   4 x 16, 256           1: 14    2: 16    4: 14    8: 13
+//   4 x 64, 2048          4: 37    8: 28    16: 25   32: 25   64: 30
+//   16 x 128, 2048        2: 57    4: 42    8: 36    16: 51
+//   64 x 128, 2048        1: 90    2: 75    4: 89
+//   160 x 64, 2048        1: 97    2: 128   3: 112
 AttendPlan plan_attend_latent(int n_sets, int k, int heads) {
   AttendPlan best{};
   const int wg_heads = latent_wg_heads(heads);
@@ -707,8 +715,9 @@ AttendPlan plan_attend_latent(int n_sets, int k, int heads) {
     const int splits = std::max(1, (tiles + per - 1) / per);
     if (splits != want && want != least) continue;        // the same split as a smaller one
     const double waves = (double)((base * splits + kComputeUnits - 1) / kComputeUnits);
-    double cost = waves * (per + kStartTiles);
-    if (splits > 1) cost += kJoinTiles + (double)base * splits * std::min(heads, wg_heads) * kJoinTilesPerRow;
+    double cost = waves * (per + (wg_heads == 32 ? 11 : 16));
+    const double rows = (double)n_sets * heads;
+    if (splits > 1) cost += 7 + 8e-4 * rows + 1.8e-4 * rows * splits;
     if (best.splits == 0 || cost < best_cost) {
       best_cost = cost;
       best.splits = splits;

@@ -230,11 +230,17 @@ def _tensor(t, shape, what: str, types=(BF16, FP16, FP32)):
     code = _TYPES.get(str(t.dtype))
     if code not in types:
         raise ValueError(f"{what}: dtype {t.dtype} is not supported")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)} (None: any)")
-    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+    real, strides = t.shape, t.stride()
+    same = len(real) == len(shape)
+    if same:
+        for n, m in zip(shape, real):
+            if n is not None and n != m:
+                same = False
+    if not same:
+        raise ValueError(f"{what}: shape {tuple(real)}, expected {tuple(shape)} (None: any)")
+    if strides[-1] != 1 and real[-1] > 1 and t.numel():
         raise ValueError(f"{what}: the last dimension must be contiguous")
-    return t.data_ptr(), code, t.stride()
+    return t.data_ptr(), code, strides
 
 
 def _same_device(first, *others) -> None:
@@ -249,20 +255,22 @@ class _On:
 
     def __init__(self, device, stream):
         import torch
-        self.device = device
-        if stream is None:
-            self.stream = torch.cuda.current_stream(device)
-        elif hasattr(stream, "cuda_stream"):
-            self.stream = stream
-        else:
-            self.stream = torch.cuda.ExternalStream(int(stream), device=device)
-        cur = torch.cuda.current_stream()
-        self.ctx = None if cur == self.stream else torch.cuda.stream(self.stream)
+        # the handle alone: a decode step's call is bound by the host, and a Stream object costs 2 us
+        current = torch._C._cuda_getCurrentRawStream(device.index)
+        here = torch.cuda.current_device() == device.index
+        self.handle = current if stream is None else _stream(stream)
+        self.ctx = None
+        if not here or self.handle != current:
+            if not hasattr(stream, "cuda_stream"):
+                # handle 0 is the device's default stream, which has no external form
+                stream = (torch.cuda.ExternalStream(self.handle, device=device) if self.handle
+                          else torch.cuda.default_stream(device))
+            self.ctx = torch.cuda.stream(stream)
 
     def __enter__(self) -> int:
         if self.ctx is not None:
             self.ctx.__enter__()
-        return self.stream.cuda_stream
+        return self.handle
 
     def __exit__(self, *exc):
         if self.ctx is not None:
