@@ -4,8 +4,8 @@
 //
 // Quantisation, per scale block (128 latent channels, or one head's keys or
 // values in a block of tokens): scale = max(amax / 448, 2^-126), code =
-// e4m3(x / scale), both divisions correctly rounded in 32 bits and the code
-// rounded to nearest even. An infinity takes the largest code and a NaN the NaN
+// e4m3(x / scale), both quotients in 32 bits and the code rounded to nearest
+// even. An infinity takes the largest code and a NaN the NaN
 // code; neither enters amax.
 //
 // Rotary positions: pair i of R / 2 turns by the angle pos[axis(i)] x
@@ -17,6 +17,7 @@
 // All three kernels read and write every byte once and are bound by HBM, or for
 // a decode step's few rows by the launch.
 #include <algorithm>
+#include <type_traits>
 
 #include "row_format.h"
 
@@ -70,42 +71,91 @@ __device__ __forceinline__ float2 rotary_of(const RotaryDev& r, const int32_t* _
   return cos_sin_turns((double)pos[axis] * r.turns[i]);
 }
 
-// Latent rows: one wave per row, lane i channels 8 i .. 8 i + 7 (16 lanes share
-// a scale), then lane i < 32 rotary pair i.
+// x / b by b's correctly rounded reciprocal and one correction: off by less than
+// 2^-46 of the quotient before its own rounding, given that neither the product
+// nor the remainder leaves the normal range.
+__device__ __forceinline__ float divide_by(float x, float b, float inv_b) {
+  const float q = x * inv_b;
+  return __builtin_fmaf(__builtin_fmaf(-q, b, x), inv_b, q);
+}
+
+// The largest of 16 lanes' values, in all of them.
+__device__ __forceinline__ float max_of_16(float x) {
+  auto rotated = [](float v, auto n) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x120 + n.value, 0xF, 0xF, true));
+  };
+  x = fmaxf(x, rotated(x, std::integral_constant<int, 8>{}));
+  x = fmaxf(x, rotated(x, std::integral_constant<int, 4>{}));
+  x = fmaxf(x, rotated(x, std::integral_constant<int, 2>{}));
+  return fmaxf(x, rotated(x, std::integral_constant<int, 1>{}));
+}
+
+// Latent rows: a wave takes two rows, lane i channels 8 i .. 8 i + 7 of either (16
+// lanes share a scale) and rotary pair i % 32 of row i / 32. Instructions, not
+// bytes, would bound it with a division per channel: hence one reciprocal per
+// scale where every value is finite and far enough from the least ones (65536 rows, 118 MB read and
+// written: 36 us with a row a wave and IEEE divisions, 22 us so).
+constexpr int kPackRows = 2;
+
 template <typename T, bool ALIGNED>
-__global__ __launch_bounds__(256) void k_pack_latent(PackDev a, RotaryDev rot) {
+__global__ __launch_bounds__(256) void k_pack_latent(PackDev a, RotaryDev rot, FastDiv by_layers) {
   const int lane = lane_id();
-  const int row = blockIdx.x * 4 + threadIdx.x / kWave;
-  if (row >= a.n * a.layers) return;
-  const int entry = row / a.layers, layer = row % a.layers;
-  const T* latent = static_cast<const T*>(a.a) + entry * a.a_stride[0] + layer * a.a_stride[1];
-  const T* rope = static_cast<const T*>(a.b) + entry * a.b_stride[0] + layer * a.b_stride[1];
-  uint8_t* out = a.rows + (size_t)row * kLatentRow;
-  float x[8];
-  load_f32<T, 8, ALIGNED>(latent + 8 * lane, x);
-  const int pair = lane % 32;
-  const int at0 = rot.interleaved ? 2 * pair : pair, at1 = rot.interleaved ? 2 * pair + 1 : pair + kRope / 2;
-  const float r0 = to_f32(rope[at0]), r1 = to_f32(rope[at1]);
-  float amax = 0.0f;
+  const uint32_t row0 = (blockIdx.x * 4 + threadIdx.x / kWave) * kPackRows;
+  const uint32_t rows = (uint32_t)a.n * (uint32_t)a.layers;
+  if (row0 >= rows) return;
+  float x[kPackRows][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, finite_abs(x[i]));
-#pragma unroll
-  for (int d = 1; d < 16; d *= 2) amax = fmaxf(amax, __shfl_xor(amax, d, kWave));
-  const float scale = scale_of(amax);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = to_e4m3_range(x[i], scale);
-  reinterpret_cast<uint2*>(out)[lane] = make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
-  if (lane % 16 == 0) *reinterpret_cast<float*>(out + kLatentScaleAt + lane / 16 * 4) = scale;
-  if (lane < 32) {
-    float y0 = r0, y1 = r1;
-    if (a.positions) {
-      const float2 cs = rotary_of(rot, a.positions + (size_t)entry * rot.axes, pair);
-      y0 = r0 * cs.x - r1 * cs.y;
-      y1 = r0 * cs.y + r1 * cs.x;
+  for (int r = 0; r < kPackRows; ++r) {
+    const uint32_t row = min(row0 + r, rows - 1), entry = by_layers.div(row), layer = row - entry * a.layers;
+    load_f32<T, 8, ALIGNED>(static_cast<const T*>(a.a) + entry * a.a_stride[0] + layer * a.a_stride[1] + 8 * lane, x[r]);
+  }
+  {
+    const uint32_t row = row0 + lane / 32;
+    static_assert(kPackRows == 2, "a row's rotary pairs for either half of the wave");
+    if (row < rows) {
+      const uint32_t entry = by_layers.div(row), layer = row - entry * a.layers;
+      const T* rope = static_cast<const T*>(a.b) + entry * a.b_stride[0] + layer * a.b_stride[1];
+      const int pair = lane % 32;
+      const int at0 = rot.interleaved ? 2 * pair : pair, at1 = rot.interleaved ? 2 * pair + 1 : pair + kRope / 2;
+      const float r0 = to_f32(rope[at0]), r1 = to_f32(rope[at1]);
+      float y0 = r0, y1 = r1;
+      if (a.positions) {
+        const float2 cs = rotary_of(rot, a.positions + (size_t)entry * rot.axes, pair);
+        y0 = r0 * cs.x - r1 * cs.y;
+        y1 = r0 * cs.y + r1 * cs.x;
+      }
+      __bf16* ro = reinterpret_cast<__bf16*>(a.rows + (size_t)row * kLatentRow + kRopeAt);
+      ro[at0] = (__bf16)y0;
+      ro[at1] = (__bf16)y1;
     }
-    __bf16* ro = reinterpret_cast<__bf16*>(out + kRopeAt);
-    ro[at0] = (__bf16)y0;
-    ro[at1] = (__bf16)y1;
+  }
+#pragma unroll
+  for (int r = 0; r < kPackRows; ++r) {
+    if (row0 + r >= rows) break;
+    float amax = 0.0f, odd = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      amax = fmaxf(amax, fabsf(x[r][i]));
+      odd = __builtin_fmaf(x[r][i], 0.0f, odd);   // NaN after an infinity or a NaN
+    }
+    amax = max_of_16(amax);
+    float scale = divide_by(amax, kE4m3Max, 1.0f / kE4m3Max);
+    if (__any(odd != 0.0f || !(scale >= 0x1p-60f))) {
+      amax = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, finite_abs(x[r][i]));
+      scale = scale_of(max_of_16(amax));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[r][i] = to_e4m3_range(x[r][i], scale);
+    } else {
+      const float inv = 1.0f / scale;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[r][i] = divide_by(x[r][i], scale, inv);
+    }
+    uint8_t* out = a.rows + (size_t)(row0 + r) * kLatentRow;
+    reinterpret_cast<uint2*>(out)[lane] =
+        make_uint2(e4m3x4(x[r][0], x[r][1], x[r][2], x[r][3]), e4m3x4(x[r][4], x[r][5], x[r][6], x[r][7]));
+    if (lane % 16 == 0) *reinterpret_cast<float*>(out + kLatentScaleAt + lane / 16 * 4) = scale;
   }
 }
 
@@ -166,18 +216,100 @@ __global__ __launch_bounds__(kWave) void k_pack_heads(PackDev a, RotaryDev rot) 
   }
 }
 
-// Rotary positions of [n][heads][dim] tensors. A workgroup takes `tokens` tokens
-// and a range of heads: the tokens' sines and cosines once into LDS, then V
-// pairs per lane. In place is fine: a lane reads its pairs before it writes them.
+// V pairs of a row as they are in memory, first .. first + V - 1 of `pairs`.
 template <typename T, int V>
-__global__ __launch_bounds__(256) void k_rotate(RotateDev a, RotaryDev rot) {
+struct Pairs {
+  typedef T vec __attribute__((ext_vector_type(V)));
+  typedef T vec2 __attribute__((ext_vector_type(2 * V)));
+  T a[V], b[V];
+  __device__ __forceinline__ void load(const T* x, int first, int pairs, bool interleaved) {
+    if (interleaved) {
+      vec2 v;
+      if constexpr (V > 1) v = *reinterpret_cast<const vec2*>(x + 2 * first);
+      else v = vec2{x[2 * first], x[2 * first + 1]};
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        a[j] = v[2 * j];
+        b[j] = v[2 * j + 1];
+      }
+    } else if constexpr (V > 1) {
+      const vec v = *reinterpret_cast<const vec*>(x + first), w = *reinterpret_cast<const vec*>(x + first + pairs);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        a[j] = v[j];
+        b[j] = w[j];
+      }
+    } else {
+      a[0] = x[first];
+      b[0] = x[first + pairs];
+    }
+  }
+  __device__ __forceinline__ void turn(const float2* cs) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float p = to_f32(a[j]), q = to_f32(b[j]);
+      a[j] = (T)(p * cs[j].x - q * cs[j].y);
+      b[j] = (T)(p * cs[j].y + q * cs[j].x);
+    }
+  }
+  __device__ __forceinline__ void store(T* y, int first, int pairs, bool interleaved) const {
+    if (interleaved) {
+      if constexpr (V > 1) {
+        vec2 v;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          v[2 * j] = a[j];
+          v[2 * j + 1] = b[j];
+        }
+        *reinterpret_cast<vec2*>(y + 2 * first) = v;
+      } else {
+        y[2 * first] = a[0];
+        y[2 * first + 1] = b[0];
+      }
+    } else if constexpr (V > 1) {
+      vec v, w;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        v[j] = a[j];
+        w[j] = b[j];
+      }
+      *reinterpret_cast<vec*>(y + first) = v;
+      *reinterpret_cast<vec*>(y + first + pairs) = w;
+    } else {
+      y[first] = a[0];
+      y[first + pairs] = b[0];
+    }
+  }
+};
+
+// Rotary positions of [n][heads][dim] tensors. A workgroup takes `tokens` tokens
+// and a range of heads, V pairs of a row a unit, U units a lane: their loads are
+// on their way while the tokens' sines and cosines are computed, once each, into
+// LDS. In place is fine: a lane reads its pairs before it writes them. (8191 x 32
+// heads x 128 fp32, 268 MB read and written: 42 us.)
+template <typename T, int V, int U>
+__global__ __launch_bounds__(256) void k_rotate(RotateDev a, RotaryDev rot, FastDiv by_units, FastDiv by_heads) {
   extern __shared__ float2 s_cs[];   // [tokens][pairs]
-  const int pairs = a.dim / 2;
+  const int pairs = a.dim / 2, units = pairs / V;
   const int head_parts = (a.heads + a.heads_per_block - 1) / a.heads_per_block;
   const int tok0 = blockIdx.x / head_parts * a.tokens_per_block;
   const int head0 = blockIdx.x % head_parts * a.heads_per_block;
   const int tokens = min(a.tokens_per_block, a.n - tok0);
   const int heads = min(a.heads_per_block, a.heads - head0);
+  Pairs<T, V> x[U];
+  int first[U], head[U], tok[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    // the whole range's division, whatever part of it this workgroup has: heads beyond it do nothing
+    const uint32_t e = threadIdx.x + u * 256, row = by_units.div(e);
+    tok[u] = (int)by_heads.div(row);
+    first[u] = (int)(e - row * units) * V;
+    head[u] = (int)row - tok[u] * a.heads_per_block;
+    if (head[u] >= heads) tok[u] = tokens;
+    if (tok[u] < tokens)
+      x[u].load(static_cast<const T*>(a.x) + (tok0 + tok[u]) * a.x_stride[0] + (head0 + head[u]) * a.x_stride[1],
+                first[u], pairs, rot.interleaved);
+  }
   for (int e = threadIdx.x; e < tokens * pairs; e += 256) {
     const int t = e / pairs;
     float2 cs = rotary_of(rot, a.positions + (size_t)(tok0 + t) * rot.axes, e % pairs);
@@ -185,54 +317,12 @@ __global__ __launch_bounds__(256) void k_rotate(RotateDev a, RotaryDev rot) {
     s_cs[e] = cs;
   }
   __syncthreads();
-  const int units = pairs / V;
-  typedef T vec __attribute__((ext_vector_type(V)));
-  typedef T vec2 __attribute__((ext_vector_type(2 * V)));
-  for (int e = threadIdx.x; e < tokens * heads * units; e += 256) {
-    const int i = e % units * V;
-    const int h = e / units % heads, t = e / units / heads;
-    const T* x = static_cast<const T*>(a.x) + (tok0 + t) * a.x_stride[0] + (head0 + h) * a.x_stride[1];
-    T* y = static_cast<T*>(a.out) + (tok0 + t) * a.out_stride[0] + (head0 + h) * a.out_stride[1];
-    const float2* cs = s_cs + t * pairs + i;
-    if (rot.interleaved) {
-      vec2 v;
-      if constexpr (V > 1) v = *reinterpret_cast<const vec2*>(x + 2 * i);
-      else v = vec2{x[2 * i], x[2 * i + 1]};
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float p = to_f32(v[2 * j]), q = to_f32(v[2 * j + 1]);
-        v[2 * j] = (T)(p * cs[j].x - q * cs[j].y);
-        v[2 * j + 1] = (T)(p * cs[j].y + q * cs[j].x);
-      }
-      if constexpr (V > 1) {
-        *reinterpret_cast<vec2*>(y + 2 * i) = v;
-      } else {
-        y[2 * i] = v[0];
-        y[2 * i + 1] = v[1];
-      }
-    } else {
-      vec v, w;
-      if constexpr (V > 1) {
-        v = *reinterpret_cast<const vec*>(x + i);
-        w = *reinterpret_cast<const vec*>(x + i + pairs);
-      } else {
-        v = vec{x[i]};
-        w = vec{x[i + pairs]};
-      }
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float p = to_f32(v[j]), q = to_f32(w[j]);
-        v[j] = (T)(p * cs[j].x - q * cs[j].y);
-        w[j] = (T)(p * cs[j].y + q * cs[j].x);
-      }
-      if constexpr (V > 1) {
-        *reinterpret_cast<vec*>(y + i) = v;
-        *reinterpret_cast<vec*>(y + i + pairs) = w;
-      } else {
-        y[i] = v[0];
-        y[i + pairs] = w[0];
-      }
-    }
+  for (int u = 0; u < U; ++u) {
+    if (tok[u] >= tokens) continue;
+    x[u].turn(s_cs + tok[u] * pairs + first[u]);
+    x[u].store(static_cast<T*>(a.out) + (tok0 + tok[u]) * a.out_stride[0] + (head0 + head[u]) * a.out_stride[1],
+               first[u], pairs, rot.interleaved);
   }
 }
 
@@ -240,9 +330,10 @@ template <typename T>
 static hipError_t pack_of(const PackDev& a, const RotaryDev& rot, hipStream_t s) {
   const int rows = a.n * a.layers;
   if (a.latent) {
-    const int blocks = (rows + 3) / 4;
-    if (a.aligned) k_pack_latent<T, true><<<blocks, 256, 0, s>>>(a, rot);
-    else k_pack_latent<T, false><<<blocks, 256, 0, s>>>(a, rot);
+    const int blocks = (rows + 4 * kPackRows - 1) / (4 * kPackRows);
+    const FastDiv by_layers(a.layers);
+    if (a.aligned) k_pack_latent<T, true><<<blocks, 256, 0, s>>>(a, rot, by_layers);
+    else k_pack_latent<T, false><<<blocks, 256, 0, s>>>(a, rot, by_layers);
   } else {
     k_pack_heads<T><<<rows * 2 * a.kv_heads, kWave, 0, s>>>(a, rot);
   }
@@ -255,20 +346,23 @@ hipError_t launch_pack(const PackDev& a, const RotaryDev& rot, int type, hipStre
   return pack_of<float>(a, rot, s);
 }
 
-template <typename T>
-static hipError_t rotate_of(RotateDev a, const RotaryDev& rot, hipStream_t s) {
-  constexpr int V = 4;
-  const int pairs = a.dim / 2;
-  const int units = a.aligned ? pairs / V : pairs;
-  // about 512 units per workgroup: two per lane, enough workgroups for a decode step
-  constexpr int kUnits = 512;
+template <typename T, int V>
+static void rotate_units(RotateDev a, const RotaryDev& rot, hipStream_t s) {
+  // two units a lane: enough workgroups for a decode step, and 512 units hold a head's (at most 128)
+  constexpr int U = 2, kUnits = 256 * U;
+  const int pairs = a.dim / 2, units = pairs / V;
   a.heads_per_block = std::max(1, std::min(a.heads, kUnits / units));
   a.tokens_per_block = std::max(1, std::min(a.n, std::min(kUnits / (units * a.heads_per_block), 4096 / pairs)));
   const long long blocks = (long long)((a.n + a.tokens_per_block - 1) / a.tokens_per_block) *
                            ((a.heads + a.heads_per_block - 1) / a.heads_per_block);
   const size_t lds = (size_t)a.tokens_per_block * pairs * sizeof(float2);
-  if (a.aligned) k_rotate<T, V><<<(unsigned)blocks, 256, lds, s>>>(a, rot);
-  else k_rotate<T, 1><<<(unsigned)blocks, 256, lds, s>>>(a, rot);
+  k_rotate<T, V, U><<<(unsigned)blocks, 256, lds, s>>>(a, rot, FastDiv(units), FastDiv(a.heads_per_block));
+}
+
+template <typename T>
+static hipError_t rotate_of(const RotateDev& a, const RotaryDev& rot, hipStream_t s) {
+  if (a.aligned) rotate_units<T, 4>(a, rot, s);
+  else rotate_units<T, 1>(a, rot, s);
   return hipGetLastError();
 }
 

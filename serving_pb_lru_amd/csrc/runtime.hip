@@ -1121,8 +1121,8 @@ int ula_pack_rows(const ula_pack_args* args, void* rows_dev, uint64_t stream) {
   const bool latent = u.rows.kind == ULA_ROWS_LATENT;
   if (latent && u.count) return ULA_EINVAL;
   const int64_t rows = (int64_t)u.n * u.layers;
-  // one workgroup per row and KV head, twice; 2^31 - 1 workgroups are the most
-  if (rows * (latent ? 1 : 2 * u.rows.kv_heads) >= (1ll << 31)) return ULA_EINVAL;
+  // a launch has fewer than 2^32 threads: one wave per row, or per row and KV head, twice
+  if (rows * (latent ? 1 : 2 * u.rows.kv_heads) >= (1ll << 26)) return ULA_EINVAL;
   RotaryDev rot{};
   if (u.positions && !rotary_dev(u.rotary, latent ? kRope / 2 : u.rows.head_dim / 2, &rot)) return ULA_EINVAL;
   if (rows == 0) return ULA_OK;
@@ -1156,7 +1156,8 @@ int ula_rotate(const ula_rotate_args* args, uint64_t stream) {
   int size;
   if (!element_size(u.type, &size) || u.n < 0 || u.heads < 0) return ULA_EINVAL;
   if (u.dim < 2 || u.dim % 2 || u.dim > 2 * kMostPairs || (u.inverse != 0 && u.inverse != 1)) return ULA_EINVAL;
-  if ((int64_t)u.n * u.heads >= (1ll << 31)) return ULA_EINVAL;
+  // fewer than 2^32 threads, 256 for two rows or more
+  if ((int64_t)u.n * u.heads >= (1ll << 25)) return ULA_EINVAL;
   RotaryDev rot{};
   if (!rotary_dev(u.rotary, u.dim / 2, &rot)) return ULA_EINVAL;
   if (u.n == 0 || u.heads == 0) return ULA_OK;
