@@ -13,11 +13,11 @@
 //   o_d  = sum_j p_j s_b(d)j k8_dj / l,   lse = (m + log2 l) ln 2
 // The block scales are applied in 32 bits, to the four partial products of S and
 // to p, so e4m3 codes enter the matrix instructions as they are:
-//   - first product, bf16 q: the 8-bit matrix instruction, with q as the sum of
-//     two e4m3 values (4 + 4 bits hold its 8; per head a power of two brings its
-//     largest value to 128..256, so what is lost is below 2^-17 of that). As many
-//     cycles as one 16-bit product, and no key is widened.
-//   - first product, fp16 q: the codes widened to fp16, which holds them exactly.
+//   - first product: the 8-bit matrix instruction, with q as the sum of two (bf16)
+//     or three (fp16) e4m3 values, below. Two take as many cycles as one 16-bit
+//     product, and no key is widened in the vector units, which the softmax needs
+//     (384 sets of 2047 keys and 128 heads in fp16: 365 us with 16-bit products of
+//     widened keys, 328 us with three parts).
 //   - second product: codes widened to fp16, and p s_b rounded to fp16. m follows
 //     the largest p_j max_b s_bj, which stays within 2^7..2^15, so the rounding is
 //     at most 2^-11 of the value, or 2^-25 (2^-32 of the largest) for small ones.
@@ -36,7 +36,10 @@
 // (256 sets of 2048 keys and 64 heads: 206 us with a wave that kept 32 heads to
 // itself for both products, reading and widening every key and value four times;
 // 128 us with eight equal waves that went through first product, softmax and
-// second product in turn, which left the younger wave of a SIMD waiting.)
+// second product in turn, which left the younger wave of a SIMD waiting; 110 us
+// so, of which 18 us are start and end. The 344 MB of rows alone take 86 us at
+// the rate of a large sum. In the loop the first waves' chain of products,
+// maximum, exponentials and p decides, about 2500 cycles a tile.)
 // Tiles: the first 640 bytes of each row as 16-byte pieces straight into LDS (no
 // registers), the scales transposed to [block][key]. Piece c of key j lies at
 // c ^ swizzle(j), which keeps the 16 lanes that a 16-byte read serves at once
@@ -143,20 +146,28 @@ struct QueryRaw {
   }
 };
 
-// The same as the operands of the first product.
+// The same as the operands of the first product: the latent channels, times a
+// power of two that puts the head's largest into [128, 256), as sums of e4m3
+// values, each the rounding of what the ones before leave. Two hold bf16's 8 bits
+// and three fp16's 11; what is left is below 2^-17 of the largest (e4m3 ends at
+// 2^-9). The rotary channels stay bf16, or a sum of two for fp16.
 template <typename Q8>
-struct QueryOperand;
-
-template <>
-struct QueryOperand<bf16x8> {
-  i32x8 hi[kLatentGroups], lo[kLatentGroups];   // e4m3 x 32: pieces 2 b and 2 b + 1
-  bf16x8 rope[kRope / 32];
-  float up;                                     // the power of two in hi and lo
-  __device__ __forceinline__ void take(const QueryRaw<bf16x8>& raw) {
+struct QueryOperand {
+  static constexpr bool kBf16 = std::is_same_v<Q8, bf16x8>;
+  static constexpr int kParts = kBf16 ? 2 : 3;
+  i32x8 part[kParts][kLatentGroups];            // e4m3 x 32: pieces 2 b and 2 b + 1
+  bf16x8 rope[kParts - 1][kRope / 32];
+  float up;                                     // the power of two in the parts
+  static __device__ __forceinline__ float value(uint32_t bits) {
+    if constexpr (kBf16) return __uint_as_float(bits << 16);
+    const uint16_t h = (uint16_t)bits;
+    return (float)__builtin_bit_cast(_Float16, h);
+  }
+  __device__ __forceinline__ void take(const QueryRaw<Q8>& raw) {
     vec4u x[kLatent / 32];
 #pragma unroll
     for (int t = 0; t < kLatent / 32; ++t) x[t] = __builtin_bit_cast(vec4u, raw.x[t]);
-    // The largest |q|, two values at a time: bf16 magnitudes are in the order of their bits.
+    // The largest |q|, two values at a time: magnitudes are in the order of their bits.
     u16x2 top2{};
 #pragma unroll
     for (int t = 0; t < kLatent / 32; ++t)
@@ -166,7 +177,7 @@ struct QueryOperand<bf16x8> {
         top2 = __builtin_elementwise_max(top2, __builtin_bit_cast(u16x2, mag));
       }
     uint32_t most = max((uint32_t)top2.x, (uint32_t)top2.y);
-    constexpr uint32_t kInf = 0x7F80u;
+    constexpr uint32_t kInf = kBf16 ? 0x7F80u : 0x7C00u;
     if (__any(most >= kInf)) {   // infinities, which are not e4m3 values, become NaN; the finite values set the scale
       most = 0u;
 #pragma unroll
@@ -182,37 +193,52 @@ struct QueryOperand<bf16x8> {
           x[t][w] = v;
         }
     }
-#pragma unroll
-    for (int j = 0; j < kRope / 32; ++j) rope[j] = raw.rope[j];
-    const float top = max_quads(__uint_as_float(most << 16));
-    // 2^s with top x 2^s in [128, 256); s within +-60, far beyond which q has no effect or overflows
-    const int s = top > 0.0f ? min(max(8 - __builtin_amdgcn_frexp_expf(top), -60), 60) : 0;
+    const float top = max_quads(value(most));
+    // s at most 60, so that rotary channels times 2^s stay finite beside vanishing latent ones
+    const int s = top > 0.0f ? min(8 - __builtin_amdgcn_frexp_expf(top), 60) : 0;
     up = ldexpf(1.0f, s);
 #pragma unroll
     for (int b = 0; b < kLatentGroups; ++b)
 #pragma unroll
       for (int w = 0; w < 8; ++w) {               // four values a word
-        float v[4], r[4];
+        float v[4];
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
           const uint32_t y = x[4 * b + w / 2][2 * (w % 2) + e / 2];
-          v[e] = __uint_as_float(y << 16) * up;
-          v[e + 1] = __uint_as_float(y & 0xFFFF0000u) * up;
+          v[e] = value(y & 0xFFFFu) * up;
+          v[e + 1] = value(y >> 16) * up;
         }
-        const uint32_t h = e4m3x4(v[0], v[1], v[2], v[3]);
-        const auto h0 = __builtin_amdgcn_cvt_pk_f32_fp8(h, false), h1 = __builtin_amdgcn_cvt_pk_f32_fp8(h, true);
-        r[0] = v[0] - h0[0];
-        r[1] = v[1] - h0[1];
-        r[2] = v[2] - h1[0];
-        r[3] = v[3] - h1[1];
-        hi[b][w] = (int)h;
-        lo[b][w] = (int)e4m3x4(r[0], r[1], r[2], r[3]);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+          const uint32_t h = e4m3x4(v[0], v[1], v[2], v[3]);
+          part[i][b][w] = (int)h;
+          if (i == kParts - 1) break;
+          const auto h0 = __builtin_amdgcn_cvt_pk_f32_fp8(h, false), h1 = __builtin_amdgcn_cvt_pk_f32_fp8(h, true);
+          v[0] -= h0[0];
+          v[1] -= h0[1];
+          v[2] -= h1[0];
+          v[3] -= h1[1];
+        }
       }
+#pragma unroll
+    for (int j = 0; j < kRope / 32; ++j) {
+      if constexpr (kBf16) {
+        rope[0][j] = raw.rope[j];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          rope[0][j][e] = (__bf16)(float)raw.rope[j][e];
+          rope[1][j][e] = (__bf16)((float)raw.rope[j][e] - (float)rope[0][j][e]);
+        }
+      }
+    }
   }
   __device__ __forceinline__ f32x4 rope_product(const bf16x8* kr) const {
     f32x4 s{};
 #pragma unroll
-    for (int j = 0; j < kRope / 32; ++j) s = mfma16(kr[j], rope[j], s);
+    for (int j = 0; j < kRope / 32; ++j)
+#pragma unroll
+      for (int i = 0; i < kParts - 1; ++i) s = mfma16(kr[j], rope[i][j], s);
     return s * up;
   }
   static __device__ __forceinline__ i32x8 join(const vec4u* k) {
@@ -221,43 +247,11 @@ struct QueryOperand<bf16x8> {
   // products of blocks b and b + 1, interleaved so that none waits for the one before it
   __device__ __forceinline__ void block_products(int b, const vec4u* k0, const vec4u* k1, f32x4& s0, f32x4& s1) const {
     const i32x8 x = join(k0), y = join(k1);
-    s0 = mfma16_e4m3(x, hi[b], f32x4{});
-    s1 = mfma16_e4m3(y, hi[b + 1], f32x4{});
-    s0 = mfma16_e4m3(x, lo[b], s0);
-    s1 = mfma16_e4m3(y, lo[b + 1], s1);
-  }
-};
-
-template <>
-struct QueryOperand<f16x8> {
-  f16x8 x[kLatent / 32];
-  bf16x8 rope_hi[kRope / 32], rope_lo[kRope / 32];   // fp16 as the sum of two bf16 values (8 + 8 bits hold its 11)
-  static constexpr float up = 1.0f;
-  __device__ __forceinline__ void take(const QueryRaw<f16x8>& raw) {
-#pragma unroll
-    for (int t = 0; t < kLatent / 32; ++t) x[t] = raw.x[t];
-#pragma unroll
-    for (int j = 0; j < kRope / 32; ++j)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        rope_hi[j][e] = (__bf16)(float)raw.rope[j][e];
-        rope_lo[j][e] = (__bf16)((float)raw.rope[j][e] - (float)rope_hi[j][e]);
-      }
-  }
-  __device__ __forceinline__ f32x4 rope_product(const bf16x8* kr) const {
-    f32x4 s{};
-#pragma unroll
-    for (int j = 0; j < kRope / 32; ++j) s = mfma16(kr[j], rope_lo[j], mfma16(kr[j], rope_hi[j], s));
-    return s;
-  }
-  __device__ __forceinline__ void block_products(int b, const vec4u* k0, const vec4u* k1, f32x4& s0, f32x4& s1) const {
     s0 = s1 = f32x4{};
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      s0 = mfma16(widen8<f16x8>(k0[j].x, k0[j].y), x[4 * b + 2 * j], s0);
-      s1 = mfma16(widen8<f16x8>(k1[j].x, k1[j].y), x[4 * b + 4 + 2 * j], s1);
-      s0 = mfma16(widen8<f16x8>(k0[j].z, k0[j].w), x[4 * b + 2 * j + 1], s0);
-      s1 = mfma16(widen8<f16x8>(k1[j].z, k1[j].w), x[4 * b + 4 + 2 * j + 1], s1);
+    for (int i = 0; i < kParts; ++i) {
+      s0 = mfma16_e4m3(x, part[i][b], s0);
+      s1 = mfma16_e4m3(y, part[i][b + 1], s1);
     }
   }
 };
