@@ -705,7 +705,7 @@ AttendPlan plan_attend_latent(int n_sets, int k, int heads) {
   double best_cost = 0;
   const int least = std::max(1, (k + kAttendKeys - 1) / kAttendKeys);
   for (int want = least; want <= std::max(least, std::min(tiles, kComputeUnits)); ++want) {
-    const int per = (tiles + want - 1) / want;            // tiles per split
+    const int per = std::max(1, (tiles + want - 1) / want);   // tiles per split
     const int splits = std::max(1, (tiles + per - 1) / per);
     if (splits != want && want != least) continue;        // the same split as a smaller one
     const double waves = (double)((base * splits + kComputeUnits - 1) / kComputeUnits);
@@ -715,7 +715,7 @@ AttendPlan plan_attend_latent(int n_sets, int k, int heads) {
     if (best.splits == 0 || cost < best_cost) {
       best_cost = cost;
       best.splits = splits;
-      best.split_keys = std::max(1, per) * kTileKeys;
+      best.split_keys = per * kTileKeys;
     }
   }
   return best;

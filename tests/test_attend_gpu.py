@@ -3,11 +3,18 @@
 Tolerance, from the arithmetic (no slack for anything else). With w the exact
 softmax weights, A = sum_j w_j |v_j| and u(t) half a step of type t (bf16 2^-8,
 fp16 2^-11, fp32 2^-24):
-  - each weight times value scale is rounded to bf16 once: u(bf16) A;
-  - logits are sums of at most 576 products (one rounding each in 32 bits, and
-    two for the scales): off by d = 580 u(fp32) R, R the largest sum of |q k|
-    |scale| of any logit, plus 2^-22 for the base-2 exponent and its function; a
-    logit's error changes every weight and their sum: 2 (d + 2^-22) A;
+  - each weight times value scale is rounded to fp16 once: u(fp16) A, and 2^-25 at
+    the bottom of its range. There the reference is such that the largest weight
+    times the largest value scale S is 2^6 or more in the units of the sums, so
+    n tokens' codes of at most 448 are off by n 448 S 2^-25 / 2^6;
+  - latent rows: q's channels, in parts of 4 bits, lose what is below 2^-17 of the
+    head's largest (only channels below 2^-6 of it have such bits): L, the sum of
+    that and |k| |scale|;
+  - logits are sums of at most 3 x 512 + 2 x 64 products of such parts (one
+    rounding each in 32 bits, and a few for the scales): off by
+    d = 1700 u(fp32) R + L, R the largest sum of |q k| |scale| of any logit, plus
+    2^-22 for the base-2 exponent and its function; a logit's error changes every
+    weight and their sum: 2 (d + 2^-22) A;
   - the sums over n tokens in 32 bits, numerator and denominator: 2 n u(fp32) A
     (n grows by 64 for the joins), and a handful of products: 8 u(fp32) A;
   - the result is rounded to its type once: u(type) |o| (2^-25 at the bottom of
@@ -68,6 +75,13 @@ def engine_of(rows, sets, k, **kw):
     return eng
 
 
+def value_scale(fmt, rows):
+    """The largest finite value scale of any row."""
+    at, n = (640, 4) if fmt.kind == 0 else (2 * fmt.kv_heads * fmt.head_dim * fmt.block_tokens + 4 * fmt.kv_heads, fmt.kv_heads)
+    x = np.abs(ref.f32_at(rows, at, n))
+    return np.where(np.isfinite(x), x, 0).max()
+
+
 def expected(fmt, rows, layer, sel, q, scale):
     """64-bit (out, lse, bound of out, bound of lse), without the rounding to the type."""
     outs = []
@@ -87,9 +101,14 @@ def expected(fmt, rows, layer, sel, q, scale):
         n = 0
         for at, keys, values in parts:
             o[at], lse[at], mag[at], reach = ref.attention(q[s, at], keys, values, scale)
-            dl[at] = 580 * U["fp32"] * reach + 2.0 ** -22
+            dl[at] = 1700 * U["fp32"] * reach + 2.0 ** -22
+            if fmt.kind == 0 and len(keys):
+                most = np.abs(q[s, at, :512]).max(-1, keepdims=True)
+                lost = np.where(np.abs(q[s, at, :512]) < most * 2.0 ** -6, most * 2.0 ** -17, 0)
+                dl[at] += (lost @ np.abs(keys[:, :512]).T).max(-1) * abs(scale)
             n = max(n, len(keys))
-        bound = mag * (U["bf16"] + 2 * dl[:, None] + (2 * (n + 64) + 8) * U["fp32"])
+        least = n * 448 * value_scale(fmt, rows[:, layer]) * 2.0 ** -31
+        bound = mag * (U["fp16"] + 2 * dl[:, None] + (2 * (n + 64) + 8) * U["fp32"]) + least
         outs.append((o, lse, bound, dl + (n + 70) * U["fp32"] + 4 * U["fp32"] * np.abs(np.where(np.isinf(lse), 0, lse))))
     return [np.stack(x) for x in zip(*outs)]
 
