@@ -13,11 +13,12 @@
 //   o_d  = sum_j p_j s_b(d)j k8_dj / l,   lse = (m + log2 l) ln 2
 // The block scales are applied in 32 bits, to the four partial products of S and
 // to p, so e4m3 codes enter the matrix instructions as they are:
-//   - first product: the 8-bit matrix instruction, with q as the sum of two (bf16)
-//     or three (fp16) e4m3 values, below. Two take as many cycles as one 16-bit
-//     product, and no key is widened in the vector units, which the softmax needs
-//     (384 sets of 2047 keys and 128 heads in fp16: 365 us with 16-bit products of
-//     widened keys, 328 us with three parts).
+//   - first product: codes widened to q's type, which holds them exactly. (The
+//     8-bit matrix instruction with q as a sum of e4m3 values widens nothing, and
+//     took 111 us where this took 132 us for 256 sets of 2048 keys and 64 heads.
+//     But it cuts the products of 16 channels off at 2^-13 of the largest of
+//     them before it adds them up: log-sums were off by up to 5e-4, this way by
+//     4e-6.)
 //   - second product: codes widened to fp16, and p s_b rounded to fp16. m follows
 //     the largest p_j max_b s_bj, which stays within 2^7..2^15, so the rounding is
 //     at most 2^-11 of the value, or 2^-25 (2^-32 of the largest) for small ones.
@@ -146,83 +147,19 @@ struct QueryRaw {
   }
 };
 
-// The same as the operands of the first product: the latent channels, times a
-// power of two that puts the head's largest into [128, 256), as sums of e4m3
-// values, each the rounding of what the ones before leave. Two hold bf16's 8 bits
-// and three fp16's 11; what is left is below 2^-17 of the largest (e4m3 ends at
-// 2^-9). The rotary channels stay bf16, or a sum of two for fp16.
+// The same as the operands of the first product. The keys' rotary channels are
+// bf16, so fp16 ones become the sum of two bf16 values (8 + 8 bits hold their 11).
 template <typename Q8>
 struct QueryOperand {
-  static constexpr bool kBf16 = std::is_same_v<Q8, bf16x8>;
-  static constexpr int kParts = kBf16 ? 2 : 3;
-  i32x8 part[kParts][kLatentGroups];            // e4m3 x 32: pieces 2 b and 2 b + 1
-  bf16x8 rope[kParts - 1][kRope / 32];
-  float up;                                     // the power of two in the parts
-  static __device__ __forceinline__ float value(uint32_t bits) {
-    if constexpr (kBf16) return __uint_as_float(bits << 16);
-    const uint16_t h = (uint16_t)bits;
-    return (float)__builtin_bit_cast(_Float16, h);
-  }
+  static constexpr int kRopeParts = std::is_same_v<Q8, bf16x8> ? 1 : 2;
+  Q8 x[kLatent / 32];
+  bf16x8 rope[kRopeParts][kRope / 32];
   __device__ __forceinline__ void take(const QueryRaw<Q8>& raw) {
-    vec4u x[kLatent / 32];
 #pragma unroll
-    for (int t = 0; t < kLatent / 32; ++t) x[t] = __builtin_bit_cast(vec4u, raw.x[t]);
-    // The largest |q|, two values at a time: magnitudes are in the order of their bits.
-    u16x2 top2{};
-#pragma unroll
-    for (int t = 0; t < kLatent / 32; ++t)
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t mag = x[t][w] & 0x7FFF7FFFu;
-        top2 = __builtin_elementwise_max(top2, __builtin_bit_cast(u16x2, mag));
-      }
-    uint32_t most = max((uint32_t)top2.x, (uint32_t)top2.y);
-    constexpr uint32_t kInf = kBf16 ? 0x7F80u : 0x7C00u;
-    if (__any(most >= kInf)) {   // infinities, which are not e4m3 values, become NaN; the finite values set the scale
-      most = 0u;
-#pragma unroll
-      for (int t = 0; t < kLatent / 32; ++t)
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t v = x[t][w];
-          const uint32_t first = v & 0x7FFFu, second = v >> 16 & 0x7FFFu;
-          if (first >= kInf) v |= 0x7FFFu;
-          else most = max(most, first);
-          if (second >= kInf) v |= 0x7FFF0000u;
-          else most = max(most, second);
-          x[t][w] = v;
-        }
-    }
-    const float top = max_quads(value(most));
-    // s at most 60, so that rotary channels times 2^s stay finite beside vanishing latent ones
-    const int s = top > 0.0f ? min(8 - __builtin_amdgcn_frexp_expf(top), 60) : 0;
-    up = ldexpf(1.0f, s);
-#pragma unroll
-    for (int b = 0; b < kLatentGroups; ++b)
-#pragma unroll
-      for (int w = 0; w < 8; ++w) {               // four values a word
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          const uint32_t y = x[4 * b + w / 2][2 * (w % 2) + e / 2];
-          v[e] = value(y & 0xFFFFu) * up;
-          v[e + 1] = value(y >> 16) * up;
-        }
-#pragma unroll
-        for (int i = 0; i < kParts; ++i) {
-          const uint32_t h = e4m3x4(v[0], v[1], v[2], v[3]);
-          part[i][b][w] = (int)h;
-          if (i == kParts - 1) break;
-          const auto h0 = __builtin_amdgcn_cvt_pk_f32_fp8(h, false), h1 = __builtin_amdgcn_cvt_pk_f32_fp8(h, true);
-          v[0] -= h0[0];
-          v[1] -= h0[1];
-          v[2] -= h1[0];
-          v[3] -= h1[1];
-        }
-      }
+    for (int t = 0; t < kLatent / 32; ++t) x[t] = raw.x[t];
 #pragma unroll
     for (int j = 0; j < kRope / 32; ++j) {
-      if constexpr (kBf16) {
+      if constexpr (kRopeParts == 1) {
         rope[0][j] = raw.rope[j];
       } else {
 #pragma unroll
@@ -238,20 +175,18 @@ struct QueryOperand {
 #pragma unroll
     for (int j = 0; j < kRope / 32; ++j)
 #pragma unroll
-      for (int i = 0; i < kParts - 1; ++i) s = mfma16(kr[j], rope[i][j], s);
-    return s * up;
-  }
-  static __device__ __forceinline__ i32x8 join(const vec4u* k) {
-    return i32x8{(int)k[0].x, (int)k[0].y, (int)k[0].z, (int)k[0].w, (int)k[1].x, (int)k[1].y, (int)k[1].z, (int)k[1].w};
+      for (int i = kRopeParts - 1; i >= 0; --i) s = mfma16(kr[j], rope[i][j], s);
+    return s;
   }
   // products of blocks b and b + 1, interleaved so that none waits for the one before it
   __device__ __forceinline__ void block_products(int b, const vec4u* k0, const vec4u* k1, f32x4& s0, f32x4& s1) const {
-    const i32x8 x = join(k0), y = join(k1);
     s0 = s1 = f32x4{};
 #pragma unroll
-    for (int i = 0; i < kParts; ++i) {
-      s0 = mfma16_e4m3(x, part[i][b], s0);
-      s1 = mfma16_e4m3(y, part[i][b + 1], s1);
+    for (int j = 0; j < 2; ++j) {
+      s0 = mfma16(widen8<Q8>(k0[j].x, k0[j].y), x[4 * b + 2 * j], s0);
+      s1 = mfma16(widen8<Q8>(k1[j].x, k1[j].y), x[4 * b + 4 + 2 * j], s1);
+      s0 = mfma16(widen8<Q8>(k0[j].z, k0[j].w), x[4 * b + 2 * j + 1], s0);
+      s1 = mfma16(widen8<Q8>(k1[j].z, k1[j].w), x[4 * b + 4 + 2 * j + 1], s1);
     }
   }
 };
@@ -468,7 +403,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
   } else if (wave * 16 < kHeads) {
     QueryOperand<Q8> q;
     q.take(raw);
-    const float c_log2 = a.scale_log2 / q.up;
+    const float c_log2 = a.scale_log2;
     // Register r of part u (0, 1) in quad x is key 8 x + 4 u + r. koff: this lane's
     // key of part 0, piece quad of a scale block. Piece 4 + quad is ^ 64; part 1's
     // key, four rows on, is ^ 64 (its swizzle) and + 4 rows.

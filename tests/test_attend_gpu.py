@@ -7,12 +7,9 @@ fp16 2^-11, fp32 2^-24):
     the bottom of its range. There the reference is such that the largest weight
     times the largest value scale S is 2^6 or more in the units of the sums, so
     n tokens' codes of at most 448 are off by n 448 S 2^-25 / 2^6;
-  - latent rows: q's channels, in parts of 4 bits, lose what is below 2^-17 of the
-    head's largest (only channels below 2^-6 of it have such bits): L, the sum of
-    that and |k| |scale|;
-  - logits are sums of at most 3 x 512 + 2 x 64 products of such parts (one
-    rounding each in 32 bits, and a few for the scales): off by
-    d = 1700 u(fp32) R + L, R the largest sum of |q k| |scale| of any logit, plus
+  - logits are sums of at most 512 + 2 x 64 products (one rounding each in 32 bits,
+    and a few for the scales; fp16's rotary channels are two bf16 values each):
+    off by d = 650 u(fp32) R, R the largest sum of |q k| |scale| of any logit, plus
     2^-22 for the base-2 exponent and its function; a logit's error changes every
     weight and their sum: 2 (d + 2^-22) A;
   - the sums over n tokens in 32 bits, numerator and denominator: 2 n u(fp32) A
@@ -101,11 +98,7 @@ def expected(fmt, rows, layer, sel, q, scale):
         n = 0
         for at, keys, values in parts:
             o[at], lse[at], mag[at], reach = ref.attention(q[s, at], keys, values, scale)
-            dl[at] = 1700 * U["fp32"] * reach + 2.0 ** -22
-            if fmt.kind == 0 and len(keys):
-                most = np.abs(q[s, at, :512]).max(-1, keepdims=True)
-                lost = np.where(np.abs(q[s, at, :512]) < most * 2.0 ** -6, most * 2.0 ** -17, 0)
-                dl[at] += (lost @ np.abs(keys[:, :512]).T).max(-1) * abs(scale)
+            dl[at] = 650 * U["fp32"] * reach + 2.0 ** -22
             n = max(n, len(keys))
         least = n * 448 * value_scale(fmt, rows[:, layer]) * 2.0 ** -31
         bound = mag * (U["fp16"] + 2 * dl[:, None] + (2 * (n + 64) + 8) * U["fp32"]) + least
