@@ -125,6 +125,7 @@ struct LatentLds {
   alignas(16) float scale[TILES][kLatentGroups][kTileKeys];
   float alpha[2][HEADS];                    // factor of O before the tile's second product
   alignas(16) uint32_t moved[2][4];         // whether any of 16 heads has a factor other than 1
+  alignas(8) float top[2][HEADS][2];        // of two tiles: the largest logarithm of p x scale, of either half of the keys
   const uint8_t* row[kAttendKeys];          // each key's row in this layer; zeros for padding
   uint32_t live[kAttendKeys / kTileKeys + 2];   // bit per key: not padding; none behind the last tile
   int ok;
@@ -178,16 +179,12 @@ struct QueryOperand {
       for (int i = kRopeParts - 1; i >= 0; --i) s = mfma16(kr[j], rope[i][j], s);
     return s;
   }
-  // products of blocks b and b + 1, interleaved so that none waits for the one before it
-  __device__ __forceinline__ void block_products(int b, const vec4u* k0, const vec4u* k1, f32x4& s0, f32x4& s1) const {
-    s0 = s1 = f32x4{};
+  // product of a block's keys, widened, 32 channels at a time
+  __device__ __forceinline__ f32x4 block_product(int b, const Q8* k) const {
+    f32x4 s{};
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      s0 = mfma16(widen8<Q8>(k0[j].x, k0[j].y), x[4 * b + 2 * j], s0);
-      s1 = mfma16(widen8<Q8>(k1[j].x, k1[j].y), x[4 * b + 4 + 2 * j], s1);
-      s0 = mfma16(widen8<Q8>(k0[j].z, k0[j].w), x[4 * b + 2 * j + 1], s0);
-      s1 = mfma16(widen8<Q8>(k1[j].z, k1[j].w), x[4 * b + 4 + 2 * j + 1], s1);
-    }
+    for (int j = 0; j < kScaleGroup / 32; ++j) s = mfma16(k[j], x[4 * b + j], s);
+    return s;
   }
 };
 
@@ -261,18 +258,16 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
   const int nkeys = max(0, min(a.split_keys, a.k - key0));
   const int tiles = (nkeys + kTileKeys - 1) / kTileKeys;
 
-  // The second waves look the keys' rows up and start their loads; the first waves'
-  // q, which takes longer to arrive and to convert, is on its way meanwhile.
-  QueryRaw<Q8> raw;
-  if (!second) {
-    const ReaderState state = reader_state(g);
-    const int head = hb * kHeads + wave * 16 + col;
-    const bool any = wave * 16 < kHeads && head < a.heads;
-    const uint16_t* p = static_cast<const uint16_t*>(a.q) + set * a.q_set_stride + head * a.q_head_stride;
-    if (a.q_aligned) raw.template load<true>(p, any, quad);
-    else raw.template load<false>(p, any, quad);
-    if (threadIdx.x == 0) s.ok = reader_ready(g, state, a.want_flag);
-  } else {
+  const int head32 = wave / 2 * 32;               // a first wave's 32 heads, and its half of the keys
+  const int key_half = wave % 2;
+  f32x16 o[CT][HT];                               // a second wave's alone: unset in the others, whose registers it would fill
+  float m[2], l[2];                               // of a first wave's 2 x 16 heads; l of the lane's keys alone
+
+  // Barriers: one when the rows are known, one when tile 0 is in LDS, then one per tile i = -1, 0, ..: tile
+  // i + 2 is in LDS, p of tile i is there, and nobody reads tile i - 1 any more.
+  if (second) {
+    // The second waves look the keys' rows up and start their loads; the first waves'
+    // q, which takes longer to arrive, is on its way meanwhile.
     int err = 0;
     const uint8_t* pool = g.pool + (size_t)a.layer * g.row_bytes;
     constexpr int kAtOnce = 4;                    // lookups in flight per lane
@@ -296,20 +291,8 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
       }
     }
     if (err) latch_gather(g.ctr, err);
-  }
-  barrier_keep_loads();
-  if (!s.ok) return;
-  // Tiles behind the last one are computed on whatever lies in their place and
-  // masked, so that the main loop has no branches. (Read two barriers later.)
-  if (threadIdx.x < 2) s.live[tiles + threadIdx.x] = 0;
-  if (threadIdx.x < 8) s.moved[threadIdx.x / 4][threadIdx.x % 4] = 0;   // groups without a first wave never move
-
-  f32x16 o[CT][HT];                               // a second wave's alone: unset in the others, whose registers it would fill
-  float m = -__builtin_inff(), l = 0.0f;          // of a first wave's 16 heads; l of the lane's keys alone
-
-  // Barriers: one when tile 0 is in LDS, then one per tile i = -1, 0, ..: tile
-  // i + 2 is in LDS, p of tile i is there, and nobody reads tile i - 1 any more.
-  if (second) {
+    barrier_keep_loads();
+    if (!s.ok) return;
     // This wave's six loads of a tile: five of pieces, one of a scale block. The
     // rows' addresses are read from LDS one tile earlier.
     const int sw = wave - kFirstWaves;
@@ -400,122 +383,146 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
         }
       read_rows(tile + TILES);
     }
-  } else if (wave * 16 < kHeads) {
-    QueryOperand<Q8> q;
-    q.take(raw);
-    const float c_log2 = a.scale_log2;
-    // Register r of part u (0, 1) in quad x is key 8 x + 4 u + r. koff: this lane's
-    // key of part 0, piece quad of a scale block. Piece 4 + quad is ^ 64; part 1's
-    // key, four rows on, is ^ 64 (its swizzle) and + 4 rows.
-    const int key = 8 * (col / 4) + col % 4;
-    const int koff = key * kLatentScaleAt + ((quad ^ swizzle(key)) << 4);
-    const int head = wave * 16 + col;
-    const uint32_t pwrite = lds_address(s.p) + head * kTileKeys * 2 + ((quad ^ ((head >> 2) & 3)) << 4);
-    f32x4 part[2][kLatentGroups], rope[2];        // of the tile after the one in the softmax
-    // first product of a tile in LDS, two blocks' keys at a time
-    auto products = [&](int tile) {
-      const uint32_t krow = opaque(lds_address(s.ring) + tile % TILES * kTileBytes + koff);
-      const uint32_t krow64 = opaque(krow ^ 64);
-      auto kpiece = [&](int u, int t) { return (t != u ? krow64 : krow) + u * 4 * kLatentScaleAt; };
+  } else {
+    QueryRaw<Q8> raw[2];
+    const ReaderState state = reader_state(g);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        bf16x8 kr[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) kr[j] = lds_get<bf16x8>(kpiece(u, j) + kRopeAt);
-        rope[u] = q.rope_product(kr);
-      }
-#pragma unroll
-      for (int b = 0; b < kLatentGroups; b += 2)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          vec4u k[2][2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) k[i][t] = lds_get<vec4u>(kpiece(u, t) + (b + i) * kScaleGroup);
-          q.block_products(b, k[0], k[1], part[u][b], part[u][b + 1]);
-        }
-    };
+    for (int i = 0; i < 2; ++i) {
+      const int head = hb * kHeads + head32 + 16 * i + col;
+      const bool any = head32 < kHeads && head < a.heads;
+      const uint16_t* p = static_cast<const uint16_t*>(a.q) + set * a.q_set_stride + head * a.q_head_stride;
+      if (a.q_aligned) raw[i].template load<true>(p, any, quad);
+      else raw[i].template load<false>(p, any, quad);
+    }
+    if (threadIdx.x == 0) s.ok = reader_ready(g, state, a.want_flag);
     barrier_keep_loads();
-    products(0);
-#pragma unroll 1
-    for (int tile = 0; tile <= tiles; ++tile) {   // softmax of `tile`, products of the next one
-      barrier_keep_loads();
-      const int buf = tile & 1;
-      const uint32_t scale = opaque(lds_address(s.scale) + (tile % TILES * kLatentGroups * kTileKeys + 8 * quad) * 4);
-      f32x4 sc[2][kLatentGroups], S[2];
+    if (!s.ok) return;
+    // Tiles behind the last one are computed on whatever lies in their place and
+    // masked, so that the main loop has no branches. (Read a barrier later or more.)
+    if (threadIdx.x < 2) s.live[tiles + threadIdx.x] = 0;
+    if (threadIdx.x < 8) s.moved[threadIdx.x / 4][threadIdx.x % 4] = 0;   // groups without a first wave never move
+    if (head32 < kHeads) {
+      QueryOperand<Q8> q[2];
 #pragma unroll
-      for (int b = 0; b < kLatentGroups; ++b)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) sc[u][b] = lds_get<f32x4>(scale + (kTileKeys * b + 4 * u) * 4);
-      const uint32_t live = __builtin_amdgcn_readfirstlane(s.live[tile]) >> (8 * quad);
-      float big = 0x1p-60f;                       // largest scale of the lane's keys
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        S[u] = rope[u];
+      for (int i = 0; i < 2; ++i) {
+        q[i].take(raw[i]);
+        m[i] = -__builtin_inff();
+        l[i] = 0.0f;
+      }
+      const float c_log2 = a.scale_log2;
+      // Register r in quad x is key 8 x + 4 key_half + r. koff: this lane's key as an
+      // operand, piece quad of a scale block; piece 4 + quad is ^ 64.
+      const int key = 8 * (col / 4) + 4 * key_half + col % 4;
+      const int koff = key * kLatentScaleAt + ((quad ^ swizzle(key)) << 4);
+      const int head = head32 + col;
+      const uint32_t pwrite = lds_address(s.p) + head * kTileKeys * 2 + ((quad ^ ((head >> 2) & 3)) << 4) + 8 * key_half;
+      const uint32_t at_top = lds_address(s.top) + head * 8;
+      f32x4 sc[kLatentGroups], S[2];                // of the next tile for the softmax: scales, logits in powers of two
+      // First product of a tile in LDS; the largest logarithm of p x scale of each
+      // head, over this half of the keys, goes to the wave with the other half.
+      auto logits = [&](int tile) {
+        const uint32_t krow = opaque(lds_address(s.ring) + tile % TILES * kTileBytes + koff);
+        const uint32_t krow64 = opaque(krow ^ 64);
+        const uint32_t scale = opaque(lds_address(s.scale) + (tile % TILES * kLatentGroups * kTileKeys + 8 * quad + 4 * key_half) * 4);
+        bf16x8 kr[2] = {lds_get<bf16x8>(krow + kRopeAt), lds_get<bf16x8>(krow64 + kRopeAt)};
+        const uint32_t live = __builtin_amdgcn_readfirstlane(s.live[tile]) >> (8 * quad + 4 * key_half);
+        f32x4 part[2][kLatentGroups], rope[2];
 #pragma unroll
         for (int b = 0; b < kLatentGroups; ++b) {
-          S[u] += sc[u][b] * part[u][b];
+          sc[b] = lds_get<f32x4>(scale + kTileKeys * b * 4);
+          const vec4u k0 = lds_get<vec4u>(krow + b * kScaleGroup), k1 = lds_get<vec4u>(krow64 + b * kScaleGroup);
+          const Q8 k[4] = {widen8<Q8>(k0.x, k0.y), widen8<Q8>(k0.z, k0.w), widen8<Q8>(k1.x, k1.y), widen8<Q8>(k1.z, k1.w)};
 #pragma unroll
-          for (int r = 0; r < 4; ++r) big = fmaxf(big, fabsf(sc[u][b][r]));
+          for (int i = 0; i < 2; ++i) part[i][b] = q[i].block_product(b, k);
         }
-      }
-      products(tile + 1);
-      float top = -__builtin_inff();
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+        for (int i = 0; i < 2; ++i) rope[i] = q[i].rope_product(kr);
+        float big = 0x1p-60f;                       // largest scale of the lane's keys
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          S[u][r] = live & (1u << (4 * u + r)) ? S[u][r] * c_log2 : -__builtin_inff();
-          top = fmaxf(top, S[u][r]);
+        for (int b = 0; b < kLatentGroups; ++b)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) big = fmaxf(big, fabsf(sc[b][r]));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          S[i] = rope[i];
+#pragma unroll
+          for (int b = 0; b < kLatentGroups; ++b) S[i] += sc[b] * part[i][b];
+          float top = -__builtin_inff();
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            S[i][r] = live & (1u << r) ? S[i][r] * c_log2 : -__builtin_inff();
+            top = fmaxf(top, S[i][r]);
+          }
+          top = max_quads(top + (float)__builtin_amdgcn_frexp_expf(big));
+          if (quad == 0) lds_put(at_top + (tile & 1) * kHeads * 8 + 16 * i * 8 + 4 * key_half, top);
         }
-      top = max_quads(top + (float)__builtin_amdgcn_frexp_expf(big));
-      const bool move = top > m + 15.0f;
-      const float nm = move ? top - 8.0f : m;
-      const float al = move ? __builtin_amdgcn_exp2f(m - nm) : 1.0f;
-      m = nm;
-      l *= al;
-      const float base = nm == -__builtin_inff() ? 0.0f : nm;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          S[u][r] = __builtin_amdgcn_exp2f(S[u][r] - base);
-          l += S[u][r];
-        }
-      const uint32_t pw = opaque(pwrite + buf * kLatentGroups * kHeads * kTileKeys * 2);
-#pragma unroll
-      for (int b = 0; b < kLatentGroups; ++b) {
-        f16x8 w;
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) w[4 * u + r] = (_Float16)(S[u][r] * sc[u][b][r]);
-        lds_put(pw + b * kHeads * kTileKeys * 2, w);
-      }
-      const bool moved = __any(move);
-      if (quad == 0) s.alpha[buf][head] = al;
-      if (lane == 0) s.moved[buf][wave] = moved;
-    }
-    l = sum_quads(l);
-  } else {
-    barrier_keep_loads();
+      };
+      barrier_keep_loads();
+      logits(0);
 #pragma unroll 1
-    for (int tile = 0; tile <= tiles; ++tile) barrier_keep_loads();
+      for (int tile = 0; tile <= tiles; ++tile) {   // softmax of `tile`, logits of the next one
+        barrier_keep_loads();
+        const int buf = tile & 1;
+        bool moved = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          // both halves' waves come to the same reference
+          typedef float f32x2 __attribute__((ext_vector_type(2)));
+          const f32x2 both = lds_get<f32x2>(at_top + buf * kHeads * 8 + 16 * i * 8);
+          const float top = fmaxf(both.x, both.y);
+          const bool move = top > m[i] + 15.0f;
+          const float nm = move ? top - 8.0f : m[i];
+          const float al = move ? __builtin_amdgcn_exp2f(m[i] - nm) : 1.0f;
+          m[i] = nm;
+          l[i] *= al;
+          const float base = nm == -__builtin_inff() ? 0.0f : nm;
+          float p[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            p[r] = __builtin_amdgcn_exp2f(S[i][r] - base);
+            l[i] += p[r];
+          }
+          const uint32_t pw = opaque(pwrite + (buf * kLatentGroups * kHeads + 16 * i) * kTileKeys * 2);
+#pragma unroll
+          for (int b = 0; b < kLatentGroups; ++b) {
+            typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+            f16x4 w;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) w[r] = (_Float16)(p[r] * sc[b][r]);
+            lds_put(pw + b * kHeads * kTileKeys * 2, w);
+          }
+          moved |= move;
+          if (quad == 0 && key_half == 0) s.alpha[buf][head + 16 * i] = al;
+        }
+        moved = __any(moved);
+        if (lane == 0 && key_half == 0) s.moved[buf][wave] = moved;
+        logits(tile + 1);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) l[i] = sum_quads(l[i]);
+    } else {
+      barrier_keep_loads();
+#pragma unroll 1
+      for (int tile = 0; tile <= tiles; ++tile) barrier_keep_loads();
+    }
   }
 
   // every second wave needs every head's l and m
   float* ml = reinterpret_cast<float*>(s.p);
   barrier_keep_loads();
-  if (!second && wave * 16 < kHeads && quad == 0) {
-    ml[wave * 16 + col] = m;
-    ml[kHeads + wave * 16 + col] = l;
+  if (!second && head32 < kHeads && quad == 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int head = head32 + 16 * i + col;
+      ml[head] = m[i];
+      ml[(1 + key_half) * kHeads + head] = l[i];
+    }
   }
   barrier_keep_loads();
   float inv[HT];
 #pragma unroll
   for (int h = 0; h < HT; ++h) {
-    const float lh = ml[kHeads + 32 * h + col32];
+    const float lh = ml[kHeads + 32 * h + col32] + ml[2 * kHeads + 32 * h + col32];
     inv[h] = lh != 0.0f ? 1.0f / lh : 0.0f;
     const int head = hb * kHeads + 32 * h + col32;
     if (wave == 0 && half == 0 && head < a.heads) {
