@@ -326,8 +326,9 @@ int ula_append_step(ula_ctx* ctx, int32_t group, int32_t n_app, const int32_t* l
  * ordering after the gather: the library makes the next launch that moves rows
  * out of GPU slots wait for it (see Threading). A gather that runs while the
  * group's next step fails on the device may find that step's error and write
- * nothing (ula_sync reports the error); a gather of an address appended only
- * after its step is an error, or undefined if that append runs beside it.
+ * nothing (ula_sync reports the error); an address appended, forked or renamed
+ * only after the step resolves through the mapping table (an error if the entry is
+ * not on the GPU), and is undefined if that call runs beside the gather.
  * Host errors: ULA_EINVAL, ULA_ESTATE, ULA_ENOTRESIDENT (no step yet).
  * Device errors (reported by ula_sync): ULA_ENOTRESIDENT (counter not reached,
  * or an entry not on the GPU), ULA_ERANGE. */
@@ -418,7 +419,8 @@ typedef struct {
  * channels are turned in 32 bits and rounded to bf16 once. A pure function of its
  * device inputs: nothing of an engine is involved, and it may be captured into a
  * graph. Errors: ULA_EINVAL (null pointer, n or layers < 0, unknown type, invalid
- * format or rotary, misaligned pointers), ULA_EHIP. */
+ * format or rotary, misaligned pointers, 2^26 rows or more, each counted twice per
+ * KV head for heads rows), ULA_EHIP. */
 int ula_pack_rows(const ula_pack_args* args, void* rows_dev, uint64_t stream);
 
 typedef struct {
@@ -435,7 +437,8 @@ typedef struct {
 
 /* Turn the heads of n tokens (the rotary part of queries, or its way back) by
  * their positions; each result is rounded to its type once. A pure function of
- * its device inputs; it may be captured into a graph. Errors: ULA_EINVAL, ULA_EHIP. */
+ * its device inputs; it may be captured into a graph. Errors: ULA_EINVAL (also
+ * n * heads >= 2^25), ULA_EHIP. */
 int ula_rotate(const ula_rotate_args* args, uint64_t stream);
 
 typedef struct {
@@ -467,9 +470,10 @@ size_t ula_attend_bytes(const ula_row_format* rows, int32_t n_sets, int32_t k, i
  * rows). -1 entries contribute nothing; a set with nothing else gives out = 0
  * and lse = -inf. An address listed more than once counts as often. Sums, the
  * softmax and the products' accumulators are in 32 bits; keys enter exactly,
- * softmax weights times value scales are rounded to bf16 before the second
- * product, results once to the type of out. A NaN or an infinite logit makes that
- * head's outputs NaN; no unselected row is ever read. The order of the sums
+ * softmax weights times value scales are rounded to fp16 before the second
+ * product (2^-11 of each, or 2^-32 of the set's largest), results once to the type
+ * of out. A NaN or an infinite logit makes that head's outputs NaN; no unselected
+ * row is ever read. The order of the sums
  * depends on the sizes alone, so the same call gives the same bits.
  * Results split over several workgroups are joined through the workspace, which
  * belongs to the call until the stream has run it: calls that may run at the
@@ -481,9 +485,10 @@ size_t ula_attend_bytes(const ula_row_format* rows, int32_t n_sets, int32_t k, i
  * mapping table; on another stream the call must be ordered after the step; the
  * library orders the group's later row moves after it). It may not be captured
  * into a graph, since the step it belongs to is fixed at the call: ULA_EINVAL.
- * Host errors: ULA_EINVAL, ULA_ESTATE, ULA_ENOTRESIDENT (no step yet), ULA_EHIP.
- * Device errors (reported by ula_sync): ULA_ENOTRESIDENT, ULA_ERANGE; an entry
- * with such an error counts as padding. */
+ * Host errors: ULA_EINVAL (also n_sets * heads >= 2^24, heads > 2^16, latent rows
+ * with k > 2^21, heads rows with k * block_tokens >= 2^30), ULA_ESTATE,
+ * ULA_ENOTRESIDENT (no step yet), ULA_EHIP. Device errors (reported by ula_sync):
+ * ULA_ENOTRESIDENT, ULA_ERANGE; an entry with such an error counts as padding. */
 int ula_attend(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32_t k,
                const int32_t* sel_dev, const ula_attend_args* args, uint64_t stream);
 

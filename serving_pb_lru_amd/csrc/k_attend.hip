@@ -15,7 +15,7 @@
 // to p, so e4m3 codes enter the matrix instructions as they are:
 //   - first product: codes widened to q's type, which holds them exactly. (The
 //     8-bit matrix instruction with q as a sum of e4m3 values widens nothing, and
-//     took 111 us where this took 132 us for 256 sets of 2048 keys and 64 heads.
+//     took 111 us where this takes 113 us for 256 sets of 2048 keys and 64 heads.
 //     But it cuts the products of 16 channels off at 2^-13 of the largest of
 //     them before it adds them up: log-sums were off by up to 5e-4, this way by
 //     4e-6.)
@@ -26,21 +26,23 @@
 //
 // Layout. Both products are taken transposed: S^T = K Q^T puts heads in the
 // lanes' columns and keys in registers, O^T = V^T P^T the same way. A workgroup
-// has four waves for the first product and the softmax, 16 heads each, and four
-// for the second product, 128 channels of O (one scale block) with all heads
-// each: so no wave holds another's Q, every key is read from LDS by the waves of
-// different heads and every value once. In between p goes through LDS, scaled for
-// each block and in the operand order of the second product. Each SIMD has a wave
-// of either kind, whose matrix and vector work overlap; a wave of the first kind
-// issues the products of one tile under the softmax of the tile before.
-// One barrier per tile of 32 keys.
-// (256 sets of 2048 keys and 64 heads: 206 us with a wave that kept 32 heads to
-// itself for both products, reading and widening every key and value four times;
-// 128 us with eight equal waves that went through first product, softmax and
-// second product in turn, which left the younger wave of a SIMD waiting; 110 us
-// so, of which 18 us are start and end. The 344 MB of rows alone take 86 us at
-// the rate of a large sum. In the loop the first waves' chain of products,
-// maximum, exponentials and p decides, about 2500 cycles a tile.)
+// has four waves for the first product and the softmax, 32 heads and half of a
+// tile's 32 keys each, and four for the second product, 128 channels of O (one
+// scale block) with all heads each: so no wave holds another's Q, a key is
+// widened for 32 heads at once and every value once. In between p goes through
+// LDS, scaled for each block and in the operand order of the second product. The
+// two waves of a head tell each other their largest logits through LDS as well,
+// a barrier ahead of the softmax, and so come to the same m. Each SIMD has a wave
+// of either kind, whose matrix and vector work overlap. One barrier per tile.
+// Measured, 256 sets of 2048 keys and 64 heads: 206 us with a wave that kept 32
+// heads to itself for both products, reading and widening every key and value
+// four times; 128 us with eight equal waves that went through first product,
+// softmax and second product in turn, which left the younger wave of a SIMD
+// waiting; 132 us with 16 heads and a whole tile's keys per first wave; 113 us so.
+// Of that 18 us are start and end, and the 344 MB of rows alone take 86 us at the
+// rate of a large sum. In the loop the first waves' chain of products, maximum,
+// exponentials and p decides, about 2500 cycles a tile; issuing a tile's products
+// ahead of the softmax before it does not shorten it (116 us).
 // Tiles: the first 640 bytes of each row as 16-byte pieces straight into LDS (no
 // registers), the scales transposed to [block][key]. Piece c of key j lies at
 // c ^ swizzle(j), which keeps the 16 lanes that a 16-byte read serves at once

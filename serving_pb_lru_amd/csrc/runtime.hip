@@ -877,6 +877,10 @@ int ula_rename(ula_ctx* ctx, int32_t group, int32_t src, int32_t dst, int32_t n,
     const int rc = refuse_capture(s);
     if (rc) return rc;
   }
+  {   // gathers that look entries up in the mapping table: before it changes
+    const int rc = wait_gathers(gh, s);
+    if (rc) return rc;
+  }
   // chunks in memmove's order: a chunk's destinations are never sources of a later one
   const int32_t most = (int32_t)std::min<int64_t>(ctx->dims.maxApp, n);
   const int32_t chunks = (n + most - 1) / most;
