@@ -10,7 +10,10 @@
 // rounded to fp16 (at most 2^-11 of its value). m follows the largest p vs, not
 // the largest p, so that fp16's range serves whatever the scales are: the
 // largest p vs lies between 2^7 and 2^15, and one below fp16's least value (its
-// rounding: 2^-25) is off by less than 2^-32 of it.
+// rounding: 2^-25) is off by less than 2^-32 of it. For fp16 results, which show
+// that rounding (their own is as large), what it leaves goes through a second
+// product: off by 2.1e-4 of their size instead of 3.4e-4, 21 -> 22 us for 64 sets x
+// 500 blocks of 8 tokens x 2 KV heads of 64.
 //
 // Bound by HBM: 2 x heads / kv_heads operations per byte. So a wave works by
 // itself, on one KV head's up to 16 query heads and one range of tokens, with
@@ -33,6 +36,7 @@ constexpr int kHeadsPerWave = 16;
 
 template <typename Q8, int D>
 __global__ __launch_bounds__(kHeadWaves * kWave) void k_attend_heads(GroupDev g, AttendDev a, int n_items) {
+  constexpr bool kRest = !__is_same(Q8, bf16x8);   // see above: p vs in two parts
   constexpr int kPieces = D / 16;              // 16-byte pieces of a token's key or value
   constexpr int kKeyLoads = D / 64;            // pieces of its key a lane holds (a quarter)
   constexpr int kValLoads = kTok * kPieces / kWave;
@@ -193,19 +197,23 @@ __global__ __launch_bounds__(kHeadWaves * kWave) void k_attend_heads(GroupDev g,
       for (int t = 0; t < D / 16; ++t) o[t] *= al;
     }
     const float base = m == -__builtin_inff() ? 0.0f : m;
-    f16x8 p;
+    f16x8 p, rest;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float w = __builtin_amdgcn_exp2f(S[u][r] - base);
         l += w;
-        p[4 * u + r] = (_Float16)(w * sv[u][r]);
+        const float x = w * sv[u][r];
+        p[4 * u + r] = (_Float16)x;
+        if constexpr (kRest) rest[4 * u + r] = (_Float16)(x - (float)p[4 * u + r]);
       }
 #pragma unroll
     for (int t = 0; t < D / 16; ++t) {
       const i32x2 v8 = lds_read_transposed(vrow ^ (t << 4));
-      o[t] = mfma16(widen8<f16x8>((uint32_t)v8.x, (uint32_t)v8.y), p, o[t]);
+      const f16x8 v = widen8<f16x8>((uint32_t)v8.x, (uint32_t)v8.y);
+      o[t] = mfma16(v, p, o[t]);
+      if constexpr (kRest) o[t] = mfma16(v, rest, o[t]);
     }
   }
   if (err) latch_gather(g.ctr, err);
@@ -231,6 +239,11 @@ __global__ __launch_bounds__(kHeadWaves * kWave) void k_attend_heads(GroupDev g,
 
 // Splits so that about kWaveTarget waves run (8 per compute unit), each with at
 // least kLeastTiles tiles: a split costs its start and the join's traffic.
+// Measured, kernel + join, us, for 16 sets x 2048 tokens x 8 KV heads of 128 (70 MB)
+// and 64 sets x 500 blocks of 8 tokens x 2 KV heads of 64 (65 MB):
+//   1024 waves 24 + 4 and 28 + 4;  2048 waves 21 + 4 and 21 + 5;  4096 the same;
+//   2048 waves of at least 8 tiles 25 + 4 and 22 + 5, of at least 2 as of 4.
+// The rows alone take 17 us and 16 us at the rate of a large sum.
 AttendPlan plan_attend_heads(int n_sets, int tokens, int heads, int kv_heads) {
   constexpr int kWaveTarget = 256 * 8, kLeastTiles = 4;
   AttendPlan p{};
