@@ -26,10 +26,10 @@
 //
 // Layout. Both products are taken transposed: S^T = K Q^T puts heads in the
 // lanes' columns and keys in registers, O^T = V^T P^T the same way. A workgroup
-// has four waves for the first product and the softmax, 32 heads and half of a
-// tile's 32 keys each, and four for the second product, 128 channels of O (one
+// has four waves for the first product and the softmax, half of its heads (16 or
+// 32) and half of a tile's 32 keys each, and four for the second product, 128 channels of O (one
 // scale block) with all heads each: so no wave holds another's Q, a key is
-// widened for 32 heads at once and every value once. In between p goes through
+// widened for all of a wave's heads at once and every value once. In between p goes through
 // LDS, scaled for each block and in the operand order of the second product. The
 // two waves of a head tell each other their largest logits through LDS as well,
 // a barrier ahead of the softmax, and so come to the same m. Each SIMD has a wave
@@ -235,7 +235,7 @@ template <typename Q8, int HT, int TILES>
 __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g, AttendDev a) {
   constexpr int kHeads = 32 * HT;                 // heads of a workgroup
   constexpr int CT = kScaleGroup / 32;            // 32-channel tiles of a second wave's O
-  static_assert(kHeads <= 16 * kFirstWaves, "every head has a wave in the first product");
+  static_assert(2 * kHeads == 16 * HT * kFirstWaves, "every head has two waves in the first product");
   static_assert(TILES >= 4, "a tile on its way beside the three in use");
   __shared__ LatentLds<kHeads, TILES> s;
   static_assert(sizeof(s) <= 160 * 1024, "LDS of a compute unit");
@@ -260,10 +260,10 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
   const int nkeys = max(0, min(a.split_keys, a.k - key0));
   const int tiles = (nkeys + kTileKeys - 1) / kTileKeys;
 
-  const int head32 = wave / 2 * 32;               // a first wave's 32 heads, and its half of the keys
+  const int head0 = wave / 2 * 16 * HT;           // the first of a first wave's HT x 16 heads, and its half of the keys
   const int key_half = wave % 2;
   f32x16 o[CT][HT];                               // a second wave's alone: unset in the others, whose registers it would fill
-  float m[2], l[2];                               // of a first wave's 2 x 16 heads; l of the lane's keys alone
+  float m[HT], l[HT];                             // of a first wave's heads; l of the lane's keys alone
 
   // Barriers: one when the rows are known, one when tile 0 is in LDS, then one per tile i = -1, 0, ..: tile
   // i + 2 is in LDS, p of tile i is there, and nobody reads tile i - 1 any more.
@@ -386,12 +386,12 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
       read_rows(tile + TILES);
     }
   } else {
-    QueryRaw<Q8> raw[2];
+    QueryRaw<Q8> raw[HT];
     const ReaderState state = reader_state(g);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int head = hb * kHeads + head32 + 16 * i + col;
-      const bool any = head32 < kHeads && head < a.heads;
+    for (int i = 0; i < HT; ++i) {
+      const int head = hb * kHeads + head0 + 16 * i + col;
+      const bool any = head < a.heads;
       const uint16_t* p = static_cast<const uint16_t*>(a.q) + set * a.q_set_stride + head * a.q_head_stride;
       if (a.q_aligned) raw[i].template load<true>(p, any, quad);
       else raw[i].template load<false>(p, any, quad);
@@ -402,120 +402,114 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
     // Tiles behind the last one are computed on whatever lies in their place and
     // masked, so that the main loop has no branches. (Read a barrier later or more.)
     if (threadIdx.x < 2) s.live[tiles + threadIdx.x] = 0;
-    if (threadIdx.x < 8) s.moved[threadIdx.x / 4][threadIdx.x % 4] = 0;   // groups without a first wave never move
-    if (head32 < kHeads) {
-      QueryOperand<Q8> q[2];
+    if (threadIdx.x < 8) s.moved[threadIdx.x / 4][threadIdx.x % 4] = 0;   // one wave of two writes its heads'
+    QueryOperand<Q8> q[HT];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        q[i].take(raw[i]);
-        m[i] = -__builtin_inff();
-        l[i] = 0.0f;
+    for (int i = 0; i < HT; ++i) {
+      q[i].take(raw[i]);
+      m[i] = -__builtin_inff();
+      l[i] = 0.0f;
+    }
+    const float c_log2 = a.scale_log2;
+    // Register r in quad x is key 8 x + 4 key_half + r. koff: this lane's key as an
+    // operand, piece quad of a scale block; piece 4 + quad is ^ 64.
+    const int key = 8 * (col / 4) + 4 * key_half + col % 4;
+    const int koff = key * kLatentScaleAt + ((quad ^ swizzle(key)) << 4);
+    const int head = head0 + col;
+    const uint32_t pwrite = lds_address(s.p) + head * kTileKeys * 2 + ((quad ^ ((head >> 2) & 3)) << 4) + 8 * key_half;
+    const uint32_t at_top = lds_address(s.top) + head * 8;
+    f32x4 sc[kLatentGroups], S[HT];                // of the next tile for the softmax: scales, logits in powers of two
+    // First product of a tile in LDS; the largest logarithm of p x scale of each
+    // head, over this half of the keys, goes to the wave with the other half.
+    auto logits = [&](int tile) {
+      const uint32_t krow = opaque(lds_address(s.ring) + tile % TILES * kTileBytes + koff);
+      const uint32_t krow64 = opaque(krow ^ 64);
+      const uint32_t scale = opaque(lds_address(s.scale) + (tile % TILES * kLatentGroups * kTileKeys + 8 * quad + 4 * key_half) * 4);
+      bf16x8 kr[2] = {lds_get<bf16x8>(krow + kRopeAt), lds_get<bf16x8>(krow64 + kRopeAt)};
+      const uint32_t live = __builtin_amdgcn_readfirstlane(s.live[tile]) >> (8 * quad + 4 * key_half);
+      f32x4 part[HT][kLatentGroups], rope[HT];
+#pragma unroll
+      for (int b = 0; b < kLatentGroups; ++b) {
+        sc[b] = lds_get<f32x4>(scale + kTileKeys * b * 4);
+        const vec4u k0 = lds_get<vec4u>(krow + b * kScaleGroup), k1 = lds_get<vec4u>(krow64 + b * kScaleGroup);
+        const Q8 k[4] = {widen8<Q8>(k0.x, k0.y), widen8<Q8>(k0.z, k0.w), widen8<Q8>(k1.x, k1.y), widen8<Q8>(k1.z, k1.w)};
+#pragma unroll
+        for (int i = 0; i < HT; ++i) part[i][b] = q[i].block_product(b, k);
       }
-      const float c_log2 = a.scale_log2;
-      // Register r in quad x is key 8 x + 4 key_half + r. koff: this lane's key as an
-      // operand, piece quad of a scale block; piece 4 + quad is ^ 64.
-      const int key = 8 * (col / 4) + 4 * key_half + col % 4;
-      const int koff = key * kLatentScaleAt + ((quad ^ swizzle(key)) << 4);
-      const int head = head32 + col;
-      const uint32_t pwrite = lds_address(s.p) + head * kTileKeys * 2 + ((quad ^ ((head >> 2) & 3)) << 4) + 8 * key_half;
-      const uint32_t at_top = lds_address(s.top) + head * 8;
-      f32x4 sc[kLatentGroups], S[2];                // of the next tile for the softmax: scales, logits in powers of two
-      // First product of a tile in LDS; the largest logarithm of p x scale of each
-      // head, over this half of the keys, goes to the wave with the other half.
-      auto logits = [&](int tile) {
-        const uint32_t krow = opaque(lds_address(s.ring) + tile % TILES * kTileBytes + koff);
-        const uint32_t krow64 = opaque(krow ^ 64);
-        const uint32_t scale = opaque(lds_address(s.scale) + (tile % TILES * kLatentGroups * kTileKeys + 8 * quad + 4 * key_half) * 4);
-        bf16x8 kr[2] = {lds_get<bf16x8>(krow + kRopeAt), lds_get<bf16x8>(krow64 + kRopeAt)};
-        const uint32_t live = __builtin_amdgcn_readfirstlane(s.live[tile]) >> (8 * quad + 4 * key_half);
-        f32x4 part[2][kLatentGroups], rope[2];
+#pragma unroll
+      for (int i = 0; i < HT; ++i) rope[i] = q[i].rope_product(kr);
+      float big = 0x1p-60f;                       // largest scale of the lane's keys
+#pragma unroll
+      for (int b = 0; b < kLatentGroups; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) big = fmaxf(big, fabsf(sc[b][r]));
+#pragma unroll
+      for (int i = 0; i < HT; ++i) {
+        S[i] = rope[i];
+#pragma unroll
+        for (int b = 0; b < kLatentGroups; ++b) S[i] += sc[b] * part[i][b];
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          S[i][r] = live & (1u << r) ? S[i][r] * c_log2 : -__builtin_inff();
+          top = fmaxf(top, S[i][r]);
+        }
+        top = max_quads(top + (float)__builtin_amdgcn_frexp_expf(big));
+        if (quad == 0) lds_put(at_top + (tile & 1) * kHeads * 8 + 16 * i * 8 + 4 * key_half, top);
+      }
+    };
+    barrier_keep_loads();
+    logits(0);
+#pragma unroll 1
+    for (int tile = 0; tile <= tiles; ++tile) {   // softmax of `tile`, logits of the next one
+      barrier_keep_loads();
+      const int buf = tile & 1;
+      bool moved = false;
+#pragma unroll
+      for (int i = 0; i < HT; ++i) {
+        // both halves' waves come to the same reference
+        typedef float f32x2 __attribute__((ext_vector_type(2)));
+        const f32x2 both = lds_get<f32x2>(at_top + buf * kHeads * 8 + 16 * i * 8);
+        const float top = fmaxf(both.x, both.y);
+        const bool move = top > m[i] + 15.0f;
+        const float nm = move ? top - 8.0f : m[i];
+        const float al = move ? __builtin_amdgcn_exp2f(m[i] - nm) : 1.0f;
+        m[i] = nm;
+        l[i] *= al;
+        const float base = nm == -__builtin_inff() ? 0.0f : nm;
+        float p[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          p[r] = __builtin_amdgcn_exp2f(S[i][r] - base);
+          l[i] += p[r];
+        }
+        const uint32_t pw = opaque(pwrite + (buf * kLatentGroups * kHeads + 16 * i) * kTileKeys * 2);
 #pragma unroll
         for (int b = 0; b < kLatentGroups; ++b) {
-          sc[b] = lds_get<f32x4>(scale + kTileKeys * b * 4);
-          const vec4u k0 = lds_get<vec4u>(krow + b * kScaleGroup), k1 = lds_get<vec4u>(krow64 + b * kScaleGroup);
-          const Q8 k[4] = {widen8<Q8>(k0.x, k0.y), widen8<Q8>(k0.z, k0.w), widen8<Q8>(k1.x, k1.y), widen8<Q8>(k1.z, k1.w)};
+          typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+          f16x4 w;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) part[i][b] = q[i].block_product(b, k);
+          for (int r = 0; r < 4; ++r) w[r] = (_Float16)(p[r] * sc[b][r]);
+          lds_put(pw + b * kHeads * kTileKeys * 2, w);
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) rope[i] = q[i].rope_product(kr);
-        float big = 0x1p-60f;                       // largest scale of the lane's keys
-#pragma unroll
-        for (int b = 0; b < kLatentGroups; ++b)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) big = fmaxf(big, fabsf(sc[b][r]));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          S[i] = rope[i];
-#pragma unroll
-          for (int b = 0; b < kLatentGroups; ++b) S[i] += sc[b] * part[i][b];
-          float top = -__builtin_inff();
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            S[i][r] = live & (1u << r) ? S[i][r] * c_log2 : -__builtin_inff();
-            top = fmaxf(top, S[i][r]);
-          }
-          top = max_quads(top + (float)__builtin_amdgcn_frexp_expf(big));
-          if (quad == 0) lds_put(at_top + (tile & 1) * kHeads * 8 + 16 * i * 8 + 4 * key_half, top);
-        }
-      };
-      barrier_keep_loads();
-      logits(0);
-#pragma unroll 1
-      for (int tile = 0; tile <= tiles; ++tile) {   // softmax of `tile`, logits of the next one
-        barrier_keep_loads();
-        const int buf = tile & 1;
-        bool moved = false;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          // both halves' waves come to the same reference
-          typedef float f32x2 __attribute__((ext_vector_type(2)));
-          const f32x2 both = lds_get<f32x2>(at_top + buf * kHeads * 8 + 16 * i * 8);
-          const float top = fmaxf(both.x, both.y);
-          const bool move = top > m[i] + 15.0f;
-          const float nm = move ? top - 8.0f : m[i];
-          const float al = move ? __builtin_amdgcn_exp2f(m[i] - nm) : 1.0f;
-          m[i] = nm;
-          l[i] *= al;
-          const float base = nm == -__builtin_inff() ? 0.0f : nm;
-          float p[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            p[r] = __builtin_amdgcn_exp2f(S[i][r] - base);
-            l[i] += p[r];
-          }
-          const uint32_t pw = opaque(pwrite + (buf * kLatentGroups * kHeads + 16 * i) * kTileKeys * 2);
-#pragma unroll
-          for (int b = 0; b < kLatentGroups; ++b) {
-            typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-            f16x4 w;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) w[r] = (_Float16)(p[r] * sc[b][r]);
-            lds_put(pw + b * kHeads * kTileKeys * 2, w);
-          }
-          moved |= move;
-          if (quad == 0 && key_half == 0) s.alpha[buf][head + 16 * i] = al;
-        }
-        moved = __any(moved);
-        if (lane == 0 && key_half == 0) s.moved[buf][wave] = moved;
-        logits(tile + 1);
+        moved |= move;
+        if (quad == 0 && key_half == 0) s.alpha[buf][head + 16 * i] = al;
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) l[i] = sum_quads(l[i]);
-    } else {
-      barrier_keep_loads();
-#pragma unroll 1
-      for (int tile = 0; tile <= tiles; ++tile) barrier_keep_loads();
+      moved = __any(moved);
+      if (lane == 0 && key_half == 0) s.moved[buf][wave] = moved;
+      logits(tile + 1);
     }
+#pragma unroll
+    for (int i = 0; i < HT; ++i) l[i] = sum_quads(l[i]);
   }
 
   // every second wave needs every head's l and m
   float* ml = reinterpret_cast<float*>(s.p);
   barrier_keep_loads();
-  if (!second && head32 < kHeads && quad == 0) {
+  if (!second && quad == 0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int head = head32 + 16 * i + col;
+    for (int i = 0; i < HT; ++i) {
+      const int head = head0 + 16 * i + col;
       ml[head] = m[i];
       ml[(1 + key_half) * kHeads + head] = l[i];
     }
@@ -624,42 +618,41 @@ __global__ __launch_bounds__(kJoinThreads) void k_attend_join(GroupDev g, Attend
   if (threadIdx.x == 0 && a.lse) a.lse[row] = sum != 0.0f ? (top + log2f(sum)) * kLn2 : -__builtin_inff();
 }
 
-constexpr int latent_wg_heads(int heads) { return heads <= 32 ? 32 : 64; }
-
-// How a call's keys are split over workgroups (one per compute unit at a time):
-// the number of splits with the least estimated time, in units of one tile's
-// time on one compute unit (1.1 us with 64 heads, 0.8 us with 32). A workgroup
-// costs its tiles plus its start and end (lookups, q, results: 18 us with 64
-// heads, 9 us with 32). With more than one split the join costs a launch, on the
-// host too (7 tiles; 4 on the device), a part for each row and one for each split
-// of a row. Measured, kernel and join, us:
-//   sets x heads, keys    splits
-//   1 x 16, 2048          1: 61    8: 19    16: 16   32: 15   64: 16
-//   4 x 16, 256           1: 14    2: 16    4: 14    8: 13
-//   4 x 64, 2048          4: 37    8: 28    16: 25   32: 25   64: 30
-//   16 x 128, 2048        2: 57    4: 42    8: 36    16: 51
-//   64 x 128, 2048        1: 90    2: 75    4: 89
-//   160 x 64, 2048        1: 97    2: 128   3: 112
+// How a call's heads and keys are split over workgroups (one per compute unit at
+// a time): 32 or 64 heads each, and the number of splits, with the least estimated
+// time in us. A workgroup takes 0.85 us (32 heads) or 1.2 us (64) per tile and 14
+// or 20 us for its start and end (lookups, q, results). With more than one split
+// the join costs a launch, on the host too (7; 4 on the device), a part for each
+// row and one for each split of a row. Measured, kernel + join, us:
+//   sets x heads, keys   32 heads a workgroup, splits         64 heads, splits
+//   1 x 16, 2048         8: 19   16: 16   32: 16   64: 15
+//   4 x 16, 256          1: 14   2: 16    4: 13    8: 13
+//   4 x 64, 2048         8: 22   16: 20   32: 22              8: 29   16: 26   32: 27
+//   16 x 128, 2048       1: 63   2: 45    4: 36               4: 45   8: 37
+//   64 x 128, 2048       1: 73   2: 95                        1: 101  2: 79
+//   64 x 64, 700         1: 29   2: 32                        1: 42   2: 40
+//   160 x 64, 2048       1: 132  3: 141                       1: 101  3: 114
 AttendPlan plan_attend_latent(int n_sets, int k, int heads) {
   AttendPlan best{};
-  const int wg_heads = latent_wg_heads(heads);
-  best.head_blocks = (heads + wg_heads - 1) / wg_heads;
-  const long long base = (long long)n_sets * best.head_blocks;
   const int tiles = (k + kTileKeys - 1) / kTileKeys;
-  double best_cost = 0;
   const int least = std::max(1, (k + kAttendKeys - 1) / kAttendKeys);
-  for (int want = least; want <= std::max(least, std::min(tiles, kComputeUnits)); ++want) {
-    const int per = std::max(1, (tiles + want - 1) / want);   // tiles per split
-    const int splits = std::max(1, (tiles + per - 1) / per);
-    if (splits != want && want != least) continue;        // the same split as a smaller one
-    const double waves = (double)((base * splits + kComputeUnits - 1) / kComputeUnits);
-    double cost = waves * (per + (wg_heads == 32 ? 11 : 16));
-    const double rows = (double)n_sets * heads;
-    if (splits > 1) cost += 7 + 8e-4 * rows + 1.8e-4 * rows * splits;
-    if (best.splits == 0 || cost < best_cost) {
-      best_cost = cost;
-      best.splits = splits;
-      best.split_keys = per * kTileKeys;
+  const double rows = (double)n_sets * heads;
+  double best_cost = 0;
+  for (const int wg_heads : {32, 64}) {
+    const int head_blocks = (heads + wg_heads - 1) / wg_heads;
+    if (wg_heads == 64 && head_blocks == (heads + 31) / 32) break;   // the same workgroups, half empty
+    const long long base = (long long)n_sets * head_blocks;
+    const double tile_us = wg_heads == 32 ? 0.85 : 1.2, start_us = wg_heads == 32 ? 14.0 : 20.0;
+    for (int want = least; want <= std::max(least, std::min(tiles, kComputeUnits)); ++want) {
+      const int per = std::max(1, (tiles + want - 1) / want);   // tiles per split
+      const int splits = std::max(1, (tiles + per - 1) / per);
+      if (splits != want && want != least) continue;            // the same split as a smaller one
+      double cost = (double)((base * splits + kComputeUnits - 1) / kComputeUnits) * (per * tile_us + start_us);
+      if (splits > 1) cost += 7 + 9e-4 * rows + 2e-4 * rows * splits;
+      if (best.splits == 0 || cost < best_cost) {
+        best_cost = cost;
+        best = {splits, per * kTileKeys, head_blocks};
+      }
     }
   }
   return best;
@@ -672,7 +665,7 @@ static void launch_latent(const GroupDev& g, const AttendDev& a, int n_sets, hip
 
 template <typename Q8>
 static hipError_t launch_latent_of(const GroupDev& g, const AttendDev& a, int n_sets, hipStream_t s) {
-  if (a.heads <= 32) launch_latent<Q8, 1, 5>(g, a, n_sets, s);
+  if (a.head_blocks == (a.heads + 31) / 32) launch_latent<Q8, 1, 5>(g, a, n_sets, s);
   else launch_latent<Q8, 2, 5>(g, a, n_sets, s);
   return hipGetLastError();
 }
