@@ -229,7 +229,8 @@ __device__ __forceinline__ void each_key(bool on, uint32_t key, uint32_t bits, F
   if (left >> lane_id() & 1ull) f(bits, 1);
 }
 
-// Release of finished entries (app_la[0..n), validated on the host): a GPU slot
+// Release of finished entries (addresses first .. first + n - 1, or app_la[0..n) if
+// first is -1; validated on the host): a GPU slot
 // leaves whichever bucket holds it and joins the free set, a host slot joins the
 // free host set (its staging record cleared, so no later miss reads a staged
 // copy of the released row); the address becomes absent. Bucket words and span
@@ -241,7 +242,7 @@ __device__ __forceinline__ void each_key(bool on, uint32_t key, uint32_t bits, F
 // a wavefront adds its lanes' shares up first, and a workgroup the totals.
 // (65536 entries released in order: 882 us with an atomic for each entry and
 // count, 10 us so.)
-__global__ __launch_bounds__(256) void k_release(GroupDev g, int32_t n) {
+__global__ __launch_bounds__(256) void k_release(GroupDev g, int32_t first, int32_t n) {
   __shared__ int s_bucket[kMaxBuckets];
   __shared__ int s_free, s_host, s_free_lo, s_host_lo;
   for (int i = threadIdx.x; i < g.NB; i += blockDim.x) s_bucket[i] = 0;
@@ -255,7 +256,7 @@ __global__ __launch_bounds__(256) void k_release(GroupDev g, int32_t n) {
     const int i = base + (int)threadIdx.x;
     uint32_t loc = kAbsent;
     if (i < n) {
-      const int32_t la = g.app_la[i];
+      const int32_t la = first >= 0 ? first + i : g.app_la[i];
       loc = g.map[la];
       if (loc == kAbsent) latch(g.ctr, ULA_ESTATE);   // the host checked this: an inconsistent state
       else g.map[la] = kAbsent;
@@ -318,11 +319,11 @@ __global__ __launch_bounds__(256) void k_release(GroupDev g, int32_t n) {
   }
 }
 
-hipError_t launch_release(const GroupDev& g, int32_t n, hipStream_t s) {
+hipError_t launch_release(const GroupDev& g, int32_t first, int32_t n, hipStream_t s) {
   if (n <= 0) return hipSuccess;
   int blocks = (n + 255) / 256;
   if (blocks > 1024) blocks = 1024;
-  k_release<<<blocks, 256, 0, s>>>(g, n);
+  k_release<<<blocks, 256, 0, s>>>(g, first, n);
   return hipGetLastError();
 }
 

@@ -779,7 +779,9 @@ int ula_release(ula_ctx* ctx, int32_t group, int32_t n, const int32_t* la_host, 
     HIP_TRY(launch_writeback(g, std::max<int32_t>(gh.last_pairs, 1), s));
     gh.written_back = gh.steps;
   }
-  for (int32_t off = 0; off < n; off += (int32_t)d.maxApp) {
+  // one run of addresses, as a request's mostly are, needs no list on the device
+  if (runs.size() == 1) HIP_TRY(launch_release(g, runs[0].first, n, s));
+  for (int32_t off = 0; off < n && runs.size() > 1; off += (int32_t)d.maxApp) {
     const int32_t cnt = (int32_t)std::min<int64_t>(n - off, d.maxApp);
     if (ctx->static_dev >= 0) {
       // no pinned staging buffers: copy from the caller's memory and wait for it
@@ -794,7 +796,7 @@ int ula_release(ula_ctx* ctx, int32_t group, int32_t n, const int32_t* la_host, 
       HIP_TRY(hipMemcpyAsync(g.app_la, gh.stage[k], sizeof(int32_t) * cnt, hipMemcpyHostToDevice, s));
       HIP_TRY(hipEventRecord(gh.stage_ev[k], s));
     }
-    HIP_TRY(launch_release(g, cnt, s));
+    HIP_TRY(launch_release(g, -1, cnt, s));
   }
   for (const Run& r : runs) mark_range(gh, r.first, r.n, false);
   gh.n_appended -= n;

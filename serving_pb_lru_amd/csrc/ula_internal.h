@@ -244,7 +244,7 @@ hipError_t launch_tag_append(const GroupDev& g, const SmallAppend& a, const uint
                              const int32_t* sel, int32_t n, uint32_t t, hipStream_t s);
 hipError_t launch_place(const GroupDev& g, int32_t n, const uint8_t* rows, hipStream_t s);
 hipError_t launch_place_ring(const GroupDev& g, int32_t n, const uint8_t* rows, hipStream_t s);
-hipError_t launch_release(const GroupDev& g, int32_t n, hipStream_t s);
+hipError_t launch_release(const GroupDev& g, int32_t first, int32_t n, hipStream_t s);
 // copies of entries src0 .. under addresses dst0 .. into the places of app_dst, or
 // into the append's staging buffers; new addresses for entries (k_entries.hip)
 hipError_t launch_fork_place(const GroupDev& g, int32_t src0, int32_t dst0, int32_t n, hipStream_t s);

@@ -230,6 +230,22 @@ def test_refusals_change_nothing():
         m.close()
 
 
+@pytest.mark.parametrize("n", [1, 1023, 1024, 1025, 4095, 4096, 4097, 6000])
+def test_renames_of_many_sizes(n):
+    """Either side of a workgroup's entries, to a range of its own and up and down by a few addresses."""
+    m = Model(17, N=13000, P=5000, H=1200, max_append=6100)
+    try:
+        m.append(np.arange(50, 50 + n))
+        for src, dst in [(50, 6500), (6500, 6507), (6507, 6400), (6400, 0), (0, 1), (1, 12999 - n)]:
+            m.rename(src, dst, n)
+            m.same(f"{n} entries from {src} to {dst}")
+        m.release(np.arange(12999 - n, 12999))
+        m.same("end", True)
+        m.eng.sync()
+    finally:
+        m.close()
+
+
 @pytest.mark.parametrize("policy", [0, 1])
 def test_releases_of_many_orders(policy):
     """Batches that share words and spans of the bitmaps in every way: in order, reversed, scattered, one
