@@ -428,7 +428,8 @@ typedef struct {
   int32_t n, heads, dim;     /* tokens, heads, channels of a head: even, 2..256, all turned */
   int32_t inverse;           /* 1: turn back, which is also the gradient of the turn */
   const void* x;             /* [n][heads][dim], last dimension contiguous */
-  void* out;                 /* the same shape; x itself with the same strides, or no overlap */
+  void* out;                 /* the same shape; x itself with the same strides, or no overlap;
+                                its own rows share no elements (ULA_EINVAL if a stride says so) */
   int64_t x_stride[2];       /* strides in elements: token, head */
   int64_t out_stride[2];
   const int32_t* positions;  /* [n][axes] packed */
@@ -438,7 +439,7 @@ typedef struct {
 /* Turn the heads of n tokens (the rotary part of queries, or its way back) by
  * their positions; each result is rounded to its type once. A pure function of
  * its device inputs; it may be captured into a graph. Errors: ULA_EINVAL (also
- * n * heads >= 2^25), ULA_EHIP. */
+ * more rows than a launch takes: n * heads < 2^25 always fits), ULA_EHIP. */
 int ula_rotate(const ula_rotate_args* args, uint64_t stream);
 
 typedef struct {
@@ -478,7 +479,7 @@ size_t ula_attend_bytes(const ula_row_format* rows, int32_t n_sets, int32_t k, i
  * Results split over several workgroups are joined through the workspace, which
  * belongs to the call until the stream has run it: calls that may run at the
  * same time need workspaces of their own. q, out, lse and the workspace must not
- * overlap. q and out rows whose pointer and strides keep them 16-byte aligned are
+ * overlap, nor rows of out (ULA_EINVAL if one of its strides says so). q and out rows whose pointer and strides keep them 16-byte aligned are
  * read and written in vectors, others element by element.
  * Which entries, streams and errors: as for ula_gather (the selection is looked
  * up through the group's last step where it is that step's, else through the

@@ -252,11 +252,12 @@ __global__ __launch_bounds__(256) void k_release(GroupDev g, int32_t first, int3
   }
   if (block_failed(g.ctr)) return;
   __syncthreads();
-  for (int base = blockIdx.x * blockDim.x; base < n; base += gridDim.x * blockDim.x) {
-    const int i = base + (int)threadIdx.x;
+  // unsigned: n may be near 2^31
+  for (uint32_t base = blockIdx.x * blockDim.x; base < (uint32_t)n; base += gridDim.x * blockDim.x) {
+    const uint32_t i = base + threadIdx.x;
     uint32_t loc = kAbsent;
-    if (i < n) {
-      const int32_t la = first >= 0 ? first + i : g.app_la[i];
+    if (i < (uint32_t)n) {
+      const int32_t la = first >= 0 ? first + (int32_t)i : g.app_la[i];
       loc = g.map[la];
       if (loc == kAbsent) latch(g.ctr, ULA_ESTATE);   // the host checked this: an inconsistent state
       else g.map[la] = kAbsent;

@@ -346,22 +346,29 @@ hipError_t launch_pack(const PackDev& a, const RotaryDev& rot, int type, hipStre
   return pack_of<float>(a, rot, s);
 }
 
+// Workgroups of a turn: two units a lane, which is enough of them for a decode step
+// and holds a head's units (at most 128).
+constexpr int kRotateUnits = 2, kRotateVector = 4;
+long long plan_rotate(RotateDev* a) {
+  constexpr int kUnits = 256 * kRotateUnits;
+  const int pairs = a->dim / 2, units = a->aligned ? pairs / kRotateVector : pairs;
+  a->heads_per_block = std::max(1, std::min(a->heads, kUnits / units));
+  a->tokens_per_block = std::max(1, std::min(a->n, std::min(kUnits / (units * a->heads_per_block), 4096 / pairs)));
+  return (long long)((a->n + (long long)a->tokens_per_block - 1) / a->tokens_per_block) *
+         ((a->heads + a->heads_per_block - 1) / a->heads_per_block);
+}
+
 template <typename T, int V>
 static void rotate_units(RotateDev a, const RotaryDev& rot, hipStream_t s) {
-  // two units a lane: enough workgroups for a decode step, and 512 units hold a head's (at most 128)
-  constexpr int U = 2, kUnits = 256 * U;
-  const int pairs = a.dim / 2, units = pairs / V;
-  a.heads_per_block = std::max(1, std::min(a.heads, kUnits / units));
-  a.tokens_per_block = std::max(1, std::min(a.n, std::min(kUnits / (units * a.heads_per_block), 4096 / pairs)));
-  const long long blocks = (long long)((a.n + a.tokens_per_block - 1) / a.tokens_per_block) *
-                           ((a.heads + a.heads_per_block - 1) / a.heads_per_block);
+  const long long blocks = plan_rotate(&a);
+  const int pairs = a.dim / 2;
   const size_t lds = (size_t)a.tokens_per_block * pairs * sizeof(float2);
-  k_rotate<T, V, U><<<(unsigned)blocks, 256, lds, s>>>(a, rot, FastDiv(units), FastDiv(a.heads_per_block));
+  k_rotate<T, V, kRotateUnits><<<(unsigned)blocks, 256, lds, s>>>(a, rot, FastDiv(pairs / V), FastDiv(a.heads_per_block));
 }
 
 template <typename T>
 static hipError_t rotate_of(const RotateDev& a, const RotaryDev& rot, hipStream_t s) {
-  if (a.aligned) rotate_units<T, 4>(a, rot, s);
+  if (a.aligned) rotate_units<T, kRotateVector>(a, rot, s);
   else rotate_units<T, 1>(a, rot, s);
   return hipGetLastError();
 }

@@ -835,9 +835,11 @@ int ula_fork(ula_ctx* ctx, int32_t group, int32_t src, int32_t dst, int32_t n, u
     const int rc = wait_gathers(gh, s);
     if (rc) return rc;
   }
-  for (int64_t done = 0; done < n; done += d.maxApp) {
+  // a chunk's places are in app_dst, and its 16-byte pieces are counted in 32 bits
+  const int64_t most = std::min<int64_t>(d.maxApp, 0xFFFFFFFFll / (d.slot_bytes / 16));
+  for (int64_t done = 0; done < n; done += most) {
     const int32_t off = (int32_t)done;
-    const int32_t cnt = (int32_t)std::min<int64_t>(n - done, d.maxApp);
+    const int32_t cnt = (int32_t)std::min<int64_t>(n - done, most);
     if (ring) {
       HIP_TRY(launch_fork_collect(g, src + off, dst + off, cnt, s));
       const PlanArgs a = ring_append_plan(cnt, (int32_t)(gh.steps % d.B), (int32_t)d.B);
@@ -1156,18 +1158,22 @@ int ula_pack_rows(const ula_pack_args* args, void* rows_dev, uint64_t stream) {
   return ULA_OK;
 }
 
+// Whether rows of `width` elements, n of them a stride apart, share elements.
+static bool rows_overlap(int32_t n, int64_t stride, int64_t width) {
+  return n > 1 && stride < width && stride > -width;
+}
+
 int ula_rotate(const ula_rotate_args* args, uint64_t stream) {
   if (!args) return ULA_EINVAL;
   const ula_rotate_args& u = *args;
   int size;
   if (!element_size(u.type, &size) || u.n < 0 || u.heads < 0) return ULA_EINVAL;
   if (u.dim < 2 || u.dim % 2 || u.dim > 2 * kMostPairs || (u.inverse != 0 && u.inverse != 1)) return ULA_EINVAL;
-  // fewer than 2^32 threads, 256 for two rows or more
-  if ((int64_t)u.n * u.heads >= (1ll << 25)) return ULA_EINVAL;
   RotaryDev rot{};
   if (!rotary_dev(u.rotary, u.dim / 2, &rot)) return ULA_EINVAL;
   if (u.n == 0 || u.heads == 0) return ULA_OK;
   if (!u.x || !u.out || !u.positions) return ULA_EINVAL;
+  if (rows_overlap(u.n, u.out_stride[0], u.dim) || rows_overlap(u.heads, u.out_stride[1], u.dim)) return ULA_EINVAL;
   if (((uintptr_t)u.x | (uintptr_t)u.out) % size || (uintptr_t)u.positions % 4) return ULA_EINVAL;
   RotateDev a{};
   a.x = u.x;
@@ -1185,6 +1191,7 @@ int ula_rotate(const ula_rotate_args* args, uint64_t stream) {
   a.heads = u.heads;
   a.dim = u.dim;
   a.inverse = u.inverse;
+  if (plan_rotate(&a) >= (1ll << 24)) return ULA_EINVAL;   // a launch has fewer than 2^32 threads, 256 each
   HIP_TRY(launch_rotate(a, rot, u.type, reinterpret_cast<hipStream_t>(stream)));
   return ULA_OK;
 }
@@ -1239,6 +1246,7 @@ int ula_attend(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32
   if (n_sets > 0) {
     if ((k > 0 && !sel_dev) || !u.q || !u.out) return ULA_EINVAL;
     if (((uintptr_t)u.q | (uintptr_t)u.out) % 2 || (uintptr_t)u.lse % 4 || (uintptr_t)sel_dev % 4) return ULA_EINVAL;
+    if (rows_overlap(n_sets, u.out_set_stride, width) || rows_overlap(u.heads, u.out_head_stride, width)) return ULA_EINVAL;
     if (need && (!u.workspace || u.workspace_bytes < need || (uintptr_t)u.workspace % 16)) return ULA_EINVAL;
   }
   GroupHost& gh = ctx->groups[group];

@@ -255,6 +255,8 @@ class _On:
 
     def __init__(self, device, stream):
         import torch
+        if getattr(stream, "device", device) != device:
+            raise ValueError(f"tensors on {device}, a stream of {stream.device}")
         # the handle alone: a decode step's call is bound by the host, and a Stream object costs 2 us
         current = torch._C._cuda_getCurrentRawStream(device.index)
         here = torch.cuda.current_device() == device.index
@@ -505,7 +507,7 @@ class Engine:
         args.q, args.type, st = _tensor(q, (n_sets, None, width), "ula_attend q", (BF16, FP16))
         args.q_set_stride, args.q_head_stride, args.heads = st[0], st[1], heads
         args.scale = 1.0 / width ** 0.5 if scale is None else scale
-        _same_device(q, sel, out, lse)
+        _same_device(q, sel, out, lse, self.ws)
         with _On(q.device, stream) as s:
             if out is None:
                 out = torch.empty((n_sets, heads, back), dtype=q.dtype, device=q.device)

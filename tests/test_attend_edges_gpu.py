@@ -283,6 +283,10 @@ def test_errors():
         many = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
         run = lambda n, k: ula.lib().ula_attend(eng.ctx, 0, 0, n, k, many.data_ptr(), ula.ctypes.byref(args), 0)
         assert run(3, 1) == run(1, 33) == run(-1, 1) == run(1, -1) == -1
+        for strides in [(512, 0), (511, 512), (2048, 511), (0, 512)]:     # rows of out that share elements
+            args.out_set_stride, args.out_head_stride = strides
+            assert run(2 if strides[0] < 512 else 1, 1) == -1, strides
+        args.out_set_stride, args.out_head_stride = 2048, 512
         args.q = q.data_ptr() + 1
         assert run(1, 1) == -1
         args.q, args.type = q.data_ptr(), ula.FP32
@@ -301,6 +305,50 @@ def test_errors():
         check(fmt, rows, 0, sel.cpu().numpy(), q, 1 / 24, out, lse, "bf16")
     finally:
         eng.close()
+
+
+def test_rows_past_32_bits():
+    """A pool of more than 2^32 bytes: attention, fork and release of entries at its end."""
+    import torch
+    from serving_pb_lru_amd import latent_rows
+    fmt, chunk = latent_rows(), 65536
+    n = (1 << 32) // 656 // chunk * chunk + 2 * chunk
+    rng = np.random.default_rng(18)
+    from serving_pb_lru_amd import Engine
+    eng = Engine(num_groups=1, layers=1, row_bytes=656, ring=2, logical_capacity=n, gpu_slots=n, host_slots=0,
+                 max_sets=2, max_k=64, max_append=chunk)
+    try:
+        filler = torch.zeros((chunk, 1, 656), dtype=torch.uint8, device="cuda")
+        for at in range(0, n - chunk, chunk):
+            eng.append(0, np.arange(at, at + chunk, dtype=np.int32), filler)
+        last = n - chunk
+        some = latent_rows_of(rng, 500, 1)
+        eng.append(0, np.arange(last, last + 500, dtype=np.int32), some)
+        eng.fork(0, last, last + 1000, 500)
+        sel = rng.choice(500, (2, 64), replace=False).astype(np.int32)
+        sel[1] += 1000
+        d = torch.from_numpy(sel + last).cuda()
+        assert last * 656 > 1 << 32
+        eng.step(0, d)
+        q = queries(rng, fmt, 2, 8)
+        out, lse = eng.attend(0, 0, d, q, fmt)
+        eng.sync()
+        check(fmt, some, 0, sel - np.array([[0], [1000]], np.int32), q, 1 / 24, out, lse, "bf16")
+        eng.release(0, np.arange(last - 5000, last + 500, dtype=np.int32))
+        assert np.array_equal(eng.read_rows(0, np.arange(last + 1000, last + 1500, dtype=np.int32)), some)
+        eng.sync()
+    finally:
+        eng.close()
+
+
+def test_a_stream_of_another_device_is_refused():
+    import torch
+    from serving_pb_lru_amd import rotate
+
+    class Elsewhere:
+        cuda_stream, device = 0, torch.device("cuda", 1)
+    with pytest.raises(ValueError):
+        rotate(torch.zeros((1, 1, 64), device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"), stream=Elsewhere())
 
 
 @pytest.mark.parametrize("address,name", [(1 << 20, "ERANGE"), (-2, "ERANGE"), (59, "ENOTRESIDENT")])

@@ -108,8 +108,12 @@ def test_rotate_refuses():
     assert L.ula_rotate(None, 0) == EINVAL
     for kw in [dict(type=3), dict(n=-1), dict(heads=-1), dict(dim=0), dict(dim=63), dict(dim=258), dict(dim=-2),
                dict(inverse=2), dict(inverse=-1), dict(x=None), dict(out=None), dict(positions=None), dict(x=P + 1),
-               dict(out=P + 1), dict(type=ula.FP32, x=P + 2), dict(positions=P + 1), dict(n=1 << 20, heads=32)]:
+               dict(out=P + 1), dict(type=ula.FP32, x=P + 2), dict(positions=P + 1), dict(n=1 << 30, heads=32)]:
         assert call(rotate_args(**kw)) == EINVAL, kw
+    for strides in [(0, 64), (64, 0), (63, 128), (64, -63), (32, 64)]:      # rows of out that share elements
+        a = rotate_args(n=2, heads=2)
+        a.out_stride[:] = strides
+        assert call(a) == EINVAL, strides
     for rot in BAD_ROTARY:
         assert call(rotate_args(rotary=rot)) == EINVAL, rot
     assert call(rotate_args(n=0, x=None, out=None, positions=None)) == 0

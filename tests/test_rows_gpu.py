@@ -316,6 +316,28 @@ def test_graph_of_both_replays():
         assert torch.equal(rows, want[0]) and torch.equal(back, want[1]), i
 
 
+def test_tensors_past_32_bits():
+    """Outputs and inputs of more than 2^32 bytes (rows) and elements (the turn): their ends equal calls
+    of the ends alone."""
+    import torch
+    from serving_pb_lru_amd import latent_rows, pack_rows, rotate
+    n = (1 << 32) // 656 + 1000
+    lat = torch.zeros((n, 1, 512), dtype=torch.bfloat16, device="cuda")
+    rope = torch.zeros((n, 1, 64), dtype=torch.bfloat16, device="cuda")
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    lat[-700:].normal_()
+    rope[-700:].normal_()
+    rows = pack_rows(latent_rows(), lat, rope, pos)
+    assert torch.equal(rows[-700:], pack_rows(latent_rows(), lat[-700:], rope[-700:], pos[-700:]))
+    del lat, rope, rows
+    n = (1 << 32) // (128 * 128) + 9
+    x = torch.zeros((n, 128, 128), dtype=torch.bfloat16, device="cuda")
+    x[-12:].normal_()
+    want = rotate(x[-12:], pos[:n][-12:])
+    rotate(x, pos[:n], out=x)
+    assert torch.equal(x[-12:], want) and not bool(x[:100].any())
+
+
 def test_two_streams():
     import torch
     from serving_pb_lru_amd import rotate
