@@ -42,7 +42,8 @@
 // Of that 18 us are start and end, and the 344 MB of rows alone take 86 us at the
 // rate of a large sum. In the loop the first waves' chain of products, maximum,
 // exponentials and p decides, about 2500 cycles a tile; issuing a tile's products
-// ahead of the softmax before it does not shorten it (116 us).
+// ahead of the softmax before it does not shorten it (116 us), nor does p in 32
+// bits scaled by the second waves, with a sixth tile in the LDS that frees (117 us).
 // Tiles: the first 640 bytes of each row as 16-byte pieces straight into LDS (no
 // registers), the scales transposed to [block][key]. Piece c of key j lies at
 // c ^ swizzle(j), which keeps the 16 lanes that a 16-byte read serves at once
@@ -126,7 +127,7 @@ struct LatentLds {
   alignas(1024) _Float16 p[2][kLatentGroups][HEADS][kTileKeys];
   alignas(16) float scale[TILES][kLatentGroups][kTileKeys];
   float alpha[2][HEADS];                    // factor of O before the tile's second product
-  alignas(16) uint32_t moved[2][4];         // whether any of 16 heads has a factor other than 1
+  alignas(16) uint32_t moved[2][4];         // whether any head of a first wave has a factor other than 1
   alignas(8) float top[2][HEADS][2];        // of two tiles: the largest logarithm of p x scale, of either half of the keys
   const uint8_t* row[kAttendKeys];          // each key's row in this layer; zeros for padding
   uint32_t live[kAttendKeys / kTileKeys + 2];   // bit per key: not padding; none behind the last tile
