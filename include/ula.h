@@ -419,8 +419,8 @@ typedef struct {
  * channels are turned in 32 bits and rounded to bf16 once. A pure function of its
  * device inputs: nothing of an engine is involved, and it may be captured into a
  * graph. Errors: ULA_EINVAL (null pointer, n or layers < 0, unknown type, invalid
- * format or rotary, misaligned pointers, 2^26 rows or more, each counted twice per
- * KV head for heads rows), ULA_EHIP. */
+ * format or rotary, misaligned pointers, 2^26 rows or more, or heads rows of 2^34
+ * keys' elements or more), ULA_EHIP. */
 int ula_pack_rows(const ula_pack_args* args, void* rows_dev, uint64_t stream);
 
 typedef struct {

@@ -159,63 +159,6 @@ __global__ __launch_bounds__(256) void k_pack_latent(PackDev a, RotaryDev rot, F
   }
 }
 
-// Heads rows: one wave per (row, KV head, keys or values): the block's values,
-// keys turned, go to LDS in 32 bits while amax is taken, then to codes.
-constexpr int kBlockMost = 2048;   // block_tokens x head_dim of a row of at most 4096 bytes
-
-template <typename T>
-__global__ __launch_bounds__(kWave) void k_pack_heads(PackDev a, RotaryDev rot) {
-  __shared__ float s[kBlockMost];
-  const int lane = lane_id();
-  const int per_row = 2 * a.kv_heads;
-  const int row = blockIdx.x / per_row;
-  const int h = blockIdx.x % per_row % a.kv_heads;
-  const bool value = blockIdx.x % per_row >= a.kv_heads;
-  const int entry = row / a.layers, layer = row % a.layers;
-  const int block = a.block_tokens, dim = a.head_dim, half = dim / 2;
-  const long long* st = value ? a.b_stride : a.a_stride;
-  const T* src = static_cast<const T*>(value ? a.b : a.a) + entry * st[0] + layer * st[1] + h * st[3];
-  const int count = a.count ? min(max(a.count[entry], 0), block) : block;
-  float amax = 0.0f;
-  for (int e = lane; e < block * half; e += kWave) {
-    const int tok = e / half, i = e % half;
-    const int at0 = rot.interleaved ? 2 * i : i, at1 = rot.interleaved ? 2 * i + 1 : i + half;
-    float y0 = 0.0f, y1 = 0.0f;
-    if (tok < count) {
-      const float x0 = to_f32(src[tok * st[2] + at0]), x1 = to_f32(src[tok * st[2] + at1]);
-      y0 = x0;
-      y1 = x1;
-      if (!value && a.positions) {
-        const float2 cs = rotary_of(rot, a.positions + ((size_t)entry * block + tok) * rot.axes, i);
-        y0 = x0 * cs.x - x1 * cs.y;
-        y1 = x0 * cs.y + x1 * cs.x;
-      }
-    }
-    s[tok * dim + at0] = y0;
-    s[tok * dim + at1] = y1;
-    amax = fmaxf(amax, fmaxf(finite_abs(y0), finite_abs(y1)));
-  }
-#pragma unroll
-  for (int d = 1; d < kWave; d *= 2) amax = fmaxf(amax, __shfl_xor(amax, d, kWave));
-  __syncthreads();
-  const float scale = scale_of(amax);
-  uint8_t* out = a.rows + (size_t)row * a.row_bytes;
-  const int part = block * dim;
-  uint32_t* codes = reinterpret_cast<uint32_t*>(out + (value ? a.kv_heads * part : 0) + h * part);
-  for (int e = lane; e < part / 4; e += kWave) {
-    const f32x4 x = *reinterpret_cast<const f32x4*>(&s[4 * e]);
-    codes[e] = e4m3x4(to_e4m3_range(x[0], scale), to_e4m3_range(x[1], scale), to_e4m3_range(x[2], scale),
-                      to_e4m3_range(x[3], scale));
-  }
-  uint8_t* tail = out + 2 * a.kv_heads * part;
-  if (lane == 0) reinterpret_cast<float*>(tail)[(value ? a.kv_heads : 0) + h] = scale;
-  if (h == 0 && !value) {   // the token count and the zeros behind it
-    int32_t* words = reinterpret_cast<int32_t*>(tail + 8 * a.kv_heads);
-    const int n = (int)(out + a.row_bytes - reinterpret_cast<uint8_t*>(words)) / 4;
-    if (lane < n) words[lane] = lane == 0 ? count : 0;
-  }
-}
-
 // V pairs of a row as they are in memory, first .. first + V - 1 of `pairs`.
 template <typename T, int V>
 struct Pairs {
@@ -282,6 +225,140 @@ struct Pairs {
   }
 };
 
+// Heads rows. A workgroup takes 256 units of four pairs of one side (keys in the
+// first half of the grid, values in the second): whole scale blocks (a row, a KV
+// head), of `units` lanes each (a power of two, 8 to 128), whose largest value is
+// found by shuffles, and through LDS where a block is more than a wave. The sines
+// of the workgroup's tokens are computed once for all their heads, into LDS, while
+// the values are on their way. (65536 rows of 8 KV heads of 128, turned, 403 MB
+// read and written: 683 us with a wave per scale block and single elements,
+// 124 us so.)
+constexpr int kPackThreads = 256;
+
+template <typename T, bool ALIGNED>
+__global__ __launch_bounds__(kPackThreads) void k_pack_heads(PackDev a, RotaryDev rot, int units, uint32_t side_blocks,
+                                                            FastDiv by_heads, FastDiv by_layers) {
+  extern __shared__ float2 s_cs[];   // [entry][token][pair] from the workgroup's first entry on
+  __shared__ float s_max[kPackThreads / kWave];
+  const bool value = blockIdx.x >= side_blocks;
+  const int dim = a.head_dim, half = dim / 2, block = a.block_tokens, per_token = dim / 8;
+  const uint32_t per = kPackThreads / units;                      // scale blocks here
+  const uint32_t all = (uint32_t)a.n * (uint32_t)a.layers * (uint32_t)a.kv_heads;
+  const uint32_t first = (blockIdx.x - (value ? side_blocks : 0u)) * per;
+  const uint32_t mine = first + threadIdx.x / units;
+  const bool there = mine < all;
+  const uint32_t at = min(mine, all - 1);
+  const uint32_t row = by_heads.div(at), h = at - row * a.kv_heads;
+  const uint32_t entry = by_layers.div(row), layer = row - entry * a.layers;
+  const int unit = (int)threadIdx.x % units, tok = unit / per_token, pair = unit % per_token * 4;
+  const int count = a.count ? min(max(a.count[entry], 0), block) : block;
+  const bool live = tok < count;
+
+  Pairs<T, 4> x;
+  if (live) {
+    const long long* st = value ? a.b_stride : a.a_stride;
+    const T* src = static_cast<const T*>(value ? a.b : a.a) + entry * st[0] + layer * st[1] + tok * st[2] + h * st[3];
+    if constexpr (ALIGNED) {
+      x.load(src, pair, half, rot.interleaved);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x.a[j] = src[rot.interleaved ? 2 * (pair + j) : pair + j];
+        x.b[j] = src[rot.interleaved ? 2 * (pair + j) + 1 : pair + j + half];
+      }
+    }
+  }
+  const uint32_t entry0 = by_layers.div(by_heads.div(first));
+  if (!value && a.positions) {
+    const uint32_t last = by_layers.div(by_heads.div(min(first + per, all) - 1));
+    const int tokens = (int)(last - entry0 + 1) * block;
+    for (int e = threadIdx.x; e < tokens * half; e += kPackThreads)
+      s_cs[e] = rotary_of(rot, a.positions + ((size_t)entry0 * block + e / half) * rot.axes, e % half);
+    __syncthreads();
+  }
+  float y[2][4];                                                  // first and second of each pair
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    y[0][j] = live ? to_f32(x.a[j]) : 0.0f;
+    y[1][j] = live ? to_f32(x.b[j]) : 0.0f;
+  }
+  if (!value && a.positions) {
+    const float2* cs = s_cs + ((size_t)(entry - entry0) * block + tok) * half + pair;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float p = y[0][j], q = y[1][j];
+      y[0][j] = p * cs[j].x - q * cs[j].y;
+      y[1][j] = p * cs[j].y + q * cs[j].x;
+    }
+  }
+  auto largest = [&](float v) {                                   // of the scale block; every lane calls it
+    for (int d = 1; d < min(units, kWave); d *= 2) v = fmaxf(v, __shfl_xor(v, d, kWave));
+    if (units > kWave) {
+      __syncthreads();
+      if (lane_id() == 0) s_max[threadIdx.x / kWave] = v;
+      __syncthreads();
+      const int w0 = (int)threadIdx.x / units * (units / kWave);
+      for (int w = 0; w < units / kWave; ++w) v = fmaxf(v, s_max[w0 + w]);
+    }
+    return v;
+  };
+  float amax = 0.0f, odd = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      amax = fmaxf(amax, fabsf(y[i][j]));
+      odd = __builtin_fmaf(y[i][j], 0.0f, odd);                   // NaN after an infinity or a NaN
+    }
+  amax = largest(odd == 0.0f ? amax : __builtin_inff());
+  float scale = divide_by(amax, kE4m3Max, 1.0f / kE4m3Max);
+  const bool far = !(scale >= 0x1p-60f && scale < __builtin_inff());
+  // one answer for the whole workgroup where a scale block is more than a wave: largest() has barriers then
+  if (units > kWave ? __syncthreads_or(far) : __any(far)) {
+    float finite = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) finite = fmaxf(finite, finite_abs(y[i][j]));
+    scale = scale_of(largest(finite));
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[i][j] = to_e4m3_range(y[i][j], scale);
+  } else {
+    const float inv = 1.0f / scale;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[i][j] = divide_by(y[i][j], scale, inv);
+  }
+  if (!there) return;
+  uint8_t* out = a.rows + (size_t)row * a.row_bytes;
+  const int part = block * dim;
+  uint8_t* codes = out + (value ? a.kv_heads * part : 0) + h * part + tok * dim;
+  if (rot.interleaved) {
+    *reinterpret_cast<uint2*>(codes + 2 * pair) = make_uint2(e4m3x4(y[0][0], y[1][0], y[0][1], y[1][1]),
+                                                            e4m3x4(y[0][2], y[1][2], y[0][3], y[1][3]));
+  } else {
+    *reinterpret_cast<uint32_t*>(codes + pair) = e4m3x4(y[0][0], y[0][1], y[0][2], y[0][3]);
+    *reinterpret_cast<uint32_t*>(codes + half + pair) = e4m3x4(y[1][0], y[1][1], y[1][2], y[1][3]);
+  }
+  uint8_t* tail = out + 2 * a.kv_heads * part;
+  if (unit == 0) reinterpret_cast<float*>(tail)[(value ? a.kv_heads : 0) + h] = scale;
+  if (h == 0 && !value) {   // the token count and the zeros behind it, fewer words than a block has lanes
+    int32_t* words = reinterpret_cast<int32_t*>(tail + 8 * a.kv_heads);
+    const int n = (int)(out + a.row_bytes - reinterpret_cast<uint8_t*>(words)) / 4;
+    if (unit < n) words[unit] = unit == 0 ? count : 0;
+  }
+}
+
+// Units of a scale block, and workgroups of either side.
+static int pack_units(const PackDev& a) { return a.block_tokens * a.head_dim / 8; }
+long long pack_heads_blocks(const PackDev& a) {
+  const long long per = kPackThreads / pack_units(a);
+  return ((long long)a.n * a.layers * a.kv_heads + per - 1) / per;
+}
+
 // Rotary positions of [n][heads][dim] tensors. A workgroup takes `tokens` tokens
 // and a range of heads, V pairs of a row a unit, U units a lane: their loads are
 // on their way while the tokens' sines and cosines are computed, once each, into
@@ -335,7 +412,14 @@ static hipError_t pack_of(const PackDev& a, const RotaryDev& rot, hipStream_t s)
     if (a.aligned) k_pack_latent<T, true><<<blocks, 256, 0, s>>>(a, rot, by_layers);
     else k_pack_latent<T, false><<<blocks, 256, 0, s>>>(a, rot, by_layers);
   } else {
-    k_pack_heads<T><<<rows * 2 * a.kv_heads, kWave, 0, s>>>(a, rot);
+    const int units = pack_units(a), per = kPackThreads / units;
+    const uint32_t blocks = (uint32_t)pack_heads_blocks(a);
+    // entries that `per` scale blocks touch, which need not begin with a row's first
+    const size_t entries = (per + a.kv_heads - 1) / a.kv_heads + 1;
+    const size_t lds = a.positions ? entries * a.block_tokens * (a.head_dim / 2) * sizeof(float2) : 0;
+    const FastDiv by_heads(a.kv_heads), by_layers(a.layers);
+    if (a.aligned) k_pack_heads<T, true><<<2 * blocks, kPackThreads, lds, s>>>(a, rot, units, blocks, by_heads, by_layers);
+    else k_pack_heads<T, false><<<2 * blocks, kPackThreads, lds, s>>>(a, rot, units, blocks, by_heads, by_layers);
   }
   return hipGetLastError();
 }

@@ -79,6 +79,7 @@ struct RotateDev {
 };
 
 hipError_t launch_pack(const PackDev& a, const RotaryDev& rot, int type, hipStream_t s);
+long long pack_heads_blocks(const PackDev& a);   // workgroups of heads rows, of either side
 long long plan_rotate(RotateDev* a);   // fills the workgroup's part in; how many there are
 hipError_t launch_rotate(const RotateDev& a, const RotaryDev& rot, int type, hipStream_t s);
 

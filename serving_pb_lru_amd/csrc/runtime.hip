@@ -1129,8 +1129,9 @@ int ula_pack_rows(const ula_pack_args* args, void* rows_dev, uint64_t stream) {
   const bool latent = u.rows.kind == ULA_ROWS_LATENT;
   if (latent && u.count) return ULA_EINVAL;
   const int64_t rows = (int64_t)u.n * u.layers;
-  // a launch has fewer than 2^32 threads: one wave per row, or per row and KV head, twice
-  if (rows * (latent ? 1 : 2 * u.rows.kv_heads) >= (1ll << 26)) return ULA_EINVAL;
+  // a launch has fewer than 2^32 threads: a wave per row, or 8 to 128 per row, KV head and side
+  if (rows >= (1ll << 26)) return ULA_EINVAL;
+  if (!latent && 2 * rows * u.rows.kv_heads * (u.rows.block_tokens * u.rows.head_dim / 8) >= (1ll << 32)) return ULA_EINVAL;
   RotaryDev rot{};
   if (u.positions && !rotary_dev(u.rotary, latent ? kRope / 2 : u.rows.head_dim / 2, &rot)) return ULA_EINVAL;
   if (rows == 0) return ULA_OK;
@@ -1149,7 +1150,14 @@ int ula_pack_rows(const ula_pack_args* args, void* rows_dev, uint64_t stream) {
   a.n = u.n;
   a.layers = u.layers;
   a.latent = latent;
-  a.aligned = (uintptr_t)u.a % 16 == 0 && u.a_stride[0] * size % 16 == 0 && u.a_stride[1] * size % 16 == 0;
+  if (latent) {
+    a.aligned = (uintptr_t)u.a % 16 == 0 && u.a_stride[0] * size % 16 == 0 && u.a_stride[1] * size % 16 == 0;
+  } else {   // vectors of four pairs, as a turn's
+    const int vec = (rot.interleaved ? 8 : 4) * size;
+    a.aligned = ((uintptr_t)u.a | (uintptr_t)u.b) % vec == 0;
+    for (int i = 0; i < 4; ++i)
+      if (u.a_stride[i] * size % vec || u.b_stride[i] * size % vec) a.aligned = 0;
+  }
   a.kv_heads = u.rows.kv_heads;
   a.head_dim = u.rows.head_dim;
   a.block_tokens = u.rows.block_tokens;

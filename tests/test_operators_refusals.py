@@ -83,7 +83,7 @@ def test_pack_refuses():
                dict(type=ula.FP32, a=P + 2), dict(type=ula.FP32, b=P + 2), dict(count=P),
                dict(n=1 << 13, layers=1 << 13), dict(fmt=ula.RowFormat(1, 1, 65, 1)),
                dict(positions=P + 2, rotary=(1, (32,))), dict(fmt=head_rows(1, 64), count=P + 1),
-               dict(fmt=head_rows(8, 128), n=1 << 22, layers=1)]:
+               dict(fmt=head_rows(8, 128), n=1 << 25, layers=1)]:
         assert call(pack_args(**kw)) == EINVAL, kw
     assert call(pack_args(), None) == EINVAL and call(pack_args(), P + 8) == EINVAL
     for rot in BAD_ROTARY:

@@ -208,6 +208,37 @@ def test_heads_rows(n, layers, kv, dim, block, kind, axes, inter, part):
         check_codes(codes, ref.f32_at(rows, 2 * size + 4 * kv * which, kv), per_head(x), per_head(d))
 
 
+@pytest.mark.parametrize("kv,dim,block", [(1, 64, 1), (8, 128, 1), (3, 64, 8), (1, 64, 16), (1, 128, 8), (2, 128, 4)])
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+def test_heads_values_at_the_ends(kv, dim, block, kind):
+    """Infinities, NaN, zeros and subnormals in some scale blocks beside ordinary ones, of less and of
+    more than a wave; strided sources give the same rows."""
+    import torch
+    from serving_pb_lru_amd import head_rows, pack_rows
+    rng = np.random.default_rng([kv, dim, block])
+    info = torch.finfo(torch_type(kind))
+    n = 40
+    x = rng.standard_normal((2, n, 1, block, kv, dim))
+    x[0, 3, 0, :, 0] = 0.0
+    x[0, 5, 0, 0, 0, 1], x[0, 7, 0, block - 1, kv - 1, dim - 1], x[1, 9, 0, 0, 0, 0] = np.inf, -np.inf, np.nan
+    x[0, 11, 0, :, 0] = np.nan
+    x[1, 13, 0, :, kv - 1] *= info.tiny
+    x[0, 15] = info.max
+    t = on_gpu(x, kind)
+    fmt = head_rows(kv, dim, block)
+    rows = pack_rows(fmt, t[0], t[1])
+    part = kv * dim * block
+    got = rows.cpu().numpy()
+    for side in (0, 1):
+        v = f64(t[side]).transpose(0, 1, 3, 2, 4).reshape(n, 1, kv, block * dim)
+        codes = got[..., side * part:(side + 1) * part].reshape(n, 1, kv, block * dim)
+        check_codes(codes, ref.f32_at(got, 2 * part + 4 * kv * side, kv), v)
+    wide = torch.zeros((n, 1, block, kv, dim + 3), dtype=t.dtype, device="cuda")
+    wide[..., 1:dim + 1] = t[0]
+    swapped = t[1].transpose(2, 3).contiguous().transpose(2, 3)
+    assert torch.equal(pack_rows(fmt, wide[..., 1:dim + 1], swapped), rows)
+
+
 # tokens, heads, dim, type, axes, interleaved, inverse, far
 ROTATE = [(1, 1, 2, "fp32", 1, True, False, False), (3, 5, 6, "bf16", 1, False, False, True),
           (16, 128, 64, "bf16", 1, True, False, False), (100, 3, 126, "fp16", 2, True, True, False),
