@@ -53,16 +53,28 @@ __device__ __forceinline__ float to_e4m3_range(float x, float scale) {
 __device__ __forceinline__ float2 cos_sin_turns(double turns) {
   turns -= rint(turns);                        // [-1/2, 1/2]
   const double q = rint(4.0 * turns);          // quarter turns
-  const float x = (float)((turns - 0.25 * q) * 6.283185307179586476925);   // [-pi/4, pi/4]
+  const float x = (float)(__builtin_fma(q, -0.25, turns) * 6.283185307179586476925);   // [-pi/4, pi/4]
   const float y = x * x;
-  const float s = x + x * y * (-1.0f / 6 + y * (1.0f / 120 + y * (-1.0f / 5040 + y * (1.0f / 362880))));
-  const float c = 1.0f + y * (-0.5f + y * (1.0f / 24 + y * (-1.0f / 720 + y * (1.0f / 40320 + y * (-1.0f / 3628800)))));
+  // every fused step spelled out, so that all kernels get the same bits
+  auto f = [](float a, float b, float c) { return __builtin_fmaf(a, b, c); };
+  const float s = f(x * y, f(y, f(y, f(y, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), x);
+  const float c = f(y, f(y, f(y, f(y, f(y, -1.0f / 3628800, 1.0f / 40320), -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
   switch ((int)q & 3) {
     case 0: return make_float2(c, s);
     case 1: return make_float2(-s, c);
     case 2: return make_float2(-c, -s);
     default: return make_float2(s, -c);
   }
+}
+
+// The pair (p, q) turned by (cos, sin), with the rounding steps spelled out: the
+// compiler's own fusing differs from kernel to kernel, and strides must not change
+// bits. (The empty assembly keeps a following conversion to fp16 out of the fma:
+// the fused form rounds once, the others twice, which differs in one of 10^5.)
+__device__ __forceinline__ float2 turned(float p, float q, float2 cs) {
+  float a = __builtin_fmaf(p, cs.x, -(q * cs.y)), b = __builtin_fmaf(p, cs.y, q * cs.x);
+  asm("" : "+v"(a), "+v"(b));
+  return make_float2(a, b);
 }
 
 // Turn of pair i at a token whose positions start at pos.
@@ -121,8 +133,9 @@ __global__ __launch_bounds__(256) void k_pack_latent(PackDev a, RotaryDev rot, F
       float y0 = r0, y1 = r1;
       if (a.positions) {
         const float2 cs = rotary_of(rot, a.positions + (size_t)entry * rot.axes, pair);
-        y0 = r0 * cs.x - r1 * cs.y;
-        y1 = r0 * cs.y + r1 * cs.x;
+        const float2 y = turned(r0, r1, cs);
+        y0 = y.x;
+        y1 = y.y;
       }
       __bf16* ro = reinterpret_cast<__bf16*>(a.rows + (size_t)row * kLatentRow + kRopeAt);
       ro[at0] = (__bf16)y0;
@@ -190,9 +203,9 @@ struct Pairs {
   __device__ __forceinline__ void turn(const float2* cs) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const float p = to_f32(a[j]), q = to_f32(b[j]);
-      a[j] = (T)(p * cs[j].x - q * cs[j].y);
-      b[j] = (T)(p * cs[j].y + q * cs[j].x);
+      const float2 y = turned(to_f32(a[j]), to_f32(b[j]), cs[j]);
+      a[j] = (T)y.x;
+      b[j] = (T)y.y;
     }
   }
   __device__ __forceinline__ void store(T* y, int first, int pairs, bool interleaved) const {
@@ -286,9 +299,9 @@ __global__ __launch_bounds__(kPackThreads) void k_pack_heads(PackDev a, RotaryDe
     const float2* cs = s_cs + ((size_t)(entry - entry0) * block + tok) * half + pair;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float p = y[0][j], q = y[1][j];
-      y[0][j] = p * cs[j].x - q * cs[j].y;
-      y[1][j] = p * cs[j].y + q * cs[j].x;
+      const float2 t = turned(y[0][j], y[1][j], cs[j]);
+      y[0][j] = t.x;
+      y[1][j] = t.y;
     }
   }
   auto largest = [&](float v) {                                   // of the scale block; every lane calls it

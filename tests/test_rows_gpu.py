@@ -243,7 +243,7 @@ def test_heads_values_at_the_ends(kv, dim, block, kind):
 ROTATE = [(1, 1, 2, "fp32", 1, True, False, False), (3, 5, 6, "bf16", 1, False, False, True),
           (16, 128, 64, "bf16", 1, True, False, False), (100, 3, 126, "fp16", 2, True, True, False),
           (257, 33, 128, "fp32", 3, False, True, True), (7, 9, 256, "fp16", 1, False, False, False),
-          (600, 1, 40, "bf16", 3, True, False, True), (2, 700, 256, "fp32", 2, False, False, False)]
+          (165, 5, 256, "fp16", 3, False, False, True), (600, 1, 40, "bf16", 3, True, False, True), (2, 700, 256, "fp32", 2, False, False, False)]
 
 
 @pytest.mark.parametrize("n,heads,dim,kind,axes,inter,inverse,far", ROTATE)
