@@ -251,9 +251,11 @@ def _same_device(first, *others) -> None:
 
 class _On:
     """Makes a tensor's device current and `stream` (None: that device's current stream) the
-    stream that what is allocated inside belongs to; as a context it gives the stream's handle."""
+    stream that what is allocated inside belongs to; as a context it gives the stream's handle.
+    On another stream than the caller's, `inputs` are kept from reuse until that stream is done
+    with them, and what give() names until the caller's stream is."""
 
-    def __init__(self, device, stream):
+    def __init__(self, device, stream, *inputs):
         import torch
         if getattr(stream, "device", device) != device:
             raise ValueError(f"tensors on {device}, a stream of {stream.device}")
@@ -268,6 +270,15 @@ class _On:
                 stream = (torch.cuda.ExternalStream(self.handle, device=device) if self.handle
                           else torch.cuda.default_stream(device))
             self.ctx = torch.cuda.stream(stream)
+            self.caller = torch.cuda.current_stream(device)
+            for t in inputs:
+                if t is not None:
+                    t.record_stream(stream)
+
+    def give(self, *outputs) -> None:
+        if self.ctx is not None:
+            for t in outputs:
+                t.record_stream(self.caller)
 
     def __enter__(self) -> int:
         if self.ctx is not None:
@@ -341,9 +352,11 @@ def pack_rows(fmt: RowFormat, a, b, positions=None, sections=None, theta: float 
     args.n, args.layers = n, layers
     _keep, args.positions, args.rotary = _rotary(positions, sections, theta, interleaved, pairs, lead, "pack_rows")
     _same_device(a, b, positions, counts, out)
-    with _On(a.device, stream) as s:
+    on = _On(a.device, stream, a, b, positions, counts, out)
+    with on as s:
         if out is None:
             out = torch.empty((n, layers, row_bytes), dtype=torch.uint8, device=a.device)
+            on.give(out)
         ptr = _dev(out, "uint8", n * layers * row_bytes, "pack_rows out")
         _check(lib().ula_pack_rows(ctypes.byref(args), ptr, s), "ula_pack_rows")
     return out
@@ -363,9 +376,11 @@ def rotate(x, positions, sections=None, theta: float = 10000.0, interleaved: boo
         raise ValueError("rotate positions: required")
     args.inverse = int(bool(inverse))
     _same_device(x, positions, out)
-    with _On(x.device, stream) as s:
+    on = _On(x.device, stream, x, positions, out)
+    with on as s:
         if out is None:
             out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            on.give(out)
         args.out, code, st_out = _tensor(out, x.shape, "rotate out")
         if code != args.type:
             raise ValueError(f"rotate out: dtype {out.dtype}, expected {x.dtype}")
@@ -508,15 +523,18 @@ class Engine:
         args.q_set_stride, args.q_head_stride, args.heads = st[0], st[1], heads
         args.scale = 1.0 / width ** 0.5 if scale is None else scale
         _same_device(q, sel, out, lse, self.ws)
-        with _On(q.device, stream) as s:
+        on = _On(q.device, stream, q, sel, out, lse)
+        with on as s:
             if out is None:
                 out = torch.empty((n_sets, heads, back), dtype=q.dtype, device=q.device)
+                on.give(out)
             args.out, code, st = _tensor(out, (n_sets, heads, back), "ula_attend out")
             if code != args.type:
                 raise ValueError(f"ula_attend out: dtype {out.dtype}, expected {q.dtype}")
             args.out_set_stride, args.out_head_stride = st[0], st[1]
             if lse is None:
                 lse = torch.empty((n_sets, heads), dtype=torch.float32, device=q.device)
+                on.give(lse)
             args.lse = _dev(lse, "float32", n_sets * heads, "ula_attend lse")
             args.workspace_bytes = lib().ula_attend_bytes(ctypes.byref(fmt), n_sets, k, heads)
             if args.workspace_bytes:

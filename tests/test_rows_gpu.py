@@ -383,3 +383,29 @@ def test_two_streams():
         second = rotate(x, pos, inverse=True, stream=b)
         torch.cuda.synchronize()
         assert torch.equal(first, want[0]) and torch.equal(second, want[1])
+
+
+def test_tensors_dropped_while_another_stream_reads_them():
+    """Inputs freed right after a call on a busy stream are not reused before it has read them, nor a
+    result that the caller's stream still reads."""
+    import torch
+    from serving_pb_lru_amd import rotate
+    pos = torch.arange(64, dtype=torch.int32, device="cuda")
+    x = torch.randn((64, 16, 128), device="cuda")
+    want = rotate(x, pos)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)               # about 0.1 s
+    got = rotate(x, pos, stream=side)
+    del x
+    others = [torch.full((64, 16, 128), 7.0, device="cuda") for _ in range(4)]
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got, want)
+    torch.cuda._sleep(200_000_000)
+    copy = got.clone()
+    del got
+    with torch.cuda.stream(side):
+        others += [torch.full((64, 16, 128), 9.0, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want) and len(others) == 8
