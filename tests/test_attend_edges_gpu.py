@@ -341,6 +341,34 @@ def test_rows_past_32_bits():
         eng.close()
 
 
+def test_groups_and_layers():
+    """Two groups of three layers with rows and steps of their own, read layer by layer."""
+    import torch
+    from serving_pb_lru_amd import Engine, latent_rows
+    fmt = latent_rows()
+    rng = np.random.default_rng(19)
+    rows = [latent_rows_of(rng, 90, 3) for _ in range(2)]
+    eng = Engine(num_groups=2, layers=3, row_bytes=656, ring=3, logical_capacity=90, gpu_slots=64, host_slots=64,
+                 max_sets=3, max_k=20)
+    try:
+        for g in range(2):
+            eng.append(g, rng.permutation(90).astype(np.int32)[:0], np.zeros((0, 3, 656), np.uint8))
+            eng.append(g, np.arange(90, dtype=np.int32), rows[g])
+        for t in range(3):
+            sels = [selection(rng, 90, 3, 20, 2) for _ in range(2)]
+            dev = [torch.from_numpy(x).cuda() for x in sels]
+            for g in range(2):
+                eng.step(g, dev[g])
+            for layer in range(3):
+                for g in (1, 0):
+                    q = queries(rng, fmt, 3, 7)
+                    out, lse = eng.attend(g, layer, dev[g], q, fmt)
+                    check(fmt, rows[g], layer, sels[g], q, 1 / 24, out, lse, "bf16")
+        eng.sync()
+    finally:
+        eng.close()
+
+
 def test_a_stream_of_another_device_is_refused():
     import torch
     from serving_pb_lru_amd import rotate
