@@ -20,8 +20,9 @@
 //     them before it adds them up: log-sums were off by up to 5e-4, this way by
 //     4e-6.)
 //   - second product: codes widened to fp16, and p s_b rounded to fp16. m follows
-//     the largest p_j max_b s_bj, which stays within 2^7..2^15, so the rounding is
-//     at most 2^-11 of the value, or 2^-25 (2^-32 of the largest) for small ones.
+//     the largest p_j max_b s_bj of any key, which stays within 2^7..2^15 (a scale
+//     below 2^-60 counts as that), so the rounding is at most 2^-11 of the value, or
+//     2^-25 (2^-32 of the largest) for small ones.
 // Both products have 32-bit accumulators.
 //
 // Layout. Both products are taken transposed: S^T = K Q^T puts heads in the
@@ -122,7 +123,16 @@ constexpr int kSecondWaves = kWaves - kFirstWaves;
 constexpr int kLoadsPerWave = (kTileLoads + kLatentGroups) / kSecondWaves;   // a second wave's vector loads per tile
 static_assert(kSecondWaves == kLatentGroups, "one scale block per second wave");
 
-template <int HEADS, int TILES>
+// The bf16 values whose sum a 16-bit rotary channel of q is.
+template <typename Q8>
+constexpr int kRopeParts = std::is_same_v<Q8, bf16x8> ? 1 : 2;
+// fp16 queries of 64 heads: the second rotary parts of a first wave's last 16 heads wait in LDS, since
+// registers for them are spilled, and read back in every tile (384 sets of 2047 keys and 128 heads:
+// 345 us with 16 bytes spilled, 304 us so).
+template <typename Q8, int HT>
+constexpr bool kRestInLds = HT == 2 && kRopeParts<Q8> == 2;
+
+template <int HEADS, int TILES, bool REST>
 struct LatentLds {
   alignas(1024) uint8_t ring[TILES][kTileBytes];
   // p x scale of two tiles: [block][head][key], key chunk c (8 keys) of head h at c ^ ((h >> 2) & 3)
@@ -131,6 +141,7 @@ struct LatentLds {
   float alpha[2][HEADS];                    // factor of O before the tile's second product
   alignas(16) uint32_t moved[2][4];         // whether any head of a first wave has a factor other than 1
   alignas(8) float top[2][HEADS][2];        // of two tiles: the largest logarithm of p x scale, of either half of the keys
+  bf16x8 rest[REST ? kFirstWaves / 2 : 0][kRope / 32][kWave];
   const uint8_t* row[kAttendKeys];          // each key's row in this layer; zeros for padding
   uint32_t live[kAttendKeys / kTileKeys + 2];   // bit per key: not padding; none behind the last tile
   int ok;
@@ -157,15 +168,14 @@ struct QueryRaw {
 // bf16, so fp16 ones become the sum of two bf16 values (8 + 8 bits hold their 11).
 template <typename Q8>
 struct QueryOperand {
-  static constexpr int kRopeParts = std::is_same_v<Q8, bf16x8> ? 1 : 2;
   Q8 x[kLatent / 32];
-  bf16x8 rope[kRopeParts][kRope / 32];
+  bf16x8 rope[kRopeParts<Q8>][kRope / 32];
   __device__ __forceinline__ void take(const QueryRaw<Q8>& raw) {
 #pragma unroll
     for (int t = 0; t < kLatent / 32; ++t) x[t] = raw.x[t];
 #pragma unroll
     for (int j = 0; j < kRope / 32; ++j) {
-      if constexpr (kRopeParts == 1) {
+      if constexpr (kRopeParts<Q8> == 1) {
         rope[0][j] = raw.rope[j];
       } else {
 #pragma unroll
@@ -181,7 +191,7 @@ struct QueryOperand {
 #pragma unroll
     for (int j = 0; j < kRope / 32; ++j)
 #pragma unroll
-      for (int i = kRopeParts - 1; i >= 0; --i) s = mfma16(kr[j], rope[i][j], s);
+      for (int i = kRopeParts<Q8> - 1; i >= 0; --i) s = mfma16(kr[j], rope[i][j], s);
     return s;
   }
   // product of a block's keys, widened, 32 channels at a time
@@ -240,7 +250,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
   constexpr int CT = kScaleGroup / 32;            // 32-channel tiles of a second wave's O
   static_assert(2 * kHeads == 16 * HT * kFirstWaves, "every head has two waves in the first product");
   static_assert(TILES >= 4, "a tile on its way beside the three in use");
-  __shared__ LatentLds<kHeads, TILES> s;
+  __shared__ LatentLds<kHeads, TILES, kRestInLds<Q8, HT>> s;
   static_assert(sizeof(s) <= 160 * 1024, "LDS of a compute unit");
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);   // uniform: its branches are scalar
@@ -413,6 +423,11 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
       m[i] = -__builtin_inff();
       l[i] = 0.0f;
     }
+    if constexpr (kRestInLds<Q8, HT>) {            // read a barrier later
+      if (key_half == 0)
+#pragma unroll
+        for (int j = 0; j < kRope / 32; ++j) s.rest[wave / 2][j][lane] = q[HT - 1].rope[1][j];
+    }
     const float c_log2 = a.scale_log2;
     // Register r in quad x is key 8 x + 4 key_half + r. koff: this lane's key as an
     // operand, piece quad of a scale block; piece 4 + quad is ^ 64.
@@ -429,6 +444,10 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
       const uint32_t krow64 = opaque(krow ^ 64);
       const uint32_t scale = opaque(lds_address(s.scale) + (tile % TILES * kLatentGroups * kTileKeys + 8 * quad + 4 * key_half) * 4);
       bf16x8 kr[2] = {lds_get<bf16x8>(krow + kRopeAt), lds_get<bf16x8>(krow64 + kRopeAt)};
+      if constexpr (kRestInLds<Q8, HT>)
+#pragma unroll
+        for (int j = 0; j < kRope / 32; ++j)
+          q[HT - 1].rope[1][j] = lds_get<bf16x8>(lds_address(s.rest) + ((wave / 2 * (kRope / 32) + j) * kWave + lane) * 16);
       const uint32_t live = __builtin_amdgcn_readfirstlane(s.live[tile]) >> (8 * quad + 4 * key_half);
       f32x4 part[HT][kLatentGroups], rope[HT];
 #pragma unroll
@@ -441,23 +460,32 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
       }
 #pragma unroll
       for (int i = 0; i < HT; ++i) rope[i] = q[i].rope_product(kr);
-      float big = 0x1p-60f;                       // largest scale of the lane's keys
-#pragma unroll
-      for (int b = 0; b < kLatentGroups; ++b)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) big = fmaxf(big, fabsf(sc[b][r]));
 #pragma unroll
       for (int i = 0; i < HT; ++i) {
         S[i] = rope[i];
 #pragma unroll
         for (int b = 0; b < kLatentGroups; ++b) S[i] += sc[b] * part[i][b];
+      }
+      __builtin_amdgcn_sched_barrier(0);          // the partial products' registers are free from here
+      // each key's largest scale as a power of two, from above: a key of large weight must not take a
+      // neighbour's (p x scale would then vanish in fp16); scales below 2^-60 count as that
+      float power[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float big = 0x1p-60f;
+#pragma unroll
+        for (int b = 0; b < kLatentGroups; ++b) big = fmaxf(big, fabsf(sc[b][r]));
+        power[r] = (float)__builtin_amdgcn_frexp_expf(big);
+      }
+#pragma unroll
+      for (int i = 0; i < HT; ++i) {
         float top = -__builtin_inff();
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           S[i][r] = live & (1u << r) ? S[i][r] * c_log2 : -__builtin_inff();
-          top = fmaxf(top, S[i][r]);
+          top = fmaxf(top, S[i][r] + power[r]);
         }
-        top = max_quads(top + (float)__builtin_amdgcn_frexp_expf(big));
+        top = max_quads(top);
         if (quad == 0) lds_put(at_top + (tile & 1) * kHeads * 8 + 16 * i * 8 + 4 * key_half, top);
       }
     };
