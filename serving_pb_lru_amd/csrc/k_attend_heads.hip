@@ -9,11 +9,11 @@
 // instructions and the scales are applied in 32 bits, to S and to p. p vs is then
 // rounded to fp16 (at most 2^-11 of its value). m follows the largest p vs, not
 // the largest p, so that fp16's range serves scales from 2^-60 to 2^80 (p itself
-// stays in the range of 32 bits): the largest p vs lies between 2^7 and 2^15, and one below fp16's least value (its
-// rounding: 2^-25) is off by less than 2^-32 of it. For fp16 results, which show
-// that rounding (their own is as large), what it leaves goes through a second
-// product: off by 2.1e-4 of their size instead of 3.4e-4, 21 -> 22 us for 64 sets x
-// 500 blocks of 8 tokens x 2 KV heads of 64.
+// stays in the range of 32 bits): the largest p vs lies between 2^7 and 2^15, and
+// one below fp16's least value (its rounding: 2^-25) is off by less than 2^-32 of
+// it. For fp16 results, which show that rounding (their own is as large), what it
+// leaves goes through a second product: off by 2.1e-4 of their size instead of
+// 3.4e-4, 21 -> 22 us for 64 sets x 500 blocks of 8 tokens x 2 KV heads of 64.
 //
 // Bound by HBM: 2 x heads / kv_heads operations per byte. So a wave works by
 // itself, on one KV head's up to 16 query heads and one range of tokens, with
