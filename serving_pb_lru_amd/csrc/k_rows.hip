@@ -381,7 +381,7 @@ template <typename T, int V, int U>
 __global__ __launch_bounds__(256) void k_rotate(RotateDev a, RotaryDev rot, FastDiv by_units, FastDiv by_heads) {
   extern __shared__ float2 s_cs[];   // [tokens][pairs]
   const int pairs = a.dim / 2, units = pairs / V;
-  const int head_parts = (a.heads + a.heads_per_block - 1) / a.heads_per_block;
+  const int head_parts = 1 + (a.heads - 1) / a.heads_per_block;   // heads may be near 2^31
   const int tok0 = blockIdx.x / head_parts * a.tokens_per_block;
   const int head0 = blockIdx.x % head_parts * a.heads_per_block;
   const int tokens = min(a.tokens_per_block, a.n - tok0);
@@ -452,7 +452,7 @@ long long plan_rotate(RotateDev* a) {
   a->heads_per_block = std::max(1, std::min(a->heads, kUnits / units));
   a->tokens_per_block = std::max(1, std::min(a->n, std::min(kUnits / (units * a->heads_per_block), 4096 / pairs)));
   return (long long)((a->n + (long long)a->tokens_per_block - 1) / a->tokens_per_block) *
-         ((a->heads + a->heads_per_block - 1) / a->heads_per_block);
+         (1 + (a->heads - 1) / a->heads_per_block);
 }
 
 template <typename T, int V>
