@@ -446,7 +446,7 @@ typedef struct {
   ula_row_format rows;       /* the group's rows; its bytes must equal the configuration's row_bytes */
   int32_t type;              /* of q and out: ULA_BF16 or ULA_FP16 */
   int32_t heads;             /* query heads, >= 1; heads rows: a multiple of kv_heads */
-  float scale;               /* factor of the logits, finite */
+  float scale;               /* factor of the logits, finite (times log2(e) too) */
   const void* q;             /* [n_sets][heads][576 (latent) or head_dim], last dimension contiguous */
   int64_t q_set_stride;      /* strides in elements */
   int64_t q_head_stride;

@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <limits>
 #include <mutex>
 #include <new>
 #include <string>
@@ -1249,7 +1250,8 @@ int ula_attend(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32
   if (!plan_attend(&u.rows, n_sets, k, u.heads, &plan, &width)) return ULA_EINVAL;
   if (ula_row_format_bytes(&u.rows) != (size_t)ctx->dims.row_bytes) return ULA_EINVAL;
   if (u.type != ULA_BF16 && u.type != ULA_FP16) return ULA_EINVAL;
-  if (!std::isfinite(u.scale)) return ULA_EINVAL;
+  const double scale_log2 = u.scale * 1.4426950408889634;   // what the kernels multiply by, in 32 bits
+  if (!(std::fabs(scale_log2) <= std::numeric_limits<float>::max())) return ULA_EINVAL;   // NaN too
   const size_t need = attend_bytes(plan, n_sets, u.heads, width);
   if (n_sets > 0) {
     if ((k > 0 && !sel_dev) || !u.q || !u.out) return ULA_EINVAL;
@@ -1279,7 +1281,7 @@ int ula_attend(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32
   a.out_set_stride = u.out_set_stride;
   a.out_head_stride = u.out_head_stride;
   a.want_flag = (long long)gh.steps;
-  a.scale_log2 = (float)(u.scale * 1.4426950408889634);
+  a.scale_log2 = (float)scale_log2;
   a.k = k;
   a.heads = u.heads;
   a.layer = layer;
