@@ -474,21 +474,25 @@ size_t ula_attend_bytes(const ula_row_format* rows, int32_t n_sets, int32_t k, i
  * softmax weights times value scales are rounded to fp16 before the second
  * product (2^-11 of each, or 2^-32 of the set's largest; value scales are meant to
  * lie between 2^-60 and 2^80: smaller ones count as 2^-60 in that largest, and with
- * larger ones small weights are lost), results once to the type of out. A NaN or an infinite logit makes that head's outputs NaN; no unselected
- * row is ever read. The order of the sums
- * depends on the sizes alone, so the same call gives the same bits.
+ * larger ones small weights are lost), results once to the type of out. A logit
+ * that is NaN or +infinity makes that head's outputs and log-sum NaN; an entry of
+ * logit -infinity has no weight, and a set with no other gives 0 and -inf. No
+ * unselected row is ever read. The order of the sums depends on the sizes alone, so
+ * the same call gives the same bits.
  * Results split over several workgroups are joined through the workspace, which
  * belongs to the call until the stream has run it: calls that may run at the
  * same time need workspaces of their own. q, out, lse and the workspace must not
- * overlap, nor rows of out (ULA_EINVAL if one of its strides says so). q and out rows whose pointer and strides keep them 16-byte aligned are
- * read and written in vectors, others element by element.
+ * overlap, nor rows of out (ULA_EINVAL if one of its strides says so). q and out
+ * rows whose pointer and strides keep them 16-byte aligned are read and written in
+ * vectors, others element by element.
  * Which entries, streams and errors: as for ula_gather (the selection is looked
  * up through the group's last step where it is that step's, else through the
  * mapping table; on another stream the call must be ordered after the step; the
  * library orders the group's later row moves after it). It may not be captured
  * into a graph, since the step it belongs to is fixed at the call: ULA_EINVAL.
  * Host errors: ULA_EINVAL (also n_sets * heads >= 2^24, heads > 2^16, latent rows
- * with k > 2^21, heads rows with k * block_tokens >= 2^30), ULA_ESTATE,
+ * with k > 2^21, heads rows with k * block_tokens >= 2^30, or a launch of 2^23
+ * workgroups, which n_sets * heads * (1 + k / 2048) < 2^22 never makes), ULA_ESTATE,
  * ULA_ENOTRESIDENT (no step yet), ULA_EHIP. Device errors (reported by ula_sync):
  * ULA_ENOTRESIDENT, ULA_ERANGE; an entry with such an error counts as padding. */
 int ula_attend(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32_t k,
