@@ -249,6 +249,16 @@ def _same_device(first, *others) -> None:
             raise ValueError(f"tensors on {first.device} and {t.device}")
 
 
+def _no_gradient(what: str, *tensors) -> None:
+    """Refuses tensors whose history autograd would expect the result to carry: these calls record none."""
+    import torch
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if getattr(t, "requires_grad", False):
+                raise ValueError(f"{what}: a tensor requires a gradient, which this call does not record "
+                                 "(detach it, or call under torch.no_grad())")
+
+
 class _On:
     """Makes a tensor's device current and `stream` (None: that device's current stream) the
     stream that what is allocated inside belongs to; as a context it gives the stream's handle.
@@ -320,8 +330,10 @@ def pack_rows(fmt: RowFormat, a, b, positions=None, sections=None, theta: float 
     [n][layers][512] and rotary channels [n][layers][64], or for heads rows keys and values
     [n][layers][block_tokens][kv_heads][head_dim] with `counts` (int32 [n], tokens in use).
     With int32 positions ([n][axes], heads rows [n][block_tokens][axes]) the rotary channels, or
-    the whole keys, are turned first; sections: pairs of each axis."""
+    the whole keys, are turned first; sections: pairs of each axis. No gradient is recorded:
+    inputs that require one are refused."""
     import torch
+    _no_gradient("pack_rows", a, b)
     args = UlaPackArgs()
     args.rows = fmt
     row_bytes = fmt.row_bytes
@@ -364,9 +376,11 @@ def pack_rows(fmt: RowFormat, a, b, positions=None, sections=None, theta: float 
 
 def rotate(x, positions, sections=None, theta: float = 10000.0, interleaved: bool = False, inverse: bool = False,
            out=None, stream=None):
-    """x [n][heads][dim] turned by int32 positions [n][axes] (or [n]); inverse turns back. out:
-    a tensor of x's shape and dtype, x itself for in place."""
+    """x [n][heads][dim] turned by int32 positions [n][axes] (or [n]); inverse turns back,
+    which is also the gradient of the turn; it is not recorded, so an x that requires one is refused.
+    out: a tensor of x's shape and dtype, x itself for in place."""
     import torch
+    _no_gradient("rotate", x, out)
     args = UlaRotateArgs()
     args.x, args.type, st = _tensor(x, (None, None, None), "rotate x")
     args.n, args.heads, args.dim = x.shape
@@ -508,8 +522,10 @@ class Engine:
         """(out, lse): attention of q [n_sets][heads][576 or head_dim] (bf16 or fp16) over the selected
         entries' rows of one layer, which are in format `fmt`. out [n_sets][heads][512 or head_dim] in
         q's dtype, lse fp32 [n_sets][heads]. scale: factor of the logits, default 1 / sqrt(q's width).
-        The workspace of a split call is allocated here, on the call's stream."""
+        The workspace of a split call is allocated here, on the call's stream. No gradient is recorded:
+        a q that requires one is refused."""
         import torch
+        _no_gradient("ula_attend", q, out, lse)
         n_sets, k = _sets(sel)
         args = UlaAttendArgs()
         args.rows = fmt
