@@ -517,7 +517,6 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
         const uint32_t pw = opaque(pwrite + (buf * kLatentGroups * kHeads + 16 * i) * kTileKeys * 2);
 #pragma unroll
         for (int b = 0; b < kLatentGroups; ++b) {
-          typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
           f16x4 w;
 #pragma unroll
           for (int r = 0; r < 4; ++r) w[r] = (_Float16)(p[r] * sc[b][r]);

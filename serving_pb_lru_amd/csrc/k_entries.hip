@@ -29,7 +29,8 @@ __device__ __forceinline__ const uint8_t* rows_at(const GroupDev& g, uint32_t lo
 // (app_dst[i]: a free slot, so never one that is read here), published as
 // address dst0 + i. One read and one write of every row; four pieces per lane in
 // flight. The loads of a location are the same for a row's 16-byte pieces and
-// hit the caches.
+// hit the caches. (Pieces are counted in 32 bits: a configuration's max_append
+// has fewer than 2^31, and a step of the loop is at most 2^23.)
 __global__ __launch_bounds__(256) void k_fork_place(GroupDev g, int32_t src0, int32_t dst0, int32_t n,
                                                     FastDiv per_slot) {
   if (status_of(g.ctr)) return;
@@ -46,7 +47,7 @@ __global__ __launch_bounds__(256) void k_fork_place(GroupDev g, int32_t src0, in
     for (int u = 0; u < U; ++u) {
       const uint32_t idx = base + u * stride;
       some[u] = false;
-      if (idx >= base && idx < total) {   // the sum may wrap past 32 bits
+      if (idx < total) {
         i[u] = per_slot.div(idx);
         const uint32_t loc = g.map[src0 + (int32_t)i[u]];
         d[u] = g.app_dst[i[u]];
@@ -61,7 +62,6 @@ __global__ __launch_bounds__(256) void k_fork_place(GroupDev g, int32_t src0, in
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (some[u]) place_piece(g, d[u], base + u * stride - i[u] * chunks, dst0 + (int32_t)i[u], v[u]);
-    if (base + U * stride < base) break;
   }
 }
 

@@ -98,13 +98,11 @@ hipError_t launch_attend_join(const GroupDev& g, const AttendDev& a, int type, i
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // Eight e4m3 codes (low byte first) as bf16 or fp16: exact, both hold every e4m3
 // value, so the scales can wait until the products are in 32 bits.
@@ -130,9 +128,6 @@ __device__ __forceinline__ V8 widen8(uint32_t lo, uint32_t hi) {
 // D += A B with A 32 x 16, B 16 x 32: lane l holds row (column) l % 32 and the
 // eight k from 8 (l / 32); D's column is l % 32, its register r the row
 // 8 (r / 4) + 4 (l / 32) + r % 4.
-__device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-}
 __device__ __forceinline__ f32x16 mfma32(f16x8 a, f16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }

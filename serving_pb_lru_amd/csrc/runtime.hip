@@ -836,11 +836,9 @@ int ula_fork(ula_ctx* ctx, int32_t group, int32_t src, int32_t dst, int32_t n, u
     const int rc = wait_gathers(gh, s);
     if (rc) return rc;
   }
-  // a chunk's places are in app_dst, and its 16-byte pieces are counted in 32 bits
-  const int64_t most = std::min<int64_t>(d.maxApp, 0xFFFFFFFFll / (d.slot_bytes / 16));
-  for (int64_t done = 0; done < n; done += most) {
+  for (int64_t done = 0; done < n; done += d.maxApp) {   // a chunk's places are in app_dst
     const int32_t off = (int32_t)done;
-    const int32_t cnt = (int32_t)std::min<int64_t>(n - done, most);
+    const int32_t cnt = (int32_t)std::min<int64_t>(n - done, d.maxApp);
     if (ring) {
       HIP_TRY(launch_fork_collect(g, src + off, dst + off, cnt, s));
       const PlanArgs a = ring_append_plan(cnt, (int32_t)(gh.steps % d.B), (int32_t)d.B);
