@@ -390,71 +390,92 @@ static void mark_range(GroupHost& gh, int32_t first, int32_t n, bool on) {
   });
 }
 
-// How many runs of consecutive addresses a batch is, in its order, and whether the
-// host's work goes by runs: requests own ranges, so a whole request's batch is a few
-// runs, while a decode step's is one address from each request. (Checking and marking
-// 65536 addresses in one run 154 us by runs, 690 us one by one; 256 scattered ones 6.2 us
-// by runs, 2.4 us one by one.)
-static int32_t count_runs(const int32_t* la, int32_t n) {
-  int32_t runs = n > 0 ? 1 : 0;
-  for (int32_t i = 1; i < n; ++i) runs += la[i] != (int64_t)la[i - 1] + 1;
-  return runs;
-}
-static bool by_runs(int32_t runs, int32_t n) { return runs <= n / 4; }
-
+// A batch of addresses, its runs of consecutive ones counted in its order, and
+// whether it ascends (so that none is in it twice). Requests own ranges, so a whole
+// request's batch is a few runs, whose host work goes by runs; a decode step's is one
+// address from each request, taken one by one. (Checking and marking 65536 addresses
+// of one run takes 33 us so, 640 us sorted and one by one; every 64th of 2^22 100 us,
+// shuffled 4 ms; 256 scattered ones 2.1 us, as runs 6.2 us.)
 struct Run {
   int32_t first, n;
 };
-template <typename F>
-static void for_runs(const int32_t* la, int32_t n, F f) {
-  for (int32_t i = 0; i < n;) {
-    int32_t e = i + 1;
-    while (e < n && la[e] == (int64_t)la[e - 1] + 1) ++e;
-    f(Run{la[i], e - i});
-    i = e;
+struct Batch {
+  const int32_t* la;
+  int32_t n, runs;
+  bool ascends;
+  Batch(const int32_t* la_, int32_t n_) : la(la_), n(n_), runs(n_ > 0 ? 1 : 0), ascends(true) {
+    int32_t breaks = 0, falls = 0;
+    for (int32_t i = 1; i < n; ++i) {
+      breaks += (uint32_t)la[i] - (uint32_t)la[i - 1] != 1u;   // -1 after 2^31 - 1 falls too, and is refused
+      falls += la[i] <= la[i - 1];
+    }
+    runs += breaks;
+    ascends = falls == 0;
   }
+  bool by_runs() const { return runs <= n / 4; }
+  template <typename F>   // f(run), true to go on
+  bool each_run(F f) const {
+    if (runs == 1) return f(Run{la[0], n});
+    for (int32_t i = 0; i < n;) {
+      int32_t e = i + 1;
+      while (e < n && (uint32_t)la[e] - (uint32_t)la[e - 1] == 1u) ++e;
+      if (!f(Run{la[i], e - i})) return false;
+      i = e;
+    }
+    return true;
+  }
+};
+
+static bool any_twice(const Batch& b) {
+  if (b.ascends) return false;
+  if (!b.by_runs()) {
+    std::vector<int32_t> sorted(b.la, b.la + b.n);
+    std::sort(sorted.begin(), sorted.end());
+    return std::adjacent_find(sorted.begin(), sorted.end()) != sorted.end();
+  }
+  std::vector<Run> r;
+  r.reserve(b.runs);
+  b.each_run([&](const Run& x) {
+    r.push_back(x);
+    return true;
+  });
+  std::sort(r.begin(), r.end(), [](const Run& x, const Run& y) { return x.first < y.first; });
+  for (size_t i = 1; i < r.size(); ++i)
+    if (r[i].first < r[i - 1].first + r[i - 1].n) return true;
+  return false;
 }
 
-static bool is_appended(const GroupHost& gh, int32_t la) {
-  return gh.appended[(uint32_t)la >> 6] >> (la & 63) & 1ull;
-}
-
-// The checks of a batch of `runs` runs: every address in [0, N) (ULA_ERANGE), none
-// twice (ULA_EDUP), and all of them appended or none (`wanted`; else `code`).
-static int check_batch(const GroupHost& gh, const int32_t* la, int32_t n, int32_t runs, int64_t N, bool wanted,
-                       int code) {
-  if (by_runs(runs, n)) {
-    std::vector<Run> r;
-    r.reserve(runs);
-    for_runs(la, n, [&](const Run& x) { r.push_back(x); });
-    for (const Run& x : r)
-      if (x.first < 0 || (int64_t)x.first + x.n > N) return ULA_ERANGE;
-    auto before = [](const Run& a, const Run& b) { return a.first < b.first; };
-    if (!std::is_sorted(r.begin(), r.end(), before)) std::sort(r.begin(), r.end(), before);
-    for (size_t i = 1; i < r.size(); ++i)
-      if (r[i].first < r[i - 1].first + r[i - 1].n) return ULA_EDUP;
-    for (const Run& x : r)
-      if (!(wanted ? all_appended(gh, x.first, x.n) : none_appended(gh, x.first, x.n))) return code;
-    return ULA_OK;
+// The checks of a batch: every address in [0, N) (ULA_ERANGE), none twice (ULA_EDUP),
+// and all of them appended or none (`wanted`; else `code`).
+static int check_batch(const GroupHost& gh, const Batch& b, int64_t N, bool wanted, int code) {
+  if (b.n == 0) return ULA_OK;
+  int32_t least = b.la[0], most = b.la[b.n - 1];
+  for (int32_t i = 0; i < b.n && !b.ascends; ++i) {
+    least = std::min(least, b.la[i]);
+    most = std::max(most, b.la[i]);
   }
-  for (int32_t i = 0; i < n; ++i)
-    if (la[i] < 0 || la[i] >= N) return ULA_ERANGE;
-  std::vector<int32_t> sorted(la, la + n);
-  std::sort(sorted.begin(), sorted.end());
-  if (std::adjacent_find(sorted.begin(), sorted.end()) != sorted.end()) return ULA_EDUP;
-  for (int32_t i = 0; i < n; ++i)
-    if (is_appended(gh, la[i]) != wanted) return code;
+  if (least < 0 || most >= N) return ULA_ERANGE;
+  if (any_twice(b)) return ULA_EDUP;
+  if (b.by_runs())
+    return b.each_run([&](const Run& x) {
+      return wanted ? all_appended(gh, x.first, x.n) : none_appended(gh, x.first, x.n);
+    }) ? ULA_OK : code;
+  for (int32_t i = 0; i < b.n; ++i)
+    if ((bool)(gh.appended[(uint32_t)b.la[i] >> 6] >> (b.la[i] & 63) & 1ull) != wanted) return code;
   return ULA_OK;
 }
 
-static void mark_batch(GroupHost& gh, const int32_t* la, int32_t n, int32_t runs, bool on) {
-  if (by_runs(runs, n)) {
-    for_runs(la, n, [&](const Run& x) { mark_range(gh, x.first, x.n, on); });
+static void mark_batch(GroupHost& gh, const Batch& b, bool on) {
+  if (b.by_runs()) {
+    b.each_run([&](const Run& x) {
+      mark_range(gh, x.first, x.n, on);
+      return true;
+    });
     return;
   }
-  for (int32_t i = 0; i < n; ++i) {
-    const uint64_t bit = 1ull << (la[i] & 63);
-    uint64_t& word = gh.appended[(uint32_t)la[i] >> 6];
+  for (int32_t i = 0; i < b.n; ++i) {
+    const uint64_t bit = 1ull << (b.la[i] & 63);
+    uint64_t& word = gh.appended[(uint32_t)b.la[i] >> 6];
     word = on ? word | bit : word & ~bit;
   }
 }
@@ -681,16 +702,16 @@ int ula_destroy(ula_ctx* ctx) {
 }
 
 // Host validation of an append batch (nothing changes on error).
-static int validate_append(const ula_ctx* ctx, const GroupHost& gh, int32_t n, const int32_t* la_host) {
+static int validate_append(const ula_ctx* ctx, const GroupHost& gh, const Batch& b) {
   const Dims& d = ctx->dims;
-  if (const int rc = check_batch(gh, la_host, n, count_runs(la_host, n), d.N, false, ULA_EDUP)) return rc;
-  if (gh.n_appended + n > d.P + d.H) return ULA_EHOSTFULL;
+  if (const int rc = check_batch(gh, b, d.N, false, ULA_EDUP)) return rc;
+  if (gh.n_appended + b.n > d.P + d.H) return ULA_EHOSTFULL;
   return ULA_OK;
 }
 
-static void note_appended(GroupHost& gh, int32_t n, const int32_t* la_host) {
-  mark_batch(gh, la_host, n, count_runs(la_host, n), true);
-  gh.n_appended += n;
+static void note_appended(GroupHost& gh, const Batch& b) {
+  mark_batch(gh, b, true);
+  gh.n_appended += b.n;
 }
 
 int ula_append(ula_ctx* ctx, int32_t group, int32_t n, const int32_t* la_host, const void* rows,
@@ -702,8 +723,9 @@ int ula_append(ula_ctx* ctx, int32_t group, int32_t n, const int32_t* la_host, c
   if (!la_host || !rows) return ULA_EINVAL;
   GroupHost& gh = ctx->groups[group];
   const Dims& d = ctx->dims;
+  const Batch batch(la_host, n);
   {
-    const int rc = validate_append(ctx, gh, n, la_host);   // the whole batch first
+    const int rc = validate_append(ctx, gh, batch);   // the whole batch first
     if (rc) return rc;
   }
 
@@ -785,7 +807,7 @@ int ula_append(ula_ctx* ctx, int32_t group, int32_t n, const int32_t* la_host, c
       HIP_TRY(launch_place(g, cnt, src, s));
     }
   }
-  note_appended(gh, n, la_host);
+  note_appended(gh, batch);
   return ULA_OK;
 }
 
@@ -798,8 +820,8 @@ int ula_release(ula_ctx* ctx, int32_t group, int32_t n, const int32_t* la_host, 
   GroupHost& gh = ctx->groups[group];
   const Dims& d = ctx->dims;
   // validate the whole batch first; nothing changes on error
-  const int32_t runs = count_runs(la_host, n);
-  if (const int rc = check_batch(gh, la_host, n, runs, d.N, true, ULA_ERANGE)) return rc;
+  const Batch batch(la_host, n);
+  if (const int rc = check_batch(gh, batch, d.N, true, ULA_ERANGE)) return rc;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const GroupDev& g = gh.d;
   {   // a released GPU slot may be taken by the next append: pending gathers first
@@ -813,8 +835,8 @@ int ula_release(ula_ctx* ctx, int32_t group, int32_t n, const int32_t* la_host, 
     gh.written_back = gh.steps;
   }
   // one run of addresses, as a request's mostly are, needs no list on the device
-  if (runs == 1) HIP_TRY(launch_release(g, la_host[0], n, s));
-  for (int32_t off = 0; off < n && runs > 1; off += (int32_t)d.maxApp) {
+  if (batch.runs == 1) HIP_TRY(launch_release(g, la_host[0], n, s));
+  for (int32_t off = 0; off < n && batch.runs > 1; off += (int32_t)d.maxApp) {
     const int32_t cnt = (int32_t)std::min<int64_t>(n - off, d.maxApp);
     if (ctx->static_dev >= 0) {
       // no pinned staging buffers: copy from the caller's memory and wait for it
@@ -831,7 +853,7 @@ int ula_release(ula_ctx* ctx, int32_t group, int32_t n, const int32_t* la_host, 
     }
     HIP_TRY(launch_release(g, -1, cnt, s));
   }
-  mark_batch(gh, la_host, n, runs, false);
+  mark_batch(gh, batch, false);
   gh.n_appended -= n;
   gh.last_n = 0;   // the last step's resolved selection may name released entries
   return ULA_OK;
@@ -1047,9 +1069,10 @@ int ula_append_step(ula_ctx* ctx, int32_t group, int32_t n_app, const int32_t* l
     if (rc) return rc;
   }
   if (n_app < 0) return ULA_EINVAL;
-  if (n_app > 0) {
-    if (!la_host || !rows) return ULA_EINVAL;
-    const int rc = validate_append(ctx, ctx->groups[group], n_app, la_host);
+  if (n_app > 0 && (!la_host || !rows)) return ULA_EINVAL;
+  const Batch batch(la_host, n_app);
+  {
+    const int rc = validate_append(ctx, ctx->groups[group], batch);
     if (rc) return rc;
   }
   if (n_app > 0 && n_app <= small_append_limit(ctx->dims.policy) && n_app <= ctx->dims.maxApp &&
@@ -1061,7 +1084,7 @@ int ula_append_step(ula_ctx* ctx, int32_t group, int32_t n_app, const int32_t* l
     std::memcpy(a.las, la_host, sizeof(int32_t) * n_app);
     const int rc = step_impl(ctx, group, n_sets, k, sel_dev, stream, &a, static_cast<const uint8_t*>(rows));
     if (rc) return rc;
-    note_appended(ctx->groups[group], n_app, la_host);
+    note_appended(ctx->groups[group], batch);
     return ULA_OK;
   }
   if (n_app > 0) {
