@@ -205,9 +205,10 @@ __global__ __launch_bounds__(256) void k_writeback(GroupDev g, FastDiv per_slot)
 
 // Calls f(bits, lanes) once for each distinct key among the wavefront's lanes with
 // `on` set, in the first of them: how many lanes have the key and (with BITS)
-// their bits together. The first kLeaders keys are found one after another; a lane whose key is
-// not among them calls for itself, which bounds the work of a wavefront of
-// scattered entries. Every lane of the wavefront must call it.
+// their bits together. The first kLeaders keys are found one after another, a key that
+// one lane alone has counting as two; a lane whose key is not among them calls for
+// itself, which bounds the work of a wavefront of scattered entries. Every lane of the
+// wavefront must call it.
 template <bool BITS, typename F>
 __device__ __forceinline__ void each_key(bool on, uint32_t key, uint32_t bits, F&& f) {
   constexpr int kLeaders = 4;
@@ -217,13 +218,16 @@ __device__ __forceinline__ void each_key(bool on, uint32_t key, uint32_t bits, F
     const int lead = __builtin_ctzll(left);
     const uint32_t k = (uint32_t)__builtin_amdgcn_readlane((int)key, lead);
     const bool mine = on && key == k;
+    const unsigned long long same = __ballot(mine);
+    const int lanes = __popcll(same);
     uint32_t all = mine ? bits : 0u;
-    if constexpr (BITS) {
+    if (lanes == 1) {
+      ++i;
+    } else if constexpr (BITS) {
 #pragma unroll
       for (int d = kWave / 2; d >= 1; d >>= 1) all |= (uint32_t)__shfl_xor((int)all, d, kWave);
     }
-    const unsigned long long same = __ballot(mine);
-    if (lane_id() == lead) f(all, __popcll(same));
+    if (lane_id() == lead) f(all, lanes);
     left &= ~same;
   }
   if (left >> lane_id() & 1ull) f(bits, 1);
