@@ -22,7 +22,7 @@
 //   - second product: codes widened to fp16, and p s_b rounded to fp16. m follows
 //     the largest p_j max_b s_bj of any key, which stays within 2^7..2^15 (a scale
 //     below 2^-60 counts as that), so the rounding is at most 2^-11 of the value, or
-//     2^-25 (2^-32 of the largest) for small ones. That is a choice: bf16 results do
+//     2^-25 (2^-32 of the largest) for small ones. That is a choice: bf16 results
 //     hardly show it (1.68e-3 of their size off, 1.66e-3 without), fp16 ones are 2.9e-4 off
 //     in place of 2.1e-4. What the rounding leaves, in a second product (p in 32 bits in
 //     LDS, scaled and split by the second waves), took 398 us where this takes 303 us
