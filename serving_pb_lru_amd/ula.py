@@ -425,6 +425,7 @@ class Engine:
         self.device_bytes = nbytes
         self.host_bytes = L.ula_host_bytes(ctypes.byref(self.cfg))
         self.ws = None if static_workspace else torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.device = torch.device("cuda", torch.cuda.current_device()) if static_workspace else self.ws.device
         self.host = None
         if self.host_bytes:
             self.host = L.ula_host_alloc(self.host_bytes)
@@ -470,11 +471,13 @@ class Engine:
 
     def fork(self, group: int, src: int, dst: int, n: int, stream=None) -> None:
         """Copy entries src .. src + n - 1 to the new addresses dst .. dst + n - 1."""
-        _check(lib().ula_fork(self.ctx, group, src, dst, n, _stream(stream)), "ula_fork")
+        with _On(self.device, stream) as s:
+            _check(lib().ula_fork(self.ctx, group, src, dst, n, s), "ula_fork")
 
     def rename(self, group: int, src: int, dst: int, n: int, stream=None) -> None:
         """Give entries src .. src + n - 1 the addresses dst .. dst + n - 1; no row moves."""
-        _check(lib().ula_rename(self.ctx, group, src, dst, n, _stream(stream)), "ula_rename")
+        with _On(self.device, stream) as s:
+            _check(lib().ula_rename(self.ctx, group, src, dst, n, s), "ula_rename")
 
     def step(self, group: int, sel, stream=None) -> None:
         """sel: torch CUDA int32 tensor [n_sets][k] (or [k] for one set)."""
@@ -538,7 +541,7 @@ class Engine:
         args.q, args.type, st = _tensor(q, (n_sets, None, width), "ula_attend q", (BF16, FP16))
         args.q_set_stride, args.q_head_stride, args.heads = st[0], st[1], heads
         args.scale = 1.0 / width ** 0.5 if scale is None else scale
-        _same_device(q, sel, out, lse, self.ws)
+        _same_device(q, sel, out, lse, self)
         on = _On(q.device, stream, q, sel, out, lse)
         with on as s:
             if out is None:
