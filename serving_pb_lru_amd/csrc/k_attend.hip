@@ -45,11 +45,13 @@
 // four times; 128 us with eight equal waves that went through first product,
 // softmax and second product in turn, which left the younger wave of a SIMD
 // waiting; 132 us with 16 heads and a whole tile's keys per first wave; 113 us so.
-// Of that 18 us are start and end, and the 344 MB of rows alone take 86 us at the
-// rate of a large sum. In the loop the first waves' chain of products, maximum,
-// exponentials and p decides, about 2500 cycles a tile; issuing a tile's products
-// ahead of the softmax before it does not shorten it (116 us), nor does p in 32
-// bits scaled by the second waves, with a sixth tile in the LDS that frees (117 us).
+// Of that 18 us are start and end, and the 344 MB of rows alone take 58 us at the
+// rate of a large copy. In the loop the first waves' chain of products, maximum,
+// exponentials and p takes about 2500 cycles a tile; vector instructions fill 56% of
+// a SIMD's cycles and matrix instructions 32%, and the two hardly overlap. Issuing
+// a tile's products ahead of the softmax before it does not shorten it (116 us), nor
+// does p in 32 bits scaled by the second waves, with a sixth tile in the LDS that
+// frees (117 us).
 // Sixteen waves of 16 heads or 64 channels read keys and p from LDS twice as often
 // and widen keys twice as often: 159 us.
 // Tiles: the first 640 bytes of each row as 16-byte pieces straight into LDS (no

@@ -524,7 +524,8 @@ class Engine:
                lse=None, stream=None):
         """(out, lse): attention of q [n_sets][heads][576 or head_dim] (bf16 or fp16) over the selected
         entries' rows of one layer, which are in format `fmt`. out [n_sets][heads][512 or head_dim] in
-        q's dtype, lse fp32 [n_sets][heads]. scale: factor of the logits, default 1 / sqrt(q's width).
+        q's dtype, lse fp32 [n_sets][heads]. scale: factor of the logits, default 1 / sqrt(q's width);
+        pass it for latent rows, whose models scale by a head's width before absorption, not by 576.
         The workspace of a split call is allocated here, on the call's stream. No gradient is recorded:
         a q that requires one is refused."""
         import torch
