@@ -16,8 +16,9 @@
 // 3.4e-4, 21 -> 22 us for 64 sets x 500 blocks of 8 tokens x 2 KV heads of 64.
 //
 // Only 2 x heads / kv_heads operations per byte, so loads in flight count most (two
-// waves a SIMD still wait half of their time, and 2.2 TB/s come from HBM). A wave works
-// by itself, on one KV head's up to 16 query heads and one range of tokens, with no barrier, and many waves per compute unit keep loads in flight; waves of
+// waves a SIMD still wait half of their time, and 2.2 TB/s come from HBM). A wave
+// works by itself, on one KV head's up to 16 query heads and one range of tokens,
+// with no barrier, and many waves per compute unit keep loads in flight; waves of
 // one workgroup take neighbouring KV heads of the same tokens, whose parts of a
 // row share cache lines. 32 tokens at a time: keys go from memory to registers
 // as the operand of S^T = K Q^T (heads in the lanes' columns), values through a
