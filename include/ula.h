@@ -472,10 +472,10 @@ size_t ula_attend_bytes(const ula_row_format* rows, int32_t n_sets, int32_t k, i
  * and lse = -inf. An address listed more than once counts as often. Sums, the
  * softmax and the products' accumulators are in 32 bits; keys enter exactly,
  * softmax weights times value scales are rounded to fp16 before the second
- * product (2^-11 of each, or 2^-32 of the set's largest; heads rows with fp16
- * results keep what that leaves in another product; value scales are meant to lie
- * between 2^-60 and 2^80: smaller ones count as 2^-60 in that largest, and with
- * larger ones small weights are lost), results once to the type of out. A logit
+ * product (2^-11 of each, or 2^-32 of the set's largest; for fp16 results what that
+ * leaves goes through another: 2^-22 of each; value scales are meant to lie between
+ * 2^-60 and 2^80: smaller ones count as 2^-60 in that largest, and with larger ones
+ * small weights are lost), results once to the type of out. A logit
  * that is NaN or +infinity makes that head's outputs and log-sum NaN; an entry of
  * logit -infinity has no weight, and a set with no other gives 0 and -inf. No
  * unselected row is ever read. The order of the sums depends on the sizes alone, so

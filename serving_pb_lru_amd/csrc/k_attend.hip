@@ -22,24 +22,23 @@
 //   - second product: codes widened to fp16, and p s_b rounded to fp16. m follows
 //     the largest p_j max_b s_bj of any key, which stays within 2^7..2^15 (a scale
 //     below 2^-60 counts as that), so the rounding is at most 2^-11 of the value, or
-//     2^-25 (2^-32 of the largest) for small ones. That is a choice: bf16 results
-//     hardly show it (1.68e-3 of their size off, 1.66e-3 without), fp16 ones are 2.9e-4 off
-//     in place of 2.1e-4. What the rounding leaves, in a second product (p in 32 bits in
-//     LDS, scaled and split by the second waves), took 398 us where this takes 303 us
-//     for 384 sets of 2047 keys and 128 heads, since the second waves then have twice
-//     the matrix work.
+//     2^-25 (2^-32 of the largest) for small ones. bf16 results hardly show it
+//     (1.68e-3 of their size off, 1.66e-3 without). fp16 results would: for them
+//     what it leaves goes through a second product with the same values (2.07e-4
+//     off, as a result of 64 bits rounded once, 2.9e-4 without; 384 sets of 2047 keys
+//     and 128 heads 368 us, 300 us without).
 // Both products have 32-bit accumulators.
 //
 // Layout. Both products are taken transposed: S^T = K Q^T puts heads in the
 // lanes' columns and keys in registers, O^T = V^T P^T the same way. A workgroup
 // has four waves for the first product and the softmax, half of its heads (16 or
-// 32) and half of a tile's 32 keys each, and four for the second product, 128 channels of O (one
-// scale block) with all heads each: so no wave holds another's Q, a key is
-// widened for all of a wave's heads at once and every value once. In between p goes through
-// LDS, scaled for each block and in the operand order of the second product. The
-// two waves of a head tell each other their largest logits through LDS as well,
-// a barrier ahead of the softmax, and so come to the same m. Each SIMD has a wave
-// of either kind, whose matrix and vector work overlap. One barrier per tile.
+// 32) and half of a tile's 32 keys each, and four for the second product, 128
+// channels of O (one scale block) with all heads each: so no wave holds another's
+// Q, a key is widened for all of a wave's heads at once and every value once. In
+// between p goes through LDS in the operand order of the second product, scaled for
+// each block (fp16 queries: in 32 bits, scaled and split by the second waves). The two waves of a head tell each other their largest
+// logits through LDS as well, a barrier ahead of the softmax, and so come to the
+// same m. Each SIMD has a wave of either kind. One barrier per tile.
 // Measured, 256 sets of 2048 keys and 64 heads: 206 us with a wave that kept 32
 // heads to itself for both products, reading and widening every key and value
 // four times; 128 us with eight equal waves that went through first product,
@@ -130,25 +129,23 @@ constexpr int kSecondWaves = kWaves - kFirstWaves;
 constexpr int kLoadsPerWave = (kTileLoads + kLatentGroups) / kSecondWaves;   // a second wave's vector loads per tile
 static_assert(kSecondWaves == kLatentGroups, "one scale block per second wave");
 
-// The bf16 values whose sum a 16-bit rotary channel of q is.
+// fp16 results: p x scale in two parts, which the second waves make of p in 32 bits.
 template <typename Q8>
-constexpr int kRopeParts = std::is_same_v<Q8, bf16x8> ? 1 : 2;
-// fp16 queries of 64 heads: the second rotary parts of a first wave's last 16 heads wait in LDS, since
-// registers for them are spilled, and read back in every tile (384 sets of 2047 keys and 128 heads:
-// 345 us with 16 bytes spilled, 304 us so).
-template <typename Q8, int HT>
-constexpr bool kRestInLds = HT == 2 && kRopeParts<Q8> == 2;
+constexpr bool kTwoParts = !std::is_same_v<Q8, bf16x8>;
 
-template <int HEADS, int TILES, bool REST>
+template <typename Q8, int HT, int TILES>
 struct LatentLds {
+  static constexpr int HEADS = 32 * HT;
+  // bytes of a key's p: one in 32 bits, or one for each block in 16
+  static constexpr int kKeyBytes = kTwoParts<Q8> ? 4 : 2 * kLatentGroups;
   alignas(1024) uint8_t ring[TILES][kTileBytes];
-  // p x scale of two tiles: [block][head][key], key chunk c (8 keys) of head h at c ^ ((h >> 2) & 3)
-  alignas(1024) _Float16 p[2][kLatentGroups][HEADS][kTileKeys];
+  // p of two tiles. One part: p x scale, [block][head][key], key chunk c (8 keys) of head h at
+  // c ^ ((h >> 2) & 3). Two parts: p, [head][key], key chunk c (4 keys) of head h at c ^ ((h >> 1) & 7).
+  alignas(1024) uint8_t p[2][HEADS * kTileKeys * kKeyBytes];
   alignas(16) float scale[TILES][kLatentGroups][kTileKeys];
   float alpha[2][HEADS];                    // factor of O before the tile's second product
   alignas(16) uint32_t moved[2][4];         // whether any head of a first wave has a factor other than 1
   alignas(8) float top[2][HEADS][2];        // of two tiles: the largest logarithm of p x scale, of either half of the keys
-  bf16x8 rest[REST ? kFirstWaves / 2 : 0][kRope / 32][kWave];
   const uint8_t* row[kAttendKeys];          // each key's row in this layer; zeros for padding
   uint32_t live[kAttendKeys / kTileKeys + 2];   // bit per key: not padding; none behind the last tile
   int ok;
@@ -175,14 +172,15 @@ struct QueryRaw {
 // bf16, so fp16 ones become the sum of two bf16 values (8 + 8 bits hold their 11).
 template <typename Q8>
 struct QueryOperand {
+  static constexpr int kRopeParts = std::is_same_v<Q8, bf16x8> ? 1 : 2;
   Q8 x[kLatent / 32];
-  bf16x8 rope[kRopeParts<Q8>][kRope / 32];
+  bf16x8 rope[kRopeParts][kRope / 32];
   __device__ __forceinline__ void take(const QueryRaw<Q8>& raw) {
 #pragma unroll
     for (int t = 0; t < kLatent / 32; ++t) x[t] = raw.x[t];
 #pragma unroll
     for (int j = 0; j < kRope / 32; ++j) {
-      if constexpr (kRopeParts<Q8> == 1) {
+      if constexpr (kRopeParts == 1) {
         rope[0][j] = raw.rope[j];
       } else {
 #pragma unroll
@@ -198,7 +196,7 @@ struct QueryOperand {
 #pragma unroll
     for (int j = 0; j < kRope / 32; ++j)
 #pragma unroll
-      for (int i = kRopeParts<Q8> - 1; i >= 0; --i) s = mfma16(kr[j], rope[i][j], s);
+      for (int i = kRopeParts - 1; i >= 0; --i) s = mfma16(kr[j], rope[i][j], s);
     return s;
   }
   // product of a block's keys, widened, 32 channels at a time
@@ -254,10 +252,11 @@ __device__ __forceinline__ void store_heads(uint8_t* box, const f32x16 (&o)[CT][
 template <typename Q8, int HT, int TILES>
 __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g, AttendDev a) {
   constexpr int kHeads = 32 * HT;                 // heads of a workgroup
+  constexpr bool kTwo = kTwoParts<Q8>;
   constexpr int CT = kScaleGroup / 32;            // 32-channel tiles of a second wave's O
   static_assert(2 * kHeads == 16 * HT * kFirstWaves, "every head has two waves in the first product");
   static_assert(TILES >= 4, "a tile on its way beside the three in use");
-  __shared__ LatentLds<kHeads, TILES, kRestInLds<Q8, HT>> s;
+  __shared__ LatentLds<Q8, HT, TILES> s;
   static_assert(sizeof(s) <= 160 * 1024, "LDS of a compute unit");
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);   // uniform: its branches are scalar
@@ -357,7 +356,12 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
     const int vkey = 8 * half + col / 2;
     const int voff = vkey * kLatentScaleAt + (((quad % 2) ^ swizzle(vkey)) << 4) + (col & 1) * 8 + sw * kScaleGroup;
     static_assert(kLatentScaleAt % 128 == 0 && kTileBytes % 128 == 0, "the swizzle's bits are free in every row address");
-    const uint32_t pread = lds_address(s.p) + (sw * kHeads + col32) * kTileKeys * 2 + ((half ^ ((col32 >> 2) & 3)) << 4);
+    // this lane's chunk of head col32: keys 8 half .. of a tile's first 16
+    const uint32_t pread = lds_address(s.p) +
+                           (kTwo ? col32 * kTileKeys * 4 + ((2 * half ^ ((col32 >> 1) & 7)) << 4)
+                                 : (sw * kHeads + col32) * kTileKeys * 2 + ((half ^ ((col32 >> 2) & 3)) << 4));
+    float minus = -1.0f;                          // one the compiler does not know: a fused step takes it, a difference two
+    asm volatile("" : "+s"(minus));
     if (tiles >= TILES - 1) wait_loads<(TILES - 2) * kLoadsPerWave>();
     else wait_loads<0>();
     barrier_keep_loads();
@@ -373,11 +377,11 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
       if (tile < 0) continue;
       const int buf = tile & 1;
       const uint32_t vrow = opaque(lds_address(s.ring) + tile % TILES * kTileBytes + voff);
-      // chunk 2 x + half of this lane's head: ^ 32 for x
-      const uint32_t prow = opaque(pread + buf * kLatentGroups * kHeads * kTileKeys * 2);
+      // the second 16 keys: ^ 32, or ^ 64 in 32 bits
+      const uint32_t prow = opaque(pread + buf * (uint32_t)sizeof(s.p[0]));
       const vec4u mv = lds_get<vec4u>(lds_address(s.moved) + buf * 16);
       i32x2 v8[CT][2];
-      f16x8 p[HT][2];
+      f16x8 p[HT][2], rest[HT][2];
 #pragma unroll
       for (int t = 0; t < CT; ++t)
 #pragma unroll
@@ -385,7 +389,30 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
 #pragma unroll
       for (int h = 0; h < HT; ++h)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) p[h][x] = lds_get<f16x8>((prow ^ (32 * x)) + 32 * h * kTileKeys * 2);
+        for (int x = 0; x < 2; ++x) {
+          if constexpr (kTwo) {
+            const uint32_t scale = lds_address(s.scale) + ((tile % TILES * kLatentGroups + sw) * kTileKeys + 16 * x + 8 * half) * 4;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const f32x4 w = lds_get<f32x4>((prow ^ (64 * x + 16 * y)) + 32 * h * kTileKeys * 4);
+              const f32x4 sc = lds_get<f32x4>(scale + 16 * y);
+#pragma unroll
+              for (int e = 0; e < 4; e += 2) {
+                // (the empty assembly keeps the product and its rounding one step each for both uses)
+                f32x2 v = {w[e] * sc[e], w[e + 1] * sc[e + 1]};
+                asm("" : "+v"(v));
+                f16x2 hi = __builtin_convertvector(v, f16x2);
+                asm("" : "+v"(hi));
+                p[h][x][4 * y + e] = hi.x;
+                p[h][x][4 * y + e + 1] = hi.y;
+                rest[h][x][4 * y + e] = (_Float16)__builtin_fmaf((float)hi.x, minus, v.x);
+                rest[h][x][4 * y + e + 1] = (_Float16)__builtin_fmaf((float)hi.y, minus, v.y);
+              }
+            }
+          } else {
+            p[h][x] = lds_get<f16x8>((prow ^ (32 * x)) + 32 * h * kTileKeys * 2);
+          }
+        }
       if (tile + TILES - 1 < tiles) issue(tile + TILES - 1);
       if (__builtin_amdgcn_readfirstlane(mv.x | mv.y | mv.z | mv.w)) {   // a reference moved: O's factors
 #pragma unroll
@@ -401,7 +428,10 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
         for (int x = 0; x < 2; ++x) {
           const f16x8 v = widen8<f16x8>((uint32_t)v8[t][x].x, (uint32_t)v8[t][x].y);
 #pragma unroll
-          for (int h = 0; h < HT; ++h) o[t][h] = mfma32(v, p[h][x], o[t][h]);
+          for (int h = 0; h < HT; ++h) {
+            o[t][h] = mfma32(v, p[h][x], o[t][h]);
+            if constexpr (kTwo) o[t][h] = mfma32(v, rest[h][x], o[t][h]);
+          }
         }
       read_rows(tile + TILES);
     }
@@ -430,18 +460,15 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
       m[i] = -__builtin_inff();
       l[i] = 0.0f;
     }
-    if constexpr (kRestInLds<Q8, HT>) {            // read a barrier later
-      if (key_half == 0)
-#pragma unroll
-        for (int j = 0; j < kRope / 32; ++j) s.rest[wave / 2][j][lane] = q[HT - 1].rope[1][j];
-    }
     const float c_log2 = a.scale_log2;
     // Register r in quad x is key 8 x + 4 key_half + r. koff: this lane's key as an
     // operand, piece quad of a scale block; piece 4 + quad is ^ 64.
     const int key = 8 * (col / 4) + 4 * key_half + col % 4;
     const int koff = key * kLatentScaleAt + ((quad ^ swizzle(key)) << 4);
     const int head = head0 + col;
-    const uint32_t pwrite = lds_address(s.p) + head * kTileKeys * 2 + ((quad ^ ((head >> 2) & 3)) << 4) + 8 * key_half;
+    const uint32_t pwrite = lds_address(s.p) +
+                            (kTwo ? head * kTileKeys * 4 + (((2 * quad + key_half) ^ ((head >> 1) & 7)) << 4)
+                                  : head * kTileKeys * 2 + ((quad ^ ((head >> 2) & 3)) << 4) + 8 * key_half);
     const uint32_t at_top = lds_address(s.top) + head * 8;
     f32x4 sc[kLatentGroups], S[HT];                // of the next tile for the softmax: scales, logits in powers of two
     // First product of a tile in LDS; the largest logarithm of p x scale of each
@@ -451,10 +478,6 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
       const uint32_t krow64 = opaque(krow ^ 64);
       const uint32_t scale = opaque(lds_address(s.scale) + (tile % TILES * kLatentGroups * kTileKeys + 8 * quad + 4 * key_half) * 4);
       bf16x8 kr[2] = {lds_get<bf16x8>(krow + kRopeAt), lds_get<bf16x8>(krow64 + kRopeAt)};
-      if constexpr (kRestInLds<Q8, HT>)
-#pragma unroll
-        for (int j = 0; j < kRope / 32; ++j)
-          q[HT - 1].rope[1][j] = lds_get<bf16x8>(lds_address(s.rest) + ((wave / 2 * (kRope / 32) + j) * kWave + lane) * 16);
       const uint32_t live = __builtin_amdgcn_readfirstlane(s.live[tile]) >> (8 * quad + 4 * key_half);
       f32x4 part[HT][kLatentGroups], rope[HT];
 #pragma unroll
@@ -506,7 +529,6 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
 #pragma unroll
       for (int i = 0; i < HT; ++i) {
         // both halves' waves come to the same reference
-        typedef float f32x2 __attribute__((ext_vector_type(2)));
         const f32x2 both = lds_get<f32x2>(at_top + buf * kHeads * 8 + 16 * i * 8);
         const float top = fmaxf(both.x, both.y);
         const bool move = top > m[i] + 15.0f;
@@ -515,19 +537,23 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
         m[i] = nm;
         l[i] *= al;
         const float base = nm == -__builtin_inff() ? 0.0f : nm;
-        float p[4];
+        f32x4 p;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           p[r] = __builtin_amdgcn_exp2f(S[i][r] - base);
           l[i] += p[r];
         }
-        const uint32_t pw = opaque(pwrite + (buf * kLatentGroups * kHeads + 16 * i) * kTileKeys * 2);
+        const uint32_t pw = opaque(pwrite + buf * (uint32_t)sizeof(s.p[0]) + 16 * i * kTileKeys * (kTwo ? 4 : 2));
+        if constexpr (kTwo) {
+          lds_put(pw, p);
+        } else {
 #pragma unroll
-        for (int b = 0; b < kLatentGroups; ++b) {
-          f16x4 w;
+          for (int b = 0; b < kLatentGroups; ++b) {
+            f16x4 w;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) w[r] = (_Float16)(p[r] * sc[b][r]);
-          lds_put(pw + b * kHeads * kTileKeys * 2, w);
+            for (int r = 0; r < 4; ++r) w[r] = (_Float16)(p[r] * sc[b][r]);
+            lds_put(pw + b * kHeads * kTileKeys * 2, w);
+          }
         }
         moved |= move;
         if (quad == 0 && key_half == 0) s.alpha[buf][head + 16 * i] = al;
