@@ -499,6 +499,41 @@ size_t ula_attend_bytes(const ula_row_format* rows, int32_t n_sets, int32_t k, i
 int ula_attend(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32_t k,
                const int32_t* sel_dev, const ula_attend_args* args, uint64_t stream);
 
+typedef struct {
+  ula_attend_args attend;    /* of one node: strides of sets and heads; lse is [n_sets][nodes][heads] packed,
+                                q, out, the workspace and the rest as for ula_attend */
+  int32_t nodes;             /* drafted tokens of each set, 1..64 */
+  int64_t q_node_stride;     /* strides in elements: q and out are [n_sets][nodes][heads][...] */
+  int64_t out_node_stride;
+  const void* drafts;        /* the drafted tokens' rows, packed as ula_pack_rows writes them, 16-byte aligned:
+                                [n_sets][ceil(nodes / block_tokens)][layers_per_group] rows (latent rows: a
+                                token a block) */
+  const uint64_t* visible;   /* [n_sets][nodes]: bit j says that the node sees drafted token j */
+} ula_tree_args;
+
+/* Bytes of workspace that ula_attend_tree needs (0: none, or an invalid argument,
+ * which ula_attend_tree reports). A pure host function. */
+size_t ula_attend_tree_bytes(const ula_row_format* rows, int32_t n_sets, int32_t k, int32_t nodes, int32_t heads);
+
+/* Attention of a tree of drafted tokens over the cache (section 4: a step verifies
+ * tokens that a draft model proposed): every node of a set attends to the set's
+ * selected entries, as in ula_attend, and to those drafted tokens whose bit its mask
+ * has (its ancestors and itself, as a rule). The drafted tokens' rows come from the
+ * caller: nothing is appended before they are accepted. Selected rows are read once
+ * for all nodes of a set. Drafted token j of a set is token j % block_tokens of its
+ * block j / block_tokens; tokens behind a block's count, and bits from `nodes` on, are
+ * never used. A node that sees nothing, in a set with nothing selected, gives 0 and
+ * -inf. A drafted token's row reaches only the nodes that see it, whatever it holds: one
+ * with a NaN code among its latent channels or its values, or a value scale (latent rows: a scale) that is not
+ * finite, makes the heads that see it NaN, log-sums too. The rest (formula, rounding,
+ * order of the sums, which entries, streams, errors) is as for ula_attend; drafts and
+ * visible may be read until the stream has run the call. Host errors: also ULA_EINVAL
+ * for nodes outside 1..64, null or misaligned drafts (16 bytes) or visible (8 bytes), rows
+ * of out that share elements (each stride is looked at), n_sets * nodes * heads >= 2^24
+ * or nodes * heads > 2^16. */
+int ula_attend_tree(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32_t k, const int32_t* sel_dev,
+                    const ula_tree_args* args, uint64_t stream);
+
 /* Wait for `stream`, then report the first latched device error of any group
  * (poisoning the context) or ULA_OK (section 3: a host waiter for the steps'
  * completion). per_group_out (nullable, num_groups entries) receives each

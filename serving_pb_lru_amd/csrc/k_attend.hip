@@ -133,7 +133,11 @@ static_assert(kSecondWaves == kLatentGroups, "one scale block per second wave");
 template <typename Q8>
 constexpr bool kTwoParts = !std::is_same_v<Q8, bf16x8>;
 
-template <typename Q8, int HT, int TILES>
+// Keys that a work item takes: a tree's drafted tokens come on top of a whole selection.
+template <bool TREE>
+constexpr int kItemKeys = kAttendKeys + (TREE ? kTreeNodes : 0);
+
+template <typename Q8, int HT, int TILES, bool TREE>
 struct LatentLds {
   static constexpr int HEADS = 32 * HT;
   // bytes of a key's p: one in 32 bits, or one for each block in 16
@@ -146,8 +150,9 @@ struct LatentLds {
   float alpha[2][HEADS];                    // factor of O before the tile's second product
   alignas(16) uint32_t moved[2][4];         // whether any head of a first wave has a factor other than 1
   alignas(8) float top[2][HEADS][2];        // of two tiles: the largest logarithm of p x scale, of either half of the keys
-  const uint8_t* row[kAttendKeys];          // each key's row in this layer; zeros for padding
-  uint32_t live[kAttendKeys / kTileKeys + 2];   // bit per key: not padding; none behind the last tile
+  const uint8_t* row[kItemKeys<TREE>];      // each key's row in this layer; zeros for padding
+  uint32_t live[kItemKeys<TREE> / kTileKeys + 2];   // bit per key: not padding; none behind the last tile
+  uint32_t bad[TREE ? kItemKeys<TREE> / kTileKeys + 2 : 1];   // bit per drafted token: its row holds a NaN
   int ok;
 };
 
@@ -249,14 +254,14 @@ __device__ __forceinline__ void store_heads(uint8_t* box, const f32x16 (&o)[CT][
 }
 
 // HT tiles of 32 heads; TILES tiles in the ring.
-template <typename Q8, int HT, int TILES>
+template <typename Q8, int HT, int TILES, bool TREE>
 __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g, AttendDev a) {
   constexpr int kHeads = 32 * HT;                 // heads of a workgroup
   constexpr bool kTwo = kTwoParts<Q8>;
   constexpr int CT = kScaleGroup / 32;            // 32-channel tiles of a second wave's O
   static_assert(2 * kHeads == 16 * HT * kFirstWaves, "every head has two waves in the first product");
   static_assert(TILES >= 4, "a tile on its way beside the three in use");
-  __shared__ LatentLds<Q8, HT, TILES> s;
+  __shared__ LatentLds<Q8, HT, TILES, TREE> s;
   static_assert(sizeof(s) <= 160 * 1024, "LDS of a compute unit");
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);   // uniform: its branches are scalar
@@ -299,15 +304,24 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
       for (int j = 0; j < kAtOnce; ++j) {
         const int i = i0 + j * kSecondWaves * kWave + lane;
         at[j].la = -1;
-        if (i < nkeys) at[j] = look_up(g, a.sel, set * a.k + key0 + i, a.n_res);
+        if constexpr (TREE) {
+          if (i < nkeys && key0 + i < a.sel_k) at[j] = look_up(g, a.sel, set * a.sel_k + key0 + i, a.n_res);
+        } else {
+          if (i < nkeys) at[j] = look_up(g, a.sel, set * a.k + key0 + i, a.n_res);
+        }
       }
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) {
         const int first = i0 + j * kSecondWaves * kWave;   // uniform: whole waves take part in the ballot
         if (first >= n) break;
         const uint32_t slot = slot_of(g, at[j], a.n_res, err);
-        s.row[first + lane] = slot != kAbsent ? pool + (size_t)slot * g.slot_bytes : g_zero_row;
-        const unsigned long long live = __ballot(slot != kAbsent);
+        const uint8_t* row = slot != kAbsent ? pool + (size_t)slot * g.slot_bytes : g_zero_row;
+        if constexpr (TREE) {
+          const int draft = key0 + first + lane - a.history_tiles * kTileKeys;
+          if (draft >= 0 && draft < a.nodes) row = a.drafts + ((long long)set * a.nodes + draft) * a.draft_stride;
+        }
+        s.row[first + lane] = row;
+        const unsigned long long live = __ballot(row != g_zero_row);
         if (lane < 2) s.live[first / 32 + lane] = (uint32_t)(live >> (32 * lane));
       }
     }
@@ -341,6 +355,32 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
     auto issue = [&](int tile) {
       const int at = tile % TILES;
       const uint32_t ring = lds_address(s.ring) + at * kTileBytes;
+      if constexpr (TREE) {
+        // A drafted token is seen by some nodes only, and 0 x NaN in the second product would reach the
+        // others: NaN codes and scales that are not finite become 0, and `bad` tells the softmax of the
+        // nodes that see them. Through registers, so these loads (and all before them) have arrived.
+        if (key0 / kTileKeys + tile >= a.history_tiles) {
+#pragma unroll
+          for (int i = 0; i < kPieceLoads; ++i) {
+            const int p = (i * kSecondWaves + sw) * kWave + lane;
+            const vec4u v = *reinterpret_cast<const vec4u*>(row[i] + source[i]);
+            bool any = false;
+            const vec4u clean = without_nan_codes(v, any);
+            const bool codes = source[i] < kRopeAt;
+            lds_put(ring + p * 16, codes ? clean : v);
+            if (codes && any) atomicOr(&s.bad[tile], 1u << (p / kTilePieces));
+          }
+          if (lane < kTileKeys) {
+            float scale = *reinterpret_cast<const float*>(row[kPieceLoads] + source[kPieceLoads]);
+            if (!(fabsf(scale) < __builtin_inff())) {
+              scale = 0.0f;
+              atomicOr(&s.bad[tile], 1u << lane);
+            }
+            s.scale[at][sw][lane] = scale;
+          }
+          return;
+        }
+      }
 #pragma unroll
       for (int i = 0; i < kPieceLoads; ++i) lds_load16(row[i] + source[i], ring + (i * kSecondWaves + sw) * kWave * 16);
       if (lane < kTileKeys)
@@ -437,12 +477,23 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
     }
   } else {
     QueryRaw<Q8> raw[HT];
+    unsigned long long sees[HT];                   // a tree: the drafted tokens that the row's node sees
     const ReaderState state = reader_state(g);
+    if constexpr (TREE) {
+      for (int i = threadIdx.x; i < kItemKeys<TREE> / kTileKeys + 2; i += kFirstWaves * kWave) s.bad[i] = 0;
+    }
 #pragma unroll
     for (int i = 0; i < HT; ++i) {
       const int head = hb * kHeads + head0 + 16 * i + col;
       const bool any = head < a.heads;
-      const uint16_t* p = static_cast<const uint16_t*>(a.q) + set * a.q_set_stride + head * a.q_head_stride;
+      const uint16_t* p = static_cast<const uint16_t*>(a.q) + set * a.q_set_stride;
+      if constexpr (TREE) {
+        const int node = (int)a.by_heads.div(head);
+        p += node * a.q_node_stride + (head - node * (int)a.by_heads.d) * a.q_head_stride;
+        sees[i] = any ? a.visible[(size_t)set * a.nodes + node] : 0;
+      } else {
+        p += head * a.q_head_stride;
+      }
       if (a.q_aligned) raw[i].template load<true>(p, any, quad);
       else raw[i].template load<false>(p, any, quad);
     }
@@ -479,6 +530,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
       const uint32_t scale = opaque(lds_address(s.scale) + (tile % TILES * kLatentGroups * kTileKeys + 8 * quad + 4 * key_half) * 4);
       bf16x8 kr[2] = {lds_get<bf16x8>(krow + kRopeAt), lds_get<bf16x8>(krow64 + kRopeAt)};
       const uint32_t live = __builtin_amdgcn_readfirstlane(s.live[tile]) >> (8 * quad + 4 * key_half);
+      const int draft = TREE ? key0 / kTileKeys + tile - a.history_tiles : -1;   // a tile of drafted tokens, or < 0
       f32x4 part[HT][kLatentGroups], rope[HT];
 #pragma unroll
       for (int b = 0; b < kLatentGroups; ++b) {
@@ -510,9 +562,19 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
 #pragma unroll
       for (int i = 0; i < HT; ++i) {
         float top = -__builtin_inff();
+        uint32_t mine = live;
+        if constexpr (TREE) {
+          if (draft >= 0) {
+            mine &= (uint32_t)(sees[i] >> (32 * (draft & 1))) >> (8 * quad + 4 * key_half);
+            const uint32_t bad = __builtin_amdgcn_readfirstlane(s.bad[tile]) >> (8 * quad + 4 * key_half);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (bad & (1u << r)) S[i][r] = __builtin_nanf("");
+          }
+        }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          S[i][r] = live & (1u << r) ? S[i][r] * c_log2 : -__builtin_inff();
+          S[i][r] = mine & (1u << r) ? S[i][r] * c_log2 : -__builtin_inff();
           top = fmaxf(top, S[i][r] + power[r]);
         }
         top = max_quads(top);
@@ -600,7 +662,13 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
     const bool aligned = a.out_aligned;
     using Out = std::conditional_t<std::is_same_v<Q8, bf16x8>, __bf16, _Float16>;
     store_heads<Out>(s.ring[0], o, inv, hb * kHeads, a.heads, [&](int head, int ch, const vec4u v) {
-      uint16_t* p = out + head * a.out_head_stride + ch;
+      uint16_t* p = out + ch;
+      if constexpr (TREE) {
+        const int node = (int)a.by_heads.div(head);
+        p += node * a.out_node_stride + (head - node * (int)a.by_heads.d) * a.out_head_stride;
+      } else {
+        p += head * a.out_head_stride;
+      }
       if (aligned) {
         *reinterpret_cast<vec4u*>(p) = v;
       } else {
@@ -672,12 +740,14 @@ __global__ __launch_bounds__(kJoinThreads) void k_attend_join(GroupDev g, Attend
     for (int e = 0; e < 4; ++e) acc[e] += v[e];
     sum += s_w[j];
   }
-  const int set = (int)(row / a.heads), head = (int)(row % a.heads);
+  const int set = (int)(row / a.heads), at_head = (int)(row % a.heads);
+  const int node = (int)a.by_heads.div(at_head), head = at_head - node * (int)a.by_heads.d;
   const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
   float v[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) v[e] = acc[e] * inv;
-  store4<Q8>(static_cast<uint16_t*>(a.out) + set * a.out_set_stride + head * a.out_head_stride + c, v, a.out_aligned);
+  store4<Q8>(static_cast<uint16_t*>(a.out) + set * a.out_set_stride + node * a.out_node_stride + head * a.out_head_stride + c, v,
+             a.out_aligned);
   if (threadIdx.x == 0 && a.lse) a.lse[row] = sum != 0.0f ? (top + log2f(sum)) * kLn2 : -__builtin_inff();
 }
 
@@ -695,10 +765,10 @@ __global__ __launch_bounds__(kJoinThreads) void k_attend_join(GroupDev g, Attend
 //   64 x 128, 2048       1: 73   2: 95                        1: 101  2: 79
 //   64 x 64, 700         1: 29   2: 32                        1: 42   2: 40
 //   160 x 64, 2048       1: 132  3: 141                       1: 101  3: 114
-AttendPlan plan_attend_latent(int n_sets, int k, int heads) {
+AttendPlan plan_attend_latent(int n_sets, int k, int heads, int most_keys) {
   AttendPlan best{};
   const int tiles = (k + kTileKeys - 1) / kTileKeys;
-  const int least = std::max(1, (k + kAttendKeys - 1) / kAttendKeys);
+  const int least = std::max(1, (k + most_keys - 1) / most_keys);
   const double rows = (double)n_sets * heads;
   double best_cost = 0;
   for (const int wg_heads : {32, 64}) {
@@ -721,20 +791,25 @@ AttendPlan plan_attend_latent(int n_sets, int k, int heads) {
   return best;
 }
 
-template <typename Q8, int HT, int TILES>
-static void launch_latent(const GroupDev& g, const AttendDev& a, int n_sets, hipStream_t s) {
-  k_attend_latent<Q8, HT, TILES><<<n_sets * a.head_blocks * a.splits, kWaves * kWave, 0, s>>>(g, a);
+AttendPlan plan_tree_latent(int n_sets, int tiles, int rows) {
+  static_assert(kTileTokens == kTileKeys, "a tree's tiles are those of the kernel");
+  return plan_attend_latent(n_sets, tiles * kTileKeys, rows, kItemKeys<true>);
 }
 
-template <typename Q8>
-static hipError_t launch_latent_of(const GroupDev& g, const AttendDev& a, int n_sets, hipStream_t s) {
-  if (a.head_blocks == (a.heads + 31) / 32) launch_latent<Q8, 1, 5>(g, a, n_sets, s);
-  else launch_latent<Q8, 2, 5>(g, a, n_sets, s);
+template <typename Q8, bool TREE>
+static hipError_t launch_latent(const GroupDev& g, const AttendDev& a, int n_sets, hipStream_t s) {
+  const int blocks = n_sets * a.head_blocks * a.splits;
+  if (a.head_blocks == (a.heads + 31) / 32) k_attend_latent<Q8, 1, 5, TREE><<<blocks, kWaves * kWave, 0, s>>>(g, a);
+  else k_attend_latent<Q8, 2, 5, TREE><<<blocks, kWaves * kWave, 0, s>>>(g, a);
   return hipGetLastError();
 }
 
 hipError_t launch_attend_latent(const GroupDev& g, const AttendDev& a, int type, int n_sets, hipStream_t s) {
-  return type == ULA_BF16 ? launch_latent_of<bf16x8>(g, a, n_sets, s) : launch_latent_of<f16x8>(g, a, n_sets, s);
+  return type == ULA_BF16 ? launch_latent<bf16x8, false>(g, a, n_sets, s) : launch_latent<f16x8, false>(g, a, n_sets, s);
+}
+
+hipError_t launch_tree_latent(const GroupDev& g, const AttendDev& a, int type, int n_sets, hipStream_t s) {
+  return type == ULA_BF16 ? launch_latent<bf16x8, true>(g, a, n_sets, s) : launch_latent<f16x8, true>(g, a, n_sets, s);
 }
 
 hipError_t launch_attend_join(const GroupDev& g, const AttendDev& a, int type, int n_sets, int width, hipStream_t s) {

@@ -28,6 +28,7 @@ static_assert(kLatentRow == 656, "latent row bytes");
 constexpr float kE4m3Max = 448.0f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kAttendKeys = 2048;                      // most keys one latent work item takes
+constexpr int kTreeNodes = 64;                         // most drafted tokens of a tree: bits of a mask
 constexpr int kAttendMaxSplits = 1024;             // parts of a row that the join takes
 constexpr int kJoinThreads = 256;
 
@@ -46,6 +47,14 @@ struct AttendDev {
   int32_t splits, split_keys, head_blocks;
   int32_t q_aligned, out_aligned;   // 16-byte vector accesses are possible
   int32_t kv_heads, block_shift;    // heads rows
+  FastDiv by_heads;                 // a row of heads as (node, head); without a tree node 0
+  // A tree of drafted tokens. `heads` is then nodes x heads, and a set's keys are the
+  // selected entries, padding up to whole tiles (history_tiles), and the drafted tokens.
+  long long q_node_stride, out_node_stride;
+  const uint8_t* drafts;            // this layer's row of a set's first block of drafted tokens
+  const unsigned long long* visible;   // [n_sets][nodes]
+  long long draft_stride;           // bytes from one block's row to the next
+  int32_t nodes, sel_k, history_tiles;
 };
 
 // Rotary positions: pair i turns by pos[axis] x turns[i] turns; the axis is 0 for
@@ -87,10 +96,19 @@ struct AttendPlan {
   int32_t splits, split_keys, head_blocks;
 };
 
-AttendPlan plan_attend_latent(int n_sets, int k, int heads);
+AttendPlan plan_attend_latent(int n_sets, int k, int heads, int most_keys = kAttendKeys);
 AttendPlan plan_attend_heads(int n_sets, int tokens, int heads, int kv_heads);
+// The same for a tree: rows of nodes x heads, keys as AttendDev says.
+constexpr int kTileTokens = 32;
+inline long long tree_tiles(long long tokens, int nodes) {
+  return (tokens + kTileTokens - 1) / kTileTokens + (nodes + kTileTokens - 1) / kTileTokens;
+}
+AttendPlan plan_tree_latent(int n_sets, int tiles, int rows);
+AttendPlan plan_tree_heads(int n_sets, int tiles, int rows, int kv_heads);
 
 hipError_t launch_attend_latent(const GroupDev& g, const AttendDev& a, int type, int n_sets, hipStream_t s);
+hipError_t launch_tree_latent(const GroupDev& g, const AttendDev& a, int type, int n_sets, hipStream_t s);
+hipError_t launch_tree_heads(const GroupDev& g, const AttendDev& a, int type, int n_sets, int head_dim, hipStream_t s);
 hipError_t launch_attend_heads(const GroupDev& g, const AttendDev& a, int type, int n_sets, int head_dim,
                                hipStream_t s);
 hipError_t launch_attend_join(const GroupDev& g, const AttendDev& a, int type, int n_sets, int width, hipStream_t s);
@@ -234,6 +252,18 @@ __device__ __forceinline__ void store4(uint16_t* p, const float* v, bool aligned
 #pragma unroll
     for (int e = 0; e < 4; ++e) p[e] = x.u[e];
   }
+}
+
+// 16 e4m3 codes with those that are NaN replaced by 0; `any` if there are some.
+__device__ __forceinline__ vec4u without_nan_codes(vec4u v, bool& any) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // a byte's low seven bits are all set where adding 1 to them carries into the eighth
+    const uint32_t nan = ((v[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+    any |= nan != 0;
+    v[i] &= ~((nan >> 7) * 0xFFu);
+  }
+  return v;
 }
 
 // Entry r of a selection and of the step's resolved selection, as loaded: apart

@@ -1290,27 +1290,71 @@ size_t ula_attend_bytes(const ula_row_format* rows, int32_t n_sets, int32_t k, i
   return attend_bytes(plan, n_sets, heads, width);
 }
 
-int ula_attend(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32_t k, const int32_t* sel_dev,
-               const ula_attend_args* args, uint64_t stream) {
-  if (!ctx || !args) return ULA_EINVAL;
+// The sizes of a tree's attention: `rows` are its nodes x heads.
+static bool plan_tree(const ula_row_format* f, int32_t n_sets, int32_t k, int32_t nodes, int32_t heads, AttendPlan* plan,
+                      int* width) {
+  if (ula_row_format_bytes(f) == 0 || n_sets < 0 || k < 0 || nodes < 1 || nodes > kTreeNodes) return false;
+  if (heads < 1 || (int64_t)nodes * heads > (1 << 16)) return false;
+  const int32_t rows = nodes * heads;
+  if ((int64_t)n_sets * k >= (1ll << 30) || (int64_t)n_sets * rows >= (1ll << 24)) return false;
+  if (f->kind == ULA_ROWS_LATENT) {
+    if (k > kAttendKeys * kAttendMaxSplits) return false;
+    *plan = plan_tree_latent(n_sets, (int)tree_tiles(k, nodes), rows);
+    *width = kLatent;
+  } else {
+    if (heads % f->kv_heads) return false;
+    if ((int64_t)k * f->block_tokens >= (1ll << 30)) return false;
+    *plan = plan_tree_heads(n_sets, (int)tree_tiles((int64_t)k * f->block_tokens, nodes), rows, f->kv_heads);
+    *width = f->head_dim;
+  }
+  return plan->splits <= kAttendMaxSplits && (int64_t)n_sets * plan->head_blocks * plan->splits < (1ll << 23);
+}
+
+size_t ula_attend_tree_bytes(const ula_row_format* rows, int32_t n_sets, int32_t k, int32_t nodes, int32_t heads) {
+  AttendPlan plan;
+  int width;
+  if (!plan_tree(rows, n_sets, k, nodes, heads, &plan, &width)) return 0;
+  return attend_bytes(plan, n_sets, nodes * heads, width);
+}
+
+// Checks of a reader of the group's rows.
+static int validate_reader(const ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32_t k) {
+  if (!ctx) return ULA_EINVAL;
   if (ctx->poisoned) return ULA_ESTATE;
   if (group < 0 || group >= ctx->cfg.num_groups) return ULA_EINVAL;
   if (layer < 0 || layer >= ctx->cfg.layers_per_group) return ULA_EINVAL;
   if (n_sets < 0 || k < 0 || n_sets > ctx->cfg.max_sets || k > ctx->cfg.max_k) return ULA_EINVAL;
-  const ula_attend_args& u = *args;
+  return ULA_OK;
+}
+
+// An attention call without a tree (tree == nullptr) or with one.
+static int attend_impl(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32_t k, const int32_t* sel_dev,
+                       const ula_attend_args& u, const ula_tree_args* tree, uint64_t stream) {
+  {
+    const int rc = validate_reader(ctx, group, layer, n_sets, k);
+    if (rc) return rc;
+  }
   AttendPlan plan;
   int width;
-  if (!plan_attend(&u.rows, n_sets, k, u.heads, &plan, &width)) return ULA_EINVAL;
+  const int32_t nodes = tree ? tree->nodes : 1;
+  if (tree ? !plan_tree(&u.rows, n_sets, k, nodes, u.heads, &plan, &width)
+           : !plan_attend(&u.rows, n_sets, k, u.heads, &plan, &width))
+    return ULA_EINVAL;
   if (ula_row_format_bytes(&u.rows) != (size_t)ctx->dims.row_bytes) return ULA_EINVAL;
   if (u.type != ULA_BF16 && u.type != ULA_FP16) return ULA_EINVAL;
   const double scale_log2 = u.scale * 1.4426950408889634;   // what the kernels multiply by, in 32 bits
   if (!(std::fabs(scale_log2) <= std::numeric_limits<float>::max())) return ULA_EINVAL;   // NaN too
-  const size_t need = attend_bytes(plan, n_sets, u.heads, width);
+  const int32_t rows = nodes * u.heads;
+  const size_t need = attend_bytes(plan, n_sets, rows, width);
   if (n_sets > 0) {
     if ((k > 0 && !sel_dev) || !u.q || !u.out) return ULA_EINVAL;
     if (((uintptr_t)u.q | (uintptr_t)u.out) % 2 || (uintptr_t)u.lse % 4 || (uintptr_t)sel_dev % 4) return ULA_EINVAL;
     if (rows_overlap(n_sets, u.out_set_stride, width) || rows_overlap(u.heads, u.out_head_stride, width)) return ULA_EINVAL;
     if (need && (!u.workspace || u.workspace_bytes < need || (uintptr_t)u.workspace % 16)) return ULA_EINVAL;
+    if (tree) {
+      if (!tree->drafts || (uintptr_t)tree->drafts % 16 || !tree->visible || (uintptr_t)tree->visible % 8) return ULA_EINVAL;
+      if (rows_overlap(nodes, tree->out_node_stride, width)) return ULA_EINVAL;
+    }
   }
   GroupHost& gh = ctx->groups[group];
   if (gh.steps == 0) return ULA_ENOTRESIDENT;
@@ -1320,6 +1364,7 @@ int ula_attend(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32
     const int rc = refuse_capture(s);
     if (rc) return rc;
   }
+  const bool latent = u.rows.kind == ULA_ROWS_LATENT;
   AttendDev a{};
   a.sel = sel_dev;
   a.q = u.q;
@@ -1328,7 +1373,7 @@ int ula_attend(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32
   a.part_o = static_cast<float*>(u.workspace);
   if (need)
     a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(u.workspace) +
-                                          align_up((size_t)n_sets * u.heads * plan.splits * width * sizeof(float)));
+                                          align_up((size_t)n_sets * rows * plan.splits * width * sizeof(float)));
   a.q_set_stride = u.q_set_stride;
   a.q_head_stride = u.q_head_stride;
   a.out_set_stride = u.out_set_stride;
@@ -1336,7 +1381,7 @@ int ula_attend(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32
   a.want_flag = (long long)gh.steps;
   a.scale_log2 = (float)scale_log2;
   a.k = k;
-  a.heads = u.heads;
+  a.heads = rows;
   a.layer = layer;
   a.n_res = gh.last_n;
   a.splits = plan.splits;
@@ -1344,17 +1389,44 @@ int ula_attend(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32
   a.head_blocks = plan.head_blocks;
   a.q_aligned = ((uintptr_t)u.q % 16 == 0 && u.q_set_stride % 8 == 0 && u.q_head_stride % 8 == 0) ? 1 : 0;
   a.out_aligned = ((uintptr_t)u.out % 16 == 0 && u.out_set_stride % 8 == 0 && u.out_head_stride % 8 == 0) ? 1 : 0;
-  GroupDev g = gh.d;
-  g.res = res_for(ctx, gh, gh.steps);
-  if (u.rows.kind == ULA_ROWS_LATENT) {
-    HIP_TRY(launch_attend_latent(g, a, u.type, n_sets, s));
-  } else {
+  if (!latent) {
     a.kv_heads = u.rows.kv_heads;
     while ((1 << a.block_shift) < u.rows.block_tokens) ++a.block_shift;
-    HIP_TRY(launch_attend_heads(g, a, u.type, n_sets, u.rows.head_dim, s));
   }
+  const FastDiv by_heads(u.heads);
+  a.by_heads = by_heads;
+  if (tree) {
+    a.q_node_stride = tree->q_node_stride;
+    a.out_node_stride = tree->out_node_stride;
+    if (a.q_node_stride % 8) a.q_aligned = 0;
+    if (a.out_node_stride % 8) a.out_aligned = 0;
+    a.drafts = static_cast<const uint8_t*>(tree->drafts) + (size_t)layer * ctx->dims.row_bytes;
+    a.draft_stride = (long long)ctx->dims.slot_bytes;
+    a.visible = reinterpret_cast<const unsigned long long*>(tree->visible);
+    a.nodes = nodes;
+    a.sel_k = k;
+    a.history_tiles = (int32_t)((((int64_t)k << a.block_shift) + kTileTokens - 1) / kTileTokens);
+    a.k = a.history_tiles * kTileTokens + nodes;   // key places of a set (latent rows)
+    if (!latent) a.by_heads = FastDiv(u.heads / u.rows.kv_heads);
+  }
+  GroupDev g = gh.d;
+  g.res = res_for(ctx, gh, gh.steps);
+  if (latent) HIP_TRY(tree ? launch_tree_latent(g, a, u.type, n_sets, s) : launch_attend_latent(g, a, u.type, n_sets, s));
+  else HIP_TRY(tree ? launch_tree_heads(g, a, u.type, n_sets, u.rows.head_dim, s)
+                    : launch_attend_heads(g, a, u.type, n_sets, u.rows.head_dim, s));
+  a.by_heads = by_heads;
   if (plan.splits > 1) HIP_TRY(launch_attend_join(g, a, u.type, n_sets, width, s));
   return note_gather(gh, s);
+}
+
+int ula_attend(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32_t k, const int32_t* sel_dev,
+               const ula_attend_args* args, uint64_t stream) {
+  return args ? attend_impl(ctx, group, layer, n_sets, k, sel_dev, *args, nullptr, stream) : ULA_EINVAL;
+}
+
+int ula_attend_tree(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32_t k, const int32_t* sel_dev,
+                    const ula_tree_args* args, uint64_t stream) {
+  return args ? attend_impl(ctx, group, layer, n_sets, k, sel_dev, args->attend, args, stream) : ULA_EINVAL;
 }
 
 static int read_counters(ula_ctx* ctx, std::vector<Counters>& out) {

@@ -72,6 +72,11 @@ class UlaAttendArgs(ctypes.Structure):
                 ("lse", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class UlaTreeArgs(ctypes.Structure):
+    _fields_ = [("attend", UlaAttendArgs), ("nodes", ctypes.c_int32), ("q_node_stride", ctypes.c_int64),
+                ("out_node_stride", ctypes.c_int64), ("drafts", ctypes.c_void_p), ("visible", ctypes.c_void_p)]
+
+
 class UlaRotary(ctypes.Structure):
     _fields_ = [("axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 3), ("interleaved", ctypes.c_int32),
                 ("theta", ctypes.c_double)]
@@ -114,6 +119,10 @@ SIGNATURES = [
     ("ula_attend_bytes", ctypes.c_size_t, [ctypes.POINTER(RowFormat), ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
     ("ula_attend", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                   ctypes.c_void_p, ctypes.POINTER(UlaAttendArgs), ctypes.c_uint64]),
+    ("ula_attend_tree_bytes", ctypes.c_size_t, [ctypes.POINTER(RowFormat), ctypes.c_int32, ctypes.c_int32,
+                                                ctypes.c_int32, ctypes.c_int32]),
+    ("ula_attend_tree", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                       ctypes.c_void_p, ctypes.POINTER(UlaTreeArgs), ctypes.c_uint64]),
     ("ula_fork", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                 ctypes.c_uint64]),
     ("ula_rename", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
@@ -404,6 +413,27 @@ def rotate(x, positions, sections=None, theta: float = 10000.0, interleaved: boo
     return out
 
 
+def tree_masks(parents) -> np.ndarray:
+    """Masks for attend_tree (int64, shaped as `parents`, [nodes] or [n_sets][nodes], at most 64 nodes) of trees
+    given by each node's parent, an earlier node's number or -1 for a root: bit j of a node is set for each node j
+    on its way to the root, itself too. numpy in, numpy out."""
+    parents = np.asarray(parents)
+    if parents.dtype.kind not in "iu" or parents.ndim not in (1, 2):
+        raise ValueError("tree_masks: integers [nodes] or [n_sets][nodes] are required")
+    nodes = parents.shape[-1]
+    if nodes > 64:
+        raise ValueError(f"tree_masks: {nodes} nodes, at most 64")
+    rows = parents.reshape(-1, nodes).astype(np.int64)
+    if ((rows < -1) | (rows >= np.arange(nodes))).any():
+        raise ValueError("tree_masks: a parent is an earlier node's number or -1")
+    out = np.zeros(rows.shape, np.uint64)
+    each = np.arange(len(rows))
+    for t in range(nodes):
+        above = np.where(rows[:, t] >= 0, out[each, np.maximum(rows[:, t], 0)], np.uint64(0))
+        out[:, t] = above | np.uint64(1 << t)
+    return out.view(np.int64).reshape(parents.shape)
+
+
 class Engine:
     """One engine context: per group a GPU pool, a pinned host pool and PB-LRU state."""
 
@@ -563,6 +593,56 @@ class Engine:
             _check(lib().ula_attend(self.ctx, group, layer, n_sets, k,
                                     _dev(sel, "int32", n_sets * k, "ula_attend sel"), ctypes.byref(args), s),
                    "ula_attend")
+        return out, lse
+
+    def attend_tree(self, group: int, layer: int, sel, q, fmt: RowFormat, drafts, visible, scale: Optional[float] = None,
+                    out=None, lse=None, stream=None):
+        """(out, lse): attention of a tree of drafted tokens per set. q [n_sets][nodes][heads][576 or head_dim]
+        (bf16 or fp16, at most 64 nodes); every node attends to the set's selected entries and to the drafted
+        tokens whose bit its mask `visible` (int64 [n_sets][nodes], see tree_masks) has. drafts: their rows, not
+        appended yet, as pack_rows gives them: uint8 [n_sets * ceil(nodes / block_tokens)][layers][row_bytes].
+        out [n_sets][nodes][heads][512 or head_dim], lse fp32 [n_sets][nodes][heads]; the rest as for attend."""
+        import torch
+        _no_gradient("ula_attend_tree", q, out, lse)
+        n_sets, k = _sets(sel)
+        args = UlaTreeArgs()
+        at = args.attend
+        at.rows = fmt
+        latent = fmt.kind == ROWS_LATENT
+        width = LATENT_CHANNELS + ROPE_CHANNELS if latent else fmt.head_dim
+        back = LATENT_CHANNELS if latent else fmt.head_dim
+        if q.dim() != 4:
+            raise ValueError(f"ula_attend_tree q: shape {tuple(q.shape)}, expected ({n_sets}, None, None, {width})")
+        nodes, heads = q.shape[1:3]
+        at.q, at.type, st = _tensor(q, (n_sets, None, None, width), "ula_attend_tree q", (BF16, FP16))
+        at.q_set_stride, args.q_node_stride, at.q_head_stride = st[:3]
+        at.heads, args.nodes = heads, nodes
+        at.scale = 1.0 / width ** 0.5 if scale is None else scale
+        per_set = nodes if latent else -(-nodes // max(fmt.block_tokens, 1))
+        args.drafts = _dev(drafts, "uint8", n_sets * per_set * self.layers * self.row_bytes,
+                           "ula_attend_tree drafts")
+        args.visible = _dev(visible, "int64", n_sets * nodes, "ula_attend_tree visible")
+        _same_device(q, sel, drafts, visible, out, lse, self)
+        on = _On(q.device, stream, q, sel, drafts, visible, out, lse)
+        with on as s:
+            if out is None:
+                out = torch.empty((n_sets, nodes, heads, back), dtype=q.dtype, device=q.device)
+                on.give(out)
+            at.out, code, st = _tensor(out, (n_sets, nodes, heads, back), "ula_attend_tree out")
+            if code != at.type:
+                raise ValueError(f"ula_attend_tree out: dtype {out.dtype}, expected {q.dtype}")
+            at.out_set_stride, args.out_node_stride, at.out_head_stride = st[:3]
+            if lse is None:
+                lse = torch.empty((n_sets, nodes, heads), dtype=torch.float32, device=q.device)
+                on.give(lse)
+            at.lse = _dev(lse, "float32", n_sets * nodes * heads, "ula_attend_tree lse")
+            at.workspace_bytes = lib().ula_attend_tree_bytes(ctypes.byref(fmt), n_sets, k, nodes, heads)
+            if at.workspace_bytes:
+                work = torch.empty(at.workspace_bytes, dtype=torch.uint8, device=q.device)
+                at.workspace = work.data_ptr()
+            _check(lib().ula_attend_tree(self.ctx, group, layer, n_sets, k,
+                                         _dev(sel, "int32", n_sets * k, "ula_attend_tree sel"), ctypes.byref(args), s),
+                   "ula_attend_tree")
         return out, lse
 
     def sync(self, stream=None) -> List[tuple]:
