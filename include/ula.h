@@ -443,6 +443,36 @@ typedef struct {
 int ula_rotate(const ula_rotate_args* args, uint64_t stream);
 
 typedef struct {
+  int32_t type;              /* of q, k and the results: ULA_BF16, ULA_FP16 or ULA_FP32 */
+  int32_t n, dim;            /* tokens; channels of a head: even, 2..256 */
+  int32_t q_heads, k_heads;  /* either may be 0 */
+  int32_t rotary_dim;        /* R: the first channels, which turn: even, 0..dim (0: norms alone) */
+  int32_t weight_type;       /* of the weights: type or ULA_FP32 */
+  float eps;                 /* finite and > 0 */
+  const void* q;             /* [n][q_heads][dim], last dimension contiguous */
+  const void* k;             /* [n][k_heads][dim] */
+  void* q_out;               /* the same shapes; q and k themselves with the same strides, or no overlap with */
+  void* k_out;               /*   anything else; rows share no elements (ULA_EINVAL if a stride says so) */
+  int64_t q_stride[2];       /* strides in elements: token, head */
+  int64_t k_stride[2];
+  int64_t q_out_stride[2];
+  int64_t k_out_stride[2];
+  const void* q_weight;      /* [dim], nullable (all 1) */
+  const void* k_weight;
+  const int32_t* positions;  /* [n][axes] packed, read if rotary_dim > 0 */
+  ula_rotary rotary;         /* of R channels, read if rotary_dim > 0 */
+} ula_norm_args;
+
+/* Norms of the queries and keys of n tokens, each head by itself, and their turn in
+ * the same pass: y_i = w_i x_i / sqrt(mean of x^2 + eps) over the head's channels,
+ * then the first R channels turned as by ula_rotate. In 32 bits, rounded to the type
+ * once; rows of large values do not overflow; a row with an infinity gives 0 and NaN in its
+ * place, one with a NaN gives NaN. A pure function of its device inputs; it may be
+ * captured into a graph. Errors: ULA_EINVAL (also more rows than a launch takes:
+ * n * (q_heads + k_heads) < 2^25 always fits), ULA_EHIP. */
+int ula_norm_rotate(const ula_norm_args* args, uint64_t stream);
+
+typedef struct {
   ula_row_format rows;       /* the group's rows; its bytes must equal the configuration's row_bytes */
   int32_t type;              /* of q and out: ULA_BF16 or ULA_FP16 */
   int32_t heads;             /* query heads, >= 1; heads rows: a multiple of kv_heads */
@@ -533,6 +563,71 @@ size_t ula_attend_tree_bytes(const ula_row_format* rows, int32_t n_sets, int32_t
  * or nodes * heads > 2^16. */
 int ula_attend_tree(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32_t k, const int32_t* sel_dev,
                     const ula_tree_args* args, uint64_t stream);
+
+typedef struct {
+  ula_row_format rows;       /* the group's rows; its bytes must equal the configuration's row_bytes */
+  int32_t type;              /* of q: ULA_BF16 or ULA_FP16 */
+  int32_t nodes, heads;      /* query rows of a set: nodes (1 without a tree, at most 64) x heads */
+  float scale;               /* factor of the logits, as in the attention */
+  const void* q;             /* [n_sets][nodes][heads][576 (latent) or head_dim], last dimension contiguous */
+  int64_t q_set_stride;      /* strides in elements */
+  int64_t q_node_stride;     /* not read for one node */
+  int64_t q_head_stride;
+  const float* lse;          /* [n_sets][nodes][heads] packed, from the attention */
+  float* shares;             /* nullable, [n_sets][k] packed */
+  int64_t* scores;           /* nullable, [logical_capacity]; one of the two is required */
+} ula_weigh_args;
+
+/* The softmax weight that each selected entry got in an attention with these queries
+ * and log-sums, summed over the set's query rows:
+ *   share_j = sum_r exp(scale * q_r . key_j - lse_r)
+ * (heads rows: over an entry's tokens in use and over every head with its KV head), written to
+ * shares and added to the score of the entry's address (eviction by accumulated
+ * attention weight: see ula_lightest). Scores are whole numbers in units of 2^-32, so an address that
+ * is listed more than once gets the same score whatever the order of the adds. -1
+ * entries have share 0 and add nothing. A row whose lse is not finite counts for
+ * nothing (it attended to nothing; a rejected node is left out that way). With log-sums
+ * that cover more than these entries (a tree's drafted tokens) shares are of the whole.
+ * A share that is NaN adds nothing to the score, one above 2^22 adds that. Products, logits and
+ * sums are in 32 bits, summed in an order that depends on the sizes alone. Nothing but keys
+ * is read of the rows. q, lse, shares and scores must not overlap. Calls that add to the same scores at the
+ * same time are fine. Which entries, streams and errors: as for ula_attend. Host errors: also
+ * ULA_EINVAL for nodes outside 1..64, nodes * heads > 2^16, n_sets * nodes * heads >= 2^24, and heads rows
+ * with n_sets * k * block_tokens >= 2^30. */
+int ula_weigh(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32_t k, const int32_t* sel_dev,
+              const ula_weigh_args* args, uint64_t stream);
+
+typedef struct {
+  int64_t* scores;           /* device memory, [capacity], 8-byte aligned; read, and written if mark */
+  int32_t capacity;          /* scores there are */
+  int32_t ranges;            /* ranges of addresses */
+  const int32_t* first;      /* host memory, [ranges] each: addresses first .. last - 1, */
+  const int32_t* last;
+  const int32_t* count;      /*   and how many entries each gives up, 0..most */
+  int32_t most;              /* columns of out */
+  int32_t mark;              /* 1: the scores of the entries chosen become -1 */
+  int32_t* out;              /* device memory, [ranges][most] */
+  void* workspace;           /* device memory of ula_lightest_bytes bytes, 16-byte aligned; may be NULL for 0 */
+  size_t workspace_bytes;
+} ula_lightest_args;
+
+/* Bytes of workspace that ula_lightest needs for these ranges (0: none, or invalid
+ * arguments, which ula_lightest reports). A pure host function. */
+size_t ula_lightest_bytes(const ula_lightest_args* args);
+
+/* Of each range of addresses the `count` entries of least score (eviction by
+ * accumulated attention weight; a request's first tokens and its recent ones stay out
+ * of its range), ties by lowest address, in ascending order of address: what
+ * ula_release takes, once copied to the host. Entries of negative score are not there:
+ * absent addresses, which the caller, or mark, set to -1. Where a range has fewer, and from
+ * `count` on, out is -1. Ranges may be empty, and may overlap unless mark is set.
+ * Nothing of an engine is involved; calls that may run at the same time need workspaces of
+ * their own. It may be captured into a graph (the ranges are those of the call; the
+ * host arrays are read before it returns).
+ * Errors: ULA_EINVAL (null or misaligned pointers, negative sizes, first > last, a count outside
+ * 0..most, ranges * most >= 2^31, overlapping ranges with mark, a missing or small
+ * workspace), ULA_ERANGE (an address outside [0, capacity)), ULA_EHIP. */
+int ula_lightest(const ula_lightest_args* args, uint64_t stream);
 
 /* Wait for `stream`, then report the first latched device error of any group
  * (poisoning the context) or ULA_OK (section 3: a host waiter for the steps'

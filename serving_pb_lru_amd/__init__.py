@@ -12,8 +12,8 @@ the rows' contents: the FP8 row writer, rotary positions, attention over the
 selected rows, and copies and new addresses for entries.
 """
 
-from .ula import (Engine, RowFormat, UlaError, lib, ERROR_NAMES, head_rows, latent_rows, pack_rows, rotate,
-                  tree_masks)
+from .ula import (Engine, RowFormat, UlaError, lib, ERROR_NAMES, head_rows, latent_rows, lightest,
+                  norm_rotate, pack_rows, rotate, tree_masks)
 
-__all__ = ["Engine", "RowFormat", "UlaError", "lib", "ERROR_NAMES", "head_rows", "latent_rows", "pack_rows", "rotate",
-           "tree_masks"]
+__all__ = ["Engine", "RowFormat", "UlaError", "lib", "ERROR_NAMES", "head_rows", "latent_rows", "lightest",
+           "norm_rotate", "pack_rows", "rotate", "tree_masks"]

@@ -27,6 +27,7 @@ constexpr int kLatentRow = kLatentScaleAt + 4 * kLatentGroups;
 static_assert(kLatentRow == 656, "latent row bytes");
 constexpr float kE4m3Max = 448.0f;
 constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kLog2e = 1.44269504088896341f;
 constexpr int kAttendKeys = 2048;                      // most keys one latent work item takes
 constexpr int kTreeNodes = 64;                         // most drafted tokens of a tree: bits of a mask
 constexpr int kAttendMaxSplits = 1024;             // parts of a row that the join takes
@@ -57,6 +58,29 @@ struct AttendDev {
   int32_t nodes, sel_k, history_tiles;
 };
 
+// Device arguments of the entries' weights: rows are nodes x heads.
+struct WeighDev {
+  const int32_t* sel;
+  const void* q;
+  const float* lse;                 // [n_sets][rows]
+  float* shares;                    // nullable, [n_sets][k]
+  unsigned long long* scores;       // nullable, by address
+  long long q_set_stride, q_node_stride, q_head_stride;   // elements
+  long long want_flag;
+  FastDiv by_heads;                 // a row as (node, head); heads rows: those of one KV head
+  float scale_log2;
+  int32_t k, rows, nodes, layer, n_res, q_aligned;
+  int32_t splits, groups;
+  int32_t kv_heads, block_shift;    // heads rows
+};
+struct WeighPlan {
+  int32_t splits, groups;           // workgroups (heads rows: waves) of a set; key groups of each (latent rows)
+};
+WeighPlan plan_weigh_latent(int n_sets, int k);
+WeighPlan plan_weigh_heads(long long tokens, int shared);
+hipError_t launch_weigh_latent(const GroupDev& g, const WeighDev& a, int type, int n_sets, hipStream_t s);
+hipError_t launch_weigh_heads(const GroupDev& g, const WeighDev& a, int type, int n_sets, int head_dim, hipStream_t s);
+
 // Rotary positions: pair i turns by pos[axis] x turns[i] turns; the axis is 0 for
 // i < end0, 1 for i < end1, else 2.
 constexpr int kMostPairs = 128;
@@ -86,6 +110,21 @@ struct RotateDev {
   int32_t n, heads, dim, inverse, aligned;
   int32_t tokens_per_block, heads_per_block;
 };
+
+// Device arguments of the norms: a token's rows are its query heads, then its key heads.
+struct NormDev {
+  const void *q, *k;
+  void *q_out, *k_out;
+  const void *q_weight, *k_weight;        // nullable
+  const int32_t* positions;               // read if rotary > 0
+  long long q_stride[2], k_stride[2], q_out_stride[2], k_out_stride[2];   // elements: token, head
+  float eps;
+  int32_t n, q_heads, k_heads, dim, rotary, wide_weights, aligned;
+  int32_t tokens_per_block, heads_per_block;
+};
+
+long long plan_norm(NormDev* a);          // fills the workgroup's part in; how many there are
+hipError_t launch_norm(const NormDev& a, const RotaryDev& rot, int type, hipStream_t s);
 
 hipError_t launch_pack(const PackDev& a, const RotaryDev& rot, int type, hipStream_t s);
 long long pack_heads_blocks(const PackDev& a);   // workgroups of heads rows, of either side

@@ -13,6 +13,7 @@
 #include <string>
 #include <vector>
 
+#include "lightest.h"
 #include "row_format.h"
 
 using namespace ula;
@@ -1258,6 +1259,62 @@ int ula_rotate(const ula_rotate_args* args, uint64_t stream) {
   return ULA_OK;
 }
 
+int ula_norm_rotate(const ula_norm_args* args, uint64_t stream) {
+  if (!args) return ULA_EINVAL;
+  const ula_norm_args& u = *args;
+  int size;
+  if (!element_size(u.type, &size) || u.n < 0 || u.q_heads < 0 || u.k_heads < 0) return ULA_EINVAL;
+  if ((int64_t)u.q_heads + u.k_heads > (1 << 24)) return ULA_EINVAL;
+  if (u.dim < 2 || u.dim % 2 || u.dim > 2 * kMostPairs) return ULA_EINVAL;
+  if (u.rotary_dim < 0 || u.rotary_dim % 2 || u.rotary_dim > u.dim) return ULA_EINVAL;
+  if (u.weight_type != u.type && u.weight_type != ULA_FP32) return ULA_EINVAL;
+  if (!(u.eps > 0) || !std::isfinite(u.eps)) return ULA_EINVAL;
+  RotaryDev rot{};
+  if (u.rotary_dim && !rotary_dev(u.rotary, u.rotary_dim / 2, &rot)) return ULA_EINVAL;
+  const int wsize = u.weight_type == ULA_FP32 ? 4 : size;
+  if (((uintptr_t)u.q_weight | (uintptr_t)u.k_weight) % wsize || (uintptr_t)u.positions % 4) return ULA_EINVAL;
+  if (u.n == 0 || u.q_heads + u.k_heads == 0) return ULA_OK;
+  if (u.rotary_dim && !u.positions) return ULA_EINVAL;
+  NormDev a{};
+  // vectors of four channels, or of eight where pairs are interleaved
+  const int vec = (rot.interleaved ? 8 : 4) * size;
+  a.aligned = 1;
+  auto side = [&](int heads, const void* x, void* out, const int64_t* st, const int64_t* st_out) {
+    if (heads == 0) return true;
+    if (!x || !out || ((uintptr_t)x | (uintptr_t)out) % size) return false;
+    if (rows_overlap(u.n, st_out[0], u.dim) || rows_overlap(heads, st_out[1], u.dim)) return false;
+    if (((uintptr_t)x | (uintptr_t)out) % vec) a.aligned = 0;
+    for (int i = 0; i < 2; ++i)
+      if (st[i] * size % vec || st_out[i] * size % vec) a.aligned = 0;
+    return true;
+  };
+  if (!side(u.q_heads, u.q, u.q_out, u.q_stride, u.q_out_stride)) return ULA_EINVAL;
+  if (!side(u.k_heads, u.k, u.k_out, u.k_stride, u.k_out_stride)) return ULA_EINVAL;
+  a.q = u.q;
+  a.k = u.k;
+  a.q_out = u.q_out;
+  a.k_out = u.k_out;
+  a.q_weight = u.q_weight;
+  a.k_weight = u.k_weight;
+  a.positions = u.positions;
+  for (int i = 0; i < 2; ++i) {
+    a.q_stride[i] = u.q_stride[i];
+    a.k_stride[i] = u.k_stride[i];
+    a.q_out_stride[i] = u.q_out_stride[i];
+    a.k_out_stride[i] = u.k_out_stride[i];
+  }
+  a.eps = u.eps;
+  a.n = u.n;
+  a.q_heads = u.q_heads;
+  a.k_heads = u.k_heads;
+  a.dim = u.dim;
+  a.rotary = u.rotary_dim;
+  a.wide_weights = u.weight_type == ULA_FP32;
+  if (plan_norm(&a) >= (1ll << 24)) return ULA_EINVAL;   // a launch has fewer than 2^32 threads, 256 each
+  HIP_TRY(launch_norm(a, rot, u.type, reinterpret_cast<hipStream_t>(stream)));
+  return ULA_OK;
+}
+
 // The sizes of an attention call as a plan; false for invalid ones.
 static bool plan_attend(const ula_row_format* f, int32_t n_sets, int32_t k, int32_t heads, AttendPlan* plan,
                         int* width) {
@@ -1427,6 +1484,152 @@ int ula_attend(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32
 int ula_attend_tree(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32_t k, const int32_t* sel_dev,
                     const ula_tree_args* args, uint64_t stream) {
   return args ? attend_impl(ctx, group, layer, n_sets, k, sel_dev, args->attend, args, stream) : ULA_EINVAL;
+}
+
+int ula_weigh(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32_t k, const int32_t* sel_dev,
+              const ula_weigh_args* args, uint64_t stream) {
+  if (!args) return ULA_EINVAL;
+  {
+    const int rc = validate_reader(ctx, group, layer, n_sets, k);
+    if (rc) return rc;
+  }
+  const ula_weigh_args& u = *args;
+  if (ula_row_format_bytes(&u.rows) == 0 || ula_row_format_bytes(&u.rows) != (size_t)ctx->dims.row_bytes) return ULA_EINVAL;
+  if (u.type != ULA_BF16 && u.type != ULA_FP16) return ULA_EINVAL;
+  if (u.nodes < 1 || u.nodes > kTreeNodes || u.heads < 1 || (int64_t)u.nodes * u.heads > (1 << 16)) return ULA_EINVAL;
+  const int32_t rows = u.nodes * u.heads;
+  if ((int64_t)n_sets * k >= (1ll << 30) || (int64_t)n_sets * rows >= (1ll << 24)) return ULA_EINVAL;
+  const bool latent = u.rows.kind == ULA_ROWS_LATENT;
+  WeighPlan plan;
+  if (latent) {
+    plan = plan_weigh_latent(n_sets, k);
+  } else {
+    if (u.heads % u.rows.kv_heads) return ULA_EINVAL;
+    if ((int64_t)n_sets * k * u.rows.block_tokens >= (1ll << 30)) return ULA_EINVAL;
+    plan = plan_weigh_heads((int64_t)k * u.rows.block_tokens, rows / u.rows.kv_heads);
+  }
+  if ((int64_t)n_sets * plan.splits >= (latent ? 1ll << 23 : 1ll << 26)) return ULA_EINVAL;   // 512 threads, 64
+  const double scale_log2 = u.scale * 1.4426950408889634;   // what the kernels multiply by, in 32 bits
+  if (!(std::fabs(scale_log2) <= std::numeric_limits<float>::max())) return ULA_EINVAL;   // NaN too
+  if (n_sets > 0 && k > 0) {
+    if (!sel_dev || !u.q || !u.lse || (!u.shares && !u.scores)) return ULA_EINVAL;
+    if ((uintptr_t)u.q % 2 || ((uintptr_t)u.lse | (uintptr_t)u.shares | (uintptr_t)sel_dev) % 4) return ULA_EINVAL;
+    if ((uintptr_t)u.scores % 8) return ULA_EINVAL;
+  }
+  GroupHost& gh = ctx->groups[group];
+  if (gh.steps == 0) return ULA_ENOTRESIDENT;
+  if (n_sets == 0 || k == 0) return ULA_OK;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  {
+    const int rc = refuse_capture(s);
+    if (rc) return rc;
+  }
+  WeighDev a{};
+  a.sel = sel_dev;
+  a.q = u.q;
+  a.lse = u.lse;
+  a.shares = u.shares;
+  a.scores = reinterpret_cast<unsigned long long*>(u.scores);
+  a.q_set_stride = u.q_set_stride;
+  a.q_node_stride = u.q_node_stride;
+  a.q_head_stride = u.q_head_stride;
+  a.want_flag = (long long)gh.steps;
+  a.scale_log2 = (float)scale_log2;
+  a.k = k;
+  a.rows = rows;
+  a.nodes = u.nodes;
+  a.layer = layer;
+  a.n_res = gh.last_n;
+  a.q_aligned = (uintptr_t)u.q % 16 == 0 && u.q_set_stride % 8 == 0 && u.q_head_stride % 8 == 0 &&
+                (u.nodes == 1 || u.q_node_stride % 8 == 0);
+  a.splits = plan.splits;
+  a.groups = plan.groups;
+  a.by_heads = FastDiv(latent ? u.heads : u.heads / u.rows.kv_heads);
+  GroupDev g = gh.d;
+  g.res = res_for(ctx, gh, gh.steps);
+  if (latent) {
+    HIP_TRY(launch_weigh_latent(g, a, u.type, n_sets, s));
+  } else {
+    a.kv_heads = u.rows.kv_heads;
+    while ((1 << a.block_shift) < u.rows.block_tokens) ++a.block_shift;
+    HIP_TRY(launch_weigh_heads(g, a, u.type, n_sets, u.rows.head_dim, s));
+  }
+  return note_gather(gh, s);
+}
+
+// The next launch's ranges from `at` on, and the workspace that its long ones need.
+struct LightLaunch {
+  LightRanges ranges{};
+  size_t bins = 0, list = 0;   // bytes
+};
+static void light_launch(const ula_lightest_args& u, int32_t at, LightLaunch* l) {
+  l->ranges.n = std::min(kLightRanges, u.ranges - at);
+  l->ranges.first_range = at;
+  int64_t chunks = 0, keys = 0;
+  for (int32_t i = 0; i < l->ranges.n; ++i) {
+    LightRange& r = l->ranges.range[i];
+    r = {u.first[at + i], u.last[at + i] - u.first[at + i], u.count[at + i]};
+    if (const int n = light_chunks(r.length)) {
+      chunks += n;
+      keys += r.length;
+    }
+  }
+  l->bins = align_up((size_t)chunks * kLightBins * sizeof(uint32_t));
+  l->list = align_up((size_t)keys * sizeof(uint64_t));
+}
+
+// Checks of the ranges: ULA_OK, ULA_EINVAL or ULA_ERANGE.
+static int validate_lightest(const ula_lightest_args& u) {
+  if (u.ranges < 0 || u.most < 0 || u.capacity < 0 || (u.mark != 0 && u.mark != 1)) return ULA_EINVAL;
+  if (u.ranges > 0 && (!u.first || !u.last || !u.count)) return ULA_EINVAL;
+  if ((int64_t)u.ranges * u.most >= (1ll << 31)) return ULA_EINVAL;
+  for (int32_t i = 0; i < u.ranges; ++i) {
+    if (u.count[i] < 0 || u.count[i] > u.most || u.first[i] > u.last[i]) return ULA_EINVAL;
+    if (u.first[i] < 0 || u.last[i] > u.capacity) return ULA_ERANGE;
+  }
+  if (!u.mark) return ULA_OK;
+  // marked entries of one range would be missing in another, or not, as the launch goes
+  std::vector<std::pair<int32_t, int32_t>> r;
+  for (int32_t i = 0; i < u.ranges; ++i)
+    if (u.first[i] < u.last[i]) r.emplace_back(u.first[i], u.last[i]);
+  std::sort(r.begin(), r.end());
+  for (size_t i = 1; i < r.size(); ++i)
+    if (r[i].first < r[i - 1].second) return ULA_EINVAL;
+  return ULA_OK;
+}
+
+size_t ula_lightest_bytes(const ula_lightest_args* args) {
+  if (!args || validate_lightest(*args)) return 0;
+  size_t need = 0;
+  for (int64_t at = 0; at < args->ranges; at += kLightRanges) {
+    LightLaunch l;
+    light_launch(*args, (int32_t)at, &l);
+    need = std::max(need, l.bins + l.list);
+  }
+  return need;
+}
+
+int ula_lightest(const ula_lightest_args* args, uint64_t stream) {
+  if (!args) return ULA_EINVAL;
+  const ula_lightest_args& u = *args;
+  if (const int rc = validate_lightest(u)) return rc;
+  if (u.ranges == 0 || u.most == 0) return ULA_OK;
+  if (!u.scores || (uintptr_t)u.scores % 8 || !u.out || (uintptr_t)u.out % 4) return ULA_EINVAL;
+  const size_t need = ula_lightest_bytes(args);
+  if (need && (!u.workspace || u.workspace_bytes < need || (uintptr_t)u.workspace % 16)) return ULA_EINVAL;
+  for (int64_t at = 0; at < u.ranges; at += kLightRanges) {
+    LightLaunch l;
+    light_launch(u, (int32_t)at, &l);
+    LightDev a{};
+    a.scores = reinterpret_cast<long long*>(u.scores);
+    a.out = u.out;
+    a.bins = static_cast<uint32_t*>(u.workspace);
+    a.list = l.list ? reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(u.workspace) + l.bins) : nullptr;
+    a.most = u.most;
+    a.mark = u.mark;
+    HIP_TRY(launch_lightest(a, l.ranges, reinterpret_cast<hipStream_t>(stream)));
+  }
+  return ULA_OK;
 }
 
 static int read_counters(ula_ctx* ctx, std::vector<Counters>& out) {

@@ -77,6 +77,20 @@ class UlaTreeArgs(ctypes.Structure):
                 ("out_node_stride", ctypes.c_int64), ("drafts", ctypes.c_void_p), ("visible", ctypes.c_void_p)]
 
 
+class UlaWeighArgs(ctypes.Structure):
+    _fields_ = [("rows", RowFormat), ("type", ctypes.c_int32), ("nodes", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("q", ctypes.c_void_p), ("q_set_stride", ctypes.c_int64),
+                ("q_node_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64), ("lse", ctypes.c_void_p),
+                ("shares", ctypes.c_void_p), ("scores", ctypes.c_void_p)]
+
+
+class UlaLightestArgs(ctypes.Structure):
+    _fields_ = [("scores", ctypes.c_void_p), ("capacity", ctypes.c_int32), ("ranges", ctypes.c_int32),
+                ("first", ctypes.c_void_p), ("last", ctypes.c_void_p), ("count", ctypes.c_void_p), ("most", ctypes.c_int32),
+                ("mark", ctypes.c_int32), ("out", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 class UlaRotary(ctypes.Structure):
     _fields_ = [("axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 3), ("interleaved", ctypes.c_int32),
                 ("theta", ctypes.c_double)]
@@ -93,6 +107,16 @@ class UlaRotateArgs(ctypes.Structure):
     _fields_ = [("type", ctypes.c_int32), ("n", ctypes.c_int32), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
                 ("inverse", ctypes.c_int32), ("x", ctypes.c_void_p), ("out", ctypes.c_void_p),
                 ("x_stride", ctypes.c_int64 * 2), ("out_stride", ctypes.c_int64 * 2), ("positions", ctypes.c_void_p),
+                ("rotary", UlaRotary)]
+
+
+class UlaNormArgs(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("n", ctypes.c_int32), ("dim", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+                ("k_heads", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("weight_type", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("k_out", ctypes.c_void_p), ("q_stride", ctypes.c_int64 * 2), ("k_stride", ctypes.c_int64 * 2),
+                ("q_out_stride", ctypes.c_int64 * 2), ("k_out_stride", ctypes.c_int64 * 2),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("positions", ctypes.c_void_p),
                 ("rotary", UlaRotary)]
 
 
@@ -116,6 +140,7 @@ SIGNATURES = [
     ("ula_row_format_bytes", ctypes.c_size_t, [ctypes.POINTER(RowFormat)]),
     ("ula_pack_rows", ctypes.c_int, [ctypes.POINTER(UlaPackArgs), ctypes.c_void_p, ctypes.c_uint64]),
     ("ula_rotate", ctypes.c_int, [ctypes.POINTER(UlaRotateArgs), ctypes.c_uint64]),
+    ("ula_norm_rotate", ctypes.c_int, [ctypes.POINTER(UlaNormArgs), ctypes.c_uint64]),
     ("ula_attend_bytes", ctypes.c_size_t, [ctypes.POINTER(RowFormat), ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
     ("ula_attend", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                   ctypes.c_void_p, ctypes.POINTER(UlaAttendArgs), ctypes.c_uint64]),
@@ -123,6 +148,10 @@ SIGNATURES = [
                                                 ctypes.c_int32, ctypes.c_int32]),
     ("ula_attend_tree", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                        ctypes.c_void_p, ctypes.POINTER(UlaTreeArgs), ctypes.c_uint64]),
+    ("ula_weigh", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                 ctypes.c_void_p, ctypes.POINTER(UlaWeighArgs), ctypes.c_uint64]),
+    ("ula_lightest_bytes", ctypes.c_size_t, [ctypes.POINTER(UlaLightestArgs)]),
+    ("ula_lightest", ctypes.c_int, [ctypes.POINTER(UlaLightestArgs), ctypes.c_uint64]),
     ("ula_fork", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                 ctypes.c_uint64]),
     ("ula_rename", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
@@ -250,6 +279,19 @@ def _tensor(t, shape, what: str, types=(BF16, FP16, FP32)):
     if strides[-1] != 1 and real[-1] > 1 and t.numel():
         raise ValueError(f"{what}: the last dimension must be contiguous")
     return t.data_ptr(), code, strides
+
+
+def _host_ints(x, what: str) -> np.ndarray:
+    """A one-dimensional int32 array of integers that fit it."""
+    if isinstance(x, np.ndarray) and x.dtype == np.int32 and x.ndim == 1 and x.flags.c_contiguous:
+        return x
+    y = np.asarray(x)
+    if y.ndim != 1 or (y.size and y.dtype.kind not in "iu"):
+        raise ValueError(f"{what}: a list of integers is required")
+    z = np.ascontiguousarray(y, dtype=np.int32)
+    if (z != y).any():
+        raise ValueError(f"{what}: an integer outside 32 bits")
+    return z
 
 
 def _same_device(first, *others) -> None:
@@ -413,6 +455,101 @@ def rotate(x, positions, sections=None, theta: float = 10000.0, interleaved: boo
     return out
 
 
+def norm_rotate(q, k=None, q_weight=None, k_weight=None, positions=None, sections=None, theta: float = 10000.0,
+                interleaved: bool = False, rotary: Optional[int] = None, eps: float = 1e-6, out=None, stream=None):
+    """(q, k) with each head's channels divided by their root mean square (eps inside the root) times the weights,
+    and the first `rotary` channels (default: all) turned by int32 positions [n][axes] (or [n]; none: norms
+    alone), in one launch. q [n][heads][dim], k [n][kv_heads][dim] or None, bf16, fp16 or fp32; weights [dim] in
+    that type or fp32, or None for ones. out: a pair of tensors shaped as q and k, themselves for in place. No
+    gradient is recorded: tensors that require one are refused."""
+    import torch
+    q_out, k_out = out if out is not None else (None, None)
+    _no_gradient("norm_rotate", q, k, q_weight, k_weight, q_out, k_out)
+    args = UlaNormArgs()
+    args.q, args.type, st_q = _tensor(q, (None, None, None), "norm_rotate q")
+    n, heads, dim = q.shape
+    args.n, args.q_heads, args.dim = n, heads, dim
+    if k is not None:
+        args.k, code, st_k = _tensor(k, (n, None, dim), "norm_rotate k")
+        if code != args.type:
+            raise ValueError(f"norm_rotate: dtypes {q.dtype} and {k.dtype}")
+        args.k_heads = k.shape[1]
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("norm_rotate: a weight or result of keys, but no keys")
+    if out is not None and ((q_out is None) or (k_out is None) != (k is None)):
+        raise ValueError("norm_rotate out: a result for each of q and k is required")
+    args.weight_type = args.type
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            ptr, code, _ = _tensor(w, (dim,), f"norm_rotate {name}", (args.type, FP32))
+            setattr(args, name, ptr)
+            args.weight_type = code
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise ValueError(f"norm_rotate: weights of {q_weight.dtype} and {k_weight.dtype}")
+    if positions is None:
+        if rotary:
+            raise ValueError("norm_rotate positions: required")
+        rotary = 0
+    args.rotary_dim = dim if rotary is None else rotary
+    _keep, args.positions, args.rotary = _rotary(positions if args.rotary_dim else None, sections, theta, interleaved,
+                                                 args.rotary_dim // 2, (n,), "norm_rotate")
+    args.eps = eps
+    _same_device(q, k, q_weight, k_weight, positions, q_out, k_out)
+    on = _On(q.device, stream, q, k, q_weight, k_weight, positions, q_out, k_out)
+    with on as s:
+        if out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            on.give(q_out, *(() if k is None else (k_out,)))
+        args.q_out, code, st_out = _tensor(q_out, q.shape, "norm_rotate q_out")
+        for i in range(2):
+            args.q_stride[i], args.q_out_stride[i] = st_q[i], st_out[i]
+        same = code == args.type
+        if k is not None:
+            args.k_out, code, st_out = _tensor(k_out, k.shape, "norm_rotate k_out")
+            same = same and code == args.type
+            for i in range(2):
+                args.k_stride[i], args.k_out_stride[i] = st_k[i], st_out[i]
+        if not same:
+            raise ValueError(f"norm_rotate out: dtype other than {q.dtype}")
+        _check(lib().ula_norm_rotate(ctypes.byref(args), s), "ula_norm_rotate")
+    return q_out, k_out
+
+
+def lightest(scores, first, last, n, most: Optional[int] = None, mark: bool = False, out=None, stream=None):
+    """Of each range of addresses first[i] .. last[i] - 1 the n[i] entries of least score (ties: lowest address), as
+    int32 [ranges][most] in ascending order, -1 behind them: what Engine.release takes, once on the host. scores:
+    int64 CUDA tensor by address, as Engine.weigh adds to; negative ones are entries that are not there. first, last, n: host
+    integers (arrays or lists; n may be one number). most: columns, by default the largest n. mark: the scores of
+    those chosen become -1."""
+    import torch
+    first, last = _host_ints(first, "lightest first"), _host_ints(last, "lightest last")
+    n = _host_ints(np.full(first.shape, n) if np.ndim(n) == 0 else n, "lightest n")
+    if first.shape != last.shape or first.shape != n.shape:
+        raise ValueError(f"lightest: {first.size} first, {last.size} last addresses and {n.size} counts")
+    args = UlaLightestArgs()
+    args.scores = _dev(scores, "int64", 0, "lightest scores")
+    if scores.numel() >= 1 << 31:
+        raise ValueError("lightest scores: 2^31 or more")
+    args.capacity, args.ranges = scores.numel(), first.size
+    args.first, args.last, args.count = first.ctypes.data, last.ctypes.data, n.ctypes.data
+    args.most = (int(n.max()) if n.size else 0) if most is None else most
+    args.mark = int(bool(mark))
+    _same_device(scores, out)
+    on = _On(scores.device, stream, scores, out)
+    with on as s:
+        if out is None:
+            out = torch.empty((first.size, max(args.most, 0)), dtype=torch.int32, device=scores.device)
+            on.give(out)
+        args.out = _dev(out, "int32", first.size * max(args.most, 0), "lightest out")
+        args.workspace_bytes = lib().ula_lightest_bytes(ctypes.byref(args))
+        if args.workspace_bytes:
+            work = torch.empty(args.workspace_bytes, dtype=torch.uint8, device=scores.device)
+            args.workspace = work.data_ptr()
+        _check(lib().ula_lightest(ctypes.byref(args), s), "ula_lightest")
+    return out
+
+
 def tree_masks(parents) -> np.ndarray:
     """Masks for attend_tree (int64, shaped as `parents`, [nodes] or [n_sets][nodes], at most 64 nodes) of trees
     given by each node's parent, an earlier node's number or -1 for a root: bit j of a node is set for each node j
@@ -423,7 +560,7 @@ def tree_masks(parents) -> np.ndarray:
     nodes = parents.shape[-1]
     if nodes > 64:
         raise ValueError(f"tree_masks: {nodes} nodes, at most 64")
-    rows = parents.reshape(-1, nodes).astype(np.int64)
+    rows = parents.reshape(parents.size // nodes if nodes else 0, nodes).astype(np.int64)
     if ((rows < -1) | (rows >= np.arange(nodes))).any():
         raise ValueError("tree_masks: a parent is an earlier node's number or -1")
     out = np.zeros(rows.shape, np.uint64)
@@ -644,6 +781,38 @@ class Engine:
                                          _dev(sel, "int32", n_sets * k, "ula_attend_tree sel"), ctypes.byref(args), s),
                    "ula_attend_tree")
         return out, lse
+
+    def weigh(self, group: int, layer: int, sel, q, lse, fmt: RowFormat, scores=None, scale: Optional[float] = None,
+              out=None, stream=None):
+        """The softmax weight that each selected entry got in the attention that gave `lse`, summed over the query
+        rows: fp32 [n_sets][k] (out, if given). q [n_sets][heads][576 or head_dim] with lse [n_sets][heads], or with
+        a dimension of nodes in front of the heads, as attend and attend_tree take and give them; scale as there.
+        scores: int64 [logical_capacity] in units of 2^-32, to which each entry's weight is added at its address."""
+        import torch
+        _no_gradient("ula_weigh", q, lse, out)
+        n_sets, k = _sets(sel)
+        args = UlaWeighArgs()
+        args.rows = fmt
+        width = LATENT_CHANNELS + ROPE_CHANNELS if fmt.kind == ROWS_LATENT else fmt.head_dim
+        if q.dim() not in (3, 4):
+            raise ValueError(f"ula_weigh q: shape {tuple(q.shape)}, expected ({n_sets}, None, {width}) or one more dimension")
+        args.q, args.type, st = _tensor(q, (n_sets, *(None,) * (q.dim() - 2), width), "ula_weigh q", (BF16, FP16))
+        args.nodes, args.heads = (1, q.shape[1]) if q.dim() == 3 else q.shape[1:3]
+        args.q_set_stride, args.q_node_stride, args.q_head_stride = st[0], st[1], st[-2]
+        args.scale = 1.0 / width ** 0.5 if scale is None else scale
+        args.lse = _dev(lse, "float32", n_sets * args.nodes * args.heads, "ula_weigh lse")
+        if scores is not None:
+            args.scores = _dev(scores, "int64", self.N, "ula_weigh scores")
+        _same_device(q, sel, lse, scores, out, self)
+        on = _On(q.device, stream, q, sel, lse, scores, out)
+        with on as s:
+            if out is None:
+                out = torch.empty((n_sets, k), dtype=torch.float32, device=q.device)
+                on.give(out)
+            args.shares = _dev(out, "float32", n_sets * k, "ula_weigh out")
+            _check(lib().ula_weigh(self.ctx, group, layer, n_sets, k, _dev(sel, "int32", n_sets * k, "ula_weigh sel"),
+                                   ctypes.byref(args), s), "ula_weigh")
+        return out
 
     def sync(self, stream=None) -> List[tuple]:
         st = (UlaStepStats * self.num_groups)()
