@@ -17,7 +17,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libula.so")
 SOURCES = ["k_init.hip", "k_lookup.hip", "k_select.hip", "k_lru.hip", "k_move.hip", "k_gather.hip",
-           "k_attend.hip", "k_attend_heads.hip", "k_weigh.hip", "k_rows.hip", "k_norm.hip", "k_entries.hip", "k_lightest.hip",
+           "k_attend.hip", "k_attend_heads.hip", "k_tree_heads.hip", "k_weigh.hip", "k_rows.hip", "k_norm.hip", "k_entries.hip", "k_lightest.hip",
            "runtime.hip"]
 
 # The attention kernels hold their accumulators in vector registers (vector
@@ -26,6 +26,7 @@ SOURCES = ["k_init.hip", "k_lookup.hip", "k_select.hip", "k_lru.hip", "k_move.hi
 # and spills.
 EXTRA = {"k_attend.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
          "k_attend_heads.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+         "k_tree_heads.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
          "k_weigh.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")

@@ -123,6 +123,7 @@ __device__ __forceinline__ void scale_in_place(f32x16& x, float f) {
   }
 }
 
+constexpr int kFewSplits = 8;                     // of a tree's rows: joined by k_tree_join
 constexpr int kWaves = 8;
 constexpr int kFirstWaves = 4;                    // waves 0..3: first product and softmax
 constexpr int kSecondWaves = kWaves - kFirstWaves;
@@ -751,6 +752,50 @@ __global__ __launch_bounds__(kJoinThreads) void k_attend_join(GroupDev g, Attend
   if (threadIdx.x == 0 && a.lse) a.lse[row] = sum != 0.0f ? (top + log2f(sum)) * kLn2 : -__builtin_inff();
 }
 
+// The join of few splits of many rows, as a tree's are (46848 rows of 64 channels in 2
+// splits: 54 us with a workgroup a row as above, about 12 us so): width / 4 threads a row.
+template <typename Q8>
+__global__ __launch_bounds__(kJoinThreads) void k_tree_join(GroupDev g, AttendDev a, int width, int rows) {
+  const ReaderState state = reader_state(g);
+  const int per = width / 4;
+  const int row = blockIdx.x * (kJoinThreads / per) + threadIdx.x / per, c = threadIdx.x % per * 4;
+  if (row >= rows) return;
+  const float* lse = a.part_lse + (size_t)row * a.splits;
+  const float* po = a.part_o + (size_t)row * a.splits * width + c;
+  float w[kFewSplits], top = -__builtin_inff();
+  f32x4 v[kFewSplits];
+#pragma unroll
+  for (int i = 0; i < kFewSplits; ++i) {
+    if (i >= a.splits) break;
+    w[i] = lse[i];
+    v[i] = *reinterpret_cast<const f32x4*>(po + (size_t)i * width);
+  }
+  if (state.status || state.flag != a.want_flag) return;       // the attention said so
+#pragma unroll
+  for (int i = 0; i < kFewSplits; ++i) {
+    if (i >= a.splits) break;
+    top = fmaxf(top, w[i]);
+  }
+  const float base = top == -__builtin_inff() ? 0.0f : top;
+  f32x4 acc{};
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kFewSplits; ++i) {
+    if (i >= a.splits) break;
+    const float x = exp2f(w[i] - base);
+    sum += x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(x, v[i][e], acc[e]);
+  }
+  const int set = row / a.heads, at_head = row % a.heads;
+  const int node = (int)a.by_heads.div(at_head), head = at_head - node * (int)a.by_heads.d;
+  const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+  const float out[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
+  store4<Q8>(static_cast<uint16_t*>(a.out) + set * a.out_set_stride + node * a.out_node_stride + head * a.out_head_stride + c, out,
+             a.out_aligned);
+  if (c == 0 && a.lse) a.lse[row] = sum != 0.0f ? (top + log2f(sum)) * kLn2 : -__builtin_inff();
+}
+
 // How a call's heads and keys are split over workgroups (one per compute unit at
 // a time): 32 or 64 heads each, and the number of splits, with the least estimated
 // time in us. A workgroup takes 0.85 us (32 heads) or 1.2 us (64) per tile and 14
@@ -814,6 +859,12 @@ hipError_t launch_tree_latent(const GroupDev& g, const AttendDev& a, int type, i
 
 hipError_t launch_attend_join(const GroupDev& g, const AttendDev& a, int type, int n_sets, int width, hipStream_t s) {
   const int blocks = n_sets * a.heads;
+  if (a.nodes && a.splits <= kFewSplits) {
+    const int per = kJoinThreads / (width / 4), few = (blocks + per - 1) / per;
+    if (type == ULA_BF16) k_tree_join<bf16x8><<<few, kJoinThreads, 0, s>>>(g, a, width, blocks);
+    else k_tree_join<f16x8><<<few, kJoinThreads, 0, s>>>(g, a, width, blocks);
+    return hipGetLastError();
+  }
   if (type == ULA_BF16) k_attend_join<bf16x8><<<blocks, kJoinThreads, 0, s>>>(g, a, width);
   else k_attend_join<f16x8><<<blocks, kJoinThreads, 0, s>>>(g, a, width);
   return hipGetLastError();

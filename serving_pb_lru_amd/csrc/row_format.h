@@ -55,7 +55,7 @@ struct AttendDev {
   const uint8_t* drafts;            // this layer's row of a set's first block of drafted tokens
   const unsigned long long* visible;   // [n_sets][nodes]
   long long draft_stride;           // bytes from one block's row to the next
-  int32_t nodes, sel_k, history_tiles;
+  int32_t nodes, sel_k, history_tiles, groups;
 };
 
 // Device arguments of the entries' weights: rows are nodes x heads.
@@ -133,6 +133,7 @@ hipError_t launch_rotate(const RotateDev& a, const RotaryDev& rot, int type, hip
 
 struct AttendPlan {
   int32_t splits, split_keys, head_blocks;
+  int32_t groups;                   // a tree over heads rows: groups of 16 rows of a workgroup
 };
 
 AttendPlan plan_attend_latent(int n_sets, int k, int heads, int most_keys = kAttendKeys);
@@ -143,7 +144,7 @@ inline long long tree_tiles(long long tokens, int nodes) {
   return (tokens + kTileTokens - 1) / kTileTokens + (nodes + kTileTokens - 1) / kTileTokens;
 }
 AttendPlan plan_tree_latent(int n_sets, int tiles, int rows);
-AttendPlan plan_tree_heads(int n_sets, int tiles, int rows, int kv_heads);
+AttendPlan plan_tree_heads(int n_sets, int tiles, int rows, int kv_heads, int head_dim);
 
 hipError_t launch_attend_latent(const GroupDev& g, const AttendDev& a, int type, int n_sets, hipStream_t s);
 hipError_t launch_tree_latent(const GroupDev& g, const AttendDev& a, int type, int n_sets, hipStream_t s);

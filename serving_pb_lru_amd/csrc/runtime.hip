@@ -1361,7 +1361,7 @@ static bool plan_tree(const ula_row_format* f, int32_t n_sets, int32_t k, int32_
   } else {
     if (heads % f->kv_heads) return false;
     if ((int64_t)k * f->block_tokens >= (1ll << 30)) return false;
-    *plan = plan_tree_heads(n_sets, (int)tree_tiles((int64_t)k * f->block_tokens, nodes), rows, f->kv_heads);
+    *plan = plan_tree_heads(n_sets, (int)tree_tiles((int64_t)k * f->block_tokens, nodes), rows, f->kv_heads, f->head_dim);
     *width = f->head_dim;
   }
   return plan->splits <= kAttendMaxSplits && (int64_t)n_sets * plan->head_blocks * plan->splits < (1ll << 23);
@@ -1461,6 +1461,7 @@ static int attend_impl(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_set
     a.draft_stride = (long long)ctx->dims.slot_bytes;
     a.visible = reinterpret_cast<const unsigned long long*>(tree->visible);
     a.nodes = nodes;
+    a.groups = plan.groups;
     a.sel_k = k;
     a.history_tiles = (int32_t)((((int64_t)k << a.block_shift) + kTileTokens - 1) / kTileTokens);
     a.k = a.history_tiles * kTileTokens + nodes;   // key places of a set (latent rows)
