@@ -26,6 +26,13 @@ __device__ __forceinline__ unsigned long long score_units(float share) {
   return (unsigned long long)(long long)rint((double)x * 0x1p32);
 }
 
+// The value again, as one the compiler cannot trace back: sums of it and a constant
+// become instruction offsets, not registers kept across the loop.
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 __device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
@@ -39,11 +46,18 @@ __device__ __forceinline__ bool counts(float lse) { return fabsf(lse) < __builti
 // key group; more rows go chunk by chunk over the same keys. A key's codes stay in
 // registers as they are until a block of 128 channels is widened for both 32-row
 // products; a block's registers then take the next key group's.
+// Bound by the lines that a compute unit can have outstanding: 256 sets x 2048 keys x 64
+// heads take 95 us, in which the units ask for 530 MB (344 MB of rows, whose ends share
+// lines) and wait 860 cycles for each line, 61 of them on their way at a time. (240 us with
+// branches around the loads, whose waits were for all of them; 125 us with 16 x 16
+// products, 64 bytes of a row at a time, and spilled registers.)
 constexpr int kWeighWaves = 8;
 constexpr int kWeighKeys = 32;                       // of a wave
 constexpr int kWeighGroup = kWeighWaves * kWeighKeys;
-constexpr int kWeighRows = 64;
+constexpr int kWeighRows = 64;                       // most at a time
 constexpr int kWeighMaxGroups = 8;                   // key groups of a workgroup
+
+__device__ __align__(16) uint8_t g_no_row[kLatentRow];   // zeros
 
 template <typename Q8>
 struct WeighLds {
@@ -56,9 +70,11 @@ struct WeighLds {
   int ok;
 };
 
+// HT: rows at a time, in 32s.
 template <typename Q8, int HT>
 __global__ __launch_bounds__(kWeighWaves * kWave, 2) void k_weigh_latent(GroupDev g, WeighDev a) {
   using Lds = WeighLds<Q8>;
+  constexpr int kRows = 32 * HT;
   __shared__ Lds s;
   const int lane = lane_id(), half = lane / 32, col = lane % 32;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -70,39 +86,47 @@ __global__ __launch_bounds__(kWeighWaves * kWave, 2) void k_weigh_latent(GroupDe
 
   const uint8_t* pool = g.pool + (size_t)a.layer * g.row_bytes;
   int err = 0;
-  // this lane's key (both halves the same one) of a group: its row, or nullptr
+  // This lane's key (both halves the same one) of a group. Lookups and loads have no branches, so that the
+  // compiler knows how many are in flight behind the ones it waits for: a key that is not there looks entry 0 up
+  // and reads zeros.
   auto key_of = [&](int group) { return (group0 + group) * kWeighGroup + wave * kWeighKeys + col; };
-  auto find = [&](int group) -> const uint8_t* {
-    const int i = key_of(group);
-    if (group >= groups || i >= a.k) return nullptr;
-    const uint32_t slot = slot_of(g, look_up(g, a.sel, set * a.k + i, a.n_res), a.n_res, err);
-    return slot != kAbsent ? pool + (size_t)slot * g.slot_bytes : nullptr;
+  auto entry_of = [&](int group) { return group < groups && key_of(group) < a.k ? set * a.k + key_of(group) : -1; };
+  auto look = [&](int group) -> Lookup {
+    const int r = max(entry_of(group), 0);
+    return {g.res[r], a.sel[r]};                      // res has room for every selection of the engine
+  };
+  auto row_at = [&](int group, Lookup at) -> const uint8_t* {
+    const int r = entry_of(group);
+    if (r < 0) at.la = -1;
+    if (r >= a.n_res) at.res = make_uint2(kAbsent, kAbsent);
+    const uint32_t slot = slot_of(g, at, a.n_res, err);
+    return slot != kAbsent ? pool + (size_t)slot * g.slot_bytes : g_no_row;
   };
   // 16-byte pieces of the lane's half: pieces 2 j + half of each block, and of the rotary channels
   vec4u code[kLatentGroups][4], rope[4];
   f32x4 scale;
   auto load_block = [&](const uint8_t* row, int b) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      code[b][j] = row ? *reinterpret_cast<const vec4u*>(row + b * kScaleGroup + (2 * j + half) * 16) : vec4u{0u, 0u, 0u, 0u};
+    for (int j = 0; j < 4; ++j) code[b][j] = *reinterpret_cast<const vec4u*>(row + b * kScaleGroup + (2 * j + half) * 16);
   };
   auto load_rest = [&](const uint8_t* row) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      rope[j] = row ? *reinterpret_cast<const vec4u*>(row + kRopeAt + (2 * j + half) * 16) : vec4u{0u, 0u, 0u, 0u};
-    scale = row ? *reinterpret_cast<const f32x4*>(row + kLatentScaleAt) : f32x4{};
+    for (int j = 0; j < 4; ++j) rope[j] = *reinterpret_cast<const vec4u*>(row + kRopeAt + (2 * j + half) * 16);
+    scale = *reinterpret_cast<const f32x4*>(row + kLatentScaleAt);
   };
 
-  for (int row0 = 0; row0 < a.rows; row0 += 32 * HT) {
-    const uint8_t* row = find(0);
+  for (int row0 = 0; row0 < a.rows; row0 += kRows) {
+    const Lookup first = look(0);
+    Lookup ahead = look(1);
+    const uint8_t* row = row_at(0, first);
+    int32_t address = first.la;                        // of the row, where there is one
 #pragma unroll
     for (int b = 0; b < kLatentGroups; ++b) load_block(row, b);
     load_rest(row);
-    const uint8_t* next = find(1);
     if (row0) __syncthreads();                         // the chunk before it is done with
     // q of this chunk into LDS, eight channels a thread at a time
     constexpr int kPieces = (kLatent + kRope) / 8;
-    for (int e = threadIdx.x; e < 32 * HT * kPieces; e += kWeighWaves * kWave) {
+    for (int e = threadIdx.x; e < kRows * kPieces; e += kWeighWaves * kWave) {
       const int r = e / kPieces, c = e % kPieces;
       Q8 v{};
       // a row that counts for nothing may hold anything
@@ -126,7 +150,7 @@ __global__ __launch_bounds__(kWeighWaves * kWave, 2) void k_weigh_latent(GroupDe
         *reinterpret_cast<bf16x8*>(at + 2 * kRope) = lo;
       }
     }
-    if (threadIdx.x < 32 * HT) {
+    if (threadIdx.x < kRows) {
       const int r = row0 + threadIdx.x;
       const float lse = r < a.rows ? a.lse[(size_t)set * a.rows + r] : -__builtin_inff();
       s.minus[threadIdx.x] = counts(lse) ? lse * -kLog2e : -__builtin_inff();
@@ -135,7 +159,13 @@ __global__ __launch_bounds__(kWeighWaves * kWave, 2) void k_weigh_latent(GroupDe
     if (!s.ok) return;
 
     for (int group = 0; group < groups; ++group) {
-      const bool live = row != nullptr;
+      const bool live = row != g_no_row;
+      const uint8_t* next = row_at(group + 1, ahead);
+      const int32_t next_address = ahead.la;
+      ahead = look(group + 2);
+      // this lane's row of q: pieces of 16 channels, and of 8 rotary ones; the rest are instruction offsets
+      const uint32_t qx = opaque(lds_address(s.q) + col * Lds::kRowBytes + half * 32);
+      const uint32_t qr = opaque(lds_address(s.q) + col * Lds::kRowBytes + half * 16);
       f32x4 sc = scale;
 #pragma unroll
       for (int b = 0; b < kLatentGroups; ++b) sc[b] *= a.scale_log2;
@@ -150,8 +180,8 @@ __global__ __launch_bounds__(kWeighWaves * kWave, 2) void k_weigh_latent(GroupDe
           for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int h = 0; h < HT; ++h) {
-              const uint32_t at = lds_address(s.q) + (32 * h + col) * Lds::kRowBytes + 2 * kLatent + 2 * kRope * i + (2 * j + half) * 16;
-              part[h] = mfma32(lds_get<bf16x8>(at), __builtin_bit_cast(bf16x8, rope[j]), part[h]);
+              const uint32_t at = 32 * h * Lds::kRowBytes + 2 * kLatent + 2 * kRope * i + 2 * j * 16;
+              part[h] = mfma32(lds_get<bf16x8>(qr + at), __builtin_bit_cast(bf16x8, rope[j]), part[h]);
             }
 #pragma unroll
         for (int h = 0; h < HT; ++h)
@@ -165,6 +195,7 @@ __global__ __launch_bounds__(kWeighWaves * kWave, 2) void k_weigh_latent(GroupDe
       load_rest(next);
 #pragma unroll
       for (int b = 0; b < kLatentGroups; ++b) {
+        __builtin_amdgcn_sched_barrier(0);            // reads of q ahead of a block's products would spill
         Q8 k[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -181,8 +212,8 @@ __global__ __launch_bounds__(kWeighWaves * kWave, 2) void k_weigh_latent(GroupDe
           for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int h = 0; h < HT; ++h) {
-              const uint32_t at = lds_address(s.q) + (32 * h + col) * Lds::kRowBytes + 2 * (b * kScaleGroup + (2 * j + half) * 16 + 8 * i);
-              part[h] = mfma32(lds_get<Q8>(at), k[2 * j + i], part[h]);
+              const uint32_t at = 32 * h * Lds::kRowBytes + 2 * (b * kScaleGroup + 2 * j * 16 + 8 * i);
+              part[h] = mfma32(lds_get<Q8>(qx + at), k[2 * j + i], part[h]);
             }
 #pragma unroll
         for (int h = 0; h < HT; ++h)
@@ -198,17 +229,16 @@ __global__ __launch_bounds__(kWeighWaves * kWave, 2) void k_weigh_latent(GroupDe
       if (half == 0) {
         float& sum = s.share[wave][group][col];
         if (row0) share += sum;
-        if (row0 + 32 * HT < a.rows) {
+        if (row0 + kRows < a.rows) {
           sum = share;
         } else if (key_of(group) < a.k) {
-          const int at = set * a.k + key_of(group);
           if (!live) share = 0.0f;
-          if (a.shares) a.shares[at] = share;
-          if (a.scores && live) atomicAdd(a.scores + a.sel[at], score_units(share));
+          if (a.shares) a.shares[set * a.k + key_of(group)] = share;
+          if (a.scores && live) atomicAdd(a.scores + address, score_units(share));
         }
       }
       row = next;
-      next = find(group + 2);
+      address = next_address;
     }
   }
   if (err) latch_gather(g.ctr, err);
