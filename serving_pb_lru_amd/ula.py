@@ -462,56 +462,52 @@ def norm_rotate(q, k=None, q_weight=None, k_weight=None, positions=None, section
     alone), in one launch. q [n][heads][dim], k [n][kv_heads][dim] or None, bf16, fp16 or fp32; weights [dim] in
     that type or fp32, or None for ones. out: a pair of tensors shaped as q and k, themselves for in place. No
     gradient is recorded: tensors that require one are refused."""
-    import torch
     q_out, k_out = out if out is not None else (None, None)
     _no_gradient("norm_rotate", q, k, q_weight, k_weight, q_out, k_out)
-    args = UlaNormArgs()
-    args.q, args.type, st_q = _tensor(q, (None, None, None), "norm_rotate q")
+    q_ptr, code, st_q = _tensor(q, (None, None, None), "norm_rotate q")
     n, heads, dim = q.shape
-    args.n, args.q_heads, args.dim = n, heads, dim
+    k_ptr, kv, st_k = None, 0, (0, 0)
     if k is not None:
-        args.k, code, st_k = _tensor(k, (n, None, dim), "norm_rotate k")
-        if code != args.type:
+        k_ptr, code_k, st_k = _tensor(k, (n, None, dim), "norm_rotate k")
+        if code_k != code:
             raise ValueError(f"norm_rotate: dtypes {q.dtype} and {k.dtype}")
-        args.k_heads = k.shape[1]
+        kv = k.shape[1]
     elif k_weight is not None or k_out is not None:
         raise ValueError("norm_rotate: a weight or result of keys, but no keys")
-    if out is not None and ((q_out is None) or (k_out is None) != (k is None)):
+    if out is not None and (q_out is None or (k_out is None) != (k is None)):
         raise ValueError("norm_rotate out: a result for each of q and k is required")
-    args.weight_type = args.type
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            ptr, code, _ = _tensor(w, (dim,), f"norm_rotate {name}", (args.type, FP32))
-            setattr(args, name, ptr)
-            args.weight_type = code
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-        raise ValueError(f"norm_rotate: weights of {q_weight.dtype} and {k_weight.dtype}")
+    weight_type, qw, kw = code, None, None
+    if q_weight is not None:
+        qw, weight_type, _ = _tensor(q_weight, (dim,), "norm_rotate q_weight", (code, FP32))
+    if k_weight is not None:
+        kw, weight_type, _ = _tensor(k_weight, (dim,), "norm_rotate k_weight", (code, FP32))
+        if q_weight is not None and q_weight.dtype != k_weight.dtype:
+            raise ValueError(f"norm_rotate: weights of {q_weight.dtype} and {k_weight.dtype}")
     if positions is None:
         if rotary:
             raise ValueError("norm_rotate positions: required")
         rotary = 0
-    args.rotary_dim = dim if rotary is None else rotary
-    _keep, args.positions, args.rotary = _rotary(positions if args.rotary_dim else None, sections, theta, interleaved,
-                                                 args.rotary_dim // 2, (n,), "norm_rotate")
-    args.eps = eps
+    elif rotary is None:
+        rotary = dim
+    _keep, pos, turn = _rotary(positions if rotary else None, sections, theta, interleaved, rotary // 2, (n,), "norm_rotate")
     _same_device(q, k, q_weight, k_weight, positions, q_out, k_out)
     on = _On(q.device, stream, q, k, q_weight, k_weight, positions, q_out, k_out)
     with on as s:
         if out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
-            on.give(q_out, *(() if k is None else (k_out,)))
-        args.q_out, code, st_out = _tensor(q_out, q.shape, "norm_rotate q_out")
-        for i in range(2):
-            args.q_stride[i], args.q_out_stride[i] = st_q[i], st_out[i]
-        same = code == args.type
-        if k is not None:
-            args.k_out, code, st_out = _tensor(k_out, k.shape, "norm_rotate k_out")
-            same = same and code == args.type
-            for i in range(2):
-                args.k_stride[i], args.k_out_stride[i] = st_k[i], st_out[i]
-        if not same:
-            raise ValueError(f"norm_rotate out: dtype other than {q.dtype}")
+            q_out = q.new_empty((n, heads, dim))
+            on.give(q_out)
+            qo, st_qo, ko, st_ko = q_out.data_ptr(), (heads * dim, dim), None, (0, 0)
+            if k is not None:
+                k_out = q.new_empty((n, kv, dim))
+                on.give(k_out)
+                ko, st_ko = k_out.data_ptr(), (kv * dim, dim)
+        else:
+            qo, code_out, st_qo = _tensor(q_out, (n, heads, dim), "norm_rotate q_out")
+            ko, code_k, st_ko = (None, code, (0, 0)) if k is None else _tensor(k_out, (n, kv, dim), "norm_rotate k_out")
+            if code_out != code or code_k != code:
+                raise ValueError(f"norm_rotate out: dtype other than {q.dtype}")
+        args = UlaNormArgs(code, n, dim, heads, kv, rotary, weight_type, eps, q_ptr, k_ptr, qo, ko, st_q[:2], st_k[:2],
+                           st_qo[:2], st_ko[:2], qw, kw, pos, turn)
         _check(lib().ula_norm_rotate(ctypes.byref(args), s), "ula_norm_rotate")
     return q_out, k_out
 
@@ -742,41 +738,37 @@ class Engine:
         import torch
         _no_gradient("ula_attend_tree", q, out, lse)
         n_sets, k = _sets(sel)
-        args = UlaTreeArgs()
-        at = args.attend
-        at.rows = fmt
         latent = fmt.kind == ROWS_LATENT
         width = LATENT_CHANNELS + ROPE_CHANNELS if latent else fmt.head_dim
         back = LATENT_CHANNELS if latent else fmt.head_dim
         if q.dim() != 4:
             raise ValueError(f"ula_attend_tree q: shape {tuple(q.shape)}, expected ({n_sets}, None, None, {width})")
         nodes, heads = q.shape[1:3]
-        at.q, at.type, st = _tensor(q, (n_sets, None, None, width), "ula_attend_tree q", (BF16, FP16))
-        at.q_set_stride, args.q_node_stride, at.q_head_stride = st[:3]
-        at.heads, args.nodes = heads, nodes
-        at.scale = 1.0 / width ** 0.5 if scale is None else scale
+        q_ptr, code, st = _tensor(q, (n_sets, None, None, width), "ula_attend_tree q", (BF16, FP16))
         per_set = nodes if latent else -(-nodes // max(fmt.block_tokens, 1))
-        args.drafts = _dev(drafts, "uint8", n_sets * per_set * self.layers * self.row_bytes,
-                           "ula_attend_tree drafts")
-        args.visible = _dev(visible, "int64", n_sets * nodes, "ula_attend_tree visible")
+        drafts_ptr = _dev(drafts, "uint8", n_sets * per_set * self.layers * self.row_bytes, "ula_attend_tree drafts")
+        visible_ptr = _dev(visible, "int64", n_sets * nodes, "ula_attend_tree visible")
         _same_device(q, sel, drafts, visible, out, lse, self)
         on = _On(q.device, stream, q, sel, drafts, visible, out, lse)
         with on as s:
             if out is None:
-                out = torch.empty((n_sets, nodes, heads, back), dtype=q.dtype, device=q.device)
+                out = q.new_empty((n_sets, nodes, heads, back))
                 on.give(out)
-            at.out, code, st = _tensor(out, (n_sets, nodes, heads, back), "ula_attend_tree out")
-            if code != at.type:
-                raise ValueError(f"ula_attend_tree out: dtype {out.dtype}, expected {q.dtype}")
-            at.out_set_stride, args.out_node_stride, at.out_head_stride = st[:3]
+                out_ptr, st_out = out.data_ptr(), (nodes * heads * back, heads * back, back)
+            else:
+                out_ptr, code_out, st_out = _tensor(out, (n_sets, nodes, heads, back), "ula_attend_tree out")
+                if code_out != code:
+                    raise ValueError(f"ula_attend_tree out: dtype {out.dtype}, expected {q.dtype}")
             if lse is None:
-                lse = torch.empty((n_sets, nodes, heads), dtype=torch.float32, device=q.device)
+                lse = q.new_empty((n_sets, nodes, heads), dtype=torch.float32)
                 on.give(lse)
-            at.lse = _dev(lse, "float32", n_sets * nodes * heads, "ula_attend_tree lse")
-            at.workspace_bytes = lib().ula_attend_tree_bytes(ctypes.byref(fmt), n_sets, k, nodes, heads)
-            if at.workspace_bytes:
-                work = torch.empty(at.workspace_bytes, dtype=torch.uint8, device=q.device)
-                at.workspace = work.data_ptr()
+            lse_ptr = _dev(lse, "float32", n_sets * nodes * heads, "ula_attend_tree lse")
+            need = lib().ula_attend_tree_bytes(ctypes.byref(fmt), n_sets, k, nodes, heads)
+            work = q.new_empty(need, dtype=torch.uint8) if need else None
+            args = UlaTreeArgs(UlaAttendArgs(fmt, code, heads, 1.0 / width ** 0.5 if scale is None else scale, q_ptr, st[0],
+                                             st[2], out_ptr, st_out[0], st_out[2], lse_ptr,
+                                             work.data_ptr() if need else None, need),
+                               nodes, st[1], st_out[1], drafts_ptr, visible_ptr)
             _check(lib().ula_attend_tree(self.ctx, group, layer, n_sets, k,
                                          _dev(sel, "int32", n_sets * k, "ula_attend_tree sel"), ctypes.byref(args), s),
                    "ula_attend_tree")
@@ -788,28 +780,26 @@ class Engine:
         rows: fp32 [n_sets][k] (out, if given). q [n_sets][heads][576 or head_dim] with lse [n_sets][heads], or with
         a dimension of nodes in front of the heads, as attend and attend_tree take and give them; scale as there.
         scores: int64 [logical_capacity] in units of 2^-32, to which each entry's weight is added at its address."""
-        import torch
         _no_gradient("ula_weigh", q, lse, out)
         n_sets, k = _sets(sel)
-        args = UlaWeighArgs()
-        args.rows = fmt
         width = LATENT_CHANNELS + ROPE_CHANNELS if fmt.kind == ROWS_LATENT else fmt.head_dim
         if q.dim() not in (3, 4):
             raise ValueError(f"ula_weigh q: shape {tuple(q.shape)}, expected ({n_sets}, None, {width}) or one more dimension")
-        args.q, args.type, st = _tensor(q, (n_sets, *(None,) * (q.dim() - 2), width), "ula_weigh q", (BF16, FP16))
-        args.nodes, args.heads = (1, q.shape[1]) if q.dim() == 3 else q.shape[1:3]
-        args.q_set_stride, args.q_node_stride, args.q_head_stride = st[0], st[1], st[-2]
-        args.scale = 1.0 / width ** 0.5 if scale is None else scale
-        args.lse = _dev(lse, "float32", n_sets * args.nodes * args.heads, "ula_weigh lse")
-        if scores is not None:
-            args.scores = _dev(scores, "int64", self.N, "ula_weigh scores")
+        q_ptr, code, st = _tensor(q, (n_sets, *(None,) * (q.dim() - 2), width), "ula_weigh q", (BF16, FP16))
+        nodes, heads = (1, q.shape[1]) if q.dim() == 3 else q.shape[1:3]
+        lse_ptr = _dev(lse, "float32", n_sets * nodes * heads, "ula_weigh lse")
+        scores_ptr = None if scores is None else _dev(scores, "int64", self.N, "ula_weigh scores")
         _same_device(q, sel, lse, scores, out, self)
         on = _On(q.device, stream, q, sel, lse, scores, out)
         with on as s:
             if out is None:
-                out = torch.empty((n_sets, k), dtype=torch.float32, device=q.device)
+                out = lse.new_empty((n_sets, k))
                 on.give(out)
-            args.shares = _dev(out, "float32", n_sets * k, "ula_weigh out")
+                out_ptr = out.data_ptr()
+            else:
+                out_ptr = _dev(out, "float32", n_sets * k, "ula_weigh out")
+            args = UlaWeighArgs(fmt, code, nodes, heads, 1.0 / width ** 0.5 if scale is None else scale, q_ptr, st[0], st[1],
+                                st[-2], lse_ptr, out_ptr, scores_ptr)
             _check(lib().ula_weigh(self.ctx, group, layer, n_sets, k, _dev(sel, "int32", n_sets * k, "ula_weigh sel"),
                                    ctypes.byref(args), s), "ula_weigh")
         return out
