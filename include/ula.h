@@ -607,7 +607,7 @@ typedef struct {
   int32_t most;              /* columns of out */
   int32_t mark;              /* 1: the scores of the entries chosen become -1 */
   int32_t* out;              /* device memory, [ranges][most] */
-  void* workspace;           /* device memory of ula_lightest_bytes bytes, 16-byte aligned; may be NULL for 0 */
+  void* workspace;           /* device memory of ula_lightest_bytes bytes, 32-byte aligned; may be NULL for 0 */
   size_t workspace_bytes;
 } ula_lightest_args;
 

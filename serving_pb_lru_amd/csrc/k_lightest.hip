@@ -24,6 +24,7 @@ namespace ula {
 
 constexpr int kLightThreads = 1024;
 constexpr int kLightWaves = kLightThreads / kWave;
+constexpr int kAtOnce = 8;                           // entries of a thread in one step
 constexpr unsigned long long kNotThere = ~0ull;      // an entry of negative score
 
 __device__ __forceinline__ int bin_of(unsigned long long key) {
@@ -37,6 +38,7 @@ static_assert(64 + (62 - 6) * 32 + 31 < kLightBins, "every score has a bin");
 
 struct LightLds {
   uint32_t hist[kLightBins];
+  int counts[kAtOnce * kLightWaves + 1];
   int waves[kLightWaves + 1];
   int bin, before, within;
 };
@@ -103,36 +105,57 @@ __device__ __forceinline__ LightEnd end_within(LightLds& s, int bin, int within,
 
 // Writes the entries of this workgroup's part (keys(i), i < count, in order of address)
 // that lie before `end` to out, the first of them at place `at`; `tie` entries with the
-// end's key lie before this part. Their scores become -1 if marks is given.
+// end's key lie before this part. Their scores become -1 if marks is given. A thread
+// takes kAtOnce entries a workgroup apart; their waves' counts are summed up together.
 template <typename F>
-__device__ __forceinline__ int write_out(LightLds& s, const LightEnd& end, int count, int at, int tie, int most, int address,
-                                         int32_t* out, long long* marks, F keys) {
+__device__ __forceinline__ void write_out(LightLds& s, const LightEnd& end, int count, int at, int tie, int most, int address,
+                                          int32_t* out, long long* marks, F keys) {
   const int lane = lane_id(), wave = threadIdx.x / kWave;
-  for (int base = 0; base < count; base += kLightThreads) {
-    const int i = base + threadIdx.x;
-    const unsigned long long key = i < count ? keys(i) : kNotThere;
-    const bool equal = key == end.key;
-    // both ranks in one sum: taken below the end in the low half, equal ones in the high half
-    const unsigned long long below = __ballot(key < end.key), same = __ballot(equal);
-    if (lane == 0) s.waves[wave] = __popcll(below) | __popcll(same) << 16;
+  for (int base = 0; base < count; base += kAtOnce * kLightThreads) {
+    unsigned long long key[kAtOnce];
+    int rank[kAtOnce];                                 // among the wave's: below the end, and << 16 with its key
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = base + u * kLightThreads + threadIdx.x;
+      key[u] = i < count ? keys(i) : kNotThere;
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const unsigned long long below = __ballot(key[u] < end.key), same = __ballot(key[u] == end.key);
+      rank[u] = rank_below(below) | rank_below(same) << 16;
+      if (lane == 0) s.counts[u * kLightWaves + wave] = __popcll(below) | __popcll(same) << 16;
+    }
     __syncthreads();
-    int before = 0, all = 0;
-    for (int w = 0; w < kLightWaves; ++w) {
-      if (w == wave) before = all;
-      all += s.waves[w];
+    if (wave == 0) {                                   // at most 8192 of either: no carry into the high half
+      constexpr int kEach = kAtOnce * kLightWaves / kWave;
+      int c[kEach], sum = 0;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) sum += c[i] = s.counts[lane * kEach + i];
+      int before = wave_inclusive_sum(sum) - sum;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        s.counts[lane * kEach + i] = before;
+        before += c[i];
+      }
+      if (lane == kWave - 1) s.counts[kAtOnce * kLightWaves] = before;
     }
-    const int rank_same = tie + (before >> 16) + rank_below(same);
-    const int taken_same = min(rank_same, end.ties) - min(tie, end.ties);   // equal ones taken before this entry
-    const int place = at + (before & 0xFFFF) + rank_below(below) + taken_same;
-    if ((key < end.key || (equal && rank_same < end.ties)) && place < most) {
-      out[place] = address + i;
-      if (marks) marks[i] = -1;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int mine = s.counts[u * kLightWaves + wave] + rank[u];
+      const int nth_same = tie + (mine >> 16);
+      const int place = at + (mine & 0xFFFF) + min(nth_same, end.ties) - min(tie, end.ties);
+      const int i = base + u * kLightThreads + threadIdx.x;
+      if ((key[u] < end.key || (key[u] == end.key && nth_same < end.ties)) && place < most) {
+        out[place] = address + i;
+        if (marks) marks[i] = -1;
+      }
     }
+    const int all = s.counts[kAtOnce * kLightWaves];
     at += (all & 0xFFFF) + min(tie + (all >> 16), end.ties) - min(tie, end.ties);
     tie += all >> 16;
     __syncthreads();
   }
-  return at;
 }
 
 __global__ __launch_bounds__(kLightThreads) void k_lightest(LightDev a, LightRanges r) {
@@ -175,6 +198,7 @@ struct LightChunk {
   LightRange at;
   int range, chunk, chunks, first, count;              // first: of the range's addresses
   uint32_t* bins;                                      // of the range's first chunk
+  LightChunkEnd* ends;                                 // the same
   unsigned long long* list;                            // of the range
 };
 __device__ __forceinline__ LightChunk light_chunk(const LightDev& a, const LightRanges& r) {
@@ -195,6 +219,7 @@ __device__ __forceinline__ LightChunk light_chunk(const LightDev& a, const Light
   c.first = block * per;
   c.count = max(0, min(per, c.at.length - c.first));
   c.bins = a.bins + (size_t)(blockIdx.x - block) * kLightBins;
+  c.ends = a.ends + (blockIdx.x - block);
   c.list = a.list + lists;
   return c;
 }
@@ -205,6 +230,7 @@ __global__ __launch_bounds__(kLightThreads) void k_light_bins(LightDev a, LightR
   for (int i = threadIdx.x; i < kLightBins; i += kLightThreads) hist[i] = 0;
   __syncthreads();
   const long long* scores = a.scores + c.at.first + c.first;
+#pragma unroll 4
   for (int i = threadIdx.x; i < c.count; i += kLightThreads) {
     const long long v = scores[i];
     if (v >= 0) atomicAdd(&hist[bin_of(v)], 1u);
@@ -213,42 +239,45 @@ __global__ __launch_bounds__(kLightThreads) void k_light_bins(LightDev a, LightR
   for (int i = threadIdx.x; i < kLightBins; i += kLightThreads) c.bins[(size_t)c.chunk * kLightBins + i] = hist[i];
 }
 
-// The bin of the last entry taken, of a whole range: the bins of its chunks added up.
-// Returns how many are taken (0: none, and no bin).
-__device__ __forceinline__ int range_bin(LightLds& s, const LightChunk& c) {
-  constexpr int kPer = kLightBins / kLightThreads;
-  int mine = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int b = threadIdx.x * kPer + i;
-    uint32_t sum = 0;
-    for (int k = 0; k < c.chunks; ++k) sum += c.bins[(size_t)k * kLightBins + b];
-    s.hist[b] = sum;
-    mine += (int)sum;
-  }
-  int there;
-  block_exclusive_sum<kLightThreads>(mine, s.waves, there);
-  const int need = min(c.at.count, there);
-  if (need > 0) find_bin(s, need);
-  return need;
-}
-
-// The chunk's entries of that bin to the list, from the place of the chunk's first address on.
+// Where the range's end lies, from the bins of its chunks added up, and what the chunk
+// has before and in that bin; its entries of that bin to the list, from the place of
+// the chunk's first address on, in any order: only how many they are is looked at.
 __global__ __launch_bounds__(kLightThreads) void k_light_list(LightDev a, LightRanges r) {
   __shared__ LightLds s;
+  __shared__ int s_listed;
   const LightChunk c = light_chunk(a, r);
-  if (range_bin(s, c) == 0) return;
-  const int bin = s.bin;
+  constexpr int kPer = kLightBins / kLightThreads;
+  static_assert(kPer == 2, "two bins of a thread in one load");
+  const uint2* bins = reinterpret_cast<const uint2*>(c.bins) + threadIdx.x;
+  const uint2 own = bins[(size_t)c.chunk * kLightThreads];
+  uint2 sum = make_uint2(0, 0);
+#pragma unroll 8
+  for (int k = 0; k < c.chunks; ++k) {
+    const uint2 v = bins[(size_t)k * kLightThreads];
+    sum.x += v.x;
+    sum.y += v.y;
+  }
+  if (threadIdx.x == 0) s_listed = 0;
+  s.hist[2 * threadIdx.x] = sum.x;
+  s.hist[2 * threadIdx.x + 1] = sum.y;
+  int there;
+  block_exclusive_sum<kLightThreads>((int)(sum.x + sum.y), s.waves, there);
+  const int need = min(c.at.count, there);
+  if (need > 0) find_bin(s, need);
+  const int bin = need > 0 ? s.bin : 0;
+  int below = 0;
+  if (need > 0) {
+    const int b = 2 * threadIdx.x;
+    block_exclusive_sum<kLightThreads>((b < bin ? (int)own.x : 0) + (b + 1 < bin ? (int)own.y : 0), s.waves, below);
+  }
+  if (threadIdx.x == bin / 2)
+    c.ends[c.chunk] = {bin, need, s.before, s.within, below, need > 0 ? (int)(bin % 2 ? own.y : own.x) : 0, 0, 0};
+  if (need == 0) return;
   const long long* scores = a.scores + c.at.first + c.first;
-  int at = 0;
-  for (int base = 0; base < c.count; base += kLightThreads) {
-    const int i = base + threadIdx.x;
-    const long long v = i < c.count ? scores[i] : -1;
-    const bool in = v >= 0 && bin_of(v) == bin;
-    int total;
-    const int place = block_exclusive_sum<kLightThreads>(in, s.waves, total);
-    if (in) c.list[c.first + at + place] = (unsigned long long)v;
-    at += total;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < c.count; i += kLightThreads) {
+    const long long v = scores[i];
+    if (v >= 0 && bin_of(v) == bin) c.list[c.first + atomicAdd(&s_listed, 1)] = (unsigned long long)v;
   }
 }
 
@@ -257,25 +286,17 @@ __global__ __launch_bounds__(kLightThreads) void k_light_out(LightDev a, LightRa
   __shared__ int s_count[kLightChunks], s_below[kLightChunks];   // of each chunk: entries in the list, in bins before its bin
   const LightChunk c = light_chunk(a, r);
   int32_t* out = a.out + (long long)c.range * a.most;
-  const int need = range_bin(s, c);
-  if (c.chunk == 0)
-    for (int i = need + threadIdx.x; i < a.most; i += kLightThreads) out[i] = -1;
-  if (need == 0) return;
-  const int bin = s.bin, before = s.before, within = s.within;
-  // a wave for each chunk's bins before the end's
-  for (int k = threadIdx.x / kWave; k < c.chunks; k += kLightWaves) {
-    const uint32_t* bins = c.bins + (size_t)k * kLightBins;
-    int below = 0;
-    if (k < c.chunk)
-      for (int b = lane_id(); b < bin; b += kWave) below += (int)bins[b];
-    below = wave_sum(below);
-    if (lane_id() == 0) {
-      s_below[k] = below;
-      s_count[k] = (int)bins[bin];
-    }
+  const LightChunkEnd in = c.ends[c.chunk];
+  if (threadIdx.x < (unsigned)c.chunks) {
+    s_count[threadIdx.x] = c.ends[threadIdx.x].listed;
+    s_below[threadIdx.x] = c.ends[threadIdx.x].below;
   }
+  if (c.chunk == 0)
+    for (int i = in.need + threadIdx.x; i < a.most; i += kLightThreads) out[i] = -1;
+  if (in.need == 0) return;
+  __syncthreads();
   const int per = light_chunk_size(c.at.length);
-  const LightEnd end = end_within(s, bin, within, need - before, [&](auto f) {
+  const LightEnd end = end_within(s, in.bin, in.within, in.need - in.before, [&](auto f) {
     for (int k = threadIdx.x / kWave; k < c.chunks; k += kLightWaves)
       for (int i = lane_id(); i < s_count[k]; i += kWave) f(c.list[(size_t)k * per + i]);
   });
@@ -288,10 +309,10 @@ __global__ __launch_bounds__(kLightThreads) void k_light_out(LightDev a, LightRa
       below += key < end.key;
       same += key == end.key;
     }
+  if (threadIdx.x < (unsigned)c.chunk) below += s_below[threadIdx.x];
   int at, tie;
   block_exclusive_sum<kLightThreads>(below, s.waves, at);
   block_exclusive_sum<kLightThreads>(same, s.waves, tie);
-  for (int k = 0; k < c.chunk; ++k) at += s_below[k];
   at += min(tie, end.ties);
   long long* scores = a.scores + c.at.first + c.first;
   write_out(s, end, c.count, at, tie, a.most, c.at.first + c.first, out, a.mark ? scores : nullptr, [&](int i) {

@@ -27,10 +27,17 @@ struct LightRanges {
   int32_t n, first_range;                 // first_range: the number of range[0] among the call's
   LightRange range[kLightRanges];
 };
+// What a chunk of a long range tells the others.
+struct alignas(32) LightChunkEnd {
+  int32_t bin, need, before, within;      // of the range: the bin of its end, entries taken, in bins before, in the bin
+  int32_t below, listed;                  // of the chunk: entries in bins before, in the bin
+  int32_t unused[2];
+};
 struct LightDev {
   long long* scores;
   int32_t* out;                           // [ranges][most]
   uint32_t* bins;                         // long ranges: [chunks of all of them][kLightBins]
+  LightChunkEnd* ends;                    // [chunks of all of them]
   unsigned long long* list;               // [addresses of all of them]
   int32_t most, mark;
 };

@@ -1561,7 +1561,7 @@ int ula_weigh(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_sets, int32_
 // The next launch's ranges from `at` on, and the workspace that its long ones need.
 struct LightLaunch {
   LightRanges ranges{};
-  size_t bins = 0, list = 0;   // bytes
+  size_t bins = 0, ends = 0, list = 0;   // bytes
 };
 static void light_launch(const ula_lightest_args& u, int32_t at, LightLaunch* l) {
   l->ranges.n = std::min(kLightRanges, u.ranges - at);
@@ -1576,6 +1576,7 @@ static void light_launch(const ula_lightest_args& u, int32_t at, LightLaunch* l)
     }
   }
   l->bins = align_up((size_t)chunks * kLightBins * sizeof(uint32_t));
+  l->ends = align_up((size_t)chunks * sizeof(LightChunkEnd));
   l->list = align_up((size_t)keys * sizeof(uint64_t));
 }
 
@@ -1605,7 +1606,7 @@ size_t ula_lightest_bytes(const ula_lightest_args* args) {
   for (int64_t at = 0; at < args->ranges; at += kLightRanges) {
     LightLaunch l;
     light_launch(*args, (int32_t)at, &l);
-    need = std::max(need, l.bins + l.list);
+    need = std::max(need, l.bins + l.ends + l.list);
   }
   return need;
 }
@@ -1617,7 +1618,7 @@ int ula_lightest(const ula_lightest_args* args, uint64_t stream) {
   if (u.ranges == 0 || u.most == 0) return ULA_OK;
   if (!u.scores || (uintptr_t)u.scores % 8 || !u.out || (uintptr_t)u.out % 4) return ULA_EINVAL;
   const size_t need = ula_lightest_bytes(args);
-  if (need && (!u.workspace || u.workspace_bytes < need || (uintptr_t)u.workspace % 16)) return ULA_EINVAL;
+  if (need && (!u.workspace || u.workspace_bytes < need || (uintptr_t)u.workspace % 32)) return ULA_EINVAL;
   for (int64_t at = 0; at < u.ranges; at += kLightRanges) {
     LightLaunch l;
     light_launch(u, (int32_t)at, &l);
@@ -1625,7 +1626,11 @@ int ula_lightest(const ula_lightest_args* args, uint64_t stream) {
     a.scores = reinterpret_cast<long long*>(u.scores);
     a.out = u.out;
     a.bins = static_cast<uint32_t*>(u.workspace);
-    a.list = l.list ? reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(u.workspace) + l.bins) : nullptr;
+    if (l.list) {
+      uint8_t* at = static_cast<uint8_t*>(u.workspace);
+      a.ends = reinterpret_cast<LightChunkEnd*>(at + l.bins);
+      a.list = reinterpret_cast<unsigned long long*>(at + l.bins + l.ends);
+    }
     a.most = u.most;
     a.mark = u.mark;
     HIP_TRY(launch_lightest(a, l.ranges, reinterpret_cast<hipStream_t>(stream)));

@@ -102,8 +102,8 @@ def test_lightest_refuses():
     assert call(light_args([], [], [])) == 0 and call(light_args([3], [9], [0], out=None, scores=None)) == 0
     long = light_args([0, 0], [8192, 8193], [1, 1])
     need = L.ula_lightest_bytes(ctypes.byref(long))
-    assert need == 2 * 2048 * 4 + -(-8193 * 8 // 256) * 256
-    for kw in [dict(), dict(workspace=P, workspace_bytes=need - 1), dict(workspace=P + 8, workspace_bytes=need)]:
+    assert need == 2 * 2048 * 4 + 256 + -(-8193 * 8 // 256) * 256
+    for kw in [dict(), dict(workspace=P, workspace_bytes=need - 1), dict(workspace=P + 16, workspace_bytes=need)]:
         for name, v in kw.items():
             setattr(long, name, v)
         assert call(long) == EINVAL, kw
