@@ -153,6 +153,7 @@ struct LatentLds {
   alignas(8) float top[2][HEADS][2];        // of two tiles: the largest logarithm of p x scale, of either half of the keys
   const uint8_t* row[kItemKeys<TREE>];      // each key's row in this layer; zeros for padding
   uint32_t live[kItemKeys<TREE> / kTileKeys + 2];   // bit per key: not padding; none behind the last tile
+  uint32_t sees[3][TREE ? HEADS : 1];       // what a row sees of a tile: of the history, of the drafted tokens' two
   uint32_t bad[TREE ? kItemKeys<TREE> / kTileKeys + 2 : 1];   // bit per drafted token: its row holds a NaN
   int ok;
 };
@@ -370,6 +371,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
             const bool codes = source[i] < kRopeAt;
             lds_put(ring + p * 16, codes ? clean : v);
             if (codes && any) atomicOr(&s.bad[tile], 1u << (p / kTilePieces));
+            __builtin_amdgcn_sched_barrier(0);         // one after another: they are few, registers are fewer
           }
           if (lane < kTileKeys) {
             float scale = *reinterpret_cast<const float*>(row[kPieceLoads] + source[kPieceLoads]);
@@ -478,7 +480,6 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
     }
   } else {
     QueryRaw<Q8> raw[HT];
-    unsigned long long sees[HT];                   // a tree: the drafted tokens that the row's node sees
     const ReaderState state = reader_state(g);
     if constexpr (TREE) {
       for (int i = threadIdx.x; i < kItemKeys<TREE> / kTileKeys + 2; i += kFirstWaves * kWave) s.bad[i] = 0;
@@ -491,7 +492,12 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
       if constexpr (TREE) {
         const int node = (int)a.by_heads.div(head);
         p += node * a.q_node_stride + (head - node * (int)a.by_heads.d) * a.q_head_stride;
-        sees[i] = any ? a.visible[(size_t)set * a.nodes + node] : 0;
+        if (quad == 0 && key_half == 0) {
+          const unsigned long long sees = any ? a.visible[(size_t)set * a.nodes + node] : 0;
+          s.sees[0][head0 + 16 * i + col] = ~0u;
+          s.sees[1][head0 + 16 * i + col] = (uint32_t)sees;
+          s.sees[2][head0 + 16 * i + col] = (uint32_t)(sees >> 32);
+        }
       } else {
         p += head * a.q_head_stride;
       }
@@ -531,7 +537,11 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
       const uint32_t scale = opaque(lds_address(s.scale) + (tile % TILES * kLatentGroups * kTileKeys + 8 * quad + 4 * key_half) * 4);
       bf16x8 kr[2] = {lds_get<bf16x8>(krow + kRopeAt), lds_get<bf16x8>(krow64 + kRopeAt)};
       const uint32_t live = __builtin_amdgcn_readfirstlane(s.live[tile]) >> (8 * quad + 4 * key_half);
-      const int draft = TREE ? key0 / kTileKeys + tile - a.history_tiles : -1;   // a tile of drafted tokens, or < 0
+      uint32_t seen = 0;
+      if constexpr (TREE) {
+        const int draft = key0 / kTileKeys + tile - a.history_tiles;   // a tile of drafted tokens, or < 0
+        seen = lds_address(s.sees) + ((draft < 0 ? 0 : 1 + (draft & 1)) * kHeads + head) * 4;
+      }
       f32x4 part[HT][kLatentGroups], rope[HT];
 #pragma unroll
       for (int b = 0; b < kLatentGroups; ++b) {
@@ -550,6 +560,16 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
         for (int b = 0; b < kLatentGroups; ++b) S[i] += sc[b] * part[i][b];
       }
       __builtin_amdgcn_sched_barrier(0);          // the partial products' registers are free from here
+      if constexpr (TREE) {
+        const uint32_t spoilt = __builtin_amdgcn_readfirstlane(s.bad[tile]);
+        if (spoilt) {                               // drafted tokens that make those who see them NaN
+#pragma unroll
+          for (int i = 0; i < HT; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (spoilt >> (8 * quad + 4 * key_half + r) & 1u) S[i][r] = __builtin_nanf("");
+        }
+      }
       // each key's largest scale as a power of two, from above: a key of large weight must not take a
       // neighbour's (p x scale would then vanish in fp16); scales below 2^-60 count as that
       float power[4];
@@ -564,15 +584,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
       for (int i = 0; i < HT; ++i) {
         float top = -__builtin_inff();
         uint32_t mine = live;
-        if constexpr (TREE) {
-          if (draft >= 0) {
-            mine &= (uint32_t)(sees[i] >> (32 * (draft & 1))) >> (8 * quad + 4 * key_half);
-            const uint32_t bad = __builtin_amdgcn_readfirstlane(s.bad[tile]) >> (8 * quad + 4 * key_half);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (bad & (1u << r)) S[i][r] = __builtin_nanf("");
-          }
-        }
+        if constexpr (TREE) mine &= lds_get<uint32_t>(seen + 16 * i * 4) >> (8 * quad + 4 * key_half);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           S[i][r] = mine & (1u << r) ? S[i][r] * c_log2 : -__builtin_inff();

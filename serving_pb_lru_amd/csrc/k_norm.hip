@@ -281,7 +281,8 @@ static int norm_lanes(const NormDev& a) {
 // Tokens and heads of a workgroup. A step of it takes `step` rows (those its lanes have
 // on their way); whole tokens, up to 16, that fill their steps best, if 1024 workgroups
 // (four a compute unit) have them, else one token and as few heads as a quarter of a
-// step. (8191 tokens x 36 heads of 128: 45 us with two tokens in two steps, 000 us so.)
+// step. (8191 tokens x 36 heads of 128: 45 us with two tokens in two steps, 38 us so; the
+// bytes take 28 us at the rate of a copy.)
 long long plan_norm(NormDev* a) {
   const int lanes = norm_lanes(*a);
   const int at_once = lanes ? kNormThreads / lanes : kNormThreads / kWave;
