@@ -143,8 +143,10 @@ __global__ __launch_bounds__(kWeighWaves * kWave, 2) void k_weigh_latent(GroupDe
         bf16x8 hi, lo;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          hi[i] = (__bf16)(float)v[i];
-          lo[i] = (__bf16)((float)v[i] - (float)hi[i]);
+          __bf16 top, rest;
+          two_parts((_Float16)(float)v[i], top, rest);
+          hi[i] = top;
+          lo[i] = rest;
         }
         *reinterpret_cast<bf16x8*>(at) = hi;
         *reinterpret_cast<bf16x8*>(at + 2 * kRope) = lo;
@@ -225,6 +227,18 @@ __global__ __launch_bounds__(kWeighWaves * kWave, 2) void k_weigh_latent(GroupDe
       for (int h = 0; h < HT; ++h)
 #pragma unroll
         for (int r = 0; r < 16; ++r) share += __builtin_amdgcn_exp2f(t[h][r]);
+      if (__any(share != share)) {                    // 0 x infinity in rows that count for nothing, it may be
+        share = 0.0f;
+#pragma unroll
+        for (int h = 0; h < HT; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f32x4 m = lds_get<f32x4>(lds_address(s.minus) + (32 * h + 8 * i + 4 * half) * 4);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (m[r] != -__builtin_inff()) share += __builtin_amdgcn_exp2f(t[h][4 * i + r]);
+          }
+      }
       share = sum_halves(share);
       if (half == 0) {
         float& sum = s.share[wave][group][col];
@@ -340,8 +354,16 @@ __global__ __launch_bounds__(kWeighHeadWaves * kWave) void k_weigh_heads(GroupDe
         f32x4 S{};
 #pragma unroll
         for (int j = 0; j < 2 * kLoads; ++j) S = mfma16(q[j], k[x][j], S);
+        float part = 0.0f;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) share[x] += __builtin_amdgcn_exp2f(__builtin_fmaf(S[r], sc[x], m[r]));
+        for (int r = 0; r < 4; ++r) part += __builtin_amdgcn_exp2f(__builtin_fmaf(S[r], sc[x], m[r]));
+        if (__any(part != part)) {                     // 0 x infinity in rows that count for nothing, it may be
+          part = 0.0f;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (m[r] != -__builtin_inff()) part += __builtin_amdgcn_exp2f(__builtin_fmaf(S[r], sc[x], m[r]));
+        }
+        share[x] += part;
       }
     }
   }

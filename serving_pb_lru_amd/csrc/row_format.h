@@ -163,6 +163,17 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 
+// An fp16 value as the sum of two bf16 ones (8 + 8 bits hold its 11) of its sign, neither of them 0 unless it is:
+// the one next below it in magnitude, and the rest. So their products with an infinite channel of a key are
+// infinities of one sign.
+__device__ __forceinline__ void two_parts(_Float16 x, __bf16& hi, __bf16& lo) {
+  const float v = (float)x + 0.0f;               // -0 as 0
+  const uint32_t bits = __builtin_bit_cast(uint32_t, v);
+  const float below = __builtin_bit_cast(float, (max(bits, 1u) - 1u) & 0xffff0000u);
+  hi = (__bf16)below;
+  lo = (__bf16)(v - below);
+}
+
 // Eight e4m3 codes (low byte first) as bf16 or fp16: exact, both hold every e4m3
 // value, so the scales can wait until the products are in 32 bits.
 template <typename V8>

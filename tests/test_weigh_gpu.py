@@ -204,3 +204,68 @@ def test_strides_streams_and_order():
         eng.sync()
     finally:
         eng.close()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("name", ["latent", "heads"])
+def test_entries_of_infinite_logits(name, kind):
+    """-infinity for every row that counts: no share. +infinity or NaN (0 x infinity) for one of them: infinite or NaN,
+    of which the score takes 2^22 or nothing."""
+    import torch
+    from serving_pb_lru_amd import head_rows, latent_rows
+    rng = np.random.default_rng(13)
+    n, k, heads = 40, 33, 3
+    rows = latent_rows_of(rng, n, 1) if name == "latent" else heads_rows_of(rng, n, 1, 1, 64, 1)
+    fmt = latent_rows() if name == "latent" else head_rows(1, 64)
+    sel = np.arange(k, dtype=np.int32)[None]
+    if name == "latent":
+        rows[5, 0, 512:514] = np.array([0x7F80], "<u2").view(np.uint8)
+    else:
+        rows[5, 0, :64] = 0
+        rows[5, 0, 0] = 0x38
+        rows[5, 0, 128:132] = np.array([np.inf], "<f4").view(np.uint8)
+    for first, share in (((-1.0, -0.3, -2.0), 0.0), ((-1.0, 0.3, -2.0), np.inf), ((-1.0, 0.0, -2.0), np.nan)):
+        q = torch.from_numpy(rng.standard_normal((1, heads, 576 if name == "latent" else 64))).to(torch_type(kind)).cuda()
+        if name == "heads":
+            q[..., 1:] = 0
+        q[0, :, 512 if name == "latent" else 0] = torch.tensor(first).to(q.dtype).cuda()
+        lse = torch.full((1, heads), 9.0, device="cuda")
+        scores = torch.zeros(n, dtype=torch.int64, device="cuda")
+        eng = engine_of(rows, 1, k)
+        try:
+            dsel = torch.from_numpy(sel).cuda()
+            eng.step(0, dsel)
+            got = eng.weigh(0, 0, dsel, q, lse, fmt, scores=scores).cpu().numpy()
+            eng.sync()
+        finally:
+            eng.close()
+        assert np.isfinite(np.delete(got, 5)).all()
+        assert np.array_equal(got[0, 5], share, equal_nan=True)
+        assert int(scores[5]) == {0.0: 0, np.inf: 1 << 54}.get(share, 0)
+
+
+@pytest.mark.parametrize("name", ["latent", "heads"])
+def test_rows_that_count_for_nothing_stay_out_whatever_an_entry_holds(name):
+    """Entries with NaN codes and infinite scales in a call with no row of finite lse: shares of 0."""
+    import torch
+    from serving_pb_lru_amd import head_rows, latent_rows
+    rng = np.random.default_rng(14)
+    rows = latent_rows_of(rng, 40, 1) if name == "latent" else heads_rows_of(rng, 40, 1, 1, 64, 1)
+    fmt = latent_rows() if name == "latent" else head_rows(1, 64)
+    rows[5, 0, 3] = 0x7F
+    at = 640 if name == "latent" else 128
+    rows[9, 0, at:at + 4] = np.array([-np.inf], "<f4").view(np.uint8)
+    eng = engine_of(rows, 1, 40)
+    try:
+        sel = torch.arange(40, dtype=torch.int32, device="cuda")[None]
+        eng.step(0, sel)
+        q = torch.from_numpy(rng.standard_normal((1, 40, 576 if name == "latent" else 64))).bfloat16().cuda()
+        lse = torch.full((1, 40), float("nan"), device="cuda")
+        assert not eng.weigh(0, 0, sel, q, lse, fmt).any()
+        lse[0, 33] = 3.0
+        some = eng.weigh(0, 0, sel, q, lse, fmt)
+        lone = eng.weigh(0, 0, sel, q[:, 33:34], lse[:, 33:34].contiguous(), fmt)
+        assert torch.allclose(some, lone, rtol=1e-5, atol=0, equal_nan=True) and bool(some[0, 5].isnan())
+        eng.sync()
+    finally:
+        eng.close()
