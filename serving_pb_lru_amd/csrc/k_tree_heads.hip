@@ -15,8 +15,8 @@
 // 24 heads of 64, fp16, and 80 us where this takes 37 us for 16 sets x 16 nodes x 2048
 // tokens x 32 heads of 128 over 8, bf16.) m follows the largest w as
 // there: it moves, to leave the largest at 2^8, when one could pass 2^15, which each lane
-// tells from its own tokens. A negative vs turns the signs of its codes; one below 2^-60
-// makes them 0; from the first beyond 2^40 either way on, l adds up powers of its own
+// tells from its own tokens. A negative vs turns the signs of its codes; one below 2^-80
+// makes them 0 (so l, which adds up to 2^95 for a token then, stays finite); from the first beyond 2^40 either way on, l adds up powers of its own
 // (w / |vs| would vanish beside a token of large scale); one that is not finite, or a NaN code in a drafted token's values, makes
 // T NaN, which a node that does not see the token replaces with its mask.
 //
@@ -33,6 +33,7 @@ namespace ula {
 
 constexpr int kTok = kTileTokens;
 constexpr int kTreeWaves = 4;
+constexpr float kLeastScale = 0x1p-80f;        // of a value; what is below it counts as 0
 
 // Waves on a SIMD, by registers.
 constexpr int tree_waves(int dim, int groups) { return dim == 64 ? (groups == 1 ? 3 : 2) : (groups == 1 ? 2 : 1); }
@@ -55,7 +56,8 @@ __global__ __launch_bounds__(kTreeWaves * kWave, tree_waves(D, RT)) void k_tree_
     float o[kTreeWaves][16][kRow];
   };
   __shared__ Lds s;
-  __shared__ float s_ml[kTreeWaves][2][kRows];
+  __shared__ float s_lse[kTreeWaves][kRows];
+  __shared__ bool s_ok[kTreeWaves];
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int quad = lane / 16, col = lane % 16;
@@ -208,13 +210,13 @@ __global__ __launch_bounds__(kTreeWaves * kWave, tree_waves(D, RT)) void k_tree_
     const uint32_t now = (uint32_t)__ballot((lane % kTok & (block - 1)) < in.used);   // bit per token
     {
       const bool use = now >> (lane % kTok) & 1u;
-      const float vs = in.vs, big = fmaxf(fabsf(vs), 0x1p-60f);   // NaN: 2^-60, and the shift says so
+      const float vs = in.vs, big = fmaxf(fabsf(vs), kLeastScale);   // NaN: that, and the shift says so
       float shift = __builtin_amdgcn_logf(big);
       if (!(fabsf(vs) < __builtin_inff())) shift = __builtin_nanf("");
       // Most tiles go to LDS as they are. Else: a token out of use must not reach the products (0 x NaN); codes of
       // negative scales change sign, those of vanishing ones are 0; NaN codes of drafted tokens are 0 as well.
       if (drafted || __any(!use || !(vs >= 0x1p-40f && vs <= 0x1p40f))) {
-        const uint32_t flips = (uint32_t)__ballot(vs < 0.0f), keep = now & (uint32_t)__ballot(fabsf(vs) >= 0x1p-60f);
+        const uint32_t flips = (uint32_t)__ballot(vs < 0.0f), keep = now & (uint32_t)__ballot(fabsf(vs) >= kLeastScale);
         uint32_t nan = 0;                                      // drafted tokens with NaN codes
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -366,42 +368,37 @@ __global__ __launch_bounds__(kTreeWaves * kWave, tree_waves(D, RT)) void k_tree_
   }
   if (err) latch_gather(g.ctr, err);
 
-  // the waves' results as one: w and l in units of the largest m
+  // The waves' results as one, in units of the largest log-sum: m, which follows the largest product with a
+  // value scale, may differ by more than what 32 bits hold.
 #pragma unroll
   for (int x = 0; x < RT; ++x) {
     l[x] = sum_quads(l[x]);
-    if (quad == 0) {
-      s_ml[wave][0][16 * x + col] = ok ? m[x] : __builtin_inff();
-      s_ml[wave][1][16 * x + col] = l[x];
-    }
+    if (quad == 0) s_lse[wave][16 * x + col] = l[x] != 0.0f ? m[x] + __builtin_amdgcn_logf(l[x]) : -__builtin_inff();
   }
+  if (lane == 0) s_ok[wave] = ok;
   __syncthreads();
+  for (int w = 0; w < kTreeWaves; ++w)
+    if (!s_ok[w]) return;                                      // some wave found an error: every thread sees that
   constexpr int kLanes = kTreeWaves * kWave / 16, kPer = D / kLanes;   // threads of a row in the stores, channels of each
   const int orow = threadIdx.x / kLanes, ch = threadIdx.x % kLanes * kPer;
 #pragma unroll
   for (int x = 0; x < RT; ++x) {
-    float most = -__builtin_inff(), mw[kTreeWaves];
+    float most = -__builtin_inff();
 #pragma unroll
-    for (int w = 0; w < kTreeWaves; ++w) most = fmaxf(most, mw[w] = s_ml[w][0][16 * x + col]);
-    if (most == __builtin_inff()) return;                      // some wave found an error: every thread sees that
-    const float at = most == -__builtin_inff() ? 0.0f : most;
-    float mine = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kTreeWaves; ++w)
-      if (w == wave) mine = __builtin_amdgcn_exp2f(mw[w] - at);
+    for (int w = 0; w < kTreeWaves; ++w) most = fmaxf(most, s_lse[w][16 * x + col]);
+    const float mine = __builtin_amdgcn_exp2f(m[x] - (most == -__builtin_inff() ? 0.0f : most));
 #pragma unroll
     for (int t = 0; t < D / 16; ++t)
       *reinterpret_cast<f32x4*>(&s.o[wave][col][16 * t + 4 * quad]) = o[x][t] * mine;
     __syncthreads();
     float sum = 0.0f, peak = -__builtin_inff();
 #pragma unroll
-    for (int w = 0; w < kTreeWaves; ++w) peak = fmaxf(peak, s_ml[w][0][16 * x + orow]);
+    for (int w = 0; w < kTreeWaves; ++w) peak = fmaxf(peak, s_lse[w][16 * x + orow]);
     const float from = peak == -__builtin_inff() ? 0.0f : peak;
 #pragma unroll
-    for (int w = 0; w < kTreeWaves; ++w)
-      sum += s_ml[w][1][16 * x + orow] * __builtin_amdgcn_exp2f(s_ml[w][0][16 * x + orow] - from);
+    for (int w = 0; w < kTreeWaves; ++w) sum += __builtin_amdgcn_exp2f(s_lse[w][16 * x + orow] - from);
     const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-    const float lse2 = sum != 0.0f ? peak + log2f(sum) : -__builtin_inff();
+    const float lse2 = sum != 0.0f ? from + log2f(sum) : -__builtin_inff();
     const int hi = row0 + 16 * x + orow;
     if (hi < rows) {
       float out[kPer];
