@@ -130,9 +130,16 @@ constexpr int kSecondWaves = kWaves - kFirstWaves;
 constexpr int kLoadsPerWave = (kTileLoads + kLatentGroups) / kSecondWaves;   // a second wave's vector loads per tile
 static_assert(kSecondWaves == kLatentGroups, "one scale block per second wave");
 
-// fp16 results: p x scale in two parts, which the second waves make of p in 32 bits.
+// fp16 results: p x scale in two parts.
 template <typename Q8>
 constexpr bool kTwoParts = !std::is_same_v<Q8, bf16x8>;
+
+// The second waves make p x scale of p in 32 bits, or the first waves do. With two parts the second waves'; a
+// tree's many rows leave them waiting for the first waves, which issue an instruction every 6 cycles and nothing else (64
+// sets x 1024 rows x 2048 keys: 415 us so, 378 when the second waves do it). Few rows to a key wait for the keys,
+// and the second waves for the sake of their loads: 256 sets x 64 heads x 2048 keys 121 us so, 125 when they do it.
+template <typename Q8, bool TREE>
+constexpr bool kWholeP = kTwoParts<Q8> || TREE;
 
 // Keys that a work item takes: a tree's drafted tokens come on top of a whole selection.
 template <bool TREE>
@@ -141,11 +148,11 @@ constexpr int kItemKeys = kAttendKeys + (TREE ? kTreeNodes : 0);
 template <typename Q8, int HT, int TILES, bool TREE>
 struct LatentLds {
   static constexpr int HEADS = 32 * HT;
-  // bytes of a key's p: one in 32 bits, or one for each block in 16
-  static constexpr int kKeyBytes = kTwoParts<Q8> ? 4 : 2 * kLatentGroups;
   alignas(1024) uint8_t ring[TILES][kTileBytes];
-  // p of two tiles. One part: p x scale, [block][head][key], key chunk c (8 keys) of head h at
-  // c ^ ((h >> 2) & 3). Two parts: p, [head][key], key chunk c (4 keys) of head h at c ^ ((h >> 1) & 7).
+  // bytes of a key's p: one in 32 bits, or one for each block in 16
+  static constexpr int kKeyBytes = kWholeP<Q8, TREE> ? 4 : 2 * kLatentGroups;
+  // p of two tiles. In 16 bits: p x scale, [block][head][key], key chunk c (8 keys) of head h at
+  // c ^ ((h >> 2) & 3). In 32: p, [head][key], key chunk c (4 keys) of head h at c ^ ((h >> 1) & 7).
   alignas(1024) uint8_t p[2][HEADS * kTileKeys * kKeyBytes];
   alignas(16) float scale[TILES][kLatentGroups][kTileKeys];
   float alpha[2][HEADS];                    // factor of O before the tile's second product
@@ -153,7 +160,7 @@ struct LatentLds {
   alignas(8) float top[2][HEADS][2];        // of two tiles: the largest logarithm of p x scale, of either half of the keys
   const uint8_t* row[kItemKeys<TREE>];      // each key's row in this layer; zeros for padding
   uint32_t live[kItemKeys<TREE> / kTileKeys + 2];   // bit per key: not padding; none behind the last tile
-  uint32_t sees[3][TREE ? HEADS : 1];       // what a row sees of a tile: of the history, of the drafted tokens' two
+  uint32_t sees[2][TREE ? HEADS : 1];       // what a row sees of the drafted tokens' two tiles
   uint32_t bad[TREE ? kItemKeys<TREE> / kTileKeys + 2 : 1];   // bit per drafted token: its row holds a NaN
   int ok;
 };
@@ -267,7 +274,7 @@ __device__ __forceinline__ void store_heads(uint8_t* box, const f32x16 (&o)[CT][
 template <typename Q8, int HT, int TILES, bool TREE>
 __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g, AttendDev a) {
   constexpr int kHeads = 32 * HT;                 // heads of a workgroup
-  constexpr bool kTwo = kTwoParts<Q8>;
+  constexpr bool kTwo = kTwoParts<Q8>, kWhole = kWholeP<Q8, TREE>;
   constexpr int CT = kScaleGroup / 32;            // 32-channel tiles of a second wave's O
   static_assert(2 * kHeads == 16 * HT * kFirstWaves, "every head has two waves in the first product");
   static_assert(TILES >= 4, "a tile on its way beside the three in use");
@@ -365,37 +372,32 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
     auto issue = [&](int tile) {
       const int at = tile % TILES;
       const uint32_t ring = lds_address(s.ring) + at * kTileBytes;
-      if constexpr (TREE) {
-        // A drafted token is seen by some nodes only, and 0 x NaN in the second product would reach the
-        // others: NaN codes and scales that are not finite become 0, and `bad` tells the softmax of the
-        // nodes that see them. Through registers, so these loads (and all before them) have arrived.
-        if (key0 / kTileKeys + tile >= a.history_tiles) {
-#pragma unroll
-          for (int i = 0; i < kPieceLoads; ++i) {
-            const int p = (i * kSecondWaves + sw) * kWave + lane;
-            const vec4u v = *reinterpret_cast<const vec4u*>(row[i] + source[i]);
-            bool any = false;
-            const vec4u clean = without_nan_codes(v, any);
-            const bool codes = source[i] < kRopeAt;
-            lds_put(ring + p * 16, codes ? clean : v);
-            if (codes && any) atomicOr(&s.bad[tile], 1u << (p / kTilePieces));
-            __builtin_amdgcn_sched_barrier(0);         // one after another: they are few, registers are fewer
-          }
-          if (lane < kTileKeys) {
-            float scale = *reinterpret_cast<const float*>(row[kPieceLoads] + source[kPieceLoads]);
-            if (!(fabsf(scale) < __builtin_inff())) {
-              scale = 0.0f;
-              atomicOr(&s.bad[tile], 1u << lane);
-            }
-            s.scale[at][sw][lane] = scale;
-          }
-          return;
-        }
-      }
 #pragma unroll
       for (int i = 0; i < kPieceLoads; ++i) lds_load16(row[i] + source[i], ring + (i * kSecondWaves + sw) * kWave * 16);
       if (lane < kTileKeys)
         lds_load4(row[kPieceLoads] + source[kPieceLoads], lds_address(s.scale) + (at * kLatentGroups + sw) * kTileKeys * 4);
+    };
+    // A drafted token is seen by some nodes only, and 0 x NaN in the second product would reach the others: NaN
+    // codes and scales that are not finite become 0, and `bad` tells the softmax of the nodes that see them. Each
+    // wave looks at what it has loaded, when that has arrived and before the others are told.
+    auto clean = [&](int tile) {
+      if (tile >= tiles || key0 / kTileKeys + tile < a.history_tiles) return;
+      const uint32_t ring = lds_address(s.ring) + tile % TILES * kTileBytes;
+#pragma unroll 1
+      for (int i = 0; i < kPieceLoads; ++i) {
+        const int p = (i * kSecondWaves + sw) * kWave + lane, key = p / kTilePieces;
+        if ((p % kTilePieces ^ swizzle(key)) >= kRopeAt / 16) continue;   // rotary channels
+        bool any = false;
+        const vec4u v = without_nan_codes(lds_get<vec4u>(ring + p * 16), any);
+        if (any) {
+          lds_put(ring + p * 16, v);
+          atomicOr(&s.bad[tile], 1u << key);
+        }
+      }
+      if (lane < kTileKeys && !(fabsf(s.scale[tile % TILES][sw][lane]) < __builtin_inff())) {
+        s.scale[tile % TILES][sw][lane] = 0.0f;
+        atomicOr(&s.bad[tile], 1u << lane);
+      }
     };
 #pragma unroll 1
     for (int t = 0; t < TILES - 1 && t < tiles; ++t) {
@@ -409,12 +411,13 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
     static_assert(kLatentScaleAt % 128 == 0 && kTileBytes % 128 == 0, "the swizzle's bits are free in every row address");
     // this lane's chunk of head col32: keys 8 half .. of a tile's first 16
     const uint32_t pread = lds_address(s.p) +
-                           (kTwo ? col32 * kTileKeys * 4 + ((2 * half ^ ((col32 >> 1) & 7)) << 4)
-                                 : (sw * kHeads + col32) * kTileKeys * 2 + ((half ^ ((col32 >> 2) & 3)) << 4));
+                           (kWhole ? col32 * kTileKeys * 4 + ((2 * half ^ ((col32 >> 1) & 7)) << 4)
+                                   : (sw * kHeads + col32) * kTileKeys * 2 + ((half ^ ((col32 >> 2) & 3)) << 4));
     float minus = -1.0f;                          // one the compiler does not know: a fused step takes it, a difference two
     asm volatile("" : "+s"(minus));
     if (tiles >= TILES - 1) wait_loads<(TILES - 2) * kLoadsPerWave>();
     else wait_loads<0>();
+    if constexpr (TREE) clean(0);
     barrier_keep_loads();
     read_rows(TILES - 1);
 #pragma unroll 1
@@ -424,6 +427,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
         wait_loads<(TILES - 4) * kLoadsPerWave>();
       else
         wait_loads<0>();
+      if constexpr (TREE) clean(tile + 2);
       barrier_keep_loads();
       if (tile < 0) continue;
       const int buf = tile & 1;
@@ -441,7 +445,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
       for (int h = 0; h < HT; ++h)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          if constexpr (kTwo) {
+          if constexpr (kWhole) {
             const uint32_t scale = lds_address(s.scale) + ((tile % TILES * kLatentGroups + sw) * kTileKeys + 16 * x + 8 * half) * 4;
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
@@ -451,13 +455,15 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
               for (int e = 0; e < 4; e += 2) {
                 // (the empty assembly keeps the product and its rounding one step each for both uses)
                 f32x2 v = {w[e] * sc[e], w[e + 1] * sc[e + 1]};
-                asm("" : "+v"(v));
+                if constexpr (kTwo) asm("" : "+v"(v));
                 f16x2 hi = __builtin_convertvector(v, f16x2);
-                asm("" : "+v"(hi));
+                if constexpr (kTwo) {
+                  asm("" : "+v"(hi));
+                  rest[h][x][4 * y + e] = (_Float16)__builtin_fmaf((float)hi.x, minus, v.x);
+                  rest[h][x][4 * y + e + 1] = (_Float16)__builtin_fmaf((float)hi.y, minus, v.y);
+                }
                 p[h][x][4 * y + e] = hi.x;
                 p[h][x][4 * y + e + 1] = hi.y;
-                rest[h][x][4 * y + e] = (_Float16)__builtin_fmaf((float)hi.x, minus, v.x);
-                rest[h][x][4 * y + e + 1] = (_Float16)__builtin_fmaf((float)hi.y, minus, v.y);
               }
             }
           } else {
@@ -502,9 +508,8 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
         p += node * a.q_node_stride + (head - node * (int)a.by_heads.d) * a.q_head_stride;
         if (quad == 0 && key_half == 0) {
           const unsigned long long sees = any ? a.visible[(size_t)set * a.nodes + node] : 0;
-          s.sees[0][head0 + 16 * i + col] = ~0u;
-          s.sees[1][head0 + 16 * i + col] = (uint32_t)sees;
-          s.sees[2][head0 + 16 * i + col] = (uint32_t)(sees >> 32);
+          s.sees[0][head0 + 16 * i + col] = (uint32_t)sees;
+          s.sees[1][head0 + 16 * i + col] = (uint32_t)(sees >> 32);
         }
       } else {
         p += head * a.q_head_stride;
@@ -533,8 +538,8 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
     const int koff = key * kLatentScaleAt + ((quad ^ swizzle(key)) << 4);
     const int head = head0 + col;
     const uint32_t pwrite = lds_address(s.p) +
-                            (kTwo ? head * kTileKeys * 4 + (((2 * quad + key_half) ^ ((head >> 1) & 7)) << 4)
-                                  : head * kTileKeys * 2 + ((quad ^ ((head >> 2) & 3)) << 4) + 8 * key_half);
+                            (kWhole ? head * kTileKeys * 4 + (((2 * quad + key_half) ^ ((head >> 1) & 7)) << 4)
+                                    : head * kTileKeys * 2 + ((quad ^ ((head >> 2) & 3)) << 4) + 8 * key_half);
     const uint32_t at_top = lds_address(s.top) + head * 8;
     f32x4 sc[kLatentGroups], S[HT];                // of the next tile for the softmax: scales, logits in powers of two
     // First product of a tile in LDS; the largest logarithm of p x scale of each
@@ -544,12 +549,9 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
       const uint32_t krow64 = opaque(krow ^ 64);
       const uint32_t scale = opaque(lds_address(s.scale) + (tile % TILES * kLatentGroups * kTileKeys + 8 * quad + 4 * key_half) * 4);
       bf16x8 kr[2] = {lds_get<bf16x8>(krow + kRopeAt), lds_get<bf16x8>(krow64 + kRopeAt)};
-      const uint32_t live = __builtin_amdgcn_readfirstlane(s.live[tile]) >> (8 * quad + 4 * key_half);
-      uint32_t seen = 0;
-      if constexpr (TREE) {
-        const int draft = key0 / kTileKeys + tile - a.history_tiles;   // a tile of drafted tokens, or < 0
-        seen = lds_address(s.sees) + ((draft < 0 ? 0 : 1 + (draft & 1)) * kHeads + head) * 4;
-      }
+      const uint32_t live = __builtin_amdgcn_readfirstlane(s.live[tile]);
+      const int draft = TREE ? key0 / kTileKeys + tile - a.history_tiles : -1;   // a tile of drafted tokens, or < 0
+      const bool masked = !TREE || live != ~0u || draft >= 0;   // without a tree the keys take longer than masks
       f32x4 part[HT][kLatentGroups], rope[HT];
 #pragma unroll
       for (int b = 0; b < kLatentGroups; ++b) {
@@ -569,7 +571,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
       }
       __builtin_amdgcn_sched_barrier(0);          // the partial products' registers are free from here
       if constexpr (TREE) {
-        const uint32_t spoilt = __builtin_amdgcn_readfirstlane(s.bad[tile]);
+        const uint32_t spoilt = draft >= 0 ? __builtin_amdgcn_readfirstlane(s.bad[tile]) : 0;
         if (spoilt) {                               // drafted tokens that make those who see them NaN
 #pragma unroll
           for (int i = 0; i < HT; ++i)
@@ -591,13 +593,18 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
 #pragma unroll
       for (int i = 0; i < HT; ++i) {
         float top = -__builtin_inff();
-        uint32_t mine = live;
-        if constexpr (TREE) mine &= lds_get<uint32_t>(seen + 16 * i * 4) >> (8 * quad + 4 * key_half);
+        S[i] *= c_log2;
+        if (masked) {
+          uint32_t mine = live;
+          if constexpr (TREE) {
+            if (draft >= 0) mine &= lds_get<uint32_t>(lds_address(s.sees) + ((draft & 1) * kHeads + head + 16 * i) * 4);
+          }
+          mine >>= 8 * quad + 4 * key_half;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          S[i][r] = mine & (1u << r) ? S[i][r] * c_log2 : -__builtin_inff();
-          top = fmaxf(top, S[i][r] + power[r]);
+          for (int r = 0; r < 4; ++r) S[i][r] = mine & (1u << r) ? S[i][r] : -__builtin_inff();
         }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) top = fmaxf(top, S[i][r] + power[r]);
         top = max_quads(top);
         if (quad == 0) lds_put(at_top + (tile & 1) * kHeads * 8 + 16 * i * 8 + 4 * key_half, top);
       }
@@ -626,8 +633,8 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
           p[r] = __builtin_amdgcn_exp2f(S[i][r] - base);
           l[i] += p[r];
         }
-        const uint32_t pw = opaque(pwrite + buf * (uint32_t)sizeof(s.p[0]) + 16 * i * kTileKeys * (kTwo ? 4 : 2));
-        if constexpr (kTwo) {
+        const uint32_t pw = opaque(pwrite + buf * (uint32_t)sizeof(s.p[0]) + 16 * i * kTileKeys * (kWhole ? 4 : 2));
+        if constexpr (kWhole) {
           lds_put(pw, p);
         } else {
 #pragma unroll
