@@ -327,31 +327,31 @@ __global__ __launch_bounds__(kTreeWaves * kWave, tree_waves(D, RT)) void k_tree_
 #pragma unroll
         for (int t = 0; t < D / 16; ++t) o[x][t] *= al;
       }
-      float more = 0.0f;                         // what l gains where w / |vs| may vanish
-      if (any_wide) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (T[e / 4][e % 4] != -__builtin_inff())
-            more += __builtin_amdgcn_exp2f(T[e / 4][e % 4] - shift[e / 4][e % 4] - base[x]);
-      }
-      const float before = l[x];
+      float plus = 0.0f;                         // what l gains
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
         f32x2 w = {__builtin_amdgcn_exp2f(T[e / 4][e % 4] - base[x]), __builtin_amdgcn_exp2f(T[e / 4][e % 4 + 1] - base[x])};
-        l[x] = __builtin_fmaf(w.x, inverse[e / 4][e % 4], l[x]);
-        l[x] = __builtin_fmaf(w.y, inverse[e / 4][e % 4 + 1], l[x]);
+        plus = __builtin_fmaf(w.x, inverse[e / 4][e % 4], plus);
+        plus = __builtin_fmaf(w.y, inverse[e / 4][e % 4 + 1], plus);
         f16x2 hi = __builtin_convertvector(w, f16x2);
         if constexpr (kRest) {
           asm("" : "+v"(hi));                    // one rounding for both uses
-          const f32x2 left = {__builtin_fmaf((float)hi.x, minus, w.x), __builtin_fmaf((float)hi.y, minus, w.y)};
-          const f16x2 lo = __builtin_convertvector(left, f16x2);
-          rest[at(x)][e] = lo.x;
-          rest[at(x)][e + 1] = lo.y;
+          rest[at(x)][e] = (_Float16)__builtin_fmaf((float)hi.x, minus, w.x);
+          rest[at(x)][e + 1] = (_Float16)__builtin_fmaf((float)hi.y, minus, w.y);
         }
         p[at(x)][e] = hi.x;
         p[at(x)][e + 1] = hi.y;
       }
-      if (any_wide && (wide >> x & 1u)) l[x] = before + more;
+      if (any_wide) {                            // w / |vs| may vanish
+        float more = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (T[e / 4][e % 4] != -__builtin_inff())
+            more += __builtin_amdgcn_exp2f(T[e / 4][e % 4] - shift[e / 4][e % 4] - base[x]);
+        plus = wide >> x & 1u ? more : plus;
+        asm volatile("" : "+v"(plus));           // a branch, not a selection
+      }
+      l[x] += plus;
       if constexpr (kKeepValues) {
 #pragma unroll
         for (int t = 0; t < D / 16; ++t) add(x, t, v[t], p[0], rest[0]);
