@@ -289,16 +289,20 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
   // work item: consecutive sets (which share rows under speculative selection)
   // run on one XCD at about the same time
   int item = blockIdx.x;
+  const int lead = TREE ? a.whole * a.head_blocks : 0;   // workgroups that have all of a set's keys
+  const bool whole = TREE && item < lead;
   {
-    const int per = gridDim.x / 8, rest = gridDim.x % 8;
-    const int x = item % 8;
-    item = x * per + min(x, rest) + item / 8;
+    const int n = whole ? lead : gridDim.x - lead, i = whole ? item : item - lead;
+    const int per = n / 8, rest = n % 8;
+    const int x = i % 8;
+    item = x * per + min(x, rest) + i / 8;
   }
+  const int splits = whole ? 1 : a.splits;
   const int hb = item % a.head_blocks;
-  const int split = item / a.head_blocks % a.splits;
-  const int set = item / (a.splits * a.head_blocks);
+  const int split = item / a.head_blocks % splits;
+  const int set = item / (splits * a.head_blocks) + (TREE && !whole ? a.whole : 0);
   const int key0 = split * a.split_keys;
-  const int nkeys = max(0, min(a.split_keys, a.k - key0));
+  const int nkeys = whole ? a.k : max(0, min(a.split_keys, a.k - key0));
   const int tiles = (nkeys + kTileKeys - 1) / kTileKeys;
 
   const int head0 = wave / 2 * 16 * HT;           // the first of a first wave's HT x 16 heads, and its half of the keys
@@ -676,14 +680,14 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
     const int head = hb * kHeads + 32 * h + col32;
     if (wave == 0 && half == 0 && head < a.heads) {
       const float lse2 = lh != 0.0f ? ml[32 * h + col32] + log2f(lh) : -__builtin_inff();
-      if (a.splits > 1) a.part_lse[((size_t)set * a.heads + head) * a.splits + split] = lse2;
+      if (splits > 1) a.part_lse[((size_t)(set - a.whole) * a.heads + head) * splits + split] = lse2;
       else if (a.lse) a.lse[(size_t)set * a.heads + head] = lse2 * kLn2;
     }
   }
-  if (a.splits > 1) {   // this split's own result in 32 bits, joined by k_attend_join
-    float* po = a.part_o + ((size_t)set * a.heads * a.splits + split) * kLatent;
+  if (splits > 1) {   // this split's own result in 32 bits, joined by k_attend_join
+    float* po = a.part_o + ((size_t)(set - a.whole) * a.heads * splits + split) * kLatent;
     store_heads<float>(s.ring[0], o, inv, hb * kHeads, a.heads, [&](int head, int ch, const vec4u v) {
-      *reinterpret_cast<vec4u*>(po + (size_t)head * a.splits * kLatent + ch) = v;
+      *reinterpret_cast<vec4u*>(po + (size_t)head * splits * kLatent + ch) = v;
     });
   } else {
     uint16_t* out = static_cast<uint16_t*>(a.out) + set * a.out_set_stride;
@@ -837,10 +841,10 @@ __global__ __launch_bounds__(kJoinThreads) void k_tree_join(GroupDev g, AttendDe
 //   64 x 128, 2048       1: 73   2: 95                        1: 101  2: 79
 //   64 x 64, 700         1: 29   2: 32                        1: 42   2: 40
 //   160 x 64, 2048       1: 132  3: 141                       1: 101  3: 114
-AttendPlan plan_attend_latent(int n_sets, int k, int heads, int most_keys) {
+AttendPlan plan_attend_latent(int n_sets, int k, int heads) {
   AttendPlan best{};
   const int tiles = (k + kTileKeys - 1) / kTileKeys;
-  const int least = std::max(1, (k + most_keys - 1) / most_keys);
+  const int least = std::max(1, (k + kAttendKeys - 1) / kAttendKeys);
   const double rows = (double)n_sets * heads;
   double best_cost = 0;
   for (const int wg_heads : {32, 64}) {
@@ -863,14 +867,44 @@ AttendPlan plan_attend_latent(int n_sets, int k, int heads, int most_keys) {
   return best;
 }
 
+// The same for a tree, where sets that fill the compute units evenly stay whole and the
+// others are split, so that the last round of workgroups is a short one and the join
+// has the rest alone. A tile takes 1.25 us here (64 rows; 0.9 for 32), a start and end 15.
+// Measured, all sets the same way and so, us: 24 sets x 1024 rows x 2048 keys 182, 157;
+// 33 x 1024 x 1024 157, 131; 70 x 256 x 1024 107, 83.
 AttendPlan plan_tree_latent(int n_sets, int tiles, int rows) {
   static_assert(kTileTokens == kTileKeys, "a tree's tiles are those of the kernel");
-  return plan_attend_latent(n_sets, tiles * kTileKeys, rows, kItemKeys<true>);
+  AttendPlan best{};
+  constexpr int kMostTiles = kItemKeys<true> / kTileKeys;
+  double best_cost = 0;
+  for (const int wg_rows : {32, 64}) {
+    const int blocks = (rows + wg_rows - 1) / wg_rows;
+    if (wg_rows == 64 && blocks == (rows + 31) / 32) break;        // the same workgroups, half empty
+    const double tile_us = wg_rows == 32 ? 0.9 : 1.25, start_us = 15.0;
+    const int rounds = (int)((long long)n_sets * blocks / kComputeUnits);   // full ones
+    for (const int whole : {0, tiles <= kMostTiles ? (int)((long long)rounds * kComputeUnits / blocks) : 0}) {
+      if (whole == n_sets) continue;                               // as no split at all
+      const long long base = (long long)(n_sets - whole) * blocks;
+      const int least = (tiles + kMostTiles - 1) / kMostTiles;
+      for (int want = std::max(1, least); want <= std::max(std::max(1, least), std::min(tiles, kComputeUnits)); ++want) {
+        const int per = std::max(1, (tiles + want - 1) / want), splits = std::max(1, (tiles + per - 1) / per);
+        if (splits != want && want != least) continue;             // the same split as a smaller one
+        double cost = (whole ? rounds : 0) * (tiles * tile_us + start_us) +
+                      (double)((base * splits + kComputeUnits - 1) / kComputeUnits) * (per * tile_us + start_us);
+        if (splits > 1) cost += 7 + (n_sets - whole) * (double)rows * (9e-4 + 2e-4 * splits);
+        if (best.splits == 0 || cost < best_cost) {
+          best_cost = cost;
+          best = {splits, per * kTileKeys, blocks, 0, splits > 1 ? whole : 0};
+        }
+      }
+    }
+  }
+  return best;
 }
 
 template <typename Q8, bool TREE>
 static hipError_t launch_latent(const GroupDev& g, const AttendDev& a, int n_sets, hipStream_t s) {
-  const int blocks = n_sets * a.head_blocks * a.splits;
+  const int blocks = (a.whole + (n_sets - a.whole) * a.splits) * a.head_blocks;
   if (a.head_blocks == (a.heads + 31) / 32) k_attend_latent<Q8, 1, 5, TREE><<<blocks, kWaves * kWave, 0, s>>>(g, a);
   else k_attend_latent<Q8, 2, 5, TREE><<<blocks, kWaves * kWave, 0, s>>>(g, a);
   return hipGetLastError();

@@ -39,8 +39,8 @@ struct AttendDev {
   const void* q;
   void* out;
   float* lse;              // nullable
-  float* part_o;           // [n_sets][heads][splits][width] when splits > 1
-  float* part_lse;         // [n_sets][heads][splits], base 2
+  float* part_o;           // [n_sets - whole][heads][splits][width] when splits > 1
+  float* part_lse;         // [n_sets - whole][heads][splits], base 2
   long long q_set_stride, q_head_stride, out_set_stride, out_head_stride;   // elements
   long long want_flag;
   float scale_log2;        // scale x log2(e)
@@ -55,7 +55,7 @@ struct AttendDev {
   const uint8_t* drafts;            // this layer's row of a set's first block of drafted tokens
   const unsigned long long* visible;   // [n_sets][nodes]
   long long draft_stride;           // bytes from one block's row to the next
-  int32_t nodes, sel_k, history_tiles, groups;
+  int32_t nodes, sel_k, history_tiles, groups, whole;
 };
 
 // Device arguments of the entries' weights: rows are nodes x heads.
@@ -134,9 +134,10 @@ hipError_t launch_rotate(const RotateDev& a, const RotaryDev& rot, int type, hip
 struct AttendPlan {
   int32_t splits, split_keys, head_blocks;
   int32_t groups;                   // a tree over heads rows: groups of 16 rows of a workgroup
+  int32_t whole;                    // a tree over latent rows: the first sets, which are not split
 };
 
-AttendPlan plan_attend_latent(int n_sets, int k, int heads, int most_keys = kAttendKeys);
+AttendPlan plan_attend_latent(int n_sets, int k, int heads);
 AttendPlan plan_attend_heads(int n_sets, int tokens, int heads, int kv_heads);
 // The same for a tree: rows of nodes x heads, keys as AttendDev says.
 constexpr int kTileTokens = 32;

@@ -1336,8 +1336,8 @@ static bool plan_attend(const ula_row_format* f, int32_t n_sets, int32_t k, int3
 
 static size_t attend_bytes(const AttendPlan& p, int32_t n_sets, int32_t heads, int width) {
   if (p.splits <= 1) return 0;
-  return align_up((size_t)n_sets * heads * p.splits * width * sizeof(float)) +
-         align_up((size_t)n_sets * heads * p.splits * sizeof(float));
+  const size_t parts = (size_t)(n_sets - p.whole) * heads * p.splits;
+  return align_up(parts * width * sizeof(float)) + align_up(parts * sizeof(float));
 }
 
 size_t ula_attend_bytes(const ula_row_format* rows, int32_t n_sets, int32_t k, int32_t heads) {
@@ -1430,7 +1430,7 @@ static int attend_impl(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_set
   a.part_o = static_cast<float*>(u.workspace);
   if (need)
     a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(u.workspace) +
-                                          align_up((size_t)n_sets * rows * plan.splits * width * sizeof(float)));
+                                          align_up((size_t)(n_sets - plan.whole) * rows * plan.splits * width * sizeof(float)));
   a.q_set_stride = u.q_set_stride;
   a.q_head_stride = u.q_head_stride;
   a.out_set_stride = u.out_set_stride;
@@ -1462,6 +1462,7 @@ static int attend_impl(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_set
     a.visible = reinterpret_cast<const unsigned long long*>(tree->visible);
     a.nodes = nodes;
     a.groups = plan.groups;
+    a.whole = plan.whole;
     a.sel_k = k;
     a.history_tiles = (int32_t)((((int64_t)k << a.block_shift) + kTileTokens - 1) / kTileTokens);
     a.k = a.history_tiles * kTileTokens + nodes;   // key places of a set (latent rows)
@@ -1472,8 +1473,12 @@ static int attend_impl(ula_ctx* ctx, int32_t group, int32_t layer, int32_t n_set
   if (latent) HIP_TRY(tree ? launch_tree_latent(g, a, u.type, n_sets, s) : launch_attend_latent(g, a, u.type, n_sets, s));
   else HIP_TRY(tree ? launch_tree_heads(g, a, u.type, n_sets, u.rows.head_dim, s)
                     : launch_attend_heads(g, a, u.type, n_sets, u.rows.head_dim, s));
-  a.by_heads = by_heads;
-  if (plan.splits > 1) HIP_TRY(launch_attend_join(g, a, u.type, n_sets, width, s));
+  if (plan.splits > 1) {   // of the sets that are split
+    a.by_heads = by_heads;
+    a.out = static_cast<uint16_t*>(a.out) + plan.whole * a.out_set_stride;
+    if (a.lse) a.lse += (size_t)plan.whole * rows;
+    HIP_TRY(launch_attend_join(g, a, u.type, n_sets - plan.whole, width, s));
+  }
   return note_gather(gh, s);
 }
 

@@ -133,6 +133,25 @@ def test_heads_against_the_formula(sets, k, nodes, heads, kv, dim, block, kind, 
         trees(rng, sets, nodes), heads, kind, rng)
 
 
+# sets that fill the compute units stay whole and the others are split: the last ones of many, strided results
+@pytest.mark.parametrize("sets,k,nodes,heads,kind,pad", [(257, 1500, 1, 20, "bf16", 0), (260, 300, 2, 16, "fp16", 40),
+                                                         (17, 400, 64, 16, "bf16", 0)])
+def test_whole_sets_beside_split_ones(sets, k, nodes, heads, kind, pad):
+    import ctypes
+    import torch
+    from serving_pb_lru_amd import latent_rows, ula
+    fmt, rng = latent_rows(), np.random.default_rng([sets, k, nodes])
+    need = ula.lib().ula_attend_tree_bytes(ctypes.byref(fmt), sets, k, nodes, heads)
+    assert 0 < need < sets * nodes * heads * 2 * 513 * 4          # less than two parts of every row
+    rows, drafts = latent_rows_of(rng, k + 50, 1), latent_rows_of(rng, sets * nodes, 1)
+    sel, visible = selection(rng, k + 50, sets, k, pad), trees(rng, sets, nodes)
+    q = torch.from_numpy(rng.standard_normal((sets, nodes, heads, 576))).to(torch_type(kind)).cuda()
+    room = torch.full((heads, sets, nodes, 520), 7.0, dtype=q.dtype, device="cuda")
+    out, lse = call(fmt, rows, drafts, sel, visible, q, out=room[..., :512].permute(1, 2, 0, 3))
+    check(expected(fmt, rows, drafts, 0, sel, visible, q.double().cpu().numpy(), 576 ** -0.5), out, lse, kind)
+    assert (room[..., 512:] == 7).all()
+
+
 def formats():
     from serving_pb_lru_amd import head_rows, latent_rows
     return {"latent": latent_rows(), "heads": head_rows(2, 64, 4), "heads128": head_rows(1, 128, 1)}
