@@ -246,6 +246,13 @@ __global__ __launch_bounds__(kLightThreads) void k_light_list(LightDev a, LightR
   __shared__ LightLds s;
   __shared__ int s_listed;
   const LightChunk c = light_chunk(a, r);
+  const long long* scores = a.scores + c.at.first + c.first;
+  long long ahead[kAtOnce];                            // on their way meanwhile
+#pragma unroll
+  for (int u = 0; u < kAtOnce; ++u) {
+    const int i = u * kLightThreads + threadIdx.x;
+    ahead[u] = i < c.count ? scores[i] : -1;
+  }
   constexpr int kPer = kLightBins / kLightThreads;
   static_assert(kPer == 2, "two bins of a thread in one load");
   const uint2* bins = reinterpret_cast<const uint2*>(c.bins) + threadIdx.x;
@@ -273,42 +280,60 @@ __global__ __launch_bounds__(kLightThreads) void k_light_list(LightDev a, LightR
   if (threadIdx.x == bin / 2)
     c.ends[c.chunk] = {bin, need, s.before, s.within, below, need > 0 ? (int)(bin % 2 ? own.y : own.x) : 0, 0, 0};
   if (need == 0) return;
-  const long long* scores = a.scores + c.at.first + c.first;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < c.count; i += kLightThreads) {
-    const long long v = scores[i];
+  auto list = [&](long long v) {
     if (v >= 0 && bin_of(v) == bin) c.list[c.first + atomicAdd(&s_listed, 1)] = (unsigned long long)v;
-  }
+  };
+#pragma unroll
+  for (int u = 0; u < kAtOnce; ++u) list(ahead[u]);
+  for (int i = kAtOnce * kLightThreads + threadIdx.x; i < c.count; i += kLightThreads) list(scores[i]);
 }
 
+// The list's entries are read into LDS where that holds them, and looked at there.
 __global__ __launch_bounds__(kLightThreads) void k_light_out(LightDev a, LightRanges r) {
   __shared__ LightLds s;
-  __shared__ int s_count[kLightChunks], s_below[kLightChunks];   // of each chunk: entries in the list, in bins before its bin
+  __shared__ unsigned long long s_key[kLightSpan];
+  // of each chunk: entries in the list and before it in those of the chunks before, in bins before its bin
+  __shared__ int s_count[kLightChunks], s_from[kLightChunks], s_below[kLightChunks];
   const LightChunk c = light_chunk(a, r);
   int32_t* out = a.out + (long long)c.range * a.most;
   const LightChunkEnd in = c.ends[c.chunk];
-  if (threadIdx.x < (unsigned)c.chunks) {
-    s_count[threadIdx.x] = c.ends[threadIdx.x].listed;
-    s_below[threadIdx.x] = c.ends[threadIdx.x].below;
+  if (threadIdx.x < kWave) {
+    static_assert(kLightChunks == kWave, "a lane for each chunk");
+    const bool any = (int)threadIdx.x < c.chunks;
+    const int listed = any ? c.ends[threadIdx.x].listed : 0;
+    s_count[threadIdx.x] = listed;
+    s_below[threadIdx.x] = any ? c.ends[threadIdx.x].below : 0;
+    s_from[threadIdx.x] = wave_inclusive_sum(listed) - listed;
   }
   if (c.chunk == 0)
     for (int i = in.need + threadIdx.x; i < a.most; i += kLightThreads) out[i] = -1;
   if (in.need == 0) return;
   __syncthreads();
   const int per = light_chunk_size(c.at.length);
-  const LightEnd end = end_within(s, in.bin, in.within, in.need - in.before, [&](auto f) {
+  const bool held = in.within <= kLightSpan;           // the list, in LDS
+  // each(f, n) calls f(key) for this thread's part of the first n chunks' lists
+  auto listed = [&](int n, auto f) {
+    if (held) {
+      const int all = n < c.chunks ? s_from[n] : in.within;
+      for (int i = threadIdx.x; i < all; i += kLightThreads) f(s_key[i]);
+    } else {
+      for (int k = threadIdx.x / kWave; k < n; k += kLightWaves)
+        for (int i = lane_id(); i < s_count[k]; i += kWave) f(c.list[(size_t)k * per + i]);
+    }
+  };
+  if (held) {
     for (int k = threadIdx.x / kWave; k < c.chunks; k += kLightWaves)
-      for (int i = lane_id(); i < s_count[k]; i += kWave) f(c.list[(size_t)k * per + i]);
-  });
+      for (int i = lane_id(); i < s_count[k]; i += kWave) s_key[s_from[k] + i] = c.list[(size_t)k * per + i];
+    __syncthreads();
+  }
+  const LightEnd end = end_within(s, in.bin, in.within, in.need - in.before, [&](auto f) { listed(c.chunks, f); });
   __syncthreads();
   // entries taken in the chunks before this one: whole bins, and the listed ones before the end
   int below = 0, same = 0;
-  for (int k = threadIdx.x / kWave; k < c.chunk; k += kLightWaves)
-    for (int i = lane_id(); i < s_count[k]; i += kWave) {
-      const unsigned long long key = c.list[(size_t)k * per + i];
-      below += key < end.key;
-      same += key == end.key;
-    }
+  listed(c.chunk, [&](unsigned long long key) {
+    below += key < end.key;
+    same += key == end.key;
+  });
   if (threadIdx.x < (unsigned)c.chunk) below += s_below[threadIdx.x];
   int at, tie;
   block_exclusive_sum<kLightThreads>(below, s.waves, at);
