@@ -263,8 +263,12 @@ __global__ __launch_bounds__(kWeighWaves * kWave, 2) void k_weigh_latent(GroupDe
 // ---- heads rows ----------------------------------------------------------------
 // Bound by the latency of reading the keys: a wave takes TT x 16 tokens by itself and
 // goes through the KV heads, a head's keys being contiguous, its 16 query rows (of
-// nodes and heads) at a time as the other operand; the next head's keys are on their
-// way. A token's share stays in the lane's column.
+// nodes and heads) at a time as the other operand; the next head's keys and the next
+// step's query rows are on their way. A token's share stays in the lane's column.
+// 16 sets x 2048 tokens x 32 heads of 128 over 8: 13.9 us, 36 MB (15.8 us with rows of q
+// asked for when they were needed, and branches around the keys' loads).
+__device__ __align__(16) uint8_t g_no_block[4096];     // zeros: a row is at most that long
+
 constexpr int kWeighTokens = 16;
 constexpr int kWeighHeadWaves = 4;
 
@@ -280,19 +284,27 @@ __global__ __launch_bounds__(kWeighHeadWaves * kWave) void k_weigh_heads(GroupDe
   const int per = (int)a.by_heads.d;                   // of one node
   const ReaderState state = reader_state(g);
 
+  // Lookups and loads have no branches, so that the compiler knows how many are in flight behind the ones it
+  // waits for: a token that is not there looks entry 0 up and reads zeros.
   const uint8_t* pool = g.pool + (size_t)a.layer * g.row_bytes;
   int err = 0;
   const uint8_t* row[TT];
-  bool live[TT];
-  int tok[TT];
+  int tok[TT], count[TT];
+  Lookup found[TT];
+  auto entry_of = [&](int x) { return tok[x] < a.k << a.block_shift ? set * a.k + (tok[x] >> a.block_shift) : -1; };
 #pragma unroll
   for (int x = 0; x < TT; ++x) {
     tok[x] = (tile * TT + x) * kWeighTokens + col;
-    row[x] = nullptr;
-    if (tok[x] < a.k << a.block_shift) {
-      const uint32_t slot = slot_of(g, look_up(g, a.sel, set * a.k + (tok[x] >> a.block_shift), a.n_res), a.n_res, err);
-      if (slot != kAbsent) row[x] = pool + (size_t)slot * g.slot_bytes;
-    }
+    const int r = max(entry_of(x), 0);
+    found[x] = {g.res[r], a.sel[r]};                   // res has room for every selection of the engine
+  }
+#pragma unroll
+  for (int x = 0; x < TT; ++x) {
+    const int r = entry_of(x);
+    if (r < 0) found[x].la = -1;
+    if (r >= a.n_res) found[x].res = make_uint2(kAbsent, kAbsent);
+    const uint32_t slot = slot_of(g, found[x], a.n_res, err);
+    row[x] = slot != kAbsent ? pool + (size_t)slot * g.slot_bytes : g_no_block;
   }
   int ok = 0;
   if (lane == 0) ok = reader_ready(g, state, a.want_flag);
@@ -307,77 +319,99 @@ __global__ __launch_bounds__(kWeighHeadWaves * kWave) void k_weigh_heads(GroupDe
     for (int x = 0; x < TT; ++x) {
       const uint8_t* p = row[x] + (kvh * block + (tok[x] & (block - 1))) * D + quad * (D / 4);
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) code[x][j] = row[x] ? *reinterpret_cast<const vec4u*>(p + 16 * j) : vec4u{0u, 0u, 0u, 0u};
-      ks[x] = row[x] ? *reinterpret_cast<const float*>(row[x] + scale_at + 4 * kvh) : 0.0f;
+      for (int j = 0; j < kLoads; ++j) code[x][j] = *reinterpret_cast<const vec4u*>(p + 16 * j);
+      ks[x] = *reinterpret_cast<const float*>(row[x] + scale_at + 4 * kvh);
     }
+  };
+  // Sixteen query rows of a KV head: this lane's operand of Q K^T, and the log-sum of its row.
+  struct Rows {
+    Q8 q[2 * kLoads];
+    float lse;
+  };
+  auto load_rows = [&](int kvh, int r0, Rows& to) {
+    const bool there = r0 + col < shared && kvh < a.kv_heads;
+    const int hi = there ? r0 + col : 0;               // of those there are, the first stands in for the others
+    const int node = (int)a.by_heads.div(hi), head = (there ? kvh * per : 0) + hi - node * per;
+    const float lse = a.lse[(size_t)set * a.rows + node * (a.rows / a.nodes) + head];
+    const uint16_t* p = static_cast<const uint16_t*>(a.q) + set * a.q_set_stride + node * a.q_node_stride +
+                        head * a.q_head_stride + quad * (D / 4);
+#pragma unroll
+    for (int j = 0; j < 2 * kLoads; ++j) to.q[j] = a.q_aligned ? load8<Q8, true>(p + 8 * j) : load8<Q8, false>(p + 8 * j);
+    to.lse = there ? lse : __builtin_inff();
   };
   load(0);
   float share[TT];
 #pragma unroll
   for (int x = 0; x < TT; ++x) {
     share[x] = 0.0f;
-    live[x] = false;
-    if (row[x]) live[x] = (tok[x] & (block - 1)) < *reinterpret_cast<const int32_t*>(row[x] + scale_at + 8 * a.kv_heads);
+    count[x] = *reinterpret_cast<const int32_t*>(row[x] + scale_at + 8 * a.kv_heads);
   }
-  for (int kvh = 0; kvh < a.kv_heads; ++kvh) {
-    Q8 k[TT][2 * kLoads];
-    float sc[TT];
-#pragma unroll
-    for (int x = 0; x < TT; ++x) {
-      sc[x] = ks[x] * a.scale_log2;
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        k[x][2 * j] = widen8<Q8>(code[x][j].x, code[x][j].y);
-        k[x][2 * j + 1] = widen8<Q8>(code[x][j].z, code[x][j].w);
-      }
-    }
-    if (kvh + 1 < a.kv_heads) load(kvh + 1);
-    for (int r0 = 0; r0 < shared; r0 += 16) {
-      const int hi = r0 + col;                         // the row of Q K^T that this lane's operand is
-      Q8 q[2 * kLoads];
-      float minus = -__builtin_inff();
-      const int node = (int)a.by_heads.div(hi), head = kvh * per + hi - node * per;
-      const float lse = hi < shared ? a.lse[(size_t)set * a.rows + node * (a.rows / a.nodes) + head] : __builtin_inff();
-      if (counts(lse)) {                               // a row that counts for nothing may hold anything
-        const uint16_t* p = static_cast<const uint16_t*>(a.q) + set * a.q_set_stride + node * a.q_node_stride +
-                            head * a.q_head_stride + quad * (D / 4);
-#pragma unroll
-        for (int j = 0; j < 2 * kLoads; ++j) q[j] = a.q_aligned ? load8<Q8, true>(p + 8 * j) : load8<Q8, false>(p + 8 * j);
-        minus = lse * -kLog2e;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 2 * kLoads; ++j) q[j] = Q8{};
-      }
-      float m[4];                                      // of the rows in this lane's registers, 4 quad + r
-#pragma unroll
-      for (int r = 0; r < 4; ++r) m[r] = __shfl(minus, 4 * quad + r, kWave);
+  Q8 k[TT][2 * kLoads];
+  float sc[TT];
+  int kvh = 0, r0 = 0;                                 // of the step at hand
+  // One step: rows r0 .. of KV head kvh, which are in `now`; the next step's are on their way to `then`.
+  auto step = [&](Rows& now, Rows& then) {
+    if (r0 == 0) {
 #pragma unroll
       for (int x = 0; x < TT; ++x) {
-        f32x4 S{};
+        sc[x] = ks[x] * a.scale_log2;
 #pragma unroll
-        for (int j = 0; j < 2 * kLoads; ++j) S = mfma16(q[j], k[x][j], S);
-        float part = 0.0f;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) part += __builtin_amdgcn_exp2f(__builtin_fmaf(S[r], sc[x], m[r]));
-        if (__any(part != part)) {                     // 0 x infinity in rows that count for nothing, it may be
-          part = 0.0f;
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (m[r] != -__builtin_inff()) part += __builtin_amdgcn_exp2f(__builtin_fmaf(S[r], sc[x], m[r]));
+        for (int j = 0; j < kLoads; ++j) {
+          k[x][2 * j] = widen8<Q8>(code[x][j].x, code[x][j].y);
+          k[x][2 * j + 1] = widen8<Q8>(code[x][j].z, code[x][j].w);
         }
-        share[x] += part;
       }
+      load(min(kvh + 1, a.kv_heads - 1));
     }
+    r0 += 16;
+    if (r0 >= shared) {
+      r0 = 0;
+      ++kvh;
+    }
+    load_rows(kvh, r0, then);
+    // a row that counts for nothing may hold anything
+    const bool any = counts(now.lse);
+    const float minus = any ? now.lse * -kLog2e : -__builtin_inff();
+    Q8 q[2 * kLoads];
+#pragma unroll
+    for (int j = 0; j < 2 * kLoads; ++j) q[j] = any ? now.q[j] : Q8{};
+    float m[4];                                        // of the rows in this lane's registers, 4 quad + r
+#pragma unroll
+    for (int r = 0; r < 4; ++r) m[r] = __shfl(minus, 4 * quad + r, kWave);
+#pragma unroll
+    for (int x = 0; x < TT; ++x) {
+      f32x4 S{};
+#pragma unroll
+      for (int j = 0; j < 2 * kLoads; ++j) S = mfma16(q[j], k[x][j], S);
+      float part = 0.0f;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) part += __builtin_amdgcn_exp2f(__builtin_fmaf(S[r], sc[x], m[r]));
+      if (__any(part != part)) {                       // 0 x infinity in rows that count for nothing, it may be
+        part = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (m[r] != -__builtin_inff()) part += __builtin_amdgcn_exp2f(__builtin_fmaf(S[r], sc[x], m[r]));
+      }
+      share[x] += part;
+    }
+  };
+  Rows rows_a, rows_b;
+  load_rows(0, 0, rows_a);
+  while (true) {
+    step(rows_a, rows_b);
+    if (kvh == a.kv_heads) break;
+    step(rows_b, rows_a);
+    if (kvh == a.kv_heads) break;
   }
 #pragma unroll
   for (int x = 0; x < TT; ++x) {
-    float sum = live[x] ? sum_quads(share[x]) : 0.0f;
+    float sum = (tok[x] & (block - 1)) < count[x] ? sum_quads(share[x]) : 0.0f;
     for (int d = 1; d < block; d *= 2) sum += __shfl_xor(sum, d, kWave);   // the tokens of an entry
     const int entry = tok[x] >> a.block_shift;
     if (quad == 0 && (col & (block - 1)) == 0 && entry < a.k) {
       const int at = set * a.k + entry;
       if (a.shares) a.shares[at] = sum;
-      if (a.scores && row[x]) atomicAdd(a.scores + a.sel[at], score_units(sum));
+      if (a.scores && row[x] != g_no_block) atomicAdd(a.scores + a.sel[at], score_units(sum));
     }
   }
 }
