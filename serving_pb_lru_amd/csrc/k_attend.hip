@@ -36,7 +36,7 @@
 // channels of O (one scale block) with all heads each: so no wave holds another's
 // Q, a key is widened for all of a wave's heads at once and every value once. In
 // between p goes through LDS in the operand order of the second product, scaled for
-// each block (fp16 queries: in 32 bits, scaled and split by the second waves). The two waves of a head tell each other their largest
+// each block (fp16 queries and trees: in 32 bits, scaled, and split, by the second waves). The two waves of a head tell each other their largest
 // logits through LDS as well, a barrier ahead of the softmax, and so come to the
 // same m. Each SIMD has a wave of either kind. One barrier per tile.
 // Measured, 256 sets of 2048 keys and 64 heads: 206 us with a wave that kept 32
@@ -53,6 +53,12 @@
 // frees (117 us).
 // Sixteen waves of 16 heads or 64 channels read keys and p from LDS twice as often
 // and widen keys twice as often: 159 us.
+// A tree of drafted tokens (TREE) has nodes x heads rows where the heads are, and two
+// tiles of keys at most behind the selected ones, whose rows come from the caller and
+// which a row sees by its node's mask. 64 sets x 1024 rows x 2048 keys, bf16: 360 us, of which each
+// of four rounds of workgroups spends 15 us on its start (5 us for 19 MB of q), the filling
+// of the pipeline and its end; the rest are the first waves' instructions, an
+// instruction every 6 cycles or so.
 // Tiles: the first 640 bytes of each row as 16-byte pieces straight into LDS (no
 // registers), the scales transposed to [block][key]. Piece c of key j lies at
 // c ^ swizzle(j), which keeps the 16 lanes that a 16-byte read serves at once

@@ -11,9 +11,11 @@
 // fused add and the rounding for each logit. (With 64 query rows to a key, vector
 // instructions on logits bound this, not bytes; masks, a product with vs and an
 // exponent of it for each logit, in four waves that each had their own rows' tokens, took
-// 410 us a call where this takes 144 us for 32 sets x 61 nodes x 500 blocks of 8 tokens x
-// 24 heads of 64, fp16, and 80 us where this takes 37 us for 16 sets x 16 nodes x 2048
-// tokens x 32 heads of 128 over 8, bf16.) m follows the largest w as
+// 410 us a call where this takes 130 us for 32 sets x 61 nodes x 500 blocks of 8 tokens x
+// 24 heads of 64, fp16, and 80 us where this takes 35 us for 16 sets x 16 nodes x 2048
+// tokens x 32 heads of 128 over 8, bf16. In the first of the two vector instructions now fill
+// 57% of a SIMD's cycles and matrix instructions 22%; the second has one wave a SIMD, which waits
+// 37% of its time.) m follows the largest w as
 // there: it moves, to leave the largest at 2^8, when one could pass 2^15, which each lane
 // tells from its own tokens. A negative vs turns the signs of its codes; one below 2^-80
 // makes them 0 (so l, which adds up to 2^95 for a token then, stays finite); from the first beyond 2^40 either way on, l adds up powers of its own
