@@ -9,7 +9,9 @@ bitmaps with summaries) picks what leaves the GPU. All of the per-step work
 runs in hand-written HIP kernels behind the C ABI of include/ula.h; the
 Python module `ula` only marshals arguments. Beside it stand the operators on
 the rows' contents: the FP8 row writer, rotary positions, attention over the
-selected rows, and copies and new addresses for entries.
+selected rows, copies and new addresses for entries, norms with the turn,
+attention of drafted trees, the weights that entries got, and the entries of
+least weight.
 """
 
 from .ula import (Engine, RowFormat, UlaError, lib, ERROR_NAMES, head_rows, latent_rows, lightest,
