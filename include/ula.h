@@ -591,7 +591,8 @@ typedef struct {
  * entries have share 0 and add nothing. A row whose lse is not finite counts for
  * nothing (it attended to nothing; a rejected node is left out that way). With log-sums
  * that cover more than these entries (a tree's drafted tokens) shares are of the whole.
- * A share that is NaN adds nothing to the score, one above 2^22 adds that. Products, logits and
+ * A share that is NaN adds nothing to the score, one above 2^22 adds that; a score holds
+ * 2^31 of weight, so a program that runs on for so long halves its scores before. Products, logits and
  * sums are in 32 bits, summed in an order that depends on the sizes alone. Nothing but keys
  * is read of the rows. q, lse, shares and scores must not overlap. Calls that add to the same scores at the
  * same time are fine. Which entries, streams and errors: as for ula_attend. Host errors: also
