@@ -554,6 +554,12 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
     f32x4 sc[kLatentGroups], S[HT];                // of the next tile for the softmax: scales, logits in powers of two
     // First product of a tile in LDS; the largest logarithm of p x scale of each
     // head, over this half of the keys, goes to the wave with the other half.
+    vec4u ahead[2];                                // a tree: the first block's keys of the next tile
+    auto first_keys = [&](int tile) {
+      const uint32_t krow = lds_address(s.ring) + tile % TILES * kTileBytes + koff;
+      ahead[0] = lds_get<vec4u>(krow);
+      ahead[1] = lds_get<vec4u>(krow ^ 64);
+    };
     auto logits = [&](int tile) {
       const uint32_t krow = opaque(lds_address(s.ring) + tile % TILES * kTileBytes + koff);
       const uint32_t krow64 = opaque(krow ^ 64);
@@ -566,7 +572,8 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
 #pragma unroll
       for (int b = 0; b < kLatentGroups; ++b) {
         sc[b] = lds_get<f32x4>(scale + kTileKeys * b * 4);
-        const vec4u k0 = lds_get<vec4u>(krow + b * kScaleGroup), k1 = lds_get<vec4u>(krow64 + b * kScaleGroup);
+        const vec4u k0 = TREE && b == 0 ? ahead[0] : lds_get<vec4u>(krow + b * kScaleGroup);
+        const vec4u k1 = TREE && b == 0 ? ahead[1] : lds_get<vec4u>(krow64 + b * kScaleGroup);
         const Q8 k[4] = {widen8<Q8>(k0.x, k0.y), widen8<Q8>(k0.z, k0.w), widen8<Q8>(k1.x, k1.y), widen8<Q8>(k1.z, k1.w)};
 #pragma unroll
         for (int i = 0; i < HT; ++i) part[i][b] = q[i].block_product(b, k);
@@ -620,17 +627,20 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
       }
     };
     barrier_keep_loads();
+    if constexpr (TREE) first_keys(0);
     logits(0);
 #pragma unroll 1
     for (int tile = 0; tile <= tiles; ++tile) {   // softmax of `tile`, logits of the next one
       barrier_keep_loads();
       const int buf = tile & 1;
       bool moved = false;
+      f32x2 both[HT];                             // both halves' waves come to the same reference
+#pragma unroll
+      for (int i = 0; i < HT; ++i) both[i] = lds_get<f32x2>(at_top + buf * kHeads * 8 + 16 * i * 8);
+      if constexpr (TREE) first_keys(tile + 1);
 #pragma unroll
       for (int i = 0; i < HT; ++i) {
-        // both halves' waves come to the same reference
-        const f32x2 both = lds_get<f32x2>(at_top + buf * kHeads * 8 + 16 * i * 8);
-        const float top = fmaxf(both.x, both.y);
+        const float top = fmaxf(both[i].x, both[i].y);
         const bool move = top > m[i] + 15.0f;
         const float nm = move ? top - 8.0f : m[i];
         const float al = move ? __builtin_amdgcn_exp2f(m[i] - nm) : 1.0f;
