@@ -12,10 +12,9 @@
 // instructions on logits bound this, not bytes; masks, a product with vs and an
 // exponent of it for each logit, in four waves that each had their own rows' tokens, took
 // 410 us a call where this takes 130 us for 32 sets x 61 nodes x 500 blocks of 8 tokens x
-// 24 heads of 64, fp16, and 80 us where this takes 35 us for 16 sets x 16 nodes x 2048
-// tokens x 32 heads of 128 over 8, bf16. In the first of the two vector instructions now fill
-// 57% of a SIMD's cycles and matrix instructions 22%; the second has one wave a SIMD, which waits
-// 37% of its time.) m follows the largest w as
+// 24 heads of 64, fp16, and 80 us where this takes 32 us for 16 sets x 16 nodes x 2048
+// tokens x 32 heads of 128 over 8, bf16. In the first of the two vector instructions
+// fill 57% of a SIMD's cycles and matrix instructions 22%.) m follows the largest w as
 // there: it moves, to leave the largest at 2^8, when one could pass 2^15, which each lane
 // tells from its own tokens. A negative vs turns the signs of its codes; one below 2^-80
 // makes them 0 (so l, which adds up to 2^95 for a token then, stays finite); from the first beyond 2^40 either way on, l adds up powers of its own
@@ -23,9 +22,13 @@
 // T NaN, which a node that does not see the token replaces with its mask.
 //
 // A workgroup is one KV head's RT x 16 query rows (of nodes and heads) and one range of
-// tokens; its four waves take every fourth tile of 32 tokens, each by itself as there,
-// and join their results in LDS. So a set's tokens are split over fewer
-// workgroups, whose parts go through memory, than over waves.
+// tokens; its four or eight waves take every fourth or eighth tile of 32 tokens, each by
+// itself as there, and join their results in LDS. So a set's tokens are split over fewer
+// workgroups, whose parts go through memory, than over waves. With up to 32 rows q is in
+// LDS, and a tile's products with all of them come first, a half of the keys at a time: so two
+// waves of 32 rows and heads of 128 fit a SIMD (one with q in registers: 36 us for the second of the
+// two above). With more rows q stays in registers, which leaves fewer accumulators waiting
+// (the first of the two: 130 us so, 132 us with q in LDS).
 #include <algorithm>
 #include <cmath>
 
@@ -34,14 +37,15 @@
 namespace ula {
 
 constexpr int kTok = kTileTokens;
-constexpr int kTreeWaves = 4;
 constexpr float kLeastScale = 0x1p-80f;        // of a value; what is below it counts as 0
 
-// Waves on a SIMD, by registers.
-constexpr int tree_waves(int dim, int groups) { return dim == 64 ? (groups == 1 ? 3 : 2) : (groups == 1 ? 2 : 1); }
+// Waves on a SIMD, by registers, and waves of a workgroup.
+constexpr int tree_waves(int dim, int groups) { return dim == 64 ? (groups == 1 ? 3 : 2) : (groups <= 2 ? 2 : 1); }
+constexpr int tree_group(int dim, int groups) { return dim == 128 && groups == 2 ? 8 : 4; }
 
 template <typename Q8, int D, int RT>
-__global__ __launch_bounds__(kTreeWaves * kWave, tree_waves(D, RT)) void k_tree_heads(GroupDev g, AttendDev a) {
+__global__ __launch_bounds__(tree_group(D, RT) * kWave, tree_waves(D, RT)) void k_tree_heads(GroupDev g, AttendDev a) {
+  constexpr int kTreeWaves = tree_group(D, RT);
   constexpr bool kRest = !__is_same(Q8, bf16x8);   // the weights in two parts
   constexpr int kPieces = D / 16;              // 16-byte pieces of a token's key or value
   constexpr int kKeyLoads = D / 64;            // pieces of its key a lane holds (a quarter)
@@ -49,6 +53,7 @@ __global__ __launch_bounds__(kTreeWaves * kWave, tree_waves(D, RT)) void k_tree_
   constexpr int kRows = 16 * RT;
   constexpr bool kKeepValues = D == 64;        // of a tile, widened, or else the weights of all rows: the fewer registers
   constexpr int kRow = D + 4;                  // floats of a row in the join
+  constexpr bool kAhead = RT <= 2;             // q in LDS, the first products of all rows at once
   struct WaveLds {
     alignas(1024) uint8_t v[kTok * D];
     alignas(16) float scale[kTok], shift[kTok], inverse[kTok];   // c ks, log2 |vs|, 1 / |vs|
@@ -60,6 +65,7 @@ __global__ __launch_bounds__(kTreeWaves * kWave, tree_waves(D, RT)) void k_tree_
   __shared__ Lds s;
   __shared__ float s_lse[kTreeWaves][kRows];
   __shared__ bool s_ok[kTreeWaves];
+  __shared__ Q8 s_q[kAhead ? RT * D / 32 : 1][kWave];   // q in operand order, the same for all waves
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int quad = lane / 16, col = lane % 16;
@@ -144,9 +150,9 @@ __global__ __launch_bounds__(kTreeWaves * kWave, tree_waves(D, RT)) void k_tree_
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int t = 8 * (col / 4) + 4 * u + col % 4;
-      const uint8_t* p = from + (uint64_t)ksl[u] * stride + (head_at + (t & (block - 1)) * D + quad * (D / 4));
+      const uint8_t* p = from + (uint64_t)ksl[u] * stride + (head_at + (t & (block - 1)) * D + quad * 16);
 #pragma unroll
-      for (int j = 0; j < kKeyLoads; ++j) in.k[u][j] = *reinterpret_cast<const vec4u*>(p + 16 * j);
+      for (int j = 0; j < kKeyLoads; ++j) in.k[u][j] = *reinterpret_cast<const vec4u*>(p + 64 * j);
     }
 #pragma unroll
     for (int i = 0; i < kValLoads; ++i) {
@@ -161,21 +167,38 @@ __global__ __launch_bounds__(kTreeWaves * kWave, tree_waves(D, RT)) void k_tree_
   Lookup next = look(tile0 + kTreeWaves);
   // this lane's query rows and what their nodes see of the drafted tokens
   unsigned long long sees[RT];
-  Q8 q[RT][D / 32];
+  constexpr int kQ = D / 32;                   // operands of a row group
+  Q8 q[kAhead ? 1 : RT][kQ];
+  // row hi of q from this lane's first channel on; operand j is 64 (j / 2) + 8 (j % 2) further
+  auto query = [&](int hi) {
+    const int node = (int)a.by_heads.div(hi), head = kvh * per + hi - node * per;
+    return static_cast<const uint16_t*>(a.q) + set * a.q_set_stride + node * a.q_node_stride + head * a.q_head_stride +
+           16 * quad;
+  };
+  auto operand = [&](const uint16_t* p) { return a.q_aligned ? load8<Q8, true>(p) : load8<Q8, false>(p); };
 #pragma unroll
   for (int x = 0; x < RT; ++x) {
     const int hi = row0 + 16 * x + col;
     sees[x] = 0;
+    if constexpr (!kAhead) {
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) q[x][j] = Q8{};
-    if (hi < rows) {
-      const int node = (int)a.by_heads.div(hi), head = kvh * per + hi - node * per;
-      const uint16_t* p = static_cast<const uint16_t*>(a.q) + set * a.q_set_stride + node * a.q_node_stride +
-                          head * a.q_head_stride + quad * (D / 4);
-      sees[x] = a.visible[(size_t)set * a.nodes + node];
-#pragma unroll
-      for (int j = 0; j < D / 32; ++j) q[x][j] = a.q_aligned ? load8<Q8, true>(p + 8 * j) : load8<Q8, false>(p + 8 * j);
+      for (int j = 0; j < kQ; ++j) q[x][j] = Q8{};
     }
+    if (hi < rows) {
+      sees[x] = a.visible[(size_t)set * a.nodes + (int)a.by_heads.div(hi)];
+      if constexpr (!kAhead) {
+        const uint16_t* p = query(hi);
+#pragma unroll
+        for (int j = 0; j < kQ; ++j) q[x][j] = operand(p + 64 * (j / 2) + 8 * (j % 2));
+      }
+    }
+  }
+  if constexpr (kAhead) {
+    for (int e = wave; e < RT * kQ; e += kTreeWaves) {
+      const int hi = row0 + 16 * (e / kQ) + col, j = e % kQ;
+      s_q[e][lane] = hi < rows ? operand(query(hi) + 64 * (j / 2) + 8 * (j % 2)) : Q8{};
+    }
+    __syncthreads();
   }
   f32x4 o[RT][D / 16];
   // bit x: value scales beyond 2^40 either way have come to the lane's row x, so that w / |vs| may vanish
@@ -202,8 +225,10 @@ __global__ __launch_bounds__(kTreeWaves * kWave, tree_waves(D, RT)) void k_tree_
 #pragma unroll
   for (int x = 0; x < RT; ++x) {
     asm volatile("" : "+v"(sees[x]));
+    if constexpr (!kAhead) {
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) asm volatile("" : "+v"(q[x][j]));
+      for (int j = 0; j < kQ; ++j) asm volatile("" : "+v"(q[x][j]));
+    }
   }
   if (ok) load(tile0, slot_at(tile0, first));
 #pragma unroll 1
@@ -262,14 +287,26 @@ __global__ __launch_bounds__(kTreeWaves * kWave, tree_waves(D, RT)) void k_tree_
         mine_lds.inverse[lane] = use ? __builtin_amdgcn_rcpf(big) : 0.0f;
       }
     }
-    Q8 kw[2][2 * kKeyLoads];
+    Q8 kw[kAhead ? 1 : 2][2 * kKeyLoads];
+    f32x4 products[kAhead ? RT : 1][2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u) {
+      Q8(&k)[2 * kKeyLoads] = kw[kAhead ? 0 : u];
 #pragma unroll
       for (int j = 0; j < kKeyLoads; ++j) {
-        kw[u][2 * j] = widen8<Q8>(in.k[u][j].x, in.k[u][j].y);
-        kw[u][2 * j + 1] = widen8<Q8>(in.k[u][j].z, in.k[u][j].w);
+        k[2 * j] = widen8<Q8>(in.k[u][j].x, in.k[u][j].y);
+        k[2 * j + 1] = widen8<Q8>(in.k[u][j].z, in.k[u][j].w);
       }
+      if constexpr (kAhead) {
+#pragma unroll
+        for (int x = 0; x < RT; ++x) products[x][u] = f32x4{};
+#pragma unroll
+        for (int j = 0; j < 2 * kKeyLoads; ++j)
+#pragma unroll
+          for (int x = 0; x < RT; ++x) products[x][u] = mfma16(k[j], s_q[x * kQ + j][lane], products[x][u]);
+        __builtin_amdgcn_sched_barrier(0);         // the widened keys' registers are free from here
+      }
+    }
     // loads into the registers that are free now, and the slots of the tile after that
     {
       const uint32_t slot = slot_at(tile + kTreeWaves, next);
@@ -282,7 +319,18 @@ __global__ __launch_bounds__(kTreeWaves * kWave, tree_waves(D, RT)) void k_tree_
     for (int u = 0; u < 2; ++u) {
       scale[u] = lds_get<f32x4>(lds_address(mine_lds.scale) + (8 * quad + 4 * u) * 4);
       shift[u] = lds_get<f32x4>(lds_address(mine_lds.shift) + (8 * quad + 4 * u) * 4);
-      inverse[u] = lds_get<f32x4>(lds_address(mine_lds.inverse) + (8 * quad + 4 * u) * 4);
+      if constexpr (!kAhead) inverse[u] = lds_get<f32x4>(lds_address(mine_lds.inverse) + (8 * quad + 4 * u) * 4);
+    }
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int x = 0; x < RT; ++x)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) products[x][u][r] = __builtin_fmaf(products[x][u][r], scale[u][r], shift[u][r]);
+      __builtin_amdgcn_sched_barrier(0);           // and the factors'
+#pragma unroll
+      for (int u = 0; u < 2; ++u) inverse[u] = lds_get<f32x4>(lds_address(mine_lds.inverse) + (8 * quad + 4 * u) * 4);
     }
     i32x2 v8[D / 16];                            // on their way during the first product
 #pragma unroll
@@ -305,10 +353,14 @@ __global__ __launch_bounds__(kTreeWaves * kWave, tree_waves(D, RT)) void k_tree_
       float top = -__builtin_inff();
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
+        if constexpr (kAhead) {
+          T[u] = products[x][u];
+        } else {
 #pragma unroll
-        for (int j = 0; j < 2 * kKeyLoads; ++j) T[u] = mfma16(kw[u][j], q[x][j], T[u]);
+          for (int j = 0; j < 2 * kKeyLoads; ++j) T[u] = mfma16(kw[u][j], q[x][j], T[u]);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) T[u][r] = __builtin_fmaf(T[u][r], scale[u][r], shift[u][r]);
+          for (int r = 0; r < 4; ++r) T[u][r] = __builtin_fmaf(T[u][r], scale[u][r], shift[u][r]);
+        }
       }
       if (drafted) {
         const uint32_t mine = (uint32_t)(sees[x] >> (32 * ((tile - a.history_tiles) & 1))) >> (8 * quad);
@@ -347,9 +399,12 @@ __global__ __launch_bounds__(kTreeWaves * kWave, tree_waves(D, RT)) void k_tree_
       if (any_wide) {                            // w / |vs| may vanish
         float more = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (T[e / 4][e % 4] != -__builtin_inff())
-            more += __builtin_amdgcn_exp2f(T[e / 4][e % 4] - shift[e / 4][e % 4] - base[x]);
+        for (int u = 0; u < 2; ++u) {
+          const f32x4 of_scale = kAhead ? lds_get<f32x4>(lds_address(mine_lds.shift) + (8 * quad + 4 * u) * 4) : shift[u];
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (T[u][r] != -__builtin_inff()) more += __builtin_amdgcn_exp2f(T[u][r] - of_scale[r] - base[x]);
+        }
         plus = wide >> x & 1u ? more : plus;
         asm volatile("" : "+v"(plus));           // a branch, not a selection
       }
@@ -436,11 +491,12 @@ __global__ __launch_bounds__(kTreeWaves * kWave, tree_waves(D, RT)) void k_tree_
 // unit full of them; the join takes 7 and its traffic.
 // Measured, with the join, us, rows of a workgroup 16, 32, 48, 64:
 //   32 sets x 732 rows x 2 KV heads of 64, 4061 tokens, fp16, one split: 188 155 144 137; two: 189 173 149 149
-//   16 sets x 64 rows x 8 KV heads of 128, 2064 tokens, bf16, one split: 46 36 44 55; two: 50 58 55 41
-//   32 sets x 128 rows x 8 KV heads of 128, 1040 tokens, bf16, one split: 84 78 78 68; two: 100 107 106 94
-//   1 set x 32 rows x 8 KV heads of 128, 4104 tokens, bf16, 1, 2, 4, 8 splits of 32 rows: 53 35 26 24
+//   16 sets x 64 rows x 8 KV heads of 128, 2064 tokens, bf16, one split: 45 32 44 61; two: 51 44 55 43
+//   32 sets x 128 rows x 8 KV heads of 128, 1040 tokens, bf16, one split: 84 69 79 66; two: 106 110 109 100
+//   1 set x 32 rows x 8 KV heads of 128, 4104 tokens, bf16, 1, 2, 4 splits of 32 rows: 46 32 25
+//   1 set x 512 rows x 1 KV head of 128, 2064 tokens, fp16, one split: 29 29 45 63; four: 21 21 25 31
 AttendPlan plan_tree_heads(int n_sets, int tiles, int rows, int kv_heads, int head_dim) {
-  static constexpr double kTileUs[2][4] = {{1.1, 1.25, 1.75, 2.3}, {1.3, 1.0, 1.5, 2.2}};   // heads of 64, of 128
+  static constexpr double kTileUs[2][4] = {{1.1, 1.25, 1.75, 2.3}, {1.6, 2.1, 1.9, 2.7}};   // heads of 64, of 128
   constexpr double kStartUs = 10.0;
   AttendPlan best{};
   const int of_head = rows / kv_heads;
@@ -448,12 +504,12 @@ AttendPlan plan_tree_heads(int n_sets, int tiles, int rows, int kv_heads, int he
   for (int groups = 1; groups <= 4; ++groups) {
     if (groups > 1 && of_head <= 16 * (groups - 1)) break;         // a group without rows
     const int head_blocks = kv_heads * ((of_head + 16 * groups - 1) / (16 * groups));
-    const int waves = tree_waves(head_dim, groups);
-    for (int want = 1; want <= std::max(1, std::min(tiles / kTreeWaves, 64)); ++want) {
+    const int waves = tree_waves(head_dim, groups), group = tree_group(head_dim, groups);
+    for (int want = 1; want <= std::max(1, std::min(tiles / group, 64)); ++want) {
       const int per = (tiles + want - 1) / want, splits = (tiles + per - 1) / per;
       if (splits != want) continue;                                // the same split as a smaller one
-      const double rounds = std::max(1.0, (double)n_sets * head_blocks * splits / (256.0 * waves));   // of full units
-      double cost = rounds * (kStartUs + std::ceil((double)per / kTreeWaves) * kTileUs[head_dim / 128][groups - 1]);
+      const double rounds = std::max(1.0, (double)n_sets * head_blocks * splits / (256.0 * waves * 4 / group));   // of full units
+      double cost = rounds * (kStartUs + std::ceil((double)per / group) * kTileUs[head_dim / 128][groups - 1]);
       if (splits > 1) cost += 7 + (double)n_sets * rows * splits * head_dim * 2e-6;
       if (best.splits == 0 || cost < best_cost) {
         best_cost = cost;
@@ -466,7 +522,7 @@ AttendPlan plan_tree_heads(int n_sets, int tiles, int rows, int kv_heads, int he
 
 template <typename Q8, int D, int RT>
 static hipError_t launch_groups(const GroupDev& g, const AttendDev& a, int n_sets, hipStream_t s) {
-  k_tree_heads<Q8, D, RT><<<n_sets * a.head_blocks * a.splits, kTreeWaves * kWave, 0, s>>>(g, a);
+  k_tree_heads<Q8, D, RT><<<n_sets * a.head_blocks * a.splits, tree_group(D, RT) * kWave, 0, s>>>(g, a);
   return hipGetLastError();
 }
 

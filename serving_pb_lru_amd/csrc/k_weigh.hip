@@ -317,9 +317,9 @@ __global__ __launch_bounds__(kWeighHeadWaves * kWave) void k_weigh_heads(GroupDe
   auto load = [&](int kvh) {
 #pragma unroll
     for (int x = 0; x < TT; ++x) {
-      const uint8_t* p = row[x] + (kvh * block + (tok[x] & (block - 1))) * D + quad * (D / 4);
+      const uint8_t* p = row[x] + (kvh * block + (tok[x] & (block - 1))) * D + quad * 16;
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) code[x][j] = *reinterpret_cast<const vec4u*>(p + 16 * j);
+      for (int j = 0; j < kLoads; ++j) code[x][j] = *reinterpret_cast<const vec4u*>(p + 64 * j);
       ks[x] = *reinterpret_cast<const float*>(row[x] + scale_at + 4 * kvh);
     }
   };
@@ -334,9 +334,12 @@ __global__ __launch_bounds__(kWeighHeadWaves * kWave) void k_weigh_heads(GroupDe
     const int node = (int)a.by_heads.div(hi), head = (there ? kvh * per : 0) + hi - node * per;
     const float lse = a.lse[(size_t)set * a.rows + node * (a.rows / a.nodes) + head];
     const uint16_t* p = static_cast<const uint16_t*>(a.q) + set * a.q_set_stride + node * a.q_node_stride +
-                        head * a.q_head_stride + quad * (D / 4);
+                        head * a.q_head_stride + quad * 16;
 #pragma unroll
-    for (int j = 0; j < 2 * kLoads; ++j) to.q[j] = a.q_aligned ? load8<Q8, true>(p + 8 * j) : load8<Q8, false>(p + 8 * j);
+    for (int j = 0; j < 2 * kLoads; ++j) {
+      const uint16_t* at = p + 64 * (j / 2) + 8 * (j % 2);
+      to.q[j] = a.q_aligned ? load8<Q8, true>(at) : load8<Q8, false>(at);
+    }
     to.lse = there ? lse : __builtin_inff();
   };
   load(0);
