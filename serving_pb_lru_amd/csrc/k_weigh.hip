@@ -126,29 +126,38 @@ __global__ __launch_bounds__(kWeighWaves * kWave, 2) void k_weigh_latent(GroupDe
     for (int b = 0; b < kLatentGroups; ++b) load_block(row, b);
     load_rest(row);
     if (row0) __syncthreads();                         // the chunk before it is done with
-    // q of this chunk into LDS, eight channels a thread at a time
-    constexpr int kPieces = (kLatent + kRope) / 8;
-    for (int e = threadIdx.x; e < kRows * kPieces; e += kWeighWaves * kWave) {
-      const int r = e / kPieces, c = e % kPieces;
-      Q8 v{};
+    // q of this chunk into LDS, eight channels a thread at a time, all of them and the rows' log-sums on their way
+    // together: a row that is not there stands for the set's first
+    constexpr int kPieces = (kLatent + kRope) / 8, kEach = (kRows * kPieces + kWeighWaves * kWave - 1) / (kWeighWaves * kWave);
+    Q8 v[kEach];
+    float of_row[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int e = i * kWeighWaves * kWave + threadIdx.x, r = e / kPieces, c = e % kPieces;
+      const int row = row0 + r < a.rows ? row0 + r : 0;
+      const int node = (int)a.by_heads.div(row), head = row - node * (int)a.by_heads.d;
+      const uint16_t* p = static_cast<const uint16_t*>(a.q) + set * a.q_set_stride + node * a.q_node_stride +
+                          head * a.q_head_stride + 8 * c;
+      of_row[i] = a.lse[(size_t)set * a.rows + row];
+      v[i] = a.q_aligned ? load8<Q8, true>(p) : load8<Q8, false>(p);
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int e = i * kWeighWaves * kWave + threadIdx.x, r = e / kPieces, c = e % kPieces;
+      if (r >= kRows) break;
       // a row that counts for nothing may hold anything
-      if (row0 + r < a.rows && counts(a.lse[(size_t)set * a.rows + row0 + r])) {
-        const int node = (int)a.by_heads.div(row0 + r), head = row0 + r - node * (int)a.by_heads.d;
-        const uint16_t* p = static_cast<const uint16_t*>(a.q) + set * a.q_set_stride + node * a.q_node_stride +
-                            head * a.q_head_stride + 8 * c;
-        v = a.q_aligned ? load8<Q8, true>(p) : load8<Q8, false>(p);
-      }
+      if (row0 + r >= a.rows || !counts(of_row[i])) v[i] = Q8{};
       uint8_t* at = s.q + r * Lds::kRowBytes + 16 * c;
       if (Lds::kRopeParts == 1 || c < kLatent / 8) {
-        *reinterpret_cast<Q8*>(at) = v;
+        *reinterpret_cast<Q8*>(at) = v[i];
       } else {
         bf16x8 hi, lo;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int x = 0; x < 8; ++x) {
           __bf16 top, rest;
-          two_parts((_Float16)(float)v[i], top, rest);
-          hi[i] = top;
-          lo[i] = rest;
+          two_parts((_Float16)(float)v[i][x], top, rest);
+          hi[x] = top;
+          lo[x] = rest;
         }
         *reinterpret_cast<bf16x8*>(at) = hi;
         *reinterpret_cast<bf16x8*>(at + 2 * kRope) = lo;
