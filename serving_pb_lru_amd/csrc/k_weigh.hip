@@ -92,13 +92,18 @@ __global__ __launch_bounds__(kWeighWaves * kWave, 2) void k_weigh_latent(GroupDe
   // compiler knows how many are in flight behind the ones it waits for: a key that is not there looks entry 0 up
   // and reads zeros.
   auto key_of = [&](int group) { return (group0 + group) * kWeighGroup + wave * kWeighKeys + col; };
-  auto entry_of = [&](int group) { return group < groups && key_of(group) < a.k ? set * a.k + key_of(group) : -1; };
-  auto look = [&](int group) -> Lookup {
-    const int r = max(entry_of(group), 0);
+  // step: a chunk of rows' key group; chunks follow each other without a pause
+  const int steps = (a.rows + kRows - 1) / kRows * groups;
+  auto entry_of = [&](int step) {
+    const int key = key_of(step % groups);
+    return step < steps && key < a.k ? set * a.k + key : -1;
+  };
+  auto look = [&](int step) -> Lookup {
+    const int r = max(entry_of(step), 0);
     return {g.res[r], a.sel[r]};                      // res has room for every selection of the engine
   };
-  auto row_at = [&](int group, Lookup at) -> const uint8_t* {
-    const int r = entry_of(group);
+  auto row_at = [&](int step, Lookup at) -> const uint8_t* {
+    const int r = entry_of(step);
     if (r < 0) at.la = -1;
     if (r >= a.n_res) at.res = make_uint2(kAbsent, kAbsent);
     const uint32_t slot = slot_of(g, at, a.n_res, err);
@@ -117,14 +122,15 @@ __global__ __launch_bounds__(kWeighWaves * kWave, 2) void k_weigh_latent(GroupDe
     scale = *reinterpret_cast<const f32x4*>(row + kLatentScaleAt);
   };
 
-  for (int row0 = 0; row0 < a.rows; row0 += kRows) {
-    const Lookup first = look(0);
-    Lookup ahead = look(1);
-    const uint8_t* row = row_at(0, first);
-    int32_t address = first.la;                        // of the row, where there is one
+  const Lookup first = look(0);
+  Lookup ahead = look(1);
+  const uint8_t* row = row_at(0, first);
+  int32_t address = first.la;                          // of the row, where there is one
 #pragma unroll
-    for (int b = 0; b < kLatentGroups; ++b) load_block(row, b);
-    load_rest(row);
+  for (int b = 0; b < kLatentGroups; ++b) load_block(row, b);
+  load_rest(row);
+  int step = 0;
+  for (int row0 = 0; row0 < a.rows; row0 += kRows) {
     if (row0) __syncthreads();                         // the chunk before it is done with
     // q of this chunk into LDS, eight channels a thread at a time, all of them and the rows' log-sums on their way
     // together: a row that is not there stands for the set's first
@@ -171,11 +177,11 @@ __global__ __launch_bounds__(kWeighWaves * kWave, 2) void k_weigh_latent(GroupDe
     __syncthreads();
     if (!s.ok) return;
 
-    for (int group = 0; group < groups; ++group) {
+    for (int group = 0; group < groups; ++group, ++step) {
       const bool live = row != g_no_row;
-      const uint8_t* next = row_at(group + 1, ahead);
+      const uint8_t* next = row_at(step + 1, ahead);
       const int32_t next_address = ahead.la;
-      ahead = look(group + 2);
+      ahead = look(step + 2);
       // this lane's row of q: pieces of 16 channels, and of 8 rotary ones; the rest are instruction offsets
       const uint32_t qx = opaque(lds_address(s.q) + col * Lds::kRowBytes + half * 32);
       const uint32_t qr = opaque(lds_address(s.q) + col * Lds::kRowBytes + half * 16);
