@@ -47,12 +47,13 @@ __device__ __forceinline__ bool counts(float lse) { return fabsf(lse) < __builti
 // registers as they are until a block of 128 channels is widened for both 32-row
 // products; a block's registers then take the next key group's.
 // Bound by the lines that a compute unit can have outstanding: 256 sets x 2048 keys x 64
-// heads take 95 us, in which the units ask for 530 MB (344 MB of rows, whose ends share
-// lines) and wait 860 cycles for each line, 61 of them on their way at a time. (240 us with
-// branches around the loads, whose waits were for all of them; 125 us with 16 x 16
-// products, 64 bytes of a row at a time, and spilled registers; tiles of whole rows in LDS,
-// five of them on their way, that all waves share, 16 rows of q each: the same time, and 95 us
-// against 88 where rows lie one after the other, 641 against 387 for 61 sets x 1728 rows x 1023 keys.)
+// heads take 90 us, in which the units ask for 530 MB (344 MB of rows, whose ends share
+// lines) and wait about 860 cycles for each line. (240 us a call with branches around the loads, whose
+// waits were for all of them, where this takes 104 us a call; 125 us with 16 x 16 products, 64 bytes
+// of a row at a time, and spilled registers; 109 us with rows of q asked for once their log-sum was
+// known; 108 us with tiles of whole rows in LDS, five of them on their way, that all waves share.
+// Of 1024 query rows: 16 sets x 2048 keys 99 us a call, 127 us with a pause in the keys' loads
+// between chunks of rows, 144 us with tiles in LDS.)
 constexpr int kWeighWaves = 8;
 constexpr int kWeighKeys = 32;                       // of a wave
 constexpr int kWeighGroup = kWeighWaves * kWeighKeys;
