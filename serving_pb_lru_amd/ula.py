@@ -214,14 +214,17 @@ def _check(rc: int, where: str) -> None:
         raise UlaError(rc, where, lib().ula_strerror(rc).decode())
 
 
+_DTYPES = {x: f"torch.{x}" for x in ("uint8", "int32", "int64", "float32")}
+
+
 def _dev(t, dtype: str, count: int, what: str) -> int:
     """Device pointer of a contiguous CUDA tensor of `dtype` holding at least
     `count` elements; raises ValueError otherwise (the library takes plain
     pointers and would read or write past a smaller buffer)."""
-    if not (hasattr(t, "is_cuda") and t.is_cuda):
+    if not getattr(t, "is_cuda", False):
         raise ValueError(f"{what}: a CUDA tensor is required")
-    if str(t.dtype) != f"torch.{dtype}":
-        raise ValueError(f"{what}: dtype {t.dtype}, expected torch.{dtype}")
+    if str(t.dtype) != _DTYPES[dtype]:
+        raise ValueError(f"{what}: dtype {t.dtype}, expected {_DTYPES[dtype]}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: the tensor must be contiguous")
     if t.numel() < count:
@@ -263,19 +266,17 @@ _TYPES = {"torch.bfloat16": BF16, "torch.float16": FP16, "torch.float32": FP32}
 def _tensor(t, shape, what: str, types=(BF16, FP16, FP32)):
     """(pointer, type code, strides) of a CUDA tensor of the given shape (None: any size)
     whose last dimension is contiguous."""
-    if not (hasattr(t, "is_cuda") and t.is_cuda):
+    if not getattr(t, "is_cuda", False):
         raise ValueError(f"{what}: a CUDA tensor is required")
     code = _TYPES.get(str(t.dtype))
     if code not in types:
         raise ValueError(f"{what}: dtype {t.dtype} is not supported")
     real, strides = t.shape, t.stride()
-    same = len(real) == len(shape)
-    if same:
-        for n, m in zip(shape, real):
-            if n is not None and n != m:
-                same = False
-    if not same:
+    if len(real) != len(shape):
         raise ValueError(f"{what}: shape {tuple(real)}, expected {tuple(shape)} (None: any)")
+    for n, m in zip(shape, real):
+        if n is not None and n != m:
+            raise ValueError(f"{what}: shape {tuple(real)}, expected {tuple(shape)} (None: any)")
     if strides[-1] != 1 and real[-1] > 1 and t.numel():
         raise ValueError(f"{what}: the last dimension must be contiguous")
     return t.data_ptr(), code, strides
@@ -295,9 +296,10 @@ def _host_ints(x, what: str) -> np.ndarray:
 
 
 def _same_device(first, *others) -> None:
+    device = first.device
     for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}")
 
 
 def _no_gradient(what: str, *tensors) -> None:
@@ -322,7 +324,7 @@ class _On:
             raise ValueError(f"tensors on {device}, a stream of {stream.device}")
         # the handle alone: a decode step's call is bound by the host, and a Stream object costs 2 us
         current = torch._C._cuda_getCurrentRawStream(device.index)
-        here = torch.cuda.current_device() == device.index
+        here = torch._C._cuda_getDevice() == device.index
         self.handle = current if stream is None else _stream(stream)
         self.ctx = None
         if not here or self.handle != current:
@@ -359,16 +361,14 @@ def _rotary(positions, sections, theta, interleaved, pairs: int, lead, what: str
         return None, None, r
     if positions.dim() == len(lead):
         positions = positions.unsqueeze(-1)
-    axes = positions.shape[-1]
-    if tuple(positions.shape) != (*lead, axes) or not 1 <= axes <= 3:
-        raise ValueError(f"{what} positions: shape {tuple(positions.shape)}, expected {tuple(lead)} and 1 to 3 axes")
+    shape = tuple(positions.shape)
+    axes = shape[-1]
+    if shape[:-1] != lead or not 1 <= axes <= 3:
+        raise ValueError(f"{what} positions: shape {shape}, expected {tuple(lead)} and 1 to 3 axes")
     sections = (pairs,) if sections is None and axes == 1 else sections
     if sections is None or len(sections) != axes:
         raise ValueError(f"{what}: one section for each of the {axes} axes is required")
-    n = 1
-    for x in positions.shape:
-        n *= x
-    ptr = _dev(positions, "int32", n, f"{what} positions")
+    ptr = _dev(positions, "int32", 0, f"{what} positions")   # of that shape: no fewer elements
     r.axes, r.interleaved, r.theta = axes, int(bool(interleaved)), float(theta)
     for i, s in enumerate(sections):
         r.sections[i] = int(s)
