@@ -490,9 +490,9 @@ __global__ __launch_bounds__(tree_group(D, RT) * kWave, tree_waves(D, RT)) void 
 // start and end, and for each of a wave's tiles the time in the table, that of a compute
 // unit full of them; the join takes 7 and its traffic.
 // Measured, with the join, us, rows of a workgroup 16, 32, 48, 64:
-//   32 sets x 732 rows x 2 KV heads of 64, 4061 tokens, fp16, one split: 188 155 144 137; two: 189 173 149 149
-//   16 sets x 64 rows x 8 KV heads of 128, 2064 tokens, bf16, one split: 45 32 44 61; two: 51 44 55 43
-//   32 sets x 128 rows x 8 KV heads of 128, 1040 tokens, bf16, one split: 84 69 79 66; two: 106 110 109 100
+//   32 sets x 732 rows x 2 KV heads of 64, 4061 tokens, fp16, one split: 175 162 133 131; two: 180 180 148 139
+//   16 sets x 64 rows x 8 KV heads of 128, 2064 tokens, bf16, one split: 45 33 45 54; two: 52 44 55 41
+//   32 sets x 128 rows x 8 KV heads of 128, 1040 tokens, bf16, one split: 83 70 77 66; two: 106 109 106 92
 //   1 set x 32 rows x 8 KV heads of 128, 4104 tokens, bf16, 1, 2, 4 splits of 32 rows: 46 32 25
 //   1 set x 512 rows x 1 KV head of 128, 2064 tokens, fp16, one split: 29 29 45 63; four: 21 21 25 31
 AttendPlan plan_tree_heads(int n_sets, int tiles, int rows, int kv_heads, int head_dim) {
