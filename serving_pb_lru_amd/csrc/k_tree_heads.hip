@@ -17,18 +17,19 @@
 // fill 57% of a SIMD's cycles and matrix instructions 22%.) m follows the largest w as
 // there: it moves, to leave the largest at 2^8, when one could pass 2^15, which each lane
 // tells from its own tokens. A negative vs turns the signs of its codes; one below 2^-80
-// makes them 0 (so l, which adds up to 2^95 for a token then, stays finite); from the first beyond 2^40 either way on, l adds up powers of its own
-// (w / |vs| would vanish beside a token of large scale); one that is not finite, or a NaN code in a drafted token's values, makes
-// T NaN, which a node that does not see the token replaces with its mask.
+// makes them 0 (so l, which adds up to 2^95 for a token then, stays finite); from the first
+// beyond 2^40 either way on, l adds up powers of its own (w / |vs| would vanish beside a
+// token of large scale); one that is not finite, or a NaN code in a drafted token's values,
+// makes T NaN, which a node that does not see the token replaces with its mask.
 //
 // A workgroup is one KV head's RT x 16 query rows (of nodes and heads) and one range of
 // tokens; its four or eight waves take every fourth or eighth tile of 32 tokens, each by
 // itself as there, and join their results in LDS. So a set's tokens are split over fewer
 // workgroups, whose parts go through memory, than over waves. With up to 32 rows q is in
-// LDS, and a tile's products with all of them come first, a half of the keys at a time: so two
-// waves of 32 rows and heads of 128 fit a SIMD (one with q in registers: 36 us for the second of the
-// two above). With more rows q stays in registers, which leaves fewer accumulators waiting
-// (the first of the two: 130 us so, 132 us with q in LDS).
+// LDS, and a tile's products with all of them come first, a half of the keys at a time:
+// so two waves of 32 rows and heads of 128 fit a SIMD (one with q in registers: 36 us for
+// the second of the two above). With more rows q stays in registers, which leaves fewer
+// accumulators waiting (the first of the two: 130 us so, 132 us with q in LDS).
 #include <algorithm>
 #include <cmath>
 
