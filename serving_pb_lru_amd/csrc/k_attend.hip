@@ -37,8 +37,8 @@
 // Q, a key is widened for all of a wave's heads at once and every value once. In
 // between p goes through LDS in the operand order of the second product, scaled for
 // each block (fp16 queries and trees: in 32 bits, scaled, and split, by the second waves).
-// The two waves of a head tell each other their largest logits through LDS as well, a barrier ahead of the softmax, and so come to the
-// same m. Each SIMD has a wave of either kind. One barrier per tile.
+// The two waves of a head tell each other their largest logits through LDS as well, a
+// barrier ahead of the softmax, and so come to the same m. Each SIMD has a wave of either kind. One barrier per tile.
 // Measured, 256 sets of 2048 keys and 64 heads: 206 us with a wave that kept 32
 // heads to itself for both products, reading and widening every key and value
 // four times; 128 us with eight equal waves that went through first product,
