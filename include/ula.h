@@ -558,8 +558,9 @@ size_t ula_attend_tree_bytes(const ula_row_format* rows, int32_t n_sets, int32_t
  * rows: a scale) that is not finite, makes the heads that see it NaN, log-sums too (heads
  * rows: so does a value scale of a selected entry). Heads rows' value scales below 2^-80
  * count as 0, and the largest product of weight and scale is that of the scales as they
- * are. The rest (formula, rounding, order of the sums, which entries, streams, errors) is
- * as for ula_attend; drafts and visible may be read until the stream has run the call.
+ * are. Softmax weights times value scales go through in two fp16 parts for bf16 results
+ * too (2^-22 of each, or 2^-32 of the set's largest). The rest (formula, other roundings,
+ * order of the sums, which entries, streams, errors) is as for ula_attend; drafts and visible may be read until the stream has run the call.
  * Host errors: also ULA_EINVAL
  * for nodes outside 1..64, null or misaligned drafts (16 bytes) or visible (8 bytes), rows
  * of out that share elements (each stride is looked at), n_sets * nodes * heads >= 2^24

@@ -26,7 +26,9 @@
 //     (1.68e-3 of their size off, 1.66e-3 without). fp16 results would: for them
 //     what it leaves goes through a second product with the same values (2.07e-4
 //     off, as a result of 64 bits rounded once, 2.9e-4 without; 384 sets of 2047 keys
-//     and 128 heads 368 us, 300 us without).
+//     and 128 heads 368 us, 300 us without). A tree's results of either type go that
+//     way: bf16 ones were 1e-3 of their size from those of weights in 32 bits, 6e-5 so
+//     (16 sets x 8 nodes x 2048 keys x 128 heads 123 us, 101 us without).
 // Both products have 32-bit accumulators.
 //
 // Layout. Both products are taken transposed: S^T = K Q^T puts heads in the
@@ -55,10 +57,9 @@
 // and widen keys twice as often: 159 us.
 // A tree of drafted tokens (TREE) has nodes x heads rows where the heads are, and two
 // tiles of keys at most behind the selected ones, whose rows come from the caller and
-// which a row sees by its node's mask. 64 sets x 1024 rows x 2048 keys, bf16: 360 us, of which each
+// which a row sees by its node's mask. 64 sets x 1024 rows x 2048 keys, bf16: 474 us, of which each
 // of four rounds of workgroups spends 15 us on its start (5 us for 19 MB of q), the filling
-// of the pipeline and its end; the rest are the first waves' instructions, an
-// instruction every 6 cycles or so.
+// of the pipeline and its end.
 // Tiles: the first 640 bytes of each row as 16-byte pieces straight into LDS (no
 // registers), the scales transposed to [block][key]. Piece c of key j lies at
 // c ^ swizzle(j), which keeps the 16 lanes that a 16-byte read serves at once
@@ -136,16 +137,10 @@ constexpr int kSecondWaves = kWaves - kFirstWaves;
 constexpr int kLoadsPerWave = (kTileLoads + kLatentGroups) / kSecondWaves;   // a second wave's vector loads per tile
 static_assert(kSecondWaves == kLatentGroups, "one scale block per second wave");
 
-// fp16 results: p x scale in two parts.
-template <typename Q8>
-constexpr bool kTwoParts = !std::is_same_v<Q8, bf16x8>;
-
-// The second waves make p x scale of p in 32 bits, or the first waves do. With two parts the second waves'; a
-// tree's many rows leave them waiting for the first waves, which issue an instruction every 6 cycles and nothing else (64
-// sets x 1024 rows x 2048 keys: 415 us so, 378 when the second waves do it). Few rows to a key wait for the keys,
-// and the second waves for the sake of their loads: 256 sets x 64 heads x 2048 keys 121 us so, 125 when they do it.
+// fp16 results, and a tree's: p x scale in two parts, which the second waves make of p in 32 bits. (Else the first waves
+// make it: 256 sets x 64 heads x 2048 keys 121 us so, 125 when the second waves do it.)
 template <typename Q8, bool TREE>
-constexpr bool kWholeP = kTwoParts<Q8> || TREE;
+constexpr bool kTwoParts = TREE || !std::is_same_v<Q8, bf16x8>;
 
 // Keys that a work item takes: a tree's drafted tokens come on top of a whole selection.
 template <bool TREE>
@@ -156,7 +151,7 @@ struct LatentLds {
   static constexpr int HEADS = 32 * HT;
   alignas(1024) uint8_t ring[TILES][kTileBytes];
   // bytes of a key's p: one in 32 bits, or one for each block in 16
-  static constexpr int kKeyBytes = kWholeP<Q8, TREE> ? 4 : 2 * kLatentGroups;
+  static constexpr int kKeyBytes = kTwoParts<Q8, TREE> ? 4 : 2 * kLatentGroups;
   // p of two tiles. In 16 bits: p x scale, [block][head][key], key chunk c (8 keys) of head h at
   // c ^ ((h >> 2) & 3). In 32: p, [head][key], key chunk c (4 keys) of head h at c ^ ((h >> 1) & 7).
   alignas(1024) uint8_t p[2][HEADS * kTileKeys * kKeyBytes];
@@ -280,7 +275,7 @@ __device__ __forceinline__ void store_heads(uint8_t* box, const f32x16 (&o)[CT][
 template <typename Q8, int HT, int TILES, bool TREE>
 __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g, AttendDev a) {
   constexpr int kHeads = 32 * HT;                 // heads of a workgroup
-  constexpr bool kTwo = kTwoParts<Q8>, kWhole = kWholeP<Q8, TREE>;
+  constexpr bool kTwo = kTwoParts<Q8, TREE>;
   constexpr int CT = kScaleGroup / 32;            // 32-channel tiles of a second wave's O
   static_assert(2 * kHeads == 16 * HT * kFirstWaves, "every head has two waves in the first product");
   static_assert(TILES >= 4, "a tile on its way beside the three in use");
@@ -421,7 +416,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
     static_assert(kLatentScaleAt % 128 == 0 && kTileBytes % 128 == 0, "the swizzle's bits are free in every row address");
     // this lane's chunk of head col32: keys 8 half .. of a tile's first 16
     const uint32_t pread = lds_address(s.p) +
-                           (kWhole ? col32 * kTileKeys * 4 + ((2 * half ^ ((col32 >> 1) & 7)) << 4)
+                           (kTwo ? col32 * kTileKeys * 4 + ((2 * half ^ ((col32 >> 1) & 7)) << 4)
                                    : (sw * kHeads + col32) * kTileKeys * 2 + ((half ^ ((col32 >> 2) & 3)) << 4));
     float minus = -1.0f;                          // one the compiler does not know: a fused step takes it, a difference two
     asm volatile("" : "+s"(minus));
@@ -455,7 +450,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
       for (int h = 0; h < HT; ++h)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          if constexpr (kWhole) {
+          if constexpr (kTwo) {
             const uint32_t scale = lds_address(s.scale) + ((tile % TILES * kLatentGroups + sw) * kTileKeys + 16 * x + 8 * half) * 4;
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
@@ -465,13 +460,11 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
               for (int e = 0; e < 4; e += 2) {
                 // (the empty assembly keeps the product and its rounding one step each for both uses)
                 f32x2 v = {w[e] * sc[e], w[e + 1] * sc[e + 1]};
-                if constexpr (kTwo) asm("" : "+v"(v));
+                asm("" : "+v"(v));
                 f16x2 hi = __builtin_convertvector(v, f16x2);
-                if constexpr (kTwo) {
-                  asm("" : "+v"(hi));
-                  rest[h][x][4 * y + e] = (_Float16)__builtin_fmaf((float)hi.x, minus, v.x);
-                  rest[h][x][4 * y + e + 1] = (_Float16)__builtin_fmaf((float)hi.y, minus, v.y);
-                }
+                asm("" : "+v"(hi));
+                rest[h][x][4 * y + e] = (_Float16)__builtin_fmaf((float)hi.x, minus, v.x);
+                rest[h][x][4 * y + e + 1] = (_Float16)__builtin_fmaf((float)hi.y, minus, v.y);
                 p[h][x][4 * y + e] = hi.x;
                 p[h][x][4 * y + e + 1] = hi.y;
               }
@@ -548,7 +541,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
     const int koff = key * kLatentScaleAt + ((quad ^ swizzle(key)) << 4);
     const int head = head0 + col;
     const uint32_t pwrite = lds_address(s.p) +
-                            (kWhole ? head * kTileKeys * 4 + (((2 * quad + key_half) ^ ((head >> 1) & 7)) << 4)
+                            (kTwo ? head * kTileKeys * 4 + (((2 * quad + key_half) ^ ((head >> 1) & 7)) << 4)
                                     : head * kTileKeys * 2 + ((quad ^ ((head >> 2) & 3)) << 4) + 8 * key_half);
     const uint32_t at_top = lds_address(s.top) + head * 8;
     f32x4 sc[kLatentGroups], S[HT];                // of the next tile for the softmax: scales, logits in powers of two
@@ -653,8 +646,8 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
           p[r] = __builtin_amdgcn_exp2f(S[i][r] - base);
           l[i] += p[r];
         }
-        const uint32_t pw = opaque(pwrite + buf * (uint32_t)sizeof(s.p[0]) + 16 * i * kTileKeys * (kWhole ? 4 : 2));
-        if constexpr (kWhole) {
+        const uint32_t pw = opaque(pwrite + buf * (uint32_t)sizeof(s.p[0]) + 16 * i * kTileKeys * (kTwo ? 4 : 2));
+        if constexpr (kTwo) {
           lds_put(pw, p);
         } else {
 #pragma unroll
@@ -885,9 +878,11 @@ AttendPlan plan_attend_latent(int n_sets, int k, int heads) {
 
 // The same for a tree, where sets that fill the compute units evenly stay whole and the
 // others are split, so that the last round of workgroups is a short one and the join
-// has the rest alone. A tile takes 1.25 us here (64 rows; 0.9 for 32), a start and end 15.
-// Measured, all sets the same way and so, us: 24 sets x 1024 rows x 2048 keys 182, 157;
-// 33 x 1024 x 1024 157, 131; 70 x 256 x 1024 107, 83.
+// has the rest alone. A tile is taken for 1.25 us here (64 rows; 0.9 for 32), a start and end
+// for 15; with 1.6 and 1.1, which a tile with weights in two parts is nearer to, 18 calls of
+// 1 to 257 sets took the same time to 2% but for 4 sets x 128 rows x 256 keys (22.3 us so, 23.5).
+// Measured, weights in one part, all sets the same way and so, us: 24 sets x 1024 rows x
+// 2048 keys 182, 157; 33 x 1024 x 1024 157, 131; 70 x 256 x 1024 107, 83.
 AttendPlan plan_tree_latent(int n_sets, int tiles, int rows) {
   static_assert(kTileTokens == kTileKeys, "a tree's tiles are those of the kernel");
   AttendPlan best{};
