@@ -28,7 +28,7 @@
 //     off, as a result of 64 bits rounded once, 2.9e-4 without; 384 sets of 2047 keys
 //     and 128 heads 368 us, 300 us without). A tree's results of either type go that
 //     way: bf16 ones were 1e-3 of their size from those of weights in 32 bits, 6e-5 so
-//     (16 sets x 8 nodes x 2048 keys x 128 heads 123 us, 101 us without).
+//     (16 sets x 8 nodes x 2048 keys x 128 heads 125 us, 101 us without).
 // Both products have 32-bit accumulators.
 //
 // Layout. Both products are taken transposed: S^T = K Q^T puts heads in the
@@ -636,9 +636,9 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
         const float top = fmaxf(both[i].x, both[i].y);
         const bool move = top > m[i] + 15.0f;
         const float nm = move ? top - 8.0f : m[i];
-        const float al = move ? __builtin_amdgcn_exp2f(m[i] - nm) : 1.0f;
+        const float fall = move ? m[i] - nm : 0.0f, al = near_power(fall);
         m[i] = nm;
-        l[i] *= al;
+        l[i] = l[i] * far_power(fall) * al;       // (1% of the time; a branch around the far power costs as much)
         const float base = nm == -__builtin_inff() ? 0.0f : nm;
         f32x4 p;
 #pragma unroll

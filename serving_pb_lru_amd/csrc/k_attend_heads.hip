@@ -191,9 +191,9 @@ __global__ __launch_bounds__(kHeadWaves * kWave) void k_attend_heads(GroupDev g,
     if (__any(top > m + 15.0f)) {
       const bool move = top > m + 15.0f;
       const float nm = move ? top - 8.0f : m;
-      const float al = move ? __builtin_amdgcn_exp2f(m - nm) : 1.0f;
+      const float fall = move ? m - nm : 0.0f, al = near_power(fall);
       m = nm;
-      l *= al;
+      l = l * far_power(fall) * al;
 #pragma unroll
       for (int t = 0; t < D / 16; ++t) o[t] *= al;
     }

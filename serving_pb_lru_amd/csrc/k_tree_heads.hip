@@ -376,10 +376,10 @@ __global__ __launch_bounds__(tree_group(D, RT) * kWave, tree_waves(D, RT)) void 
         top = max_quads(top);
         const bool move = top > m[x] + 15.0f;
         const float nm = move ? top - 8.0f : m[x];
-        const float al = move ? __builtin_amdgcn_exp2f(m[x] - nm) : 1.0f;
+        const float fall = move ? m[x] - nm : 0.0f, al = near_power(fall);
         m[x] = nm;
         base[x] = nm == -__builtin_inff() ? 0.0f : nm;
-        l[x] *= al;
+        l[x] = l[x] * far_power(fall) * al;
 #pragma unroll
         for (int t = 0; t < D / 16; ++t) o[x][t] *= al;
       }

@@ -270,6 +270,12 @@ __device__ __forceinline__ float sum_quads(float x) {
   return sum_halves(v.x + v.y);
 }
 
+// 2^fall, fall <= 0, as two factors, for sums in units of a reference that has moved up by -fall. References follow
+// weight times value scale, so one may move by more than what 32 bits hold while the softmax weights summed so far
+// still count: their sum takes both, the far one first (1 for less than 126). Sums of weight times value vanish.
+__device__ __forceinline__ float near_power(float fall) { return __builtin_amdgcn_exp2f(fmaxf(fall, -126.0f)); }
+__device__ __forceinline__ float far_power(float fall) { return __builtin_amdgcn_exp2f(fall - fmaxf(fall, -126.0f)); }
+
 // Transposing LDS read: 16 lanes name 8 rows of 16 bytes (lane pair 2r, 2r + 1
 // the halves of row r); lane i receives byte i of rows 0..7.
 __device__ __forceinline__ i32x2 lds_read_transposed(uint32_t addr) {
