@@ -289,7 +289,7 @@ long long plan_norm(NormDev* a) {
   const int heads = a->q_heads + a->k_heads, step = kNormAhead * at_once;
   a->heads_per_block = heads;
   a->tokens_per_block = 0;
-  double best = 0;
+  double best = -1;                                    // a single token always has a plan
   for (int tokens = 1; tokens <= 16 && (tokens == 1 || a->n / tokens >= 1024); ++tokens) {
     const long long rows = (long long)tokens * heads;
     const double full = (double)rows / ((rows + step - 1) / step * step);
