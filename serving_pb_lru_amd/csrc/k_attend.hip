@@ -190,7 +190,6 @@ struct QueryOperand {
   static constexpr int kRopeParts = std::is_same_v<Q8, bf16x8> ? 1 : 2;
   Q8 x[kLatent / 32];
   bf16x8 rope[kRopeParts][kRope / 32];
-  template <bool TREE>
   __device__ __forceinline__ void take(const QueryRaw<Q8>& raw) {
 #pragma unroll
     for (int t = 0; t < kLatent / 32; ++t) x[t] = raw.x[t];
@@ -202,12 +201,7 @@ struct QueryOperand {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           __bf16 hi, lo;
-          if constexpr (TREE) {
-            two_parts(raw.rope[j][e], hi, lo);
-          } else {
-            hi = (__bf16)(float)raw.rope[j][e];
-            lo = (__bf16)((float)raw.rope[j][e] - (float)hi);
-          }
+          two_parts(raw.rope[j][e], hi, lo);
           rope[0][j][e] = hi;
           rope[1][j][e] = lo;
         }
@@ -530,7 +524,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend_latent(GroupDev g,
     QueryOperand<Q8> q[HT];
 #pragma unroll
     for (int i = 0; i < HT; ++i) {
-      q[i].template take<TREE>(raw[i]);
+      q[i].take(raw[i]);
       m[i] = -__builtin_inff();
       l[i] = 0.0f;
     }
