@@ -232,6 +232,14 @@ def _dev(t, dtype: str, count: int, what: str) -> int:
     return t.data_ptr()
 
 
+def _shaped(t, dtype: str, shape, what: str) -> int:
+    """_dev for a tensor of exactly this shape: another one would be read, or written, as something else."""
+    ptr = _dev(t, dtype, 0, what)
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return ptr
+
+
 def _sets(sel):
     """(n_sets, k) of a selection tensor [n_sets][k] or [k]."""
     return (1, sel.shape[0]) if sel.dim() == 1 else tuple(sel.shape)
@@ -531,13 +539,15 @@ def lightest(scores, first, last, n, most: Optional[int] = None, mark: bool = Fa
     args.first, args.last, args.count = first.ctypes.data, last.ctypes.data, n.ctypes.data
     args.most = (int(n.max()) if n.size else 0) if most is None else most
     args.mark = int(bool(mark))
+    if out is not None:
+        args.out = _shaped(out, "int32", (first.size, max(args.most, 0)), "lightest out")
     _same_device(scores, out)
     on = _On(scores.device, stream, scores, out)
     with on as s:
         if out is None:
             out = torch.empty((first.size, max(args.most, 0)), dtype=torch.int32, device=scores.device)
             on.give(out)
-        args.out = _dev(out, "int32", first.size * max(args.most, 0), "lightest out")
+            args.out = out.data_ptr()
         args.workspace_bytes = lib().ula_lightest_bytes(ctypes.byref(args))
         if args.workspace_bytes:
             work = torch.empty(args.workspace_bytes, dtype=torch.uint8, device=scores.device)
@@ -746,8 +756,10 @@ class Engine:
         nodes, heads = q.shape[1:3]
         q_ptr, code, st = _tensor(q, (n_sets, None, None, width), "ula_attend_tree q", (BF16, FP16))
         per_set = nodes if latent else -(-nodes // max(fmt.block_tokens, 1))
-        drafts_ptr = _dev(drafts, "uint8", n_sets * per_set * self.layers * self.row_bytes, "ula_attend_tree drafts")
-        visible_ptr = _dev(visible, "int64", n_sets * nodes, "ula_attend_tree visible")
+        drafts_ptr = _shaped(drafts, "uint8", (n_sets * per_set, self.layers, self.row_bytes), "ula_attend_tree drafts")
+        visible_ptr = _shaped(visible, "int64", (n_sets, nodes), "ula_attend_tree visible")
+        if lse is not None:
+            lse_ptr = _shaped(lse, "float32", (n_sets, nodes, heads), "ula_attend_tree lse")
         _same_device(q, sel, drafts, visible, out, lse, self)
         on = _On(q.device, stream, q, sel, drafts, visible, out, lse)
         with on as s:
@@ -762,7 +774,7 @@ class Engine:
             if lse is None:
                 lse = q.new_empty((n_sets, nodes, heads), dtype=torch.float32)
                 on.give(lse)
-            lse_ptr = _dev(lse, "float32", n_sets * nodes * heads, "ula_attend_tree lse")
+                lse_ptr = lse.data_ptr()
             need = lib().ula_attend_tree_bytes(ctypes.byref(fmt), n_sets, k, nodes, heads)
             work = q.new_empty(need, dtype=torch.uint8) if need else None
             args = UlaTreeArgs(UlaAttendArgs(fmt, code, heads, 1.0 / width ** 0.5 if scale is None else scale, q_ptr, st[0],
@@ -787,7 +799,9 @@ class Engine:
             raise ValueError(f"ula_weigh q: shape {tuple(q.shape)}, expected ({n_sets}, None, {width}) or one more dimension")
         q_ptr, code, st = _tensor(q, (n_sets, *(None,) * (q.dim() - 2), width), "ula_weigh q", (BF16, FP16))
         nodes, heads = (1, q.shape[1]) if q.dim() == 3 else q.shape[1:3]
-        lse_ptr = _dev(lse, "float32", n_sets * nodes * heads, "ula_weigh lse")
+        lse_ptr = _shaped(lse, "float32", q.shape[:-1], "ula_weigh lse")
+        if out is not None:
+            out_ptr = _shaped(out, "float32", (n_sets, k), "ula_weigh out")
         scores_ptr = None if scores is None else _dev(scores, "int64", self.N, "ula_weigh scores")
         _same_device(q, sel, lse, scores, out, self)
         on = _On(q.device, stream, q, sel, lse, scores, out)
@@ -796,8 +810,6 @@ class Engine:
                 out = lse.new_empty((n_sets, k))
                 on.give(out)
                 out_ptr = out.data_ptr()
-            else:
-                out_ptr = _dev(out, "float32", n_sets * k, "ula_weigh out")
             args = UlaWeighArgs(fmt, code, nodes, heads, 1.0 / width ** 0.5 if scale is None else scale, q_ptr, st[0], st[1],
                                 st[-2], lse_ptr, out_ptr, scores_ptr)
             _check(lib().ula_weigh(self.ctx, group, layer, n_sets, k, _dev(sel, "int32", n_sets * k, "ula_weigh sel"),
