@@ -589,7 +589,10 @@ typedef struct {
  * shares and added to the score of the entry's address (eviction by accumulated
  * attention weight: see ula_lightest). Scores are whole numbers in units of 2^-32, so an address that
  * is listed more than once gets the same score whatever the order of the adds. -1
- * entries have share 0 and add nothing. A row whose lse is not finite counts for
+ * entries have share 0 and add nothing. What the score was is not looked at: one that ula_lightest has
+ * set to -1, weighed again before its address is released (by another layer), is there again for
+ * the next choice. So all layers are weighed before a choice that marks, or its addresses' scores set to
+ * -1 once more after the last of them. A row whose lse is not finite counts for
  * nothing (it attended to nothing; a rejected node is left out that way). With log-sums
  * that cover more than these entries (a tree's drafted tokens) shares are of the whole.
  * A share that is NaN adds nothing to the score, one above 2^22 adds that; a score holds
@@ -624,7 +627,7 @@ size_t ula_lightest_bytes(const ula_lightest_args* args);
  * accumulated attention weight; a request's first tokens and its recent ones stay out
  * of its range), ties by lowest address, in ascending order of address: what
  * ula_release takes, once copied to the host. Entries of negative score are not there:
- * absent addresses, which the caller, or mark, set to -1. Where a range has fewer, and from
+ * absent addresses, which the caller, or mark, set to -1 (ula_weigh adds to those as to any). Where a range has fewer, and from
  * `count` on, out is -1. Ranges may be empty, and may overlap unless mark is set.
  * Nothing of an engine is involved; calls that may run at the same time need workspaces of
  * their own. It may be captured into a graph (the ranges are those of the call; the

@@ -7,7 +7,9 @@
 // The keys are read again: their weights need the whole row's log-sum, which an
 // attention split over workgroups has only once it is joined. Scores are whole
 // numbers in units of 2^-32 because adds of those commute: an address that several
-// sets list gets the same score whatever the order.
+// sets list gets the same score whatever the order. Negative scores are added to like
+// others: to leave them alone, their signs read with the keys, took 9% more (256 sets
+// x 2048 keys x 64 heads 102 -> 112 us a call: one more line for each key).
 //
 // Products are taken as Q K^T, so that a lane's column is one key: its scales are
 // the lane's own, the sum over rows stays in the lane, and only its parts in the

@@ -791,7 +791,8 @@ class Engine:
         """The softmax weight that each selected entry got in the attention that gave `lse`, summed over the query
         rows: fp32 [n_sets][k] (out, if given). q [n_sets][heads][576 or head_dim] with lse [n_sets][heads], or with
         a dimension of nodes in front of the heads, as attend and attend_tree take and give them; scale as there.
-        scores: int64 [logical_capacity] in units of 2^-32, to which each entry's weight is added at its address."""
+        scores: int64 [logical_capacity] in units of 2^-32, to which each entry's weight is added at its address,
+        whatever is there: weigh every layer before lightest marks, since a marked -1 would be a score again."""
         _no_gradient("ula_weigh", q, lse, out)
         n_sets, k = _sets(sel)
         width = LATENT_CHANNELS + ROPE_CHANNELS if fmt.kind == ROWS_LATENT else fmt.head_dim
