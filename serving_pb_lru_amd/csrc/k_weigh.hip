@@ -22,7 +22,8 @@
 
 namespace ula {
 
-// Adds of one call reach at most 2^22 (64 nodes x 2^16 heads): a NaN counts as 0.
+// A share is at most its rows, nodes x heads <= 2^16 for each token, with those rows' own log-sums; with
+// others it may be anything, and 2^22 is the most that one entry of a selection adds. A NaN adds 0.
 __device__ __forceinline__ unsigned long long score_units(float share) {
   const float x = fminf(fmaxf(share, 0.0f), 0x1p22f);   // NaN: 0
   return (unsigned long long)(long long)rint((double)x * 0x1p32);
