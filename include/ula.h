@@ -448,7 +448,7 @@ typedef struct {
   int32_t q_heads, k_heads;  /* either may be 0 */
   int32_t rotary_dim;        /* R: the first channels, which turn: even, 0..dim (0: norms alone) */
   int32_t weight_type;       /* of the weights: type or ULA_FP32 */
-  float eps;                 /* finite and > 0 */
+  float eps;                 /* 2^-126 .. 2^96 */
   const void* q;             /* [n][q_heads][dim], last dimension contiguous */
   const void* k;             /* [n][k_heads][dim] */
   void* q_out;               /* the same shapes; q and k themselves with the same strides, or no overlap with */

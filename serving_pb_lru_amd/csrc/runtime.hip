@@ -1268,7 +1268,9 @@ int ula_norm_rotate(const ula_norm_args* args, uint64_t stream) {
   if (u.dim < 2 || u.dim % 2 || u.dim > 2 * kMostPairs) return ULA_EINVAL;
   if (u.rotary_dim < 0 || u.rotary_dim % 2 || u.rotary_dim > u.dim) return ULA_EINVAL;
   if (u.weight_type != u.type && u.weight_type != ULA_FP32) return ULA_EINVAL;
-  if (!(u.eps > 0) || !std::isfinite(u.eps)) return ULA_EINVAL;
+  // squares below 2^-126 lose bits, which only an eps of that or more makes up for; and where squares overflow and
+  // are summed scaled, their mean is 2^120 or more, beside which an eps of up to 2^96 is nothing
+  if (!(u.eps >= 0x1p-126f && u.eps <= 0x1p96f)) return ULA_EINVAL;
   RotaryDev rot{};
   if (u.rotary_dim && !rotary_dev(u.rotary, u.rotary_dim / 2, &rot)) return ULA_EINVAL;
   const int wsize = u.weight_type == ULA_FP32 ? 4 : size;
