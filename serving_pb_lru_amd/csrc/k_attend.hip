@@ -27,7 +27,7 @@
 //     what it leaves goes through a second product with the same values (2.07e-4
 //     off, as a result of 64 bits rounded once, 2.9e-4 without; 384 sets of 2047 keys
 //     and 128 heads 368 us, 300 us without). A tree's results of either type go that
-//     way: bf16 ones were 1e-3 of their size from those of weights in 32 bits, 6e-5 so
+//     way: bf16 ones of one part were 1e-3 of their size from those of weights in 32 bits, 6e-5 so
 //     (16 sets x 8 nodes x 2048 keys x 128 heads 125 us, 101 us without).
 // Both products have 32-bit accumulators.
 //
@@ -45,7 +45,8 @@
 // heads to itself for both products, reading and widening every key and value
 // four times; 128 us with eight equal waves that went through first product,
 // softmax and second product in turn, which left the younger wave of a SIMD
-// waiting; 132 us with 16 heads and a whole tile's keys per first wave; 113 us so.
+// waiting; 132 us with 16 heads and a whole tile's keys per first wave; 113 us so
+// (116 since the sum of the weights takes two factors; a call 121).
 // Of that 18 us are start and end, and the 344 MB of rows alone take 58 us at the
 // rate of a large copy. In the loop the first waves' chain of products, maximum,
 // exponentials and p takes about 2500 cycles a tile; vector instructions fill 56% of
@@ -57,7 +58,7 @@
 // and widen keys twice as often: 159 us.
 // A tree of drafted tokens (TREE) has nodes x heads rows where the heads are, and two
 // tiles of keys at most behind the selected ones, whose rows come from the caller and
-// which a row sees by its node's mask. 64 sets x 1024 rows x 2048 keys, bf16: 474 us, of which each
+// which a row sees by its node's mask. 64 sets x 1024 rows x 2048 keys, bf16: 474 us a call, of which each
 // of four rounds of workgroups spends 15 us on its start (5 us for 19 MB of q), the filling
 // of the pipeline and its end.
 // Tiles: the first 640 bytes of each row as 16-byte pieces straight into LDS (no
@@ -875,8 +876,8 @@ AttendPlan plan_attend_latent(int n_sets, int k, int heads) {
 // has the rest alone. A tile is taken for 1.25 us here (64 rows; 0.9 for 32), a start and end
 // for 15; with 1.6 and 1.1, which a tile with weights in two parts is nearer to, 18 calls of
 // 1 to 257 sets took the same time to 2% but for 4 sets x 128 rows x 256 keys (22.3 us so, 23.5).
-// Measured, weights in one part, all sets the same way and so, us: 24 sets x 1024 rows x
-// 2048 keys 182, 157; 33 x 1024 x 1024 157, 131; 70 x 256 x 1024 107, 83.
+// Measured, all sets the same way and so, us a call: 24 sets x 1024 rows x 2048 keys 238,
+// 206; 33 x 1024 x 1024 200, 162; 70 x 256 x 1024 133, 100.
 AttendPlan plan_tree_latent(int n_sets, int tiles, int rows) {
   static_assert(kTileTokens == kTileKeys, "a tree's tiles are those of the kernel");
   AttendPlan best{};

@@ -14,9 +14,11 @@
 // instructions on logits bound this, not bytes; masks, a product with vs and an
 // exponent of it for each logit, in four waves that each had their own rows' tokens, took
 // 410 us a call where this takes 130 us for 32 sets x 61 nodes x 500 blocks of 8 tokens x
-// 24 heads of 64, fp16, and 80 us where this takes 32 us for 16 sets x 16 nodes x 2048
-// tokens x 32 heads of 128 over 8, bf16. In the first of the two vector instructions
-// fill 57% of a SIMD's cycles and matrix instructions 22%.) m follows the largest w as
+// 24 heads of 64, fp16, and 80 us where this takes 35 us, 30 of them the kernel's, for 16
+// sets x 16 nodes x 2048 tokens x 32 heads of 128 over 8, bf16. In the first of the two vector
+// instructions fill 57% of a SIMD's cycles and matrix instructions 22%; its form, 64 rows of 64
+// channels, spills 17 registers, most of them where drafted tiles branch; 48 rows spill none
+// and take 134 us.) m follows the largest w as
 // there: it moves, to leave the largest at 2^8, when one could pass 2^15, which each lane
 // tells from its own tokens. A negative vs turns the signs of its codes; one below 2^-80
 // makes them 0 (so l, which adds up to 2^95 for a token then, stays finite); from the first
@@ -29,9 +31,10 @@
 // itself as there, and join their results in LDS. So a set's tokens are split over fewer
 // workgroups, whose parts go through memory, than over waves. With up to 32 rows q is in
 // LDS, and a tile's products with all of them come first, a half of the keys at a time:
-// so two waves of 32 rows and heads of 128 fit a SIMD (one with q in registers: 36 us for
-// the second of the two above). With more rows q stays in registers, which leaves fewer
-// accumulators waiting (the first of the two: 130 us so, 132 us with q in LDS).
+// so two waves of 32 rows and heads of 128 fit a SIMD (the second of the two above: 32 us a
+// call, weights in one part, 36 us with one wave and q in registers). With more rows q stays
+// in registers, which leaves fewer accumulators waiting (the first of the two: 130 us so,
+// 132 us with q in LDS).
 #include <algorithm>
 #include <cmath>
 
@@ -489,12 +492,12 @@ __global__ __launch_bounds__(tree_group(D, RT) * kWave, tree_waves(D, RT)) void 
 // number of splits, with the least estimated time in us. A workgroup takes 10 for its
 // start and end, and for each of a wave's tiles the time in the table, that of a compute
 // unit full of them; the join takes 7 and its traffic.
-// Measured, with the join, us, rows of a workgroup 16, 32, 48, 64:
-//   32 sets x 732 rows x 2 KV heads of 64, 4061 tokens, fp16, one split: 175 162 133 131; two: 180 180 148 139
-//   16 sets x 64 rows x 8 KV heads of 128, 2064 tokens, bf16, one split: 45 33 45 54; two: 52 44 55 41
-//   32 sets x 128 rows x 8 KV heads of 128, 1040 tokens, bf16, one split: 83 70 77 66; two: 106 109 106 92
-//   1 set x 32 rows x 8 KV heads of 128, 4104 tokens, bf16, 1, 2, 4 splits of 32 rows: 46 32 25
-//   1 set x 512 rows x 1 KV head of 128, 2064 tokens, fp16, one split: 29 29 45 63; four: 21 21 25 31
+// Measured, us a call, rows of a workgroup 16, 32, 48, 64 (sets x rows of a KV head):
+//   32 sets x 732 rows x 2 KV heads of 64, 4061 tokens, fp16, one split: 182 163 134 132; two: 185 179 150 139
+//   16 sets x 64 rows x 8 KV heads of 128, 2064 tokens, bf16, one split: 43 33 47 60; two: 52 45 57 44
+//   32 sets x 128 rows x 8 KV heads of 128, 1056 tokens, bf16, one split: 84 71 84 73; two: 104 104 109 97
+//   1 set x 32 rows x 8 KV heads of 128, 4104 tokens, bf16, 1, 2, 4 splits of 32 rows: 45 32 25
+//   1 set x 512 rows x 1 KV head of 128, 2064 tokens, fp16, one split: 30 29 46 58; four: 26 24 26 30
 AttendPlan plan_tree_heads(int n_sets, int tiles, int rows, int kv_heads, int head_dim) {
   static constexpr double kTileUs[2][4] = {{1.1, 1.25, 1.75, 2.3}, {1.6, 2.1, 1.9, 2.7}};   // heads of 64, of 128
   constexpr double kStartUs = 10.0;
