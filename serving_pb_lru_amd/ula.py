@@ -465,7 +465,7 @@ def rotate(x, positions, sections=None, theta: float = 10000.0, interleaved: boo
 
 def norm_rotate(q, k=None, q_weight=None, k_weight=None, positions=None, sections=None, theta: float = 10000.0,
                 interleaved: bool = False, rotary: Optional[int] = None, eps: float = 1e-6, out=None, stream=None):
-    """(q, k) with each head's channels divided by their root mean square (eps inside the root) times the weights,
+    """(q, k) with each head's channels divided by their root mean square (eps, 2^-126 to 2^96, inside the root) times the weights,
     and the first `rotary` channels (default: all) turned by int32 positions [n][axes] (or [n]; none: norms
     alone), in one launch. q [n][heads][dim], k [n][kv_heads][dim] or None, bf16, fp16 or fp32; weights [dim] in
     that type or fp32, or None for ones. out: a pair of tensors shaped as q and k, themselves for in place. No

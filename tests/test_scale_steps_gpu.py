@@ -78,16 +78,17 @@ def tree_rows(dim, rng, logit, scales):
     return rows
 
 
-# latent rows, and heads rows of both widths in every number of row groups; sets, nodes
-@pytest.mark.parametrize("dim,groups,sets,nodes", [(None, 0, 300, 4)] + FORMS)
+# latent rows (whose scales count from 2^-60 on), and heads rows of both widths in every number of row groups
+STEPS = [(-30, 30, 0.1), (-50, 50, 0.0), (-60, 80, 0.0), (-60, 80, 0.1)]
+TREES = [(None, 0, 300, 4, *s) for s in STEPS] + [(*f, *s) for f in FORMS for s in STEPS + [(-80, 80, 0.0)]]
+
+
+@pytest.mark.parametrize("dim,groups,sets,nodes,low,high,against", TREES)
 @pytest.mark.parametrize("order", ORDERS)
-@pytest.mark.parametrize("low,high,against", [(-30, 30, 0.1), (-50, 50, 0.0), (-60, 80, 0.0), (-60, 80, 0.1), (-80, 80, 0.0)])
 def test_trees(dim, groups, sets, nodes, order, low, high, against):
     """A history in that order and drafted tokens of either end, the same in every set."""
     import torch
     from serving_pb_lru_amd import head_rows, latent_rows
-    if dim is None and low < -60:
-        pytest.skip("latent rows' scales count from 2^-60 on")
     if dim:
         plan = heads_plan(sets, N, nodes, len(HEADS), 1, dim)
         assert plan.groups == groups and plan.splits == 1
